@@ -29,6 +29,13 @@
  *   verify_step      -- append, verify_attn and spec_accept as one chain of
  *                       programmatic dependent launches
  *
+ * Three more take a batch of prompts into that loop and report on its tokens:
+ *   prompt_attn      -- causal attention of packed prompts of different
+ *                       lengths over their own bf16 keys and values
+ *   kv_append_packed -- kv_append_quant for the same packed rows
+ *   token_logprobs   -- log probability of given tokens, entropy and the most
+ *                       probable tokens of each logits row
+ *
  * Conventions for every call
  *   - Every pointer argument is a DEVICE pointer (cudaMalloc / torch CUDA
  *     memory on the current device) unless stated otherwise; the caller owns
@@ -176,6 +183,67 @@ int kv_append_quant(const sdva_kv_cache* cache, const void* k_new, const void* v
 int kv_append_quant_ragged(const sdva_kv_cache* cache, const void* k_new, const void* v_new, int num_lanes,
                            int n_new, const int32_t* n_lane, const int32_t* page_table, int max_pages_per_lane,
                            const int32_t* seq_lens, int32_t* status, sdva_stream_t stream);
+
+/*
+ * kv_append_packed -- kv_append_quant for lanes of different lengths packed
+ * one behind the other, as a prompt batch arrives (no counterpart in the
+ * pages, which start at the verify step).
+ *   cu_tokens  : int32 [num_lanes + 1] (device): lane b's new tokens are rows
+ *                [cu_tokens[b], cu_tokens[b + 1]) of k_new and v_new and go
+ *                to positions L_b, L_b + 1, ... of the lane; a lane may have
+ *                none.  Rows outside every lane's range are not read.
+ *   k_new, v_new: bf16, row t (one token) at k_new + t * k_stride elements,
+ *                [num_kv_heads][128] contiguous inside the row; total_tokens
+ *                rows.  Both 16-byte aligned, the strides at least
+ *                num_kv_heads * 128 and multiples of 8 (else
+ *                SDVA_ERR_INVALID), so slices of a fused projection do.
+ *   total_tokens: >= 0; 0 enqueues nothing and returns SDVA_OK.
+ * The cache holds afterwards what kv_append_quant of each lane on its own
+ * leaves, byte for byte; lanes are checked and skipped as there.  Offsets
+ * that do not satisfy 0 <= cu_tokens[0] <= cu_tokens[1] <= ... <=
+ * total_tokens set SDVA_STATUS_BAD_COUNT and nothing is written.
+ * Every other argument, precondition and return code is that of
+ * kv_append_quant.
+ */
+int kv_append_packed(const sdva_kv_cache* cache, const void* k_new, const void* v_new, int64_t k_stride,
+                     int64_t v_stride, int total_tokens, const int32_t* cu_tokens, int num_lanes,
+                     const int32_t* page_table, int max_pages_per_lane, const int32_t* seq_lens, int32_t* status,
+                     sdva_stream_t stream);
+
+/*
+ * prompt_attn -- causal attention of whole prompts, packed one behind the
+ * other, over their own keys and values: the attention of a prompt batch
+ * before its K/V go into the cache (no counterpart in the pages, which start
+ * at the verify step).  For row t of lane b, cu_tokens[b] <= t <
+ * cu_tokens[b + 1], and q head h of kv head g = h / (Hq / Hkv):
+ *     s_j       = sm_scale * q[t][h] . k[j][g],   cu_tokens[b] <= j <= t
+ *     lse[t][h] = log sum_j exp(s_j)
+ *     out[t][h] = sum_j exp(s_j - lse[t][h]) v[j][g]
+ *   q     : bf16, row t at q + t * q_stride elements, [num_q_heads][128]
+ *           contiguous inside the row; total_tokens rows.
+ *   k, v  : bf16, the same with k_stride, v_stride and [num_kv_heads][128].
+ *   The strides are at least heads * 128 and multiples of 8, the three
+ *   pointers and out 16-byte aligned (else SDVA_ERR_INVALID): slices of a
+ *   fused projection do.
+ *   cu_tokens: int32 [num_lanes + 1] (device); a lane may be empty.  Offsets
+ *           that do not satisfy 0 <= cu_tokens[0] <= ... <= total_tokens set
+ *           SDVA_STATUS_BAD_COUNT and nothing is written.
+ *   out   : bf16 [total_tokens][num_q_heads][128] (out)
+ *   lse   : fp32 [total_tokens][num_q_heads] (out, nullable)
+ *   Rows outside every lane's range are neither read into a result nor
+ *   written.  A row depends on its own lane's rows 0 .. t only: infinities
+ *   and NaN in later rows or other lanes do not reach it.  Inside a row they
+ *   behave as the formula does (a NaN score or +inf makes the row NaN).
+ * total_tokens >= 0 (0 enqueues nothing and returns SDVA_OK), num_lanes <=
+ * 1024, at most 128 q heads per kv head and 65535 kv heads (else
+ * SDVA_ERR_UNSUPPORTED), num_q_heads a multiple of num_kv_heads, sm_scale
+ * positive and finite.  Scores, running maximum, sum and output accumulate
+ * in fp32; the softmax weights are rounded to bf16 for the product with V.
+ * Returns SDVA_OK or a negative SDVA_ERR_*.
+ */
+int prompt_attn(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,
+                int num_q_heads, int num_kv_heads, int total_tokens, const int32_t* cu_tokens, int num_lanes,
+                float sm_scale, void* out, float* lse, int32_t* status, sdva_stream_t stream);
 
 /*
  * verify_attn_workspace_size -- bytes of device scratch verify_attn needs for
@@ -445,6 +513,48 @@ int spec_accept_sampled(const float* logits, const float* draft_probs, int num_l
                         const int32_t* drafts, const float* u_accept, const float* u_sample, int32_t* accept_len,
                         int32_t* out_tokens, int32_t* seq_lens_inout, void* workspace, size_t workspace_bytes,
                         int32_t* status, sdva_stream_t stream);
+
+/* Element types of token_logprobs' logits. */
+typedef enum {
+    SDVA_LOGITS_F32 = 0,
+    SDVA_LOGITS_BF16 = 1,
+    SDVA_LOGITS_F16 = 2
+} sdva_logits_dtype;
+
+#define SDVA_MAX_TOP 32 /* most tokens that token_logprobs lists per row */
+
+/*
+ * token_logprobs -- the log probability of one given token per logits row,
+ * with the row's entropy and its most probable tokens: what a server returns
+ * beside the tokens it accepted, and the score of a prompt's tokens (no
+ * counterpart in the pages, which return tokens alone).  For row r with
+ * values x_i, i in [0, vocab):
+ *     lse         = log sum_i exp(x_i)
+ *     logprobs[r] = x_t - lse, t = tokens[r]
+ *     entropy[r]  = -sum_i p_i log p_i,  p_i = exp(x_i - lse)
+ *     top_tokens[r][j], top_logprobs[r][j], j in [0, num_top): the tokens of
+ *       the largest x_i and their x_i - lse, largest first, ties to the
+ *       lowest index, a NaN below everything else
+ *   logits  : row r at logits + r * row_stride elements, of logits_dtype;
+ *             row_stride >= vocab.  Any alignment of the element type.
+ *   tokens  : int32 [num_rows] (device).  -1 marks a row that is not scored
+ *             (spec_accept_lazy's positions after the bonus token): its
+ *             logits are not read, logprobs, entropy and top_logprobs are 0
+ *             and top_tokens -1.  Any other id outside [0, vocab) sets
+ *             SDVA_STATUS_BAD_DRAFT and is treated as -1.
+ *   logprobs: fp32 [num_rows] (out); entropy: fp32 [num_rows] (out,
+ *             nullable); top_tokens: int32 and top_logprobs: fp32
+ *             [num_rows][num_top] (out, nullable when num_top == 0).
+ *   num_top : 0 .. SDVA_MAX_TOP and at most vocab.
+ * A token at -inf has log probability -inf and no part in the entropy.  A
+ * row without a distribution (all -inf, or holding +inf or NaN) gets NaN in
+ * logprobs, entropy and top_logprobs; its top_tokens still follow the order.
+ * Sums are fp32.  num_rows >= 0 (0 enqueues nothing and returns SDVA_OK).
+ * Returns SDVA_OK, SDVA_ERR_INVALID, SDVA_ERR_UNSUPPORTED or SDVA_ERR_CUDA.
+ */
+int token_logprobs(const void* logits, int logits_dtype, int64_t row_stride, int num_rows, int vocab,
+                   const int32_t* tokens, int num_top, float* logprobs, float* entropy, int32_t* top_tokens,
+                   float* top_logprobs, int32_t* status, sdva_stream_t stream);
 
 /*
  * sdva_debug_set_wait_limit -- diagnostic hook (no counterpart in the pages).

@@ -25,6 +25,10 @@ The calls mirror ``include/sdva.h``:
     spec_accept_sampled_workspace_size(num_lanes, window)
     spec_accept_sampled(logits, draft_probs, drafts, u_accept, u_sample, accept_len, out_tokens, workspace,
                         seq_lens_inout=None, status=None, stream=None)
+    kv_append_packed(cache, k_new, v_new, cu_tokens, page_table, seq_lens, status=None, stream=None)
+    prompt_attn(q, k, v, cu_tokens, sm_scale, out, lse=None, status=None, stream=None)
+    token_logprobs(logits, tokens, logprobs, entropy=None, top_tokens=None, top_logprobs=None, status=None,
+                   stream=None)
     sdva_status_string(code)
 """
 from __future__ import annotations
@@ -56,6 +60,10 @@ STATUS_BAD_DRAFT = 4
 STATUS_TIMEOUT = 8
 STATUS_BAD_COUNT = 16
 STATUS_BAD_TREE = 32
+LOGITS_F32 = 0
+LOGITS_BF16 = 1
+LOGITS_F16 = 2
+MAX_TOP = 32  # SDVA_MAX_TOP: most tokens token_logprobs lists per row
 LAZY_WALK_MIN_LANES = 48  # SDVA_LAZY_WALK_MIN_LANES: spec_accept_lazy walks rows from this many lanes on
 
 if not os.path.exists(LIB_PATH):
@@ -113,6 +121,13 @@ _lib.spec_accept_sampled_workspace_size.restype = ctypes.c_size_t
 _lib.spec_accept_sampled_workspace_size.argtypes = [_I, _I]
 _lib.spec_accept_sampled.restype = _I
 _lib.spec_accept_sampled.argtypes = [_P, _P, _I, _I, _I, _P, _P, _P, _P, _P, _P, _P, ctypes.c_size_t, _P, _P]
+_L = ctypes.c_int64
+_lib.kv_append_packed.restype = _I
+_lib.kv_append_packed.argtypes = [ctypes.POINTER(_KVCacheStruct), _P, _P, _L, _L, _I, _P, _I, _P, _I, _P, _P, _P]
+_lib.prompt_attn.restype = _I
+_lib.prompt_attn.argtypes = [_P, _P, _P, _L, _L, _L, _I, _I, _I, _P, _I, ctypes.c_float, _P, _P, _P, _P]
+_lib.token_logprobs.restype = _I
+_lib.token_logprobs.argtypes = [_P, _I, _L, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P]
 _lib.sdva_debug_set_wait_limit.restype = ctypes.c_longlong
 _lib.sdva_debug_set_wait_limit.argtypes = [ctypes.c_longlong]
 _lib.sdva_status_string.restype = ctypes.c_char_p
@@ -120,7 +135,7 @@ _lib.sdva_status_string.argtypes = [_I]
 
 EXPORTED = ("kv_append_quant", "kv_append_quant_ragged", "verify_attn_workspace_size", "verify_attn",
             "verify_attn_tree", "verify_attn_ragged", "verify_step", "verify_attn_noalloc", "spec_accept", "spec_accept_lazy", "spec_accept_tree",
-            "spec_accept_sampled_workspace_size", "spec_accept_sampled", "sdva_debug_set_wait_limit",
+            "spec_accept_sampled_workspace_size", "spec_accept_sampled", "kv_append_packed", "prompt_attn", "token_logprobs", "sdva_debug_set_wait_limit",
             "sdva_status_string")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
@@ -405,6 +420,118 @@ def spec_accept_sampled(logits: torch.Tensor, draft_probs: torch.Tensor | None, 
                                   _dptr(workspace, None, "workspace"), workspace.numel() * workspace.element_size(),
                                   _dptr(status, torch.int32, "status"), _stream(stream))
     _check("spec_accept_sampled", rc)
+
+
+def _rows(t: torch.Tensor, name: str) -> int:
+    """Elements between the token rows of a bf16 [T][H][128] tensor whose rows
+    are contiguous inside (a tensor of its own, or a slice of a fused projection)."""
+    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3 or t.shape[2] != HEAD_DIM:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor [T][H][{HEAD_DIM}]")
+    st = t.stride()
+    if st[2] != 1 or (st[1] != HEAD_DIM and t.shape[1] > 1):
+        raise ValueError(f"{name} must be contiguous inside a token row")
+    return st[0] if t.shape[0] > 1 else max(st[0], t.shape[1] * HEAD_DIM)
+
+
+def _expect(t: torch.Tensor, shape: tuple, name: str) -> None:
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+
+
+def _same_device(first: torch.Tensor, **others) -> None:
+    """Every tensor on the first one's device, which must be the current one
+    (the library enqueues on the current device)."""
+    if first.device.index != torch.cuda.current_device():
+        raise ValueError(f"the tensors are on {first.device}, the current device is {torch.cuda.current_device()}")
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+
+
+def kv_append_packed(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, cu_tokens: torch.Tensor,
+                     page_table: torch.Tensor, seq_lens: torch.Tensor, status: torch.Tensor | None = None,
+                     stream=None) -> None:
+    """k_new, v_new: bf16 [T][Hkv][128], token rows of any stride; cu_tokens int32
+    [B + 1]: lane b appends rows cu_tokens[b] .. cu_tokens[b + 1] - 1; page_table
+    int32 [B][max_pages]; seq_lens int32 [B]."""
+    T, B = k_new.shape[0], seq_lens.shape[0]
+    ks, vs = _rows(k_new, "k_new"), _rows(v_new, "v_new")
+    _expect(k_new, (T, cache.num_kv_heads, HEAD_DIM), "k_new")
+    _expect(v_new, (T, cache.num_kv_heads, HEAD_DIM), "v_new")
+    _expect(cu_tokens, (B + 1,), "cu_tokens")
+    _expect(page_table, (B, page_table.shape[-1]), "page_table")
+    _same_device(k_new, v_new=v_new, cu_tokens=cu_tokens, page_table=page_table, seq_lens=seq_lens,
+                 cache=cache.k_codes, status=status)
+    s = cache.struct()
+    rc = _lib.kv_append_packed(ctypes.byref(s), k_new.data_ptr(), v_new.data_ptr(), ks, vs, T,
+                               _dptr(cu_tokens, torch.int32, "cu_tokens"), B,
+                               _dptr(page_table, torch.int32, "page_table"), page_table.shape[1],
+                               _dptr(seq_lens, torch.int32, "seq_lens"), _dptr(status, torch.int32, "status"),
+                               _stream(stream))
+    _check("kv_append_packed", rc)
+
+
+def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_tokens: torch.Tensor, sm_scale: float,
+                out: torch.Tensor, lse: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                stream=None) -> None:
+    """q bf16 [T][Hq][128], k, v bf16 [T][Hkv][128], token rows of any stride;
+    cu_tokens int32 [B + 1]; out bf16 [T][Hq][128]; lse fp32 [T][Hq]."""
+    qs, ks, vs = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
+    T, Hq, Hkv = q.shape[0], q.shape[1], k.shape[1]
+    _expect(k, (T, Hkv, HEAD_DIM), "k")
+    _expect(v, (T, Hkv, HEAD_DIM), "v")
+    _expect(out, (T, Hq, HEAD_DIM), "out")
+    if lse is not None:
+        _expect(lse, (T, Hq), "lse")
+    if cu_tokens.dim() != 1:
+        raise ValueError("cu_tokens must be [B + 1]")
+    _same_device(q, k=k, v=v, cu_tokens=cu_tokens, out=out, lse=lse, status=status)
+    rc = _lib.prompt_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, Hq, Hkv, T,
+                          _dptr(cu_tokens, torch.int32, "cu_tokens"), cu_tokens.shape[0] - 1, float(sm_scale),
+                          _dptr(out, torch.bfloat16, "out"), _dptr(lse, torch.float32, "lse"),
+                          _dptr(status, torch.int32, "status"), _stream(stream))
+    _check("prompt_attn", rc)
+
+
+_LOGITS = {torch.float32: LOGITS_F32, torch.bfloat16: LOGITS_BF16, torch.float16: LOGITS_F16}
+
+
+def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: torch.Tensor,
+                   entropy: torch.Tensor | None = None, top_tokens: torch.Tensor | None = None,
+                   top_logprobs: torch.Tensor | None = None, status: torch.Tensor | None = None, stream=None) -> None:
+    """logits fp32, bf16 or fp16 [N][V] (rows of any stride) or contiguous
+    [B][W][V]; tokens int32 [N] or [B][W] (-1: row not scored); logprobs,
+    entropy fp32 like tokens; top_tokens int32, top_logprobs fp32 with a last
+    axis of the number of tokens to list (both or neither)."""
+    if logits.dtype not in _LOGITS or not logits.is_cuda:
+        raise ValueError("logits must be a float32, bfloat16 or float16 CUDA tensor")
+    lead, V = tuple(logits.shape[:-1]), logits.shape[-1]
+    if len(lead) == 1:
+        if logits.stride(1) != 1 and V > 1:
+            raise ValueError("logits must be contiguous inside a row")
+        stride = logits.stride(0) if lead[0] > 1 else max(logits.stride(0), V)
+    else:
+        if not logits.is_contiguous():
+            raise ValueError("logits must be [N][V] or contiguous")
+        stride = V
+    _expect(tokens, lead, "tokens")
+    _expect(logprobs, lead, "logprobs")
+    if entropy is not None:
+        _expect(entropy, lead, "entropy")
+    if (top_tokens is None) != (top_logprobs is None):
+        raise ValueError("top_tokens and top_logprobs go together")
+    top = 0 if top_tokens is None else top_tokens.shape[-1]
+    if top_tokens is not None:
+        _expect(top_tokens, lead + (top,), "top_tokens")
+        _expect(top_logprobs, lead + (top,), "top_logprobs")
+    _same_device(logits, tokens=tokens, logprobs=logprobs, entropy=entropy, top_tokens=top_tokens,
+                 top_logprobs=top_logprobs, status=status)
+    rc = _lib.token_logprobs(logits.data_ptr(), _LOGITS[logits.dtype], stride, tokens.numel(), V,
+                             _dptr(tokens, torch.int32, "tokens"), top, _dptr(logprobs, torch.float32, "logprobs"),
+                             _dptr(entropy, torch.float32, "entropy"), _dptr(top_tokens, torch.int32, "top_tokens"),
+                             _dptr(top_logprobs, torch.float32, "top_logprobs"),
+                             _dptr(status, torch.int32, "status"), _stream(stream))
+    _check("token_logprobs", rc)
 
 
 def raw_library() -> ctypes.CDLL:
