@@ -558,7 +558,7 @@ int token_logprobs(const void* logits, int logits_dtype, int64_t row_stride, int
 
 /*
  * sdva_debug_set_wait_limit -- diagnostic hook (no counterpart in the pages).
- * Every device-side wait of verify_attn's tensor-core kernels gives up after
+ * Every device-side wait of verify_attn's and prompt_attn's tensor-core kernels gives up after
  * `cycles` clock cycles (default about 4e9, two seconds); the CTA then
  * raises SDVA_STATUS_TIMEOUT, waits (with its own bound) for the copies and
  * tensor-core work it issued, frees its tensor memory and returns, leaving

@@ -4,76 +4,588 @@
 // For row t of a lane and q head h of kv head g:  s_j = scale q_t . k_j over
 // the lane's rows j <= t, out = sum_j exp(s_j - lse) v_j, lse = log sum exp s_j,
 // in one pass over the keys with the running maximum and sum.
+//
+// A tile is 2 x T consecutive rows of one kv head, T = 128 / G: each of its
+// two halves fills the 128 rows of a tensor-core tile with T tokens x G q
+// heads (row r = token r / G, head r % G), so that a group's heads share the
+// K/V tiles and few rows are empty whatever the group.  Twelve warps:
+//   * warp 8 (loader): takes the next tile, TMA-loads its Q and the K and V
+//     blocks of 128 keys into a ring of five 32 KB stages;
+//   * warps 9, 10 (issuers, one per half): S = Q K^T into tensor memory, then
+//     per block O += P V and the next S = Q K^T, so that one half's softmax
+//     runs under the other half's products;
+//   * warp 11 (guard): V rows behind a tile's first row are hidden from some
+//     of its rows, but a weight of 0 does not hide an infinity or a NaN from
+//     a product; it takes such values out of the V block in shared memory
+//     before the product reads it, and marks the tile, whose rows then add
+//     those they do see from global memory;
+//   * warps 0-3 and 4-7 (softmax, one warpgroup per half): a thread owns a
+//     row: reads its 128 scores, masks the last blocks, keeps the running
+//     maximum and sum, writes P as bf16 over the scores.  Once the QK of a
+//     block is done, so is the PV before it (one issuer, in order), so the
+//     thread may rescale its O in place; it does only when the maximum grows
+//     by more than kLag (a factor of 256, which fp32 sums and bf16 weights
+//     carry without loss).  At the end it divides by the sum and stores.
+// Every wait is bounded: on timeout the CTA raises SDVA_STATUS_TIMEOUT,
+// drains its copies and products, frees tensor memory and returns.
 #include <math.h>
 
-#include "sdva_common.cuh"
 #include "sdva_internal.cuh"
+#include "tc_primitives.cuh"
+#include "verify_attn_tc.cuh"
 
 namespace sdva {
 namespace {
 
+using namespace tc;
+
 constexpr int kMaxPromptLanes = 1024;
-constexpr int kThreads = 256;
+constexpr int kBlock = 128;  // keys per K or V block
+constexpr int kThreads = 384;
+constexpr int kLoaderWarp = 8, kIssueWarp = 9, kGuardWarp = 11;
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
+static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
+constexpr int kStages = 5;
+constexpr uint32_t kStageBytes = kBlock * kHeadDim * 2;  // two 64-dim panels of 128 rows x 128 bytes
+constexpr uint32_t kPanel = kStageBytes / 2;
+constexpr uint32_t kOffKv = 2 * kStageBytes;  // behind the Q of both halves
+constexpr uint32_t kOffCtl = kOffKv + kStages * kStageBytes;
+constexpr int kGuardRing = 8;  // guarded blocks between the guard and an issuer: fewer than stages
+constexpr float kLag = 8.0f;   // log2 units
+constexpr float kLog2e = 1.4426950408889634f;
+// tensor memory: S (fp32, 128 columns) of half s, overlaid by its P (bf16, 64 columns); O (fp32, 128 columns)
+__device__ __forceinline__ uint32_t col_s(int s) { return 128u * s; }
+__device__ __forceinline__ uint32_t col_o(int s) { return 256u + 128u * s; }
+constexpr uint32_t kTmemCols = 512;
+// kind::f16 with bf16 A and B (formats 1 at bits 7 and 10), fp32 D; Q K^T with both K-major, P V with V MN-major
+constexpr uint32_t kBf16 = (1u << 7) | (1u << 10);
+constexpr uint32_t kIdescQK = idesc_f16(128, kBlock, 0) | kBf16;
+constexpr uint32_t kIdescPV = idesc_f16(128, kHeadDim, 1) | kBf16;
 
 struct PromptArgs {
-  const uint16_t* q;
-  const uint16_t* k;
   const uint16_t* v;
-  long long q_stride, k_stride, v_stride;
+  long long v_stride;
   const int32_t* cu;
   uint16_t* out;
   float* lse;
   int32_t* status;
-  int Hq, G, total, num_lanes;
-  float scale_log2;
+  int Hq, Hkv, G, T, total, num_lanes;
+  float scale, scale_log2;
+  long long wait_limit;
 };
 
-// One warp per (row, q head), 4 dims a lane.
-__global__ void __launch_bounds__(kThreads) prompt_attn_kernel(PromptArgs a) {
+struct Tile {
+  int row0, len;  // the lane's first row and rows; len 0: no more tiles
+  int t0, hk;     // first row of the tile inside the lane, kv head
+  int dirty;      // the guard took values out that some of the tile's rows see
+};
+
+struct Ctl {
+  uint64_t q_full, q_free, full[kStages], empty[kStages];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2], drain[2];
+  uint64_t guarded[kGuardRing];
+  uint64_t tile_full[2], tile_free[2], tile_guarded[2];
+  Tile tile[2];
+  uint32_t tmem_base;
+  int abort;
+};
+constexpr size_t kSmemBytes = 1024 + kOffCtl + sizeof(Ctl);
+static_assert(kSmemBytes <= 232448, "shared memory budget");
+
+// K/V blocks of a half whose rows end before row `end` of the lane.
+__device__ __forceinline__ int blocks_to(int end) { return (end + kBlock - 1) / kBlock; }
+
+struct Shape {
+  int end, n[2], total;  // the tile's last row + 1; blocks of each half; blocks loaded
+  __device__ Shape(const Tile& t, int T) {
+    end = (int)min((long long)t.t0 + 2 * T, (long long)t.len);
+    n[0] = blocks_to(min(t.t0 + T, t.len));
+    n[1] = t.len - t.t0 > T ? blocks_to(end) : 0;
+    total = max(n[0], n[1]);
+  }
+};
+
+// Which tile comes r-th.  Tiles are taken with the longest rows first over
+// all lanes (a tile's work grows with its position), so that the last ones
+// are short.  A lane with n tiles has one at each position below n; between
+// two successive tile counts of the batch the number of lanes that reach a
+// position stays the same, which turns a rank into a position by one division
+// per distinct count.  Ranks a CTA asks for only grow, so it keeps its place.
+struct Order {
+  const int32_t* cu;
+  int B, span, lane;
+  int cur, next, count;  // tile counts: the largest not yet passed, the one below; lanes that reach `cur`
+  long long base;        // tiles of longer positions
+
+  __device__ int tiles(int b) const { return (cu[b + 1] - cu[b] + span - 1) / span; }
+  __device__ void scan() {
+    int c = 0, m = 0;
+    for (int b = lane; b < B; b += 32) {
+      const int n = tiles(b);
+      if (n >= cur) ++c;
+      else m = max(m, n);
+    }
+    count = __reduce_add_sync(0xffffffffu, c);
+    next = __reduce_max_sync(0xffffffffu, m);
+  }
+  __device__ void init(const int32_t* cu_, int B_, int span_, int lane_) {
+    cu = cu_;
+    B = B_;
+    span = span_;
+    lane = lane_;
+    cur = 0x7fffffff;
+    scan();
+    cur = next;
+    base = 0;
+    if (cur > 0) scan();
+  }
+  // lane and position of tile r; false when there is none
+  __device__ bool find(long long r, int* b_out, int* pos) {
+    while (cur > 0 && r >= base + (long long)count * (cur - next)) {
+      base += (long long)count * (cur - next);
+      cur = next;
+      if (cur > 0) scan();
+    }
+    if (cur <= 0) return false;
+    const long long o = r - base;
+    *pos = cur - 1 - (int)(o / count);
+    int k = (int)(o % count);  // the k-th lane of those that reach cur
+    for (int b = 0; b < B; b += 32) {
+      const unsigned has = __ballot_sync(0xffffffffu, b + lane < B && tiles(min(b + lane, B - 1)) >= cur);
+      const int c = __popc(has);
+      if (k < c) {
+        *b_out = b + (int)__fns(has, 0, k + 1);
+        return true;
+      }
+      k -= c;
+    }
+    return false;
+  }
+};
+
+__device__ __forceinline__ void give_up(Ctl* ctl, int32_t* status) {
+  if ((threadIdx.x & 31) == 0) {
+    ctl->abort = 1;
+    raise_status(status, SDVA_STATUS_TIMEOUT);
+  }
+}
+
+// One barrier with its phase, as one role sees it.
+struct Phase {
+  uint32_t bit = 0;
+  __device__ uint32_t take() {
+    const uint32_t b = bit;
+    bit ^= 1u;
+    return b;
+  }
+};
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
+          dst),
+      "l"(map), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ bool any_nonfinite(uint4 w) {
+  // an exponent of all ones carries into bit 15 of its half
+  const uint32_t c = ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+                     ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+  return (c & 0x80008000u) != 0;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    prompt_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
+                       const __grid_constant__ CUtensorMap mv, const PromptArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const gen = smem_raw + (base - smem_u32(smem_raw));
+  Ctl* const ctl = reinterpret_cast<Ctl*>(gen + kOffCtl);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
   int bad = 0;
   for (int i = threadIdx.x; i < a.num_lanes; i += kThreads) {
     const int lo = a.cu[i], hi = a.cu[i + 1];
     bad |= lo < 0 || hi < lo || hi > a.total;
   }
+  if (threadIdx.x == 0) {
+    mbar_init(smem_u32(&ctl->q_full), 1);
+    mbar_init(smem_u32(&ctl->q_free), 2);
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(smem_u32(&ctl->full[i]), 1);
+      mbar_init(smem_u32(&ctl->empty[i]), 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctl->s_full[i]), 1);
+      mbar_init(smem_u32(&ctl->p_full[i]), 4);
+      mbar_init(smem_u32(&ctl->o_full[i]), 1);
+      mbar_init(smem_u32(&ctl->o_free[i]), 4);
+      mbar_init(smem_u32(&ctl->drain[i]), 1);
+      mbar_init(smem_u32(&ctl->tile_full[i]), 1);
+      mbar_init(smem_u32(&ctl->tile_free[i]), 11);  // both issuers, the guard, eight softmax warps
+      mbar_init(smem_u32(&ctl->tile_guarded[i]), 1);
+    }
+    for (int i = 0; i < kGuardRing; ++i) mbar_init(smem_u32(&ctl->guarded[i]), 1);
+    ctl->abort = 0;
+    mbar_fence_init();
+  }
   if (__syncthreads_or(bad)) {
     if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(a.status, SDVA_STATUS_BAD_COUNT);
     return;
   }
-  const int lane = threadIdx.x & 31;
-  const long long id = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
-  if (id >= (long long)a.total * a.Hq) return;
-  const int t = (int)(id / a.Hq), h = (int)(id % a.Hq);
-  int lo = 0, hi = a.num_lanes;  // the last lane that starts at or before t
-  if (t < a.cu[0] || t >= a.cu[a.num_lanes]) return;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (a.cu[mid] <= t) lo = mid;
-    else hi = mid;
-  }
-  const size_t col = (size_t)(h / a.G) * kHeadDim + lane * 4;
-  const uint2 qw = *reinterpret_cast<const uint2*>(a.q + (size_t)t * a.q_stride + (size_t)h * kHeadDim + lane * 4);
-  const float q0 = bf16_lo(qw.x), q1 = bf16_hi(qw.x), q2 = bf16_lo(qw.y), q3 = bf16_hi(qw.y);
-  float m = __int_as_float(0xff800000), l = 0.0f, o0 = 0.0f, o1 = 0.0f, o2 = 0.0f, o3 = 0.0f;
-  for (int j = a.cu[lo]; j <= t; ++j) {
-    const uint2 kw = *reinterpret_cast<const uint2*>(a.k + (size_t)j * a.k_stride + col);
-    const uint2 vw = *reinterpret_cast<const uint2*>(a.v + (size_t)j * a.v_stride + col);
-    float s = q0 * bf16_lo(kw.x) + q1 * bf16_hi(kw.x) + q2 * bf16_lo(kw.y) + q3 * bf16_hi(kw.y);
+  if (warp == kLoaderWarp) tmem_alloc(smem_u32(&ctl->tmem_base), kTmemCols);
+  fence_before_sync();
+  __syncthreads();
+  fence_after_sync();
+  const uint32_t tmem = ctl->tmem_base;
+  volatile int* const abort_flag = &ctl->abort;
+  const long long limit = a.wait_limit;
+  auto spin = [&](uint64_t& bar, uint32_t parity) { return mbar_wait<true>(smem_u32(&bar), parity, abort_flag, limit); };
+  auto doze = [&](uint64_t& bar, uint32_t parity) { return mbar_wait<false>(smem_u32(&bar), parity, abort_flag, limit); };
+
+  if (warp >= kLoaderWarp) {
+    regs_decrease<kRegsOther>();
+    bool ok = true;
+    if (warp == kLoaderWarp) {
+      Order order;
+      order.init(a.cu, a.num_lanes, 2 * a.T, lane);
+      const uint32_t half_bytes = (uint32_t)(a.G * a.T) * 128u;  // one 64-dim panel of one half's Q
+      long long fills = 0;  // stage fills issued
+      int q_loads = 0;
+      auto load = [&](const CUtensorMap* map, int hk, int row) {
+        const int s = (int)(fills % kStages);
+        if (fills >= kStages && !doze(ctl->empty[s], (uint32_t)((fills / kStages - 1) & 1))) return false;
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&ctl->full[s]), dst = base + kOffKv + s * kStageBytes;
+          mbar_arrive_expect_tx(bar, kStageBytes);
+          tma_load_3d(dst, map, 0, hk, row, bar);
+          tma_load_3d(dst + kPanel, map, 64, hk, row, bar);
+        }
+        __syncwarp();
+        ++fills;
+        return true;
+      };
+      for (int i = 0;; ++i) {
+        const int slot = i & 1;
+        const long long r = blockIdx.x + (long long)i * gridDim.x;
+        Tile t = {0, 0, 0, (int)(r % a.Hkv), 0};
+        int b, pos;
+        if (order.find(r / a.Hkv, &b, &pos)) {
+          t.row0 = a.cu[b];
+          t.len = a.cu[b + 1] - t.row0;
+          t.t0 = pos * 2 * a.T;
+        }
+        if (i >= 2 && !(ok = doze(ctl->tile_free[slot], (uint32_t)((i / 2 - 1) & 1)))) break;
+        if (lane == 0) {
+          ctl->tile[slot] = t;
+          mbar_arrive(smem_u32(&ctl->tile_full[slot]));
+        }
+        __syncwarp();
+        if (t.len == 0) break;
+        const Shape sh(t, a.T);
+        if (i >= 1 && !(ok = doze(ctl->q_free, (uint32_t)((i - 1) & 1)))) break;
+        if (lane == 0) {
+          const uint32_t bar = smem_u32(&ctl->q_full);
+          mbar_arrive_expect_tx(bar, half_bytes * (sh.n[1] ? 4u : 2u));
+          for (int s = 0; s < (sh.n[1] ? 2 : 1); ++s)
+            for (int p = 0; p < 2; ++p)
+              tma_load_3d(base + s * kStageBytes + p * kPanel, &mq, 64 * p, t.hk * a.G, t.row0 + t.t0 + s * a.T, bar);
+        }
+        __syncwarp();
+        ++q_loads;
+        for (int j = 0; j < sh.total && ok; ++j)
+          ok = load(&mk, t.hk, t.row0 + j * kBlock) && load(&mv, t.hk, t.row0 + j * kBlock);
+        if (!ok) break;
+      }
+      if (!ok) {
+        give_up(ctl, a.status);
+        // this warp's copies still in flight (bounded)
+        int none = 0;
+        for (long long f = max(0LL, fills - kStages); f < fills; ++f)
+          mbar_wait<false>(smem_u32(&ctl->full[f % kStages]), (uint32_t)((f / kStages) & 1), &none, 400000000LL);
+        if (q_loads) mbar_wait<false>(smem_u32(&ctl->q_full), (uint32_t)((q_loads - 1) & 1), &none, 400000000LL);
+      }
+    } else if (warp < kGuardWarp) {
+      const int s = warp - kIssueWarp;
+      const uint32_t d_s = tmem + col_s(s), d_o = tmem + col_o(s);
+      long long stage0 = 0;       // stage fills of the tiles before
+      long long guard0 = 0;       // guarded blocks of the tiles before
+      Phase p_phase, o_phase;
+      bool first = true;
+      auto wait_stage = [&](long long f) { return spin(ctl->full[f % kStages], (uint32_t)((f / kStages) & 1)); };
+      auto commit_stage = [&](long long f) { mma_commit(smem_u32(&ctl->empty[f % kStages])); };
+      for (int i = 0; ok; ++i) {
+        const int slot = i & 1;
+        if (!(ok = spin(ctl->tile_full[slot], (uint32_t)((i / 2) & 1)))) break;
+        const Tile t = ctl->tile[slot];
+        if (t.len == 0) break;
+        const Shape sh(t, a.T);
+        const int n = sh.n[s], guard_from = (t.t0 + 1) / kBlock;
+        if (!(ok = spin(ctl->q_full, (uint32_t)(i & 1)))) break;
+        auto qk = [&](int j) {
+          const long long f = stage0 + 2 * j;
+          if (!wait_stage(f)) return false;
+          fence_after_sync();
+          if (lane == 0) {
+            const uint32_t qt = base + s * kStageBytes, kt = base + kOffKv + (uint32_t)(f % kStages) * kStageBytes;
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-    s *= a.scale_log2;
-    const float mn = fmaxf(m, s);
-    const float c = m == mn ? 1.0f : fast_exp2(m - mn), p = fast_exp2(s - mn);
-    m = mn;
-    l = l * c + p;
-    o0 = o0 * c + p * bf16_lo(vw.x);
-    o1 = o1 * c + p * bf16_hi(vw.x);
-    o2 = o2 * c + p * bf16_lo(vw.y);
-    o3 = o3 * c + p * bf16_hi(vw.y);
+            for (int k = 0; k < 8; ++k)
+              mma_f16_ss(d_s, sdesc_sw128(qt + kPanel * (k >> 2) + 32 * (k & 3), 1024, 1024),
+                         sdesc_sw128(kt + kPanel * (k >> 2) + 32 * (k & 3), 1024, 1024), kIdescQK, k != 0);
+            mma_commit(smem_u32(&ctl->s_full[s]));
+            commit_stage(f);
+            if (j == n - 1) mma_commit(smem_u32(&ctl->q_free));
+          }
+          __syncwarp();
+          return true;
+        };
+        if (n > 0) {
+          if (!(ok = qk(0))) break;
+          for (int j = 0; j < n; ++j) {
+            const long long f = stage0 + 2 * j + 1;
+            if (!(ok = spin(ctl->p_full[s], p_phase.take()))) break;
+            if (j == 0 && !first && !(ok = spin(ctl->o_free[s], o_phase.take()))) break;
+            if (!(ok = wait_stage(f))) break;
+            if (j >= guard_from) {
+              const long long gb = guard0 + j - guard_from;
+              if (!(ok = spin(ctl->guarded[gb % kGuardRing], (uint32_t)((gb / kGuardRing) & 1)))) break;
+            }
+            fence_after_sync();
+            if (lane == 0) {
+              const uint32_t vt = base + kOffKv + (uint32_t)(f % kStages) * kStageBytes;
+#pragma unroll
+              for (int k = 0; k < 8; ++k)
+                mma_f16_ts(d_o, d_s + 8 * k, sdesc_sw128(vt + 2048 * k, kPanel, 1024), kIdescPV, j != 0 || k != 0);
+              commit_stage(f);
+              if (j == n - 1) mma_commit(smem_u32(&ctl->o_full[s]));
+            }
+            __syncwarp();
+            if (j + 1 < n && !(ok = qk(j + 1))) break;
+          }
+          if (!ok) break;
+          first = false;
+        } else if (lane == 0) {
+          mbar_arrive(smem_u32(&ctl->q_free));
+        }
+        // blocks that only the other half reads
+        for (int j = n; j < sh.total && ok; ++j)
+          for (int k = 0; k < 2 && ok; ++k) {
+            const long long f = stage0 + 2 * j + k;
+            if ((ok = wait_stage(f)) && lane == 0) mbar_arrive(smem_u32(&ctl->empty[f % kStages]));
+          }
+        if (!ok) break;
+        stage0 += 2 * sh.total;
+        guard0 += max(0, sh.total - guard_from);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->tile_free[slot]));
+      }
+      if (!ok) give_up(ctl, a.status);
+      // the tensor core is done with everything this thread issued (bounded)
+      if (lane == 0) mma_commit(smem_u32(&ctl->drain[s]));
+      __syncwarp();
+      int none = 0;
+      mbar_wait<false>(smem_u32(&ctl->drain[s]), 0, &none, 400000000LL);
+    } else {
+      long long stage0 = 0, guard0 = 0;
+      for (int i = 0; ok; ++i) {
+        const int slot = i & 1;
+        if (!(ok = doze(ctl->tile_full[slot], (uint32_t)((i / 2) & 1)))) break;
+        const Tile t = ctl->tile[slot];
+        if (t.len == 0) break;
+        const Shape sh(t, a.T);
+        for (int j = (t.t0 + 1) / kBlock; j < sh.total; ++j, ++guard0) {
+          const long long f = stage0 + 2 * j + 1;
+          if (!(ok = doze(ctl->full[f % kStages], (uint32_t)((f / kStages) & 1)))) break;
+          uint8_t* const vt = gen + kOffKv + (uint32_t)(f % kStages) * kStageBytes;
+          const int from = max(0, t.t0 + 1 - j * kBlock) * 128;  // bytes of the rows every row of the tile sees
+          bool found = false;
+#pragma unroll 8
+          for (int o = from + 16 * lane; o < (int)kPanel; o += 512)
+            found |= any_nonfinite(*reinterpret_cast<const uint4*>(vt + o)) ||
+                     any_nonfinite(*reinterpret_cast<const uint4*>(vt + kPanel + o));
+          if (__any_sync(0xffffffffu, found)) {
+            bool seen = false;
+            for (int o = from + 2 * lane; o < (int)kPanel; o += 64)
+              for (int p = 0; p < 2; ++p) {
+                uint16_t* const x = reinterpret_cast<uint16_t*>(vt + p * kPanel + o);
+                if ((*x & 0x7F80u) == 0x7F80u) {
+                  *x = 0;
+                  seen |= j * kBlock + o / 128 < sh.end;
+                }
+              }
+            if (__any_sync(0xffffffffu, seen) && lane == 0) ctl->tile[slot].dirty = 1;
+            fence_proxy_async_smem();
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->guarded[guard0 % kGuardRing]));
+          __syncwarp();
+        }
+        if (!ok) break;
+        stage0 += 2 * sh.total;
+        if (lane == 0) {
+          mbar_arrive(smem_u32(&ctl->tile_guarded[slot]));
+          mbar_arrive(smem_u32(&ctl->tile_free[slot]));
+        }
+        __syncwarp();
+      }
+      if (!ok) give_up(ctl, a.status);
+    }
+  } else {
+    regs_increase<kRegsSoftmax>();
+    const int s = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // TMEM lane 32 * (warp % 4) in bits 16 and up
+    const uint32_t t_s = tmem + lane_base + col_s(s), t_o = tmem + lane_base + col_o(s);
+    const int r_tok = row / a.G, r_head = row % a.G;
+    const int w_tok = (row & ~31) / a.G;  // the warp's first token
+    const float ninf = __int_as_float(0xff800000);
+    Phase s_phase, o_phase;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const int slot = i & 1;
+      if (!(ok = spin(ctl->tile_full[slot], (uint32_t)((i / 2) & 1)))) break;
+      const Tile t = ctl->tile[slot];
+      if (t.len == 0) break;
+      const Shape sh(t, a.T);
+      const int n = sh.n[s], first = t.t0 + s * a.T;
+      const int tok = first + r_tok;
+      const bool valid = r_tok < a.T && tok < t.len;
+      float m = ninf;
+      float l = 0.0f;
+      for (int j = 0; j < n; ++j) {
+        if (!(ok = spin(ctl->s_full[s], s_phase.take()))) break;
+        fence_after_sync();
+        uint32_t x[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(t_s + 32 * c, x[c]);
+        tmem_wait_ld();
+        if ((j + 1) * kBlock > first + w_tok + 1) {  // some row of the warp does not see the whole block
+          const int seen = tok - j * kBlock + 1;
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (32 * c + k >= seen) x[c][k] = 0xff800000u;
+        }
+        float mx[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          mx[c] = fmaxf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
+#pragma unroll
+          for (int k = 2; k < 32; k += 2)
+            mx[c] = fmax3(mx[c], __uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1]));
+        }
+        const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
+        // the first block always grows (from -inf); a NaN never does
+        const bool grow = (top - m) * a.scale_log2 > kLag;
+        if (__any_sync(0xffffffffu, grow && valid)) {
+          const float f = grow ? fast_exp2((m - top) * a.scale_log2) : 1.0f;
+          if (grow) m = top;
+          l *= f;
+          if (j > 0) {
+#pragma unroll 1
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tmem_ld16(t_o + 16 * c, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st16(t_o + 16 * c, o);
+            }
+          }
+        }
+        const float shift = m == ninf ? 0.0f : -m * a.scale_log2;  // all scores -inf so far: weights of 0
+        const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), sh2 = f2_pack(shift, shift);
+        unsigned long long sum0 = 0ull, sum1 = 0ull;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t p[16];
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) {
+            const float2 e = f2_unpack(ffma2(f2_pack(__uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1])), sc2, sh2));
+            const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+            if (k & 2) sum1 = fadd2(sum1, f2_pack(e0, e1));
+            else sum0 = fadd2(sum0, f2_pack(e0, e1));
+            p[k / 2] = pack_bf16x2(e0, e1);
+          }
+          tmem_st16(t_s + 16 * c, p);
+        }
+        const float2 sum = f2_unpack(fadd2(sum0, sum1));
+        l += sum.x + sum.y;
+        tmem_wait_st();
+        fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[s]));
+      }
+      if (!ok) break;
+      if (!(ok = spin(ctl->tile_guarded[slot], (uint32_t)((i / 2) & 1)))) break;
+      const bool dirty = ctl->tile[slot].dirty != 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->tile_free[slot]));
+      if (n == 0) continue;
+      if (!(ok = spin(ctl->o_full[s], o_phase.take()))) break;
+      fence_after_sync();
+      const float inv = 1.0f / l;
+      const size_t at = (size_t)(t.row0 + tok) * a.Hq + (size_t)t.hk * a.G + r_head;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        tmem_ld32(t_o + 32 * c, o);
+        tmem_wait_ld();
+        if (c == 3) {
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->o_free[s]));
+        }
+#pragma unroll
+        for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
+        if (dirty && valid) {
+          // infinities and NaN that the guard took out, from the rows this one sees
+          for (int key = t.t0 + 1; key <= tok; ++key) {
+            const uint16_t* v = a.v + (size_t)(t.row0 + key) * a.v_stride + (size_t)t.hk * kHeadDim + 32 * c;
+#pragma unroll
+            for (int k = 0; k < 32; ++k) {
+              const uint32_t w = v[k];
+              if ((w & 0x7F80u) == 0x7F80u)
+                o[k] = __float_as_uint(__uint_as_float(o[k]) + __uint_as_float(w << 16));
+            }
+          }
+        }
+        if (valid) {
+          uint4* dst = reinterpret_cast<uint4*>(a.out + at * kHeadDim + 32 * c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            dst[k] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * k]), __uint_as_float(o[8 * k + 1])),
+                                pack_bf16x2(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3])),
+                                pack_bf16x2(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5])),
+                                pack_bf16x2(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7])));
+        }
+      }
+      if (valid && a.lse != nullptr) a.lse[at] = m * a.scale + logf(l);
+    }
+    if (!ok) give_up(ctl, a.status);
   }
-  const float inv = 1.0f / l;
-  *reinterpret_cast<uint2*>(a.out + ((size_t)t * a.Hq + h) * kHeadDim + lane * 4) =
-      make_uint2(pack_bf16x2(o0 * inv, o1 * inv), pack_bf16x2(o2 * inv, o3 * inv));
-  if (lane == 0 && a.lse != nullptr) a.lse[(size_t)t * a.Hq + h] = m * 0.6931471805599453f + logf(l);
+
+  fence_before_sync();
+  __syncthreads();
+  if (warp == kLoaderWarp) {
+    fence_after_sync();
+    tmem_dealloc(tmem, kTmemCols);
+  }
+}
+
+// rows x heads x 128 bf16 with `stride` elements between rows, loaded in boxes
+// of 64 dims x `heads` heads x `rows` rows with the 128-byte swizzle
+bool encode_rows(CUtensorMap* m, const void* p, int64_t stride, int num_heads, int total, int heads, int rows) {
+  EncodeTiledFn enc = encoder();
+  if (enc == nullptr) return false;
+  cuuint64_t dims[3] = {(cuuint64_t)kHeadDim, (cuuint64_t)num_heads, (cuuint64_t)total};
+  cuuint64_t strides[2] = {(cuuint64_t)kHeadDim * 2, (cuuint64_t)stride * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)rows};
+  cuuint32_t es[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, es,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -98,25 +610,39 @@ extern "C" int prompt_attn(const void* q, const void* k, const void* v, int64_t 
     return SDVA_ERR_INVALID;
   const int G = num_q_heads / num_kv_heads;
   if (num_lanes > kMaxPromptLanes || G > 128 || num_kv_heads > 65535) return SDVA_ERR_UNSUPPORTED;
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SDVA_ERR_CUDA;
   PromptArgs a;
-  a.q = static_cast<const uint16_t*>(q);
-  a.k = static_cast<const uint16_t*>(k);
   a.v = static_cast<const uint16_t*>(v);
-  a.q_stride = q_stride;
-  a.k_stride = k_stride;
   a.v_stride = v_stride;
   a.cu = cu_tokens;
   a.out = static_cast<uint16_t*>(out);
   a.lse = lse;
   a.status = status;
   a.Hq = num_q_heads;
+  a.Hkv = num_kv_heads;
   a.G = G;
+  a.T = 128 / G;
   a.total = total_tokens;
   a.num_lanes = num_lanes;
-  a.scale_log2 = sm_scale * 1.4426950408889634f;
-  const long long warps = (long long)total_tokens * num_q_heads;
-  const long long blocks = (warps + kThreads / 32 - 1) / (kThreads / 32);
-  if (blocks > 0x7fffffffLL) return SDVA_ERR_UNSUPPORTED;
-  prompt_attn_kernel<<<(unsigned)blocks, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  a.scale = sm_scale;
+  a.scale_log2 = sm_scale * kLog2e;
+  a.wait_limit = wait_limit();
+  CUtensorMap mq, mk, mv;
+  if (!encode_rows(&mq, q, q_stride, num_q_heads, total_tokens, G, a.T) ||
+      !encode_rows(&mk, k, k_stride, num_kv_heads, total_tokens, 1, kBlock) ||
+      !encode_rows(&mv, v, v_stride, num_kv_heads, total_tokens, 1, kBlock))
+    return SDVA_ERR_CUDA;
+  // the shared-memory limit is a per-device attribute of the function: set it
+  // on every call, for the device current now
+  if (cudaFuncSetAttribute(prompt_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
+      cudaSuccess)
+    return SDVA_ERR_CUDA;
+  // at most this many tiles: one per 2 T rows and a ragged one per lane
+  const long long tiles = ((long long)total_tokens / (2 * a.T) + num_lanes) * num_kv_heads;
+  prompt_attn_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kThreads, kSmemBytes,
+                       reinterpret_cast<cudaStream_t>(stream)>>>(mq, mk, mv, a);
   return cudaGetLastError() == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
 }

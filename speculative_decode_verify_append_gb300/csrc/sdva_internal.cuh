@@ -9,6 +9,9 @@
 
 namespace sdva {
 
+// Clock cycles a device wait may take (sdva_debug_set_wait_limit).
+long long wait_limit();
+
 // Each returns SDVA_OK or the call's SDVA_ERR_*; with check_only it validates
 // the arguments the same way and enqueues nothing.
 

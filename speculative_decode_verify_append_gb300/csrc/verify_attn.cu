@@ -588,6 +588,8 @@ int verify_launch(const sdva_kv_cache* cache, const void* q, int num_q_heads, in
 
 }  // namespace sdva
 
+long long sdva::wait_limit() { return g_wait_limit.load(std::memory_order_relaxed); }
+
 extern "C" long long sdva_debug_set_wait_limit(long long cycles) {
   return sdva::g_wait_limit.exchange(cycles < 0 ? sdva::kDefaultWaitLimit : cycles);
 }

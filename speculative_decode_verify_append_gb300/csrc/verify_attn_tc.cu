@@ -1513,22 +1513,6 @@ __global__ void __launch_bounds__(kMergeThreads) verify_merge_tc_kernel(TcArgs a
   }
 }
 
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encoder() {
-  static EncodeTiledFn fn = nullptr;
-  if (fn == nullptr) {
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(p);
-  }
-  return fn;
-}
-
 // One (page, kv head) of FP8 codes is 64 rows of 128 bytes; the whole pool is
 // a 2-D tensor [num_pages * Hkv * 64][128] bytes, loaded in 64-row boxes with
 // the 128-byte swizzle the MMA descriptors expect.
@@ -1545,6 +1529,18 @@ bool encode_pool_map(CUtensorMap* m, const void* pool, long long rows) {
 }
 
 }  // namespace
+
+EncodeTiledFn encoder() {
+  static EncodeTiledFn fn = nullptr;
+  if (fn == nullptr) {
+    void* p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<EncodeTiledFn>(p);
+  }
+  return fn;
+}
 
 // The split kernel, one CTA per SM; with after_append, as a programmatic
 // dependent of the kernel before it on the stream (the append of verify_step).

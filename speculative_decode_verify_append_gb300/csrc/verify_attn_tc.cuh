@@ -2,6 +2,7 @@
 // points and the tcgen05 kernels of verify_attn_tc.cu.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -33,6 +34,13 @@ struct TcArgs {
   int unit_cost;         // price of a unit's start in the partition, in pages (unit_cost_of)
   float sm_scale_log2;
 };
+
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// cuTensorMapEncodeTiled through the driver's entry point table (null: not found)
+EncodeTiledFn encoder();
 
 // The partition's price of starting a unit, in pages of the cache format.
 int unit_cost_of(int dtype);
