@@ -11,10 +11,13 @@
 // K/V tiles and few rows are empty whatever the group.  Twelve warps:
 //   * warp 8 (loader): takes the next tile, TMA-loads its Q and the K and V
 //     blocks of 128 keys into a ring of five 32 KB stages;
-//   * warps 9, 10 (issuers, one per half): S = Q K^T into tensor memory, then
-//     per block O += P V and the next S = Q K^T, so that one half's softmax
-//     runs under the other half's products;
-//   * warp 11 (guard): V rows behind a tile's first row are hidden from some
+//   * warp 9 (issuer): S = Q K^T into tensor memory, then per block O += P V
+//     and the next S = Q K^T of one half back to back, then the other half's,
+//     so that each half's softmax runs under the other's products (two
+//     issuers, one per half, interleave their products instead: both halves'
+//     scores come late and the softmaxes run together, 1,255 against
+//     1,477 TFLOP/s at 32,768 tokens);
+//   * warp 10 (guard): V rows behind a tile's first row are hidden from some
 //     of its rows, but a weight of 0 does not hide an infinity or a NaN from
 //     a product; it takes such values out of the V block in shared memory
 //     before the product reads it, and marks the tile, whose rows then add
@@ -42,7 +45,7 @@ using namespace tc;
 constexpr int kMaxPromptLanes = 1024;
 constexpr int kBlock = 128;  // keys per K or V block
 constexpr int kThreads = 384;
-constexpr int kLoaderWarp = 8, kIssueWarp = 9, kGuardWarp = 11;
+constexpr int kLoaderWarp = 8, kIssueWarp = 9, kGuardWarp = 10;
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
 constexpr int kStages = 5;
@@ -50,7 +53,7 @@ constexpr uint32_t kStageBytes = kBlock * kHeadDim * 2;  // two 64-dim panels of
 constexpr uint32_t kPanel = kStageBytes / 2;
 constexpr uint32_t kOffKv = 2 * kStageBytes;  // behind the Q of both halves
 constexpr uint32_t kOffCtl = kOffKv + kStages * kStageBytes;
-constexpr int kGuardRing = 8;  // guarded blocks between the guard and an issuer: fewer than stages
+constexpr int kGuardRing = 8;  // barriers of the guard's blocks, more than there are stages
 constexpr float kLag = 8.0f;   // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 // tensor memory: S (fp32, 128 columns) of half s, overlaid by its P (bf16, 64 columns); O (fp32, 128 columns)
@@ -82,8 +85,8 @@ struct Tile {
 
 struct Ctl {
   uint64_t q_full, q_free, full[kStages], empty[kStages];
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2], drain[2];
-  uint64_t guarded[kGuardRing];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2], drain;
+  uint64_t guard[kGuardRing];
   uint64_t tile_full[2], tile_free[2], tile_guarded[2];
   Tile tile[2];
   uint32_t tmem_base;
@@ -105,12 +108,17 @@ struct Shape {
   }
 };
 
-// Which tile comes r-th.  Tiles are taken with the longest rows first over
-// all lanes (a tile's work grows with its position), so that the last ones
-// are short.  A lane with n tiles has one at each position below n; between
+// The first V block with rows that some row of the tile does not see.
+__device__ __forceinline__ int guard_from(const Tile& t) { return (t.t0 + 1) / kBlock; }
+
+// Which tile comes r-th.  Tiles are ordered with the longest rows first over
+// all lanes (a tile's work grows with its position) and dealt to the CTAs
+// back and forth, so that whoever got the longer of two neighbours gets the
+// shorter of the next two: 8,192 tokens of 8 / 8 heads, where two rounds of
+// tiles fall to 152 CTAs, took 153 us dealt in one direction, 108 so.  A lane with n tiles has one at each position below n; between
 // two successive tile counts of the batch the number of lanes that reach a
 // position stays the same, which turns a rank into a position by one division
-// per distinct count.  Ranks a CTA asks for only grow, so it keeps its place.
+// per distinct count.  The ranks a CTA asks for only grow, so it keeps its place.
 struct Order {
   const int32_t* cu;
   int B, span, lane;
@@ -180,6 +188,17 @@ struct Phase {
   }
 };
 
+// A place in the ring of stages and the parity its fill completes with.
+struct Ring {
+  uint32_t st = 0, phase = 0;
+  __device__ void next() {
+    if (++st == kStages) {
+      st = 0;
+      phase ^= 1u;
+    }
+  }
+};
+
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int y, int z, uint32_t bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
@@ -202,7 +221,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* const gen = smem_raw + (base - smem_u32(smem_raw));
   Ctl* const ctl = reinterpret_cast<Ctl*>(gen + kOffCtl);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // broadcast: the compiler then knows it, and what follows from it, to be the same for the whole warp
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   int bad = 0;
   for (int i = threadIdx.x; i < a.num_lanes; i += kThreads) {
@@ -211,22 +231,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(&ctl->q_full), 1);
-    mbar_init(smem_u32(&ctl->q_free), 2);
+    mbar_init(smem_u32(&ctl->q_free), 1);
+    mbar_init(smem_u32(&ctl->drain), 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&ctl->full[i]), 1);
-      mbar_init(smem_u32(&ctl->empty[i]), 2);
+      mbar_init(smem_u32(&ctl->empty[i]), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctl->s_full[i]), 1);
       mbar_init(smem_u32(&ctl->p_full[i]), 4);
       mbar_init(smem_u32(&ctl->o_full[i]), 1);
       mbar_init(smem_u32(&ctl->o_free[i]), 4);
-      mbar_init(smem_u32(&ctl->drain[i]), 1);
       mbar_init(smem_u32(&ctl->tile_full[i]), 1);
-      mbar_init(smem_u32(&ctl->tile_free[i]), 11);  // both issuers, the guard, eight softmax warps
+      mbar_init(smem_u32(&ctl->tile_free[i]), 10);  // the issuer, the guard, eight softmax warps
       mbar_init(smem_u32(&ctl->tile_guarded[i]), 1);
     }
-    for (int i = 0; i < kGuardRing; ++i) mbar_init(smem_u32(&ctl->guarded[i]), 1);
+    for (int i = 0; i < kGuardRing; ++i) mbar_init(smem_u32(&ctl->guard[i]), 1);
     ctl->abort = 0;
     mbar_fence_init();
   }
@@ -238,11 +258,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   fence_before_sync();
   __syncthreads();
   fence_after_sync();
-  const uint32_t tmem = ctl->tmem_base;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
   volatile int* const abort_flag = &ctl->abort;
   const long long limit = a.wait_limit;
-  auto spin = [&](uint64_t& bar, uint32_t parity) { return mbar_wait<true>(smem_u32(&bar), parity, abort_flag, limit); };
-  auto doze = [&](uint64_t& bar, uint32_t parity) { return mbar_wait<false>(smem_u32(&bar), parity, abort_flag, limit); };
+  // (spinning instead of sleeping takes issue slots from the softmax: 1,496
+  // against 1,524 TFLOP/s at 32,768 tokens)
+  auto wait = [&](uint64_t& bar, uint32_t parity) { return mbar_wait<false>(smem_u32(&bar), parity, abort_flag, limit); };
 
   if (warp >= kLoaderWarp) {
     regs_decrease<kRegsOther>();
@@ -253,22 +274,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t half_bytes = (uint32_t)(a.G * a.T) * 128u;  // one 64-dim panel of one half's Q
       long long fills = 0;  // stage fills issued
       int q_loads = 0;
-      auto load = [&](const CUtensorMap* map, int hk, int row) {
+      long long guard0 = 0;  // guarded blocks issued
+      // a V block that the guard looks at first lands on the guard's barrier; the guard passes it on
+      auto load = [&](const CUtensorMap* map, int hk, int row, bool guarded) {
         const int s = (int)(fills % kStages);
-        if (fills >= kStages && !doze(ctl->empty[s], (uint32_t)((fills / kStages - 1) & 1))) return false;
+        if (fills >= kStages && !wait(ctl->empty[s], (uint32_t)((fills / kStages - 1) & 1))) return false;
         if (lane == 0) {
-          const uint32_t bar = smem_u32(&ctl->full[s]), dst = base + kOffKv + s * kStageBytes;
+          const uint32_t bar = smem_u32(guarded ? &ctl->guard[guard0 % kGuardRing] : &ctl->full[s]);
+          const uint32_t dst = base + kOffKv + s * kStageBytes;
           mbar_arrive_expect_tx(bar, kStageBytes);
           tma_load_3d(dst, map, 0, hk, row, bar);
           tma_load_3d(dst + kPanel, map, 64, hk, row, bar);
         }
         __syncwarp();
         ++fills;
+        guard0 += guarded;
         return true;
       };
       for (int i = 0;; ++i) {
         const int slot = i & 1;
-        const long long r = blockIdx.x + (long long)i * gridDim.x;
+        const long long r = (long long)i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
         Tile t = {0, 0, 0, (int)(r % a.Hkv), 0};
         int b, pos;
         if (order.find(r / a.Hkv, &b, &pos)) {
@@ -276,7 +301,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           t.len = a.cu[b + 1] - t.row0;
           t.t0 = pos * 2 * a.T;
         }
-        if (i >= 2 && !(ok = doze(ctl->tile_free[slot], (uint32_t)((i / 2 - 1) & 1)))) break;
+        if (i >= 2 && !(ok = wait(ctl->tile_free[slot], (uint32_t)((i / 2 - 1) & 1)))) break;
         if (lane == 0) {
           ctl->tile[slot] = t;
           mbar_arrive(smem_u32(&ctl->tile_full[slot]));
@@ -284,7 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (t.len == 0) break;
         const Shape sh(t, a.T);
-        if (i >= 1 && !(ok = doze(ctl->q_free, (uint32_t)((i - 1) & 1)))) break;
+        if (i >= 1 && !(ok = wait(ctl->q_free, (uint32_t)((i - 1) & 1)))) break;
         if (lane == 0) {
           const uint32_t bar = smem_u32(&ctl->q_full);
           mbar_arrive_expect_tx(bar, half_bytes * (sh.n[1] ? 4u : 2u));
@@ -295,108 +320,124 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++q_loads;
         for (int j = 0; j < sh.total && ok; ++j)
-          ok = load(&mk, t.hk, t.row0 + j * kBlock) && load(&mv, t.hk, t.row0 + j * kBlock);
+          ok = load(&mk, t.hk, t.row0 + j * kBlock, false) &&
+               load(&mv, t.hk, t.row0 + j * kBlock, j >= guard_from(t));
         if (!ok) break;
       }
       if (!ok) {
         give_up(ctl, a.status);
         // this warp's copies still in flight (bounded)
         int none = 0;
+        for (long long g = max(0LL, guard0 - kStages); g < guard0; ++g)
+          mbar_wait<false>(smem_u32(&ctl->guard[g % kGuardRing]), (uint32_t)((g / kGuardRing) & 1), &none, 400000000LL);
         for (long long f = max(0LL, fills - kStages); f < fills; ++f)
           mbar_wait<false>(smem_u32(&ctl->full[f % kStages]), (uint32_t)((f / kStages) & 1), &none, 400000000LL);
         if (q_loads) mbar_wait<false>(smem_u32(&ctl->q_full), (uint32_t)((q_loads - 1) & 1), &none, 400000000LL);
       }
-    } else if (warp < kGuardWarp) {
-      const int s = warp - kIssueWarp;
-      const uint32_t d_s = tmem + col_s(s), d_o = tmem + col_o(s);
-      long long stage0 = 0;       // stage fills of the tiles before
-      long long guard0 = 0;       // guarded blocks of the tiles before
-      Phase p_phase, o_phase;
-      bool first = true;
-      auto wait_stage = [&](long long f) { return spin(ctl->full[f % kStages], (uint32_t)((f / kStages) & 1)); };
-      auto commit_stage = [&](long long f) { mma_commit(smem_u32(&ctl->empty[f % kStages])); };
+    } else if (warp == kIssueWarp) {
+      // Descriptors differ in their start address alone: the low words are
+      // added up from constants, so that a product costs few instructions
+      // here (stage numbers by 64-bit remainders held the tensor core up by
+      // 700 cycles a block: 1,566 against 1,731 TFLOP/s at 32,768 tokens).
+      const uint64_t q_desc = sdesc_sw128(base, 1024, 1024);
+      const uint64_t k_desc = sdesc_sw128(base + kOffKv, 1024, 1024);
+      const uint64_t v_desc = sdesc_sw128(base + kOffKv, kPanel, 1024);
+      constexpr uint64_t kStage16 = kStageBytes >> 4, kPanel16 = kPanel >> 4;
+      Ring ring;
+      Phase p_phase[2], o_phase[2];
+      bool used[2] = {false, false};
+      // S = Q K^T for half s with the K block of stage st
+      auto qk = [&](int s, uint32_t st) {
+        const uint64_t qd = q_desc + s * kStage16, kd = k_desc + st * kStage16;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_f16_ss(tmem + col_s(s), qd + kPanel16 * (k >> 2) + 2 * (k & 3), kd + kPanel16 * (k >> 2) + 2 * (k & 3),
+                     kIdescQK, k != 0);
+        mma_commit(smem_u32(&ctl->s_full[s]));
+      };
+      // O (+)= P V for half s with the V block of stage st
+      auto pv = [&](int s, uint32_t st, bool add) {
+        const uint64_t vd = v_desc + st * kStage16;
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+          mma_f16_ts(tmem + col_o(s), tmem + col_s(s) + 8 * k, vd + 128 * k, kIdescPV, add || k != 0);
+      };
       for (int i = 0; ok; ++i) {
         const int slot = i & 1;
-        if (!(ok = spin(ctl->tile_full[slot], (uint32_t)((i / 2) & 1)))) break;
+        if (!(ok = wait(ctl->tile_full[slot], (uint32_t)((i / 2) & 1)))) break;
         const Tile t = ctl->tile[slot];
         if (t.len == 0) break;
         const Shape sh(t, a.T);
-        const int n = sh.n[s], guard_from = (t.t0 + 1) / kBlock;
-        if (!(ok = spin(ctl->q_full, (uint32_t)(i & 1)))) break;
-        auto qk = [&](int j) {
-          const long long f = stage0 + 2 * j;
-          if (!wait_stage(f)) return false;
-          fence_after_sync();
-          if (lane == 0) {
-            const uint32_t qt = base + s * kStageBytes, kt = base + kOffKv + (uint32_t)(f % kStages) * kStageBytes;
+        const int n0 = __shfl_sync(0xffffffffu, sh.n[0], 0), n1 = __shfl_sync(0xffffffffu, sh.n[1], 0);
+        const int total = max(n0, n1);
+        if (!(ok = wait(ctl->q_full, (uint32_t)(i & 1)) && wait(ctl->full[ring.st], ring.phase))) break;
+        fence_after_sync();
+        if (elect_one()) {
+          qk(0, ring.st);
+          if (n1 > 0) qk(1, ring.st);
+          mma_commit(smem_u32(&ctl->empty[ring.st]));
+          if (total == 1) mma_commit(smem_u32(&ctl->q_free));
+        }
+        __syncwarp();
+        ring.next();
+        // one half's PV and next QK back to back, then the other's: the scores
+        // of one half are out while the other half's products run
+        for (int j = 0; j < total && ok; ++j) {
+          const Ring v = ring;  // V of block j, K of block j + 1
+          ring.next();
+          const Ring k = ring;
+          if (j + 1 < total) ring.next();
+          bool v_here = false, k_here = false;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              mma_f16_ss(d_s, sdesc_sw128(qt + kPanel * (k >> 2) + 32 * (k & 3), 1024, 1024),
-                         sdesc_sw128(kt + kPanel * (k >> 2) + 32 * (k & 3), 1024, 1024), kIdescQK, k != 0);
-            mma_commit(smem_u32(&ctl->s_full[s]));
-            commit_stage(f);
-            if (j == n - 1) mma_commit(smem_u32(&ctl->q_free));
-          }
-          __syncwarp();
-          return true;
-        };
-        if (n > 0) {
-          if (!(ok = qk(0))) break;
-          for (int j = 0; j < n; ++j) {
-            const long long f = stage0 + 2 * j + 1;
-            if (!(ok = spin(ctl->p_full[s], p_phase.take()))) break;
-            if (j == 0 && !first && !(ok = spin(ctl->o_free[s], o_phase.take()))) break;
-            if (!(ok = wait_stage(f))) break;
-            if (j >= guard_from) {
-              const long long gb = guard0 + j - guard_from;
-              if (!(ok = spin(ctl->guarded[gb % kGuardRing], (uint32_t)((gb / kGuardRing) & 1)))) break;
-            }
+          for (int s = 0; s < 2; ++s) {
+            const int n = s ? n1 : n0;
+            if (j >= n) continue;
+            // nothing reads these stages after this half
+            const bool v_last = s == 1 || j >= n1, k_last = s == 1 || j + 1 >= n1, more = j + 1 < n;
+            if (!v_here && !(ok = wait(ctl->full[v.st], v.phase))) break;
+            v_here = true;
+            if (more && !k_here && !(ok = wait(ctl->full[k.st], k.phase))) break;
+            k_here |= more;
+            if (j == 0 && used[s] && !(ok = wait(ctl->o_free[s], o_phase[s].take()))) break;
+            if (!(ok = wait(ctl->p_full[s], p_phase[s].take()))) break;
             fence_after_sync();
-            if (lane == 0) {
-              const uint32_t vt = base + kOffKv + (uint32_t)(f % kStages) * kStageBytes;
-#pragma unroll
-              for (int k = 0; k < 8; ++k)
-                mma_f16_ts(d_o, d_s + 8 * k, sdesc_sw128(vt + 2048 * k, kPanel, 1024), kIdescPV, j != 0 || k != 0);
-              commit_stage(f);
-              if (j == n - 1) mma_commit(smem_u32(&ctl->o_full[s]));
+            if (elect_one()) {
+              pv(s, v.st, j > 0);
+              if (v_last) mma_commit(smem_u32(&ctl->empty[v.st]));
+              if (more) {
+                qk(s, k.st);
+                if (k_last) mma_commit(smem_u32(&ctl->empty[k.st]));
+                if (k_last && j + 2 == total) mma_commit(smem_u32(&ctl->q_free));
+              } else {
+                mma_commit(smem_u32(&ctl->o_full[s]));
+              }
             }
             __syncwarp();
-            if (j + 1 < n && !(ok = qk(j + 1))) break;
           }
-          if (!ok) break;
-          first = false;
-        } else if (lane == 0) {
-          mbar_arrive(smem_u32(&ctl->q_free));
         }
-        // blocks that only the other half reads
-        for (int j = n; j < sh.total && ok; ++j)
-          for (int k = 0; k < 2 && ok; ++k) {
-            const long long f = stage0 + 2 * j + k;
-            if ((ok = wait_stage(f)) && lane == 0) mbar_arrive(smem_u32(&ctl->empty[f % kStages]));
-          }
         if (!ok) break;
-        stage0 += 2 * sh.total;
-        guard0 += max(0, sh.total - guard_from);
-        __syncwarp();
+        used[0] = true;
+        used[1] |= n1 > 0;
         if (lane == 0) mbar_arrive(smem_u32(&ctl->tile_free[slot]));
+        __syncwarp();
       }
       if (!ok) give_up(ctl, a.status);
-      // the tensor core is done with everything this thread issued (bounded)
-      if (lane == 0) mma_commit(smem_u32(&ctl->drain[s]));
+      // the tensor core is done with everything this warp issued (bounded)
+      if (elect_one()) mma_commit(smem_u32(&ctl->drain));
       __syncwarp();
       int none = 0;
-      mbar_wait<false>(smem_u32(&ctl->drain[s]), 0, &none, 400000000LL);
-    } else {
+      mbar_wait<false>(smem_u32(&ctl->drain), 0, &none, 400000000LL);
+    } else if (warp == kGuardWarp) {
       long long stage0 = 0, guard0 = 0;
       for (int i = 0; ok; ++i) {
         const int slot = i & 1;
-        if (!(ok = doze(ctl->tile_full[slot], (uint32_t)((i / 2) & 1)))) break;
+        if (!(ok = wait(ctl->tile_full[slot], (uint32_t)((i / 2) & 1)))) break;
         const Tile t = ctl->tile[slot];
         if (t.len == 0) break;
         const Shape sh(t, a.T);
-        for (int j = (t.t0 + 1) / kBlock; j < sh.total; ++j, ++guard0) {
+        for (int j = guard_from(t); j < sh.total; ++j, ++guard0) {
           const long long f = stage0 + 2 * j + 1;
-          if (!(ok = doze(ctl->full[f % kStages], (uint32_t)((f / kStages) & 1)))) break;
+          if (!(ok = wait(ctl->guard[guard0 % kGuardRing], (uint32_t)((guard0 / kGuardRing) & 1)))) break;
           uint8_t* const vt = gen + kOffKv + (uint32_t)(f % kStages) * kStageBytes;
           const int from = max(0, t.t0 + 1 - j * kBlock) * 128;  // bytes of the rows every row of the tile sees
           bool found = false;
@@ -418,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             fence_proxy_async_smem();
             __syncwarp();
           }
-          if (lane == 0) mbar_arrive(smem_u32(&ctl->guarded[guard0 % kGuardRing]));
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->full[f % kStages]));
           __syncwarp();
         }
         if (!ok) break;
@@ -443,7 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const int slot = i & 1;
-      if (!(ok = spin(ctl->tile_full[slot], (uint32_t)((i / 2) & 1)))) break;
+      if (!(ok = wait(ctl->tile_full[slot], (uint32_t)((i / 2) & 1)))) break;
       const Tile t = ctl->tile[slot];
       if (t.len == 0) break;
       const Shape sh(t, a.T);
@@ -453,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       float m = ninf;
       float l = 0.0f;
       for (int j = 0; j < n; ++j) {
-        if (!(ok = spin(ctl->s_full[s], s_phase.take()))) break;
+        if (!(ok = wait(ctl->s_full[s], s_phase.take()))) break;
         fence_after_sync();
         uint32_t x[4][32];
 #pragma unroll
@@ -518,12 +559,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[s]));
       }
       if (!ok) break;
-      if (!(ok = spin(ctl->tile_guarded[slot], (uint32_t)((i / 2) & 1)))) break;
+      if (!(ok = wait(ctl->tile_guarded[slot], (uint32_t)((i / 2) & 1)))) break;
       const bool dirty = ctl->tile[slot].dirty != 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(&ctl->tile_free[slot]));
       if (n == 0) continue;
-      if (!(ok = spin(ctl->o_full[s], o_phase.take()))) break;
+      if (!(ok = wait(ctl->o_full[s], o_phase.take()))) break;
       fence_after_sync();
       const float inv = 1.0f / l;
       const size_t at = (size_t)(t.row0 + tok) * a.Hq + (size_t)t.hk * a.G + r_head;
