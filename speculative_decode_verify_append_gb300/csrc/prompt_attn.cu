@@ -122,12 +122,13 @@ __device__ __forceinline__ int guard_from(const Tile& t) { return (t.t0 + 1) / k
 struct Order {
   const int32_t* cu;
   int B, span, lane;
-  int cur, next, count;  // tile counts: the largest not yet passed, the one below; lanes that reach `cur`
-  long long base;        // tiles of longer positions
+  int cur, next;         // tile counts: the largest not yet passed, the one below
+  uint32_t count, base;  // lanes that reach `cur`, tiles of longer positions
 
-  __device__ int tiles(int b) const { return (cu[b + 1] - cu[b] + span - 1) / span; }
+  __device__ int tiles(int b) const { return (int)((uint32_t)(cu[b + 1] - cu[b] + span - 1) / (uint32_t)span); }
   __device__ void scan() {
-    int c = 0, m = 0;
+    uint32_t c = 0;
+    int m = 0;
     for (int b = lane; b < B; b += 32) {
       const int n = tiles(b);
       if (n >= cur) ++c;
@@ -141,28 +142,28 @@ struct Order {
     B = B_;
     span = span_;
     lane = lane_;
+    base = 0;
     cur = 0x7fffffff;
     scan();
     cur = next;
-    base = 0;
     if (cur > 0) scan();
   }
   // lane and position of tile r; false when there is none
-  __device__ bool find(long long r, int* b_out, int* pos) {
-    while (cur > 0 && r >= base + (long long)count * (cur - next)) {
-      base += (long long)count * (cur - next);
+  __device__ bool find(uint32_t r, int* b_out, int* pos) {
+    while (cur > 0 && r - base >= count * (uint32_t)(cur - next)) {
+      base += count * (uint32_t)(cur - next);
       cur = next;
       if (cur > 0) scan();
     }
     if (cur <= 0) return false;
-    const long long o = r - base;
+    const uint32_t o = r - base;
     *pos = cur - 1 - (int)(o / count);
-    int k = (int)(o % count);  // the k-th lane of those that reach cur
+    uint32_t k = o % count;  // the k-th lane of those that reach cur
     for (int b = 0; b < B; b += 32) {
-      const unsigned has = __ballot_sync(0xffffffffu, b + lane < B && tiles(min(b + lane, B - 1)) >= cur);
-      const int c = __popc(has);
+      const bool mine = b + lane < B && tiles(min(b + lane, B - 1)) >= cur;
+      const uint32_t has = __ballot_sync(0xffffffffu, mine), c = __popc(has);
       if (k < c) {
-        *b_out = b + (int)__fns(has, 0, k + 1);
+        *b_out = b + __ffs(__ballot_sync(0xffffffffu, mine && __popc(has & ((1u << lane) - 1u)) == k)) - 1;
         return true;
       }
       k -= c;
@@ -207,11 +208,11 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-__device__ __forceinline__ bool any_nonfinite(uint4 w) {
-  // an exponent of all ones carries into bit 15 of its half
-  const uint32_t c = ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
-                     ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
-  return (c & 0x80008000u) != 0;
+// Bits 15 and 31 of the result: whether some bf16 of the words has an exponent
+// of all ones (the addition carries into those bits).
+__device__ __forceinline__ uint32_t nonfinite_bits(uint4 w) {
+  return ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
+         ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -224,12 +225,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // broadcast: the compiler then knows it, and what follows from it, to be the same for the whole warp
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
-  int bad = 0;
-  for (int i = threadIdx.x; i < a.num_lanes; i += kThreads) {
-    const int lo = a.cu[i], hi = a.cu[i + 1];
-    bad |= lo < 0 || hi < lo || hi > a.total;
-  }
-  if (threadIdx.x == 0) {
+  if (warp == kLoaderWarp) {
+    if (lane < 3) prefetch_tmap(lane == 0 ? &mq : lane == 1 ? &mk : &mv);
+    tmem_alloc(smem_u32(&ctl->tmem_base), kTmemCols);
+  } else if (threadIdx.x == kIssueWarp * 32) {
     mbar_init(smem_u32(&ctl->q_full), 1);
     mbar_init(smem_u32(&ctl->q_free), 1);
     mbar_init(smem_u32(&ctl->drain), 1);
@@ -250,13 +249,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     ctl->abort = 0;
     mbar_fence_init();
   }
-  if (__syncthreads_or(bad)) {
-    if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(a.status, SDVA_STATUS_BAD_COUNT);
-    return;
+  int bad = 0;
+  for (int i = threadIdx.x; i < a.num_lanes; i += kThreads) {
+    const int lo = a.cu[i], hi = a.cu[i + 1];
+    bad |= lo < 0 || hi < lo || hi > a.total;
   }
-  if (warp == kLoaderWarp) tmem_alloc(smem_u32(&ctl->tmem_base), kTmemCols);
   fence_before_sync();
-  __syncthreads();
+  bad = __syncthreads_or(bad);
   fence_after_sync();
   const uint32_t tmem = __shfl_sync(0xffffffffu, ctl->tmem_base, 0);
   volatile int* const abort_flag = &ctl->abort;
@@ -265,7 +264,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   // against 1,524 TFLOP/s at 32,768 tokens)
   auto wait = [&](uint64_t& bar, uint32_t parity) { return mbar_wait<false>(smem_u32(&bar), parity, abort_flag, limit); };
 
-  if (warp >= kLoaderWarp) {
+  if (bad) {  // the same for the whole CTA
+    if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(a.status, SDVA_STATUS_BAD_COUNT);
+  } else if (warp >= kLoaderWarp) {
     regs_decrease<kRegsOther>();
     bool ok = true;
     if (warp == kLoaderWarp) {
@@ -293,10 +294,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       };
       for (int i = 0;; ++i) {
         const int slot = i & 1;
-        const long long r = (long long)i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        Tile t = {0, 0, 0, (int)(r % a.Hkv), 0};
+        const uint32_t r = (uint32_t)i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        Tile t = {0, 0, 0, (int)(r % (uint32_t)a.Hkv), 0};
         int b, pos;
-        if (order.find(r / a.Hkv, &b, &pos)) {
+        if (order.find(r / (uint32_t)a.Hkv, &b, &pos)) {
           t.row0 = a.cu[b];
           t.len = a.cu[b + 1] - t.row0;
           t.t0 = pos * 2 * a.T;
@@ -440,12 +441,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!(ok = wait(ctl->guard[guard0 % kGuardRing], (uint32_t)((guard0 / kGuardRing) & 1)))) break;
           uint8_t* const vt = gen + kOffKv + (uint32_t)(f % kStages) * kStageBytes;
           const int from = max(0, t.t0 + 1 - j * kBlock) * 128;  // bytes of the rows every row of the tile sees
-          bool found = false;
-#pragma unroll 8
+          uint32_t found = 0;
+#pragma unroll 4
           for (int o = from + 16 * lane; o < (int)kPanel; o += 512)
-            found |= any_nonfinite(*reinterpret_cast<const uint4*>(vt + o)) ||
-                     any_nonfinite(*reinterpret_cast<const uint4*>(vt + kPanel + o));
-          if (__any_sync(0xffffffffu, found)) {
+            found |= nonfinite_bits(*reinterpret_cast<const uint4*>(vt + o)) |
+                     nonfinite_bits(*reinterpret_cast<const uint4*>(vt + kPanel + o));
+          if (__any_sync(0xffffffffu, (found & 0x80008000u) != 0)) {
             bool seen = false;
             for (int o = from + 2 * lane; o < (int)kPanel; o += 64)
               for (int p = 0; p < 2; ++p) {
@@ -683,6 +684,7 @@ extern "C" int prompt_attn(const void* q, const void* k, const void* v, int64_t 
     return SDVA_ERR_CUDA;
   // at most this many tiles: one per 2 T rows and a ragged one per lane
   const long long tiles = ((long long)total_tokens / (2 * a.T) + num_lanes) * num_kv_heads;
+  if (tiles > 0x7fffffffLL) return SDVA_ERR_UNSUPPORTED;  // more rows of K and V than memory holds
   prompt_attn_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kThreads, kSmemBytes,
                        reinterpret_cast<cudaStream_t>(stream)>>>(mq, mk, mv, a);
   return cudaGetLastError() == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
