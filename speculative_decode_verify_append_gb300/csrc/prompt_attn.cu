@@ -88,6 +88,8 @@ struct Ctl {
   uint64_t s_full[2], p_full[2], o_full[2], o_free[2], drain;
   uint64_t guard[kGuardRing];
   uint64_t tile_full[2], tile_free[2], tile_guarded[2];
+  alignas(16) uint32_t next_cta[4];  // the answer to a request for another CTA's place
+  uint64_t next_full;
   Tile tile[2];
   uint32_t tmem_base;
   int abort;
@@ -112,13 +114,12 @@ struct Shape {
 __device__ __forceinline__ int guard_from(const Tile& t) { return (t.t0 + 1) / kBlock; }
 
 // Which tile comes r-th.  Tiles are ordered with the longest rows first over
-// all lanes (a tile's work grows with its position) and dealt to the CTAs
-// back and forth, so that whoever got the longer of two neighbours gets the
-// shorter of the next two: 8,192 tokens of 8 / 8 heads, where two rounds of
-// tiles fall to 152 CTAs, took 153 us dealt in one direction, 108 so.  A lane with n tiles has one at each position below n; between
+// all lanes (a tile's work grows with its position); the grid has a CTA per
+// tile, and a CTA that runs takes over the next one that has not started, so
+// that the work is dealt as it is done and ends with the shortest tiles.  A lane with n tiles has one at each position below n; between
 // two successive tile counts of the batch the number of lanes that reach a
 // position stays the same, which turns a rank into a position by one division
-// per distinct count.  The ranks a CTA asks for only grow, so it keeps its place.
+// per distinct count.  The ranks a CTA gets grow, so it keeps its place.
 struct Order {
   const int32_t* cu;
   int B, span, lane;
@@ -150,6 +151,7 @@ struct Order {
   }
   // lane and position of tile r; false when there is none
   __device__ bool find(uint32_t r, int* b_out, int* pos) {
+    if (r < base) init(cu, B, span, lane);
     while (cur > 0 && r - base >= count * (uint32_t)(cur - next)) {
       base += count * (uint32_t)(cur - next);
       cur = next;
@@ -208,6 +210,34 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
+__device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, int y, int z) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global.tile [%0, {%1, %2, %3}];" ::"l"(map), "r"(x), "r"(y), "r"(z)
+               : "memory");
+}
+
+// Ask for the place of a CTA of this grid that has not started: 16 bytes at
+// `dst`, completion on `bar`.
+__device__ __forceinline__ void take_over_next(uint32_t dst, uint32_t bar) {
+  mbar_arrive_expect_tx(bar, 16);
+  asm volatile(
+      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+      "r"(bar)
+      : "memory");
+}
+// Whether the answer at `src` grants one, and its block index.
+__device__ __forceinline__ bool taken_over(uint32_t src, uint32_t* cta) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\tld.shared.b128 h, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+      : "=r"(ok), "=r"(x)
+      : "r"(src)
+      : "memory");
+  *cta = x;
+  return ok != 0;
+}
+
 // Bits 15 and 31 of the result: whether some bf16 of the words has an exponent
 // of all ones (the addition carries into those bits).
 __device__ __forceinline__ uint32_t nonfinite_bits(uint4 w) {
@@ -231,6 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (threadIdx.x == kIssueWarp * 32) {
     mbar_init(smem_u32(&ctl->q_full), 1);
     mbar_init(smem_u32(&ctl->q_free), 1);
+    mbar_init(smem_u32(&ctl->next_full), 1);
     mbar_init(smem_u32(&ctl->drain), 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&ctl->full[i]), 1);
@@ -292,37 +323,69 @@ __global__ void __launch_bounds__(kThreads, 1)
         guard0 += guarded;
         return true;
       };
+      uint32_t r = blockIdx.x;
+      Tile t;
+      auto locate = [&]() {
+        int b, pos;
+        t = {0, 0, 0, (int)(r % (uint32_t)a.Hkv), 0};
+        if (!order.find(r / (uint32_t)a.Hkv, &b, &pos)) return false;
+        t.row0 = a.cu[b];
+        t.len = a.cu[b + 1] - t.row0;
+        t.t0 = pos * 2 * a.T;
+        return true;
+      };
+      uint32_t asks = 0, answers = 0;
+      auto ask = [&]() {
+        if (lane == 0) take_over_next(smem_u32(ctl->next_cta), smem_u32(&ctl->next_full));
+        __syncwarp();
+        ++asks;
+      };
+      bool more = locate();
       for (int i = 0;; ++i) {
         const int slot = i & 1;
-        const uint32_t r = (uint32_t)i * gridDim.x + ((i & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        Tile t = {0, 0, 0, (int)(r % (uint32_t)a.Hkv), 0};
-        int b, pos;
-        if (order.find(r / (uint32_t)a.Hkv, &b, &pos)) {
-          t.row0 = a.cu[b];
-          t.len = a.cu[b + 1] - t.row0;
-          t.t0 = pos * 2 * a.T;
-        }
         if (i >= 2 && !(ok = wait(ctl->tile_free[slot], (uint32_t)((i / 2 - 1) & 1)))) break;
         if (lane == 0) {
           ctl->tile[slot] = t;
           mbar_arrive(smem_u32(&ctl->tile_full[slot]));
         }
         __syncwarp();
-        if (t.len == 0) break;
+        if (!more) break;
         const Shape sh(t, a.T);
+        const int halves = sh.n[1] ? 2 : 1;
+        if (lane < 4 && (lane >> 1) < halves)  // Q waits for its place: into L2 meanwhile
+          tma_prefetch_3d(&mq, 64 * (lane & 1), t.hk * a.G, t.row0 + t.t0 + (lane >> 1) * a.T);
+        __syncwarp();
+        // the first K and V do not wait for the tile before
+        if (!(ok = load(&mk, t.hk, t.row0, false) && load(&mv, t.hk, t.row0, guard_from(t) == 0))) break;
         if (i >= 1 && !(ok = wait(ctl->q_free, (uint32_t)((i - 1) & 1)))) break;
         if (lane == 0) {
           const uint32_t bar = smem_u32(&ctl->q_full);
-          mbar_arrive_expect_tx(bar, half_bytes * (sh.n[1] ? 4u : 2u));
-          for (int s = 0; s < (sh.n[1] ? 2 : 1); ++s)
+          mbar_arrive_expect_tx(bar, half_bytes * 2u * halves);
+          for (int s = 0; s < halves; ++s)
             for (int p = 0; p < 2; ++p)
               tma_load_3d(base + s * kStageBytes + p * kPanel, &mq, 64 * p, t.hk * a.G, t.row0 + t.t0 + s * a.T, bar);
         }
         __syncwarp();
         ++q_loads;
-        for (int j = 0; j < sh.total && ok; ++j)
+        for (int j = 1; j < sh.total && ok; ++j)
           ok = load(&mk, t.hk, t.row0 + j * kBlock, false) &&
                load(&mv, t.hk, t.row0 + j * kBlock, j >= guard_from(t));
+        if (!ok) break;
+        // The next tile, asked for when the last blocks of this one are on
+        // their way (asked for at its start, the CTAs with the longest tiles
+        // take a second one before others are free: 8,192 tokens of 8 / 8
+        // heads 124 against KEPT us).  Places behind the last tile are taken
+        // over too, so that no CTA starts for them.
+        ask();
+        t = {0, 0, 0, 0, 0};
+        more = false;
+        while (!more && (ok = wait(ctl->next_full, answers & 1u))) {
+          ++answers;
+          if (!taken_over(smem_u32(ctl->next_cta), &r)) break;
+          fence_proxy_async_smem();  // the answer is read before the next one is written
+          __syncwarp();
+          if (!(more = locate())) ask();
+        }
         if (!ok) break;
       }
       if (!ok) {
@@ -333,6 +396,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mbar_wait<false>(smem_u32(&ctl->guard[g % kGuardRing]), (uint32_t)((g / kGuardRing) & 1), &none, 400000000LL);
         for (long long f = max(0LL, fills - kStages); f < fills; ++f)
           mbar_wait<false>(smem_u32(&ctl->full[f % kStages]), (uint32_t)((f / kStages) & 1), &none, 400000000LL);
+        if (asks > answers) mbar_wait<false>(smem_u32(&ctl->next_full), answers & 1u, &none, 400000000LL);
         if (q_loads) mbar_wait<false>(smem_u32(&ctl->q_full), (uint32_t)((q_loads - 1) & 1), &none, 400000000LL);
       }
     } else if (warp == kIssueWarp) {
@@ -652,10 +716,6 @@ extern "C" int prompt_attn(const void* q, const void* k, const void* v, int64_t 
     return SDVA_ERR_INVALID;
   const int G = num_q_heads / num_kv_heads;
   if (num_lanes > kMaxPromptLanes || G > 128 || num_kv_heads > 65535) return SDVA_ERR_UNSUPPORTED;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return SDVA_ERR_CUDA;
   PromptArgs a;
   a.v = static_cast<const uint16_t*>(v);
   a.v_stride = v_stride;
@@ -685,7 +745,7 @@ extern "C" int prompt_attn(const void* q, const void* k, const void* v, int64_t 
   // at most this many tiles: one per 2 T rows and a ragged one per lane
   const long long tiles = ((long long)total_tokens / (2 * a.T) + num_lanes) * num_kv_heads;
   if (tiles > 0x7fffffffLL) return SDVA_ERR_UNSUPPORTED;  // more rows of K and V than memory holds
-  prompt_attn_kernel<<<(unsigned)(tiles < sms ? tiles : sms), kThreads, kSmemBytes,
+  prompt_attn_kernel<<<(unsigned)tiles, kThreads, kSmemBytes,
                        reinterpret_cast<cudaStream_t>(stream)>>>(mq, mk, mv, a);
   return cudaGetLastError() == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
 }
