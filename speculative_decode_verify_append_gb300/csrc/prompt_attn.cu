@@ -11,24 +11,27 @@
 // K/V tiles and few rows are empty whatever the group.  Twelve warps:
 //   * warp 8 (loader): takes the next tile, TMA-loads its Q and the K and V
 //     blocks of 128 keys into a ring of five 32 KB stages;
-//   * warp 9 (issuer): S = Q K^T into tensor memory, then per block O += P V
-//     and the next S = Q K^T of one half back to back, then the other half's,
-//     so that each half's softmax runs under the other's products (two
-//     issuers, one per half, interleave their products instead: both halves'
-//     scores come late and the softmaxes run together, 1,255 against
-//     1,477 TFLOP/s at 32,768 tokens);
-//   * warp 10 (guard): V rows behind a tile's first row are hidden from some
+//   * warps 9, 10 (issuers, one per half): S = Q K^T into tensor memory, then
+//     per block O += P V and the next S = Q K^T back to back.  They take
+//     turns, so that one half's softmax runs under the other half's products
+//     and each has its waits behind it when its turn comes.  (Untied, the
+//     halves' products interleave, both halves' scores come late and their
+//     softmaxes run together; one issuer for both halves spends 300 cycles
+//     between two halves' products, waiting: 262 against 236 us at 8,192
+//     tokens, 24 / 4 heads);
+//   * warp 11 (guard): V rows behind a tile's first row are hidden from some
 //     of its rows, but a weight of 0 does not hide an infinity or a NaN from
 //     a product; it takes such values out of the V block in shared memory
 //     before the product reads it, and marks the tile, whose rows then add
 //     those they do see from global memory;
 //   * warps 0-3 and 4-7 (softmax, one warpgroup per half): a thread owns a
 //     row: reads its 128 scores, masks the last blocks, keeps the running
-//     maximum and sum, writes P as bf16 over the scores.  Once the QK of a
-//     block is done, so is the PV before it (one issuer, in order), so the
-//     thread may rescale its O in place; it does only when the maximum grows
-//     by more than kLag (a factor of 256, which fp32 sums and bf16 weights
-//     carry without loss).  At the end it divides by the sum and stores.
+//     maximum and sum, writes P as bf16 over the scores, in two parts, so that
+//     the PV of the first runs under the weights of the second.  Once the QK
+//     of a block is done, so is the PV before it (one issuer, in order), so
+//     the thread may rescale its O in place; it does only when the maximum
+//     grows by more than kLag (a factor of 256, which fp32 sums and bf16
+//     weights carry without loss).  At the end it divides by the sum and stores.
 // Every wait is bounded: on timeout the CTA raises SDVA_STATUS_TIMEOUT,
 // drains its copies and products, frees tensor memory and returns.
 #include <math.h>
@@ -45,7 +48,7 @@ using namespace tc;
 constexpr int kMaxPromptLanes = 1024;
 constexpr int kBlock = 128;  // keys per K or V block
 constexpr int kThreads = 384;
-constexpr int kLoaderWarp = 8, kIssueWarp = 9, kGuardWarp = 10;
+constexpr int kLoaderWarp = 8, kIssueWarp = 9, kGuardWarp = 11;
 constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 static_assert(256 * kRegsSoftmax + 128 * kRegsOther <= kThreads * 168, "register split");
 constexpr int kStages = 5;
@@ -84,8 +87,8 @@ struct Tile {
 };
 
 struct Ctl {
-  uint64_t q_full, q_free, full[kStages], empty[kStages];
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2], drain;
+  uint64_t q_full[2], q_free[2], full[kStages], empty[kStages];
+  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], turn[2], drain[2];
   uint64_t guard[kGuardRing];
   uint64_t tile_full[2], tile_free[2], tile_guarded[2];
   alignas(16) uint32_t next_cta[4];  // the answer to a request for another CTA's place
@@ -255,30 +258,36 @@ __global__ void __launch_bounds__(kThreads, 1)
   // broadcast: the compiler then knows it, and what follows from it, to be the same for the whole warp
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
+  Order order;  // the loader's; safe to set up from offsets that turn out bad
   if (warp == kLoaderWarp) {
     if (lane < 3) prefetch_tmap(lane == 0 ? &mq : lane == 1 ? &mk : &mv);
+    order.init(a.cu, a.num_lanes, 2 * a.T, lane);
+  } else if (warp == kGuardWarp) {
     tmem_alloc(smem_u32(&ctl->tmem_base), kTmemCols);
   } else if (threadIdx.x == kIssueWarp * 32) {
-    mbar_init(smem_u32(&ctl->q_full), 1);
-    mbar_init(smem_u32(&ctl->q_free), 1);
     mbar_init(smem_u32(&ctl->next_full), 1);
-    mbar_init(smem_u32(&ctl->drain), 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&ctl->full[i]), 1);
-      mbar_init(smem_u32(&ctl->empty[i]), 1);
+      mbar_init(smem_u32(&ctl->empty[i]), 2);
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&ctl->q_full[i]), 1);
+      mbar_init(smem_u32(&ctl->q_free[i]), 1);
+      mbar_init(smem_u32(&ctl->turn[i]), 1);
+      mbar_init(smem_u32(&ctl->drain[i]), 1);
       mbar_init(smem_u32(&ctl->s_full[i]), 1);
-      mbar_init(smem_u32(&ctl->p_full[i]), 4);
+      mbar_init(smem_u32(&ctl->p_full[i][0]), 4);
+      mbar_init(smem_u32(&ctl->p_full[i][1]), 4);
       mbar_init(smem_u32(&ctl->o_full[i]), 1);
       mbar_init(smem_u32(&ctl->o_free[i]), 4);
       mbar_init(smem_u32(&ctl->tile_full[i]), 1);
-      mbar_init(smem_u32(&ctl->tile_free[i]), 10);  // the issuer, the guard, eight softmax warps
+      mbar_init(smem_u32(&ctl->tile_free[i]), 11);  // both issuers, the guard, eight softmax warps
       mbar_init(smem_u32(&ctl->tile_guarded[i]), 1);
     }
     for (int i = 0; i < kGuardRing; ++i) mbar_init(smem_u32(&ctl->guard[i]), 1);
     ctl->abort = 0;
     mbar_fence_init();
+    mbar_arrive(smem_u32(&ctl->turn[0]));  // the first half begins
   }
   int bad = 0;
   for (int i = threadIdx.x; i < a.num_lanes; i += kThreads) {
@@ -301,11 +310,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     regs_decrease<kRegsOther>();
     bool ok = true;
     if (warp == kLoaderWarp) {
-      Order order;
-      order.init(a.cu, a.num_lanes, 2 * a.T, lane);
       const uint32_t half_bytes = (uint32_t)(a.G * a.T) * 128u;  // one 64-dim panel of one half's Q
       long long fills = 0;  // stage fills issued
-      int q_loads = 0;
+      uint32_t q_loads[2] = {0, 0};
       long long guard0 = 0;  // guarded blocks issued
       // a V block that the guard looks at first lands on the guard's barrier; the guard passes it on
       auto load = [&](const CUtensorMap* map, int hk, int row, bool guarded) {
@@ -357,16 +364,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         // the first K and V do not wait for the tile before
         if (!(ok = load(&mk, t.hk, t.row0, false) && load(&mv, t.hk, t.row0, guard_from(t) == 0))) break;
-        if (i >= 1 && !(ok = wait(ctl->q_free, (uint32_t)((i - 1) & 1)))) break;
-        if (lane == 0) {
-          const uint32_t bar = smem_u32(&ctl->q_full);
-          mbar_arrive_expect_tx(bar, half_bytes * 2u * halves);
-          for (int s = 0; s < halves; ++s)
+        for (int s = 0; s < halves; ++s) {
+          if (q_loads[s] > 0 && !(ok = wait(ctl->q_free[s], (q_loads[s] - 1) & 1u))) break;
+          if (lane == 0) {
+            const uint32_t bar = smem_u32(&ctl->q_full[s]);
+            mbar_arrive_expect_tx(bar, half_bytes * 2u);
             for (int p = 0; p < 2; ++p)
               tma_load_3d(base + s * kStageBytes + p * kPanel, &mq, 64 * p, t.hk * a.G, t.row0 + t.t0 + s * a.T, bar);
+          }
+          __syncwarp();
+          ++q_loads[s];
         }
-        __syncwarp();
-        ++q_loads;
+        if (!ok) break;
         for (int j = 1; j < sh.total && ok; ++j)
           ok = load(&mk, t.hk, t.row0 + j * kBlock, false) &&
                load(&mv, t.hk, t.row0 + j * kBlock, j >= guard_from(t));
@@ -374,7 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         // The next tile, asked for when the last blocks of this one are on
         // their way (asked for at its start, the CTAs with the longest tiles
         // take a second one before others are free: 8,192 tokens of 8 / 8
-        // heads 124 against KEPT us).  Places behind the last tile are taken
+        // heads 124 against 92 us).  Places behind the last tile are taken
         // over too, so that no CTA starts for them.
         ask();
         t = {0, 0, 0, 0, 0};
@@ -397,35 +406,50 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (long long f = max(0LL, fills - kStages); f < fills; ++f)
           mbar_wait<false>(smem_u32(&ctl->full[f % kStages]), (uint32_t)((f / kStages) & 1), &none, 400000000LL);
         if (asks > answers) mbar_wait<false>(smem_u32(&ctl->next_full), answers & 1u, &none, 400000000LL);
-        if (q_loads) mbar_wait<false>(smem_u32(&ctl->q_full), (uint32_t)((q_loads - 1) & 1), &none, 400000000LL);
+        for (int s = 0; s < 2; ++s)
+          if (q_loads[s]) mbar_wait<false>(smem_u32(&ctl->q_full[s]), (q_loads[s] - 1) & 1u, &none, 400000000LL);
       }
-    } else if (warp == kIssueWarp) {
+    } else if (warp == kIssueWarp || warp == kIssueWarp + 1) {
+      const int s = warp - kIssueWarp;
       // Descriptors differ in their start address alone: the low words are
       // added up from constants, so that a product costs few instructions
       // here (stage numbers by 64-bit remainders held the tensor core up by
       // 700 cycles a block: 1,566 against 1,731 TFLOP/s at 32,768 tokens).
-      const uint64_t q_desc = sdesc_sw128(base, 1024, 1024);
+      const uint64_t q_desc = sdesc_sw128(base + s * kStageBytes, 1024, 1024);
       const uint64_t k_desc = sdesc_sw128(base + kOffKv, 1024, 1024);
       const uint64_t v_desc = sdesc_sw128(base + kOffKv, kPanel, 1024);
       constexpr uint64_t kStage16 = kStageBytes >> 4, kPanel16 = kPanel >> 4;
+      const uint32_t d_s = tmem + col_s(s), d_o = tmem + col_o(s);
       Ring ring;
-      Phase p_phase[2], o_phase[2];
-      bool used[2] = {false, false};
-      // S = Q K^T for half s with the K block of stage st
-      auto qk = [&](int s, uint32_t st) {
-        const uint64_t qd = q_desc + s * kStage16, kd = k_desc + st * kStage16;
+      Phase p_phase, o_phase, q_phase, turn_phase;
+      bool used = false;
+      // S = Q K^T with the K block of stage st
+      auto qk = [&](uint32_t st) {
+        const uint64_t kd = k_desc + st * kStage16;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
-          mma_f16_ss(tmem + col_s(s), qd + kPanel16 * (k >> 2) + 2 * (k & 3), kd + kPanel16 * (k >> 2) + 2 * (k & 3),
-                     kIdescQK, k != 0);
+          mma_f16_ss(d_s, q_desc + kPanel16 * (k >> 2) + 2 * (k & 3), kd + kPanel16 * (k >> 2) + 2 * (k & 3), kIdescQK,
+                     k != 0);
         mma_commit(smem_u32(&ctl->s_full[s]));
+        mma_commit(smem_u32(&ctl->empty[st]));
       };
-      // O (+)= P V for half s with the V block of stage st
-      auto pv = [&](int s, uint32_t st, bool add) {
+      // O (+)= P V with keys 64 part .. + 63 of the V block of stage st
+      auto pv = [&](uint32_t st, int part, bool add) {
         const uint64_t vd = v_desc + st * kStage16;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-          mma_f16_ts(tmem + col_o(s), tmem + col_s(s) + 8 * k, vd + 128 * k, kIdescPV, add || k != 0);
+        for (int k = 0; k < 4; ++k)
+          mma_f16_ts(d_o, d_s + 32 * part + 8 * k, vd + 512 * part + 128 * k, kIdescPV, add || k != 0);
+      };
+      auto take_turn = [&]() { return wait(ctl->turn[s], turn_phase.take()); };
+      auto pass_turn = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->turn[s ^ 1]));
+      };
+      // a stage that only the other half reads
+      auto leave = [&](Ring r) {
+        if (!wait(ctl->full[r.st], r.phase)) return false;
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->empty[r.st]));
+        return true;
       };
       for (int i = 0; ok; ++i) {
         const int slot = i & 1;
@@ -433,65 +457,65 @@ __global__ void __launch_bounds__(kThreads, 1)
         const Tile t = ctl->tile[slot];
         if (t.len == 0) break;
         const Shape sh(t, a.T);
-        const int n0 = __shfl_sync(0xffffffffu, sh.n[0], 0), n1 = __shfl_sync(0xffffffffu, sh.n[1], 0);
-        const int total = max(n0, n1);
-        if (!(ok = wait(ctl->q_full, (uint32_t)(i & 1)) && wait(ctl->full[ring.st], ring.phase))) break;
-        fence_after_sync();
-        if (elect_one()) {
-          qk(0, ring.st);
-          if (n1 > 0) qk(1, ring.st);
-          mma_commit(smem_u32(&ctl->empty[ring.st]));
-          if (total == 1) mma_commit(smem_u32(&ctl->q_free));
+        const int n = __shfl_sync(0xffffffffu, sh.n[s], 0), total = __shfl_sync(0xffffffffu, sh.total, 0);
+        if (n > 0 && !(ok = wait(ctl->q_full[s], q_phase.take()) && wait(ctl->full[ring.st], ring.phase))) break;
+        if (!(ok = take_turn())) break;
+        if (n > 0) {
+          fence_after_sync();
+          if (elect_one()) {
+            qk(ring.st);
+            if (n == 1) mma_commit(smem_u32(&ctl->q_free[s]));
+          }
         }
-        __syncwarp();
+        pass_turn();
+        if (n == 0 && !(ok = leave(ring))) break;
         ring.next();
-        // one half's PV and next QK back to back, then the other's: the scores
-        // of one half are out while the other half's products run
         for (int j = 0; j < total && ok; ++j) {
           const Ring v = ring;  // V of block j, K of block j + 1
           ring.next();
           const Ring k = ring;
           if (j + 1 < total) ring.next();
-          bool v_here = false, k_here = false;
-#pragma unroll
-          for (int s = 0; s < 2; ++s) {
-            const int n = s ? n1 : n0;
-            if (j >= n) continue;
-            // nothing reads these stages after this half
-            const bool v_last = s == 1 || j >= n1, k_last = s == 1 || j + 1 >= n1, more = j + 1 < n;
-            if (!v_here && !(ok = wait(ctl->full[v.st], v.phase))) break;
-            v_here = true;
-            if (more && !k_here && !(ok = wait(ctl->full[k.st], k.phase))) break;
-            k_here |= more;
-            if (j == 0 && used[s] && !(ok = wait(ctl->o_free[s], o_phase[s].take()))) break;
-            if (!(ok = wait(ctl->p_full[s], p_phase[s].take()))) break;
-            fence_after_sync();
-            if (elect_one()) {
-              pv(s, v.st, j > 0);
-              if (v_last) mma_commit(smem_u32(&ctl->empty[v.st]));
-              if (more) {
-                qk(s, k.st);
-                if (k_last) mma_commit(smem_u32(&ctl->empty[k.st]));
-                if (k_last && j + 2 == total) mma_commit(smem_u32(&ctl->q_free));
-              } else {
-                mma_commit(smem_u32(&ctl->o_full[s]));
-              }
-            }
-            __syncwarp();
+          if (j >= n) {
+            if (!(ok = take_turn())) break;
+            pass_turn();
+            ok = leave(v) && (j + 1 == total || leave(k));
+            continue;
           }
+          const bool more = j + 1 < n;
+          const uint32_t phase = p_phase.take();
+          if (!(ok = wait(ctl->full[v.st], v.phase) && (!more || wait(ctl->full[k.st], k.phase)) &&
+                     (j > 0 || !used || wait(ctl->o_free[s], o_phase.take())) && wait(ctl->p_full[s][0], phase) &&
+                     take_turn()))
+            break;
+          fence_after_sync();
+          if (elect_one()) pv(v.st, 0, j > 0);
+          __syncwarp();
+          if (!(ok = wait(ctl->p_full[s][1], phase))) break;
+          fence_after_sync();
+          if (elect_one()) {
+            pv(v.st, 1, true);
+            mma_commit(smem_u32(&ctl->empty[v.st]));
+            if (more) {
+              qk(k.st);
+              if (j + 2 == n) mma_commit(smem_u32(&ctl->q_free[s]));
+            } else {
+              mma_commit(smem_u32(&ctl->o_full[s]));
+            }
+          }
+          pass_turn();
+          if (!more && j + 1 < total) ok = leave(k);
         }
         if (!ok) break;
-        used[0] = true;
-        used[1] |= n1 > 0;
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->tile_free[slot]));
+        used |= n > 0;
         __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->tile_free[slot]));
       }
       if (!ok) give_up(ctl, a.status);
       // the tensor core is done with everything this warp issued (bounded)
-      if (elect_one()) mma_commit(smem_u32(&ctl->drain));
+      if (elect_one()) mma_commit(smem_u32(&ctl->drain[s]));
       __syncwarp();
       int none = 0;
-      mbar_wait<false>(smem_u32(&ctl->drain), 0, &none, 400000000LL);
+      mbar_wait<false>(smem_u32(&ctl->drain[s]), 0, &none, 400000000LL);
     } else if (warp == kGuardWarp) {
       long long stage0 = 0, guard0 = 0;
       for (int i = 0; ok; ++i) {
@@ -556,8 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = sh.n[s], first = t.t0 + s * a.T;
       const int tok = first + r_tok;
       const bool valid = r_tok < a.T && tok < t.len;
-      float m = ninf;
-      float l = 0.0f;
+      float m = 0.0f, l = 0.0f;
       for (int j = 0; j < n; ++j) {
         if (!(ok = wait(ctl->s_full[s], s_phase.take()))) break;
         fence_after_sync();
@@ -573,6 +596,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int k = 0; k < 32; ++k)
               if (32 * c + k >= seen) x[c][k] = 0xff800000u;
         }
+        // The weights of the first 64 keys are taken with the maximum of the
+        // blocks before, beside this block's maximum (64 three-way maxima are
+        // a third of the work on a block); only where that lies too far off
+        // are they taken again.
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -582,11 +609,40 @@ __global__ void __launch_bounds__(kThreads, 1)
             mx[c] = fmax3(mx[c], __uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1]));
         }
         const float top = fmaxf(fmax3(mx[0], mx[1], mx[2]), mx[3]);
-        // the first block always grows (from -inf); a NaN never does
-        const bool grow = (top - m) * a.scale_log2 > kLag;
-        if (__any_sync(0xffffffffu, grow && valid)) {
-          const float f = grow ? fast_exp2((m - top) * a.scale_log2) : 1.0f;
-          if (grow) m = top;
+        uint32_t p[32];
+        unsigned long long sum0, sum1;
+        // weights of the 64 keys of chunks c0 and c0 + 1, added to the sums
+        auto weights = [&](int c0) {
+          // all scores -inf so far: weights of 0
+          const float shift = m == ninf ? 0.0f : -m * a.scale_log2;
+          const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), sh2 = f2_pack(shift, shift);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float2 e = f2_unpack(
+                  ffma2(f2_pack(__uint_as_float(x[c0 + c][k]), __uint_as_float(x[c0 + c][k + 1])), sc2, sh2));
+              const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+              if (k & 2) sum1 = fadd2(sum1, f2_pack(e0, e1));
+              else sum0 = fadd2(sum0, f2_pack(e0, e1));
+              p[16 * c + k / 2] = pack_bf16x2(e0, e1);
+            }
+        };
+        auto hand_over = [&](int part) {
+          tmem_st32(t_s + 32 * part, p);
+          tmem_wait_st();
+          fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[s][part]));
+        };
+        sum0 = sum1 = 0ull;
+        weights(0);
+        // m starts at 0, where the first block may lie below it, too; no NaN moves it
+        const float above = (top - m) * a.scale_log2;
+        const bool move = above > kLag || (j == 0 && above < -kLag);
+        if (__any_sync(0xffffffffu, move && valid)) {
+          const float f = move ? fast_exp2((m - top) * a.scale_log2) : 1.0f;
+          if (move) m = top;
           l *= f;
           if (j > 0) {
 #pragma unroll 1
@@ -599,29 +655,14 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st16(t_o + 16 * c, o);
             }
           }
+          sum0 = sum1 = 0ull;
+          weights(0);
         }
-        const float shift = m == ninf ? 0.0f : -m * a.scale_log2;  // all scores -inf so far: weights of 0
-        const unsigned long long sc2 = f2_pack(a.scale_log2, a.scale_log2), sh2 = f2_pack(shift, shift);
-        unsigned long long sum0 = 0ull, sum1 = 0ull;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t p[16];
-#pragma unroll
-          for (int k = 0; k < 32; k += 2) {
-            const float2 e = f2_unpack(ffma2(f2_pack(__uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1])), sc2, sh2));
-            const float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
-            if (k & 2) sum1 = fadd2(sum1, f2_pack(e0, e1));
-            else sum0 = fadd2(sum0, f2_pack(e0, e1));
-            p[k / 2] = pack_bf16x2(e0, e1);
-          }
-          tmem_st16(t_s + 16 * c, p);
-        }
+        hand_over(0);
+        weights(2);
         const float2 sum = f2_unpack(fadd2(sum0, sum1));
         l += sum.x + sum.y;
-        tmem_wait_st();
-        fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[s]));
+        hand_over(1);
       }
       if (!ok) break;
       if (!(ok = wait(ctl->tile_guarded[slot], (uint32_t)((i / 2) & 1)))) break;
@@ -674,7 +715,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   fence_before_sync();
   __syncthreads();
-  if (warp == kLoaderWarp) {
+  if (warp == kGuardWarp) {
     fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
   }
