@@ -1,20 +1,22 @@
 // token_logprobs.cu -- log probability of a given token per logits row, the
 // row's entropy and its most probable tokens.
 //
-// With m = max x, S = sum exp(x - m), T = sum exp(x - m) (x - m):
-//   logprob = (x_t - m) - log S,  entropy = log S - T / S,
-// all three in one pass with a running maximum per thread.  The call is bound
-// by reading the logits.
+// In log2 units, with y = (x - m) log2 e for the maximum m, S = sum 2^y and
+// T = sum 2^y y:
+//   logprob = ln 2 (y_t - log2 S),  entropy = ln 2 (log2 S - T / S),
+// all in one pass with a running maximum per thread.  The call is bound by
+// reading the logits (16-bit logits also by the work per element, about four
+// instructions).
 //
 // One cluster of up to 8 CTAs per row, joined through distributed shared
 // memory: no workspace, no second launch.  A thread reads 16-byte vectors at
-// a stride of the block and keeps the running (m, S, T) and the place of its
-// maximum.  The listed tokens come out of these maxima: no element of a
-// thread whose maximum is not among the k largest of the block's threads can
-// be among the k largest elements, so the block sorts its threads' maxima
-// (64-bit keys of value and place, bitonic in the warps, then merged pairwise)
-// and reads again only what the k threads at the top had read.  Comparing a
-// list on every element instead would cost more than the sums.
+// a stride of the block and keeps its maximum, S and T.  The listed tokens come out of these maxima: the k-th largest of the
+// maxima of 128 groups of threads is a bound that k elements reach, so only
+// threads whose maximum reaches it read their elements again (a few more
+// than k), and what reaches it is sorted.  Comparing a list on every element
+// instead would cost more than the sums.  Where that bound says little (fewer
+// than k finite values, long ties, NaN), every element is looked at again in
+// index order against sorted lists of the warps.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -22,19 +24,25 @@
 
 #include <utility>
 
-#include "sdva_common.cuh"
+#include "tc_primitives.cuh"
 
 namespace cg = cooperative_groups;
 
 namespace sdva {
 namespace {
 
-constexpr int kThreads = 512;
-constexpr int kWarps = kThreads / 32;
+using tc::f2_pack;
+using tc::f2_unpack;
+using tc::fadd2;
+using tc::ffma2;
+using tc::fmul2;
+
 constexpr int kMaxCluster = 8;
-constexpr int kUnroll = 4;            // vectors in flight per thread
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNothing = -150.0f;   // exp is 0 in fp32 from here on down: lower values need no forming
+constexpr int kBig = 512;       // threads per CTA (128 for short rows)
+constexpr int kGroups = 128;    // groups of threads whose maxima bound the list
+constexpr int kCandidates = 512;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kNothing = -200.0f;  // 2^y is 0 in fp32 from here on down: lower values need no forming
 typedef unsigned long long Key;
 
 struct LogprobArgs {
@@ -49,30 +57,41 @@ struct LogprobArgs {
   int vocab, num_top;
 };
 
-// Element types: 16 bytes as floats, and one element.
+// Element types: 16 bytes as floats, their largest, and one element.
 template <typename T>
 struct Elem;
 template <>
 struct Elem<float> {
-  static constexpr int kVec = 4;
+  static constexpr int kVec = 4, kUnroll = 4;  // elements per vector; vectors per thread and round
+  static constexpr uint32_t kNone = 0xff800000u;  // -inf
   static __device__ float one(float x) { return x; }
   static __device__ void unpack(uint4 w, float* f) {
     f[0] = __uint_as_float(w.x), f[1] = __uint_as_float(w.y), f[2] = __uint_as_float(w.z), f[3] = __uint_as_float(w.w);
   }
+  static __device__ float largest(uint4 w) {
+    return fmaxf(fmaxf(__uint_as_float(w.x), __uint_as_float(w.y)), fmaxf(__uint_as_float(w.z), __uint_as_float(w.w)));
+  }
 };
 template <>
 struct Elem<__nv_bfloat16> {
-  static constexpr int kVec = 8;
+  static constexpr int kVec = 8, kUnroll = 4;
+  static constexpr uint32_t kNone = 0xff80ff80u;
   static __device__ float one(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ void unpack(uint4 w, float* f) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) f[2 * i] = bf16_lo(u[i]), f[2 * i + 1] = bf16_hi(u[i]);
   }
+  static __device__ float largest(uint4 w) {
+    const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&w);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+  }
 };
 template <>
 struct Elem<__half> {
-  static constexpr int kVec = 8;
+  static constexpr int kVec = 8, kUnroll = 4;
+  static constexpr uint32_t kNone = 0xfc00fc00u;
   static __device__ float one(__half x) { return __half2float(x); }
   static __device__ void unpack(uint4 w, float* f) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
@@ -81,6 +100,11 @@ struct Elem<__half> {
       const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
       f[2 * i] = v.x, f[2 * i + 1] = v.y;
     }
+  }
+  static __device__ float largest(uint4 w) {
+    const __half2* h = reinterpret_cast<const __half2*>(&w);
+    const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
   }
 };
 
@@ -98,13 +122,13 @@ __device__ __forceinline__ float value_of(Key k) {
   return u == 0u ? __int_as_float(0x7fc00000) : __int_as_float(b >= 0 ? b : b ^ 0x7fffffff);
 }
 
-// Running statistics of a set of logits; s == 0: empty or all -inf.
+// Running statistics of a set of logits: m (0 where all are -inf), S, T.
 struct Stat {
   float m, s, t;
 };
-__device__ __forceinline__ Stat moved(Stat a, float m) {  // the same with reference m >= a.m
+__device__ __forceinline__ Stat moved(Stat a, float m) {  // the same about a larger m
   if (a.s == 0.0f || a.m == m) return {m, a.s, a.t};
-  const float d = fmaxf(a.m - m, kNothing), c = fast_exp2(d * kLog2e);
+  const float d = fmaxf((a.m - m) * kLog2e, kNothing), c = fast_exp2(d);
   return {m, a.s * c, (a.t + a.s * d) * c};
 }
 __device__ __forceinline__ float max_nan(float a, float b) {  // NaN if either is
@@ -136,6 +160,7 @@ __device__ __forceinline__ Key warp_merge(Key a, Key b) {
   return k;
 }
 // the 32 largest of the warps' sorted lists, in warp 0
+template <int kWarps>
 __device__ Key block_merge(Key k, Key (*buf)[32]) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 #pragma unroll
@@ -150,79 +175,88 @@ __device__ Key block_merge(Key k, Key (*buf)[32]) {
 // The part of a row that one CTA reads.  Vectors start at the row's first
 // 16-byte boundary; the few elements before it and behind the last whole
 // vector go one each to the first threads of CTA 0.
-template <typename T>
+template <typename T, int kThreads>
 struct Part {
   static constexpr int kVec = Elem<T>::kVec;
   const T* x;
-  int head, vocab, first, vectors;  // elements before the vectors; this CTA's vectors of the row
-  int extra;                        // single elements
-  int tail0;                        // index of the first element behind the vectors
+  int head, vectors;        // elements before the row's vectors; this CTA's vectors
+  int first;                // index of their first element
+  int tail0, extra;         // index of the first element behind the row's vectors; single elements
 
   __device__ Part(const T* row, int V, int part, int parts) {
     x = row;
-    vocab = V;
     const int off = (int)(reinterpret_cast<uintptr_t>(row) & 15u) / (int)sizeof(T);
     head = min(V, off ? kVec - off : 0);
     const int all = (V - head) / kVec;
     tail0 = head + all * kVec;
-    const int each = (all + parts - 1) / parts;
-    first = min(all, part * each);
-    vectors = min(all, first + each) - first;
+    const int each = (all + parts - 1) / parts, lo = min(all, part * each);
+    vectors = min(all, lo + each) - lo;
+    first = head + lo * kVec;
     extra = part == 0 ? head + V - tail0 : 0;
   }
-  __device__ uint4 load(int v) const { return __ldg(reinterpret_cast<const uint4*>(x + head) + first + v); }
-  __device__ int index(int v) const { return head + (first + v) * kVec; }
+  __device__ uint4 load(int v) const { return __ldg(reinterpret_cast<const uint4*>(x + first) + v); }
   __device__ int extra_index(int e) const { return e < head ? e : tail0 + e - head; }
-  // thread that reads element i
-  __device__ int owner(int i) const {
-    if (i < head) return i;
-    if (i >= tail0) return head + i - tail0;
-    return ((i - head) / kVec - first) % kThreads;
-  }
-  __device__ int owned(int th) const { return max(0, (vectors - th + kThreads - 1) / kThreads) * kVec + (th < extra); }
-  __device__ int owned_index(int th, int e) const {  // its e-th element
-    const int n = owned(th) - (th < extra);
-    return e < n ? index(th + e / kVec * kThreads) + e % kVec : extra_index(th);
-  }
 };
 
-// 16 logits, element j at index i0 + (j / kVec) * stride + j % kVec: into the
-// thread's statistics; m is the thread's maximum, best its first place.
-template <int kVec>
-__device__ __forceinline__ void add16(Stat& a, int& best, const float (&x)[16], int i0, int stride) {
-  float m = fmaxf(x[0], x[1]);
-#pragma unroll
-  for (int j = 2; j < 16; ++j) m = fmaxf(m, x[j]);
-  if (m > a.m || best < 0) {
-    int at = 0;
-#pragma unroll
-    for (int j = 15; j > 0; --j)
-      if (x[j] == m) at = j;
-    if (x[0] == m) at = 0;
-    best = i0 + at / kVec * stride + at % kVec;
+// 16 logits with maximum m into the thread's statistics; `top` is the
+// thread's maximum.
+__device__ __forceinline__ void add16(Stat& a, float& top, float m, const float (&x)[16]) {
+  if (m > top) {
+    top = m;
     a = moved(a, m);
   }
-  const float ref = a.m == __int_as_float(0xff800000) ? 0.0f : a.m;  // all -inf so far
-  float s[2] = {0.0f, 0.0f}, t[2] = {0.0f, 0.0f};
+  const unsigned long long c2 = f2_pack(kLog2e, kLog2e), r2 = f2_pack(-a.m, -a.m);
+  unsigned long long s[2] = {0ull, 0ull}, t[2] = {0ull, 0ull};
 #pragma unroll
-  for (int j = 0; j < 16; ++j) {
-    const float d = max_nan(x[j] - ref, kNothing), e = fast_exp2(d * kLog2e);
-    s[j & 1] += e;
-    t[j & 1] += e * d;
+  for (int j = 0; j < 16; j += 2) {
+    const unsigned long long y2 = fmul2(fadd2(f2_pack(x[j], x[j + 1]), r2), c2);
+    const float2 y = f2_unpack(y2);
+    const unsigned long long e = f2_pack(fast_exp2(y.x), fast_exp2(y.y));
+    s[(j >> 1) & 1] = fadd2(s[(j >> 1) & 1], e);
+    t[(j >> 1) & 1] = ffma2(e, y2, t[(j >> 1) & 1]);
   }
-  a.s += s[0] + s[1];
-  a.t += t[0] + t[1];
+  const float2 sum = f2_unpack(fadd2(s[0], s[1])), dot = f2_unpack(fadd2(t[0], t[1]));
+  float d = dot.x + dot.y;
+  if (d != d) {  // 0 * -inf: forbidden tokens have no part
+    d = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      const float y = max_nan((x[j] - a.m) * kLog2e, kNothing);
+      d += fast_exp2(y) * y;
+    }
+  }
+  a.s += sum.x + sum.y;
+  a.t += d;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(LogprobArgs a, int parts) {
-  constexpr int kVec = Elem<T>::kVec;
+// The statistics of n lanes' sets (a power of two), in every lane of them.
+template <int n>
+__device__ __forceinline__ Stat warp_join(Stat a) {
+  float m = a.s == 0.0f ? __int_as_float(0xff800000) : a.m;  // of an empty set it means nothing
+#pragma unroll
+  for (int o = n / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  Stat b = moved(a, m == __int_as_float(0xff800000) ? 0.0f : m);
+#pragma unroll
+  for (int o = n / 2; o > 0; o >>= 1) {
+    b.s += __shfl_xor_sync(0xffffffffu, b.s, o);
+    b.t += __shfl_xor_sync(0xffffffffu, b.t, o);
+  }
+  return b;
+}
+
+// kThreads: 512, or 128 for short rows.
+template <typename T, int kThreads>
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kernel(LogprobArgs a, int parts) {
+  constexpr int kVec = Elem<T>::kVec, kPer = 16 / kVec, kUnroll = Elem<T>::kUnroll, kWarps = kThreads / 32;
   __shared__ Stat s_stat[kWarps];
-  __shared__ Key s_keys[kWarps][32];
-  __shared__ Key s_hot[32];
-  __shared__ int s_odd;
+  __shared__ float4 s_group4[kGroups / 4];  // read four at a time
+  __shared__ Key s_keys[kCandidates];  // candidates, or the warps' lists
+  __shared__ float s_bound;
+  __shared__ int s_count, s_odd;
   __shared__ Stat c_stat[kMaxCluster];  // in CTA 0: one entry per CTA of the cluster
   __shared__ Key c_keys[kMaxCluster][32];
+  float* const s_group = reinterpret_cast<float*>(s_group4);
+  static_assert(kCandidates >= kWarps * 32, "the warps' lists share the candidates' place");
   const int row = blockIdx.x / parts, part = blockIdx.x % parts;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, th = threadIdx.x;
   const int token = a.tokens[row];
@@ -243,125 +277,165 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(LogprobArgs
   cg::cluster_group cluster = cg::this_cluster();
   auto started = cluster.barrier_arrive();
   const float ninf = __int_as_float(0xff800000);
-  const Part<T> p(static_cast<const T*>(a.logits) + (size_t)row * a.row_stride, a.vocab, part, parts);
+  const Part<T, kThreads> p(static_cast<const T*>(a.logits) + (size_t)row * a.row_stride, a.vocab, part, parts);
   float x_t = 0.0f;
   if (part == 0 && th == 0) x_t = Elem<T>::one(p.x[token]);
 
-  Stat st = {ninf, 0.0f, 0.0f};
-  int best = -1;
-  for (int v = th; v < p.vectors; v += kUnroll * kThreads) {
+  Stat st = {0.0f, 0.0f, 0.0f};
+  float top = ninf;
+  // rounds of whole vectors, the next one's loads in flight
+  auto add = [&](const uint4 (&w)[kPer]) {
+    float x[16], m = ninf;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+      Elem<T>::unpack(w[k], x + k * kVec);
+      m = fmaxf(m, Elem<T>::largest(w[k]));
+    }
+    add16(st, top, m, x);
+  };
+  constexpr int kRound = kUnroll * kThreads;
+  int v = th;
+  if (v + (kUnroll - 1) * kThreads < p.vectors) {
+    uint4 next[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) next[u] = p.load(v + u * kThreads);
+    do {
+      uint4 w[kUnroll];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) w[u] = next[u];
+      v += kRound;
+      if (v + (kUnroll - 1) * kThreads < p.vectors) {
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) next[u] = p.load(v + u * kThreads);
+      }
+#pragma unroll
+      for (int u = 0; u < kUnroll; u += kPer) {
+        uint4 g[kPer];
+#pragma unroll
+        for (int k = 0; k < kPer; ++k) g[k] = w[u + k];
+        add(g);
+      }
+    } while (v + (kUnroll - 1) * kThreads < p.vectors);
+  }
+  if (v < p.vectors) {
+    // fewer than a round: what is missing has no part in anything
     uint4 w[kUnroll];
+    constexpr uint32_t none = Elem<T>::kNone;
 #pragma unroll
     for (int u = 0; u < kUnroll; ++u)
-      if (v + u * kThreads < p.vectors) w[u] = p.load(v + u * kThreads);
-    constexpr int kPer = 16 / kVec;  // vectors per sixteen elements
+      w[u] = v + u * kThreads < p.vectors ? p.load(v + u * kThreads) : make_uint4(none, none, none, none);
 #pragma unroll
     for (int u = 0; u < kUnroll; u += kPer) {
-      float x[16];
+      uint4 g[kPer];
 #pragma unroll
-      for (int k = 0; k < kPer; ++k) {
-        if (v + (u + k) * kThreads < p.vectors) {
-          Elem<T>::unpack(w[u + k], x + k * kVec);
-        } else {
-#pragma unroll
-          for (int j = 0; j < kVec; ++j) x[k * kVec + j] = ninf;  // no part in anything
-        }
-      }
-      if (v + u * kThreads < p.vectors) add16<kVec>(st, best, x, p.index(v + u * kThreads), kThreads * kVec);
+      for (int k = 0; k < kPer; ++k) g[k] = w[u + k];
+      if (v + u * kThreads < p.vectors) add(g);
     }
   }
   if (th < p.extra) {
-    const int i = p.extra_index(th);
     float x[16];
-    x[0] = Elem<T>::one(p.x[i]);
+    x[0] = Elem<T>::one(p.x[p.extra_index(th)]);
 #pragma unroll
     for (int j = 1; j < 16; ++j) x[j] = ninf;
-    // behind the vectors in index order or before them: an equal value there keeps its place only if it comes first
-    const float m = st.m;
-    const int was = best;
-    add16<kVec>(st, best, x, i, 0);
-    if (x[0] == m && was >= 0) best = min(was, i);
+    add16(st, top, x[0], x);
   }
-  const Key own = best < 0 ? 0 : key_of(st.m, best);
 
-  // the block's statistics
-  {
-    float m = st.m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    Stat w = moved(st, m);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      w.s += __shfl_xor_sync(0xffffffffu, w.s, o);
-      w.t += __shfl_xor_sync(0xffffffffu, w.t, o);
-    }
-    if (lane == 0) s_stat[warp] = w;
-  }
+  const Stat ws = warp_join<32>(st);
+  if (lane == 0) s_stat[warp] = ws;
   if (a.num_top > 0) {
-    // the threads with the largest maxima, largest first
-    Key k = block_merge(warp_sort(own), s_keys);
-    if (warp == 0) s_hot[lane] = k;
+    float g = top;
+#pragma unroll
+    for (int o = kThreads / kGroups / 2; o > 0; o >>= 1) g = fmaxf(g, __shfl_xor_sync(0xffffffffu, g, o));
+    if (th % (kThreads / kGroups) == 0) s_group[th / (kThreads / kGroups)] = g;
+    if (th == 0) {
+      s_count = 0;
+      s_bound = ninf;
+    }
   }
   __syncthreads();
   cluster.barrier_wait(std::move(started));
-  if (warp == 0) {
-    const Stat w = lane < kWarps ? s_stat[lane] : Stat{ninf, 0.0f, 0.0f};
-    float m = w.m;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    Stat b = moved(w, m);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      b.s += __shfl_xor_sync(0xffffffffu, b.s, o);
-      b.t += __shfl_xor_sync(0xffffffffu, b.t, o);
-    }
+  if (warp == kWarps - 1) {
+    const Stat b = warp_join<kWarps>(lane < kWarps ? s_stat[lane] : Stat{0.0f, 0.0f, 0.0f});
     if (lane == 0) {
-      s_odd = b.s != b.s;
+      s_odd = b.s != b.s;  // a NaN, or +inf, which makes one
       *cluster.map_shared_rank(&c_stat[part], 0) = b;
     }
   }
   if (a.num_top > 0) {
+    // the bound: the num_top-th largest group maximum, by counting
+    if (th < kGroups) {
+      const float own = s_group[th];
+      int above = 0, same = 0;
+#pragma unroll 8
+      for (int i = 0; i < kGroups; i += 4) {
+        const float4 o = s_group4[i / 4];
+        above += (o.x > own) + (o.y > own) + (o.z > own) + (o.w > own);
+        same += (o.x == own) + (o.y == own) + (o.z == own) + (o.w == own);
+      }
+      if (above < a.num_top && above + same >= a.num_top) s_bound = own;
+    }
     __syncthreads();
-    // A NaN (or +inf, which makes one) hides its thread's maximum: then every
-    // thread's elements are looked at again.
-    const bool odd = s_odd != 0;
-    const Key least = odd ? 0 : s_hot[a.num_top - 1];
-    Key list = 0;
-    for (int h = warp; h < (odd ? kThreads : a.num_top); h += kWarps) {
-      if (!odd && s_hot[h] == 0) break;
-      const int who = odd ? h : p.owner(index_of(s_hot[h])), n = p.owned(who);
-      for (int e = lane; e - lane < n; e += 32) {
+    const float bound = s_bound;
+    bool all = s_odd != 0 || bound == ninf;
+    if (!all) {
+      auto offer = [&](float x, int i) {
+        if (x >= bound) {
+          const int at = atomicAdd(&s_count, 1);
+          if (at < kCandidates) s_keys[at] = key_of(x, i);
+        }
+      };
+      unsigned hot = __ballot_sync(0xffffffffu, top >= bound);
+      while (hot != 0 && __all_sync(0xffffffffu, s_count <= kCandidates)) {  // a count beyond the place ends the search
+        const int who = warp * 32 + __ffs(hot) - 1;
+        hot &= hot - 1;
+#pragma unroll 3
+        for (int v = who + lane * kThreads; v < p.vectors; v += 32 * kThreads) {
+          const uint4 w = p.load(v);
+          if (Elem<T>::largest(w) >= bound) {
+            float x[kVec];
+            Elem<T>::unpack(w, x);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) offer(x[j], p.first + v * kVec + j);
+          }
+        }
+        if (lane == 0 && who < p.extra) offer(Elem<T>::one(p.x[p.extra_index(who)]), p.extra_index(who));
+        __syncwarp();
+      }
+      __syncthreads();
+      const int count = s_count;
+      all = count > kCandidates;
+      if (!all && warp == 0) {
+        Key k = warp_sort(lane < count ? s_keys[lane] : 0);
+        for (int i = 32; i < count; i += 32) k = warp_merge(k, warp_sort(i + lane < count ? s_keys[i + lane] : 0));
+        cluster.map_shared_rank(&c_keys[part][0], 0)[lane] = k;
+      }
+    }
+    if (all) {  // the same for the whole CTA
+      __syncthreads();
+      Key list = 0;
+      const int n = p.vectors * kVec + p.extra;
+      for (int e0 = warp * 32; e0 < n; e0 += kThreads) {
+        const int e = e0 + lane;
         Key k = 0;
         if (e < n) {
-          const int i = p.owned_index(who, e);
+          const int i = e < p.extra ? p.extra_index(e) : p.first + e - p.extra;
           k = key_of(Elem<T>::one(p.x[i]), i);
         }
-        if (k < least) k = 0;
         const Key last = __shfl_sync(0xffffffffu, list, a.num_top - 1);
         if (__any_sync(0xffffffffu, k > last)) list = warp_merge(list, warp_sort(k));
       }
+      list = block_merge<kWarps>(list, reinterpret_cast<Key(*)[32]>(s_keys));
+      if (warp == 0) cluster.map_shared_rank(&c_keys[part][0], 0)[lane] = list;
     }
-    __syncthreads();
-    list = block_merge(list, s_keys);
-    if (warp == 0) cluster.map_shared_rank(&c_keys[part][0], 0)[lane] = list;
   }
   cluster.sync();
   if (part != 0 || warp != 0) return;
-  const Stat w = lane < parts ? c_stat[lane] : Stat{ninf, 0.0f, 0.0f};
-  float m = w.m;
-#pragma unroll
-  for (int o = kMaxCluster / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  Stat b = moved(w, m);
-#pragma unroll
-  for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
-    b.s += __shfl_xor_sync(0xffffffffu, b.s, o);
-    b.t += __shfl_xor_sync(0xffffffffu, b.t, o);
-  }
+  const Stat b = warp_join<kMaxCluster>(lane < parts ? c_stat[lane] : Stat{0.0f, 0.0f, 0.0f});
   // no distribution: all -inf, or a NaN or +inf in the row
-  const float log_s = b.s > 0.0f ? logf(b.s) : __int_as_float(0x7fc00000);
+  const float log_s = b.s > 0.0f ? log2f(b.s) : __int_as_float(0x7fc00000);
   if (lane == 0) {
-    a.logprobs[row] = x_t - b.m - log_s;
-    if (a.entropy != nullptr) a.entropy[row] = log_s - b.t / b.s;
+    a.logprobs[row] = x_t - b.m - log_s * kLn2;
+    if (a.entropy != nullptr) a.entropy[row] = (log_s - b.t / b.s) * kLn2;
   }
   if (a.num_top > 0) {
     const float ref = __shfl_sync(0xffffffffu, b.m, 0), ls = __shfl_sync(0xffffffffu, log_s, 0);
@@ -369,9 +443,37 @@ __global__ void __launch_bounds__(kThreads, 2) token_logprobs_kernel(LogprobArgs
     for (int q = 1; q < parts; ++q) k = warp_merge(k, c_keys[q][lane]);
     if (lane < a.num_top) {
       a.top_tokens[(size_t)row * a.num_top + lane] = index_of(k);
-      a.top_logprobs[(size_t)row * a.num_top + lane] = value_of(k) - ref - ls;
+      a.top_logprobs[(size_t)row * a.num_top + lane] = value_of(k) - ref - ls * kLn2;
     }
   }
+}
+
+template <typename T, int kThreads>
+int launch(const LogprobArgs& a, int num_rows, int sms, cudaStream_t stream) {
+  // CTAs per row: enough that every SM has its two of 512 threads, and no less than two rounds of loads for a thread
+  int parts = 1;
+  while (parts < kMaxCluster && (long long)num_rows * parts < 2LL * sms &&
+         a.vocab > 2LL * parts * kThreads * Elem<T>::kUnroll * Elem<T>::kVec)
+    parts *= 2;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)num_rows * parts, 1, 1);
+  cfg.blockDim = dim3(kThreads, 1, 1);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = parts;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, kThreads>, a, parts) == cudaSuccess ? SDVA_OK
+                                                                                              : SDVA_ERR_CUDA;
+}
+
+template <typename T>
+int launch(const LogprobArgs& a, int num_rows, int sms, cudaStream_t stream) {
+  return a.vocab < 8 * kBig * Elem<T>::kVec ? launch<T, 128>(a, num_rows, sms, stream)
+                                            : launch<T, kBig>(a, num_rows, sms, stream);
 }
 
 }  // namespace
@@ -395,23 +497,8 @@ extern "C" int token_logprobs(const void* logits, int logits_dtype, int64_t row_
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return SDVA_ERR_CUDA;
   const LogprobArgs a = {logits, row_stride, tokens, logprobs, entropy, top_tokens, top_logprobs, status, vocab, num_top};
-  // CTAs per row: enough that every SM has its two, and no less than one round of loads for each thread
-  int parts = 1;
-  const long long round = (long long)kThreads * (logits_dtype == SDVA_LOGITS_F32 ? 4 : 8);
-  while (parts < kMaxCluster && (long long)num_rows * parts < 2LL * sms && vocab > 2 * parts * round) parts *= 2;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)num_rows * parts, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = parts;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  const auto kernel = logits_dtype == SDVA_LOGITS_F32    ? token_logprobs_kernel<float>
-                      : logits_dtype == SDVA_LOGITS_BF16 ? token_logprobs_kernel<__nv_bfloat16>
-                                                         : token_logprobs_kernel<__half>;
-  return cudaLaunchKernelEx(&cfg, kernel, a, parts) == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return logits_dtype == SDVA_LOGITS_F32    ? launch<float>(a, num_rows, sms, s)
+         : logits_dtype == SDVA_LOGITS_BF16 ? launch<__nv_bfloat16>(a, num_rows, sms, s)
+                                            : launch<__half>(a, num_rows, sms, s);
 }
