@@ -13,7 +13,7 @@
 // a stride of the block and keeps its maximum, S and T.  The listed tokens come out of these maxima: the k-th largest of the
 // maxima of 128 groups of threads is a bound that k elements reach, so only
 // threads whose maximum reaches it read their elements again (a few more
-// than k), and what reaches it is sorted.  Comparing a list on every element
+// than k), and what reaches it is put in order by counting.  Comparing a list on every element
 // instead would cost more than the sums.  Where that bound says little (fewer
 // than k finite values, long ties, NaN), every element is looked at again in
 // index order against sorted lists of the warps.
@@ -110,17 +110,17 @@ struct Elem<__half> {
 
 // (value, index) as one number that orders by value, then lowest index; NaN
 // below -inf, the zeros equal; never 0, which stands for "none".
-__device__ __forceinline__ Key key_of(float x, int i) {
+__device__ __forceinline__ uint32_t order_of(float x) {
   const int b = __float_as_int(x + 0.0f);
-  const uint32_t u = x != x ? 0u : (uint32_t)(b >= 0 ? b : b ^ 0x7fffffff) ^ 0x80000000u;
-  return ((Key)u << 32) | (uint32_t)~i;
+  return x != x ? 0u : (uint32_t)(b >= 0 ? b : b ^ 0x7fffffff) ^ 0x80000000u;
 }
-__device__ __forceinline__ int index_of(Key k) { return (int)~(uint32_t)k; }
-__device__ __forceinline__ float value_of(Key k) {
-  const uint32_t u = (uint32_t)(k >> 32);
+__device__ __forceinline__ float of_order(uint32_t u) {
   const int b = (int)(u ^ 0x80000000u);
   return u == 0u ? __int_as_float(0x7fc00000) : __int_as_float(b >= 0 ? b : b ^ 0x7fffffff);
 }
+__device__ __forceinline__ Key key_of(float x, int i) { return ((Key)order_of(x) << 32) | (uint32_t)~i; }
+__device__ __forceinline__ int index_of(Key k) { return (int)~(uint32_t)k; }
+__device__ __forceinline__ float value_of(Key k) { return of_order((uint32_t)(k >> 32)); }
 
 // Running statistics of a set of logits: m (0 where all are -inf), S, T.
 struct Stat {
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
   __shared__ Stat s_stat[kWarps];
   __shared__ float4 s_group4[kGroups / 4];  // read four at a time
   __shared__ Key s_keys[kCandidates];  // candidates, or the warps' lists
-  __shared__ float s_bound;
+  __shared__ uint32_t s_bound;
   __shared__ int s_count, s_odd;
   __shared__ Stat c_stat[kMaxCluster];  // in CTA 0: one entry per CTA of the cluster
   __shared__ Key c_keys[kMaxCluster][32];
@@ -349,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
     if (th % (kThreads / kGroups) == 0) s_group[th / (kThreads / kGroups)] = g;
     if (th == 0) {
       s_count = 0;
-      s_bound = ninf;
+      s_bound = 0xffffffffu;
     }
   }
   __syncthreads();
@@ -362,20 +362,23 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
     }
   }
   if (a.num_top > 0) {
-    // the bound: the num_top-th largest group maximum, by counting
-    if (th < kGroups) {
-      const float own = s_group[th];
-      int above = 0, same = 0;
-#pragma unroll 8
-      for (int i = 0; i < kGroups; i += 4) {
-        const float4 o = s_group4[i / 4];
+    // The bound, the num_top-th largest group maximum: the smallest with
+    // fewer than num_top above it.  A group's threads share the comparisons.
+    {
+      constexpr int kShare = kThreads / kGroups;
+      const float own = s_group[th / kShare];
+      int above = 0;
+#pragma unroll
+      for (int i = 0; i < kGroups / 4 / kShare; ++i) {
+        const float4 o = s_group4[i * kShare + th % kShare];
         above += (o.x > own) + (o.y > own) + (o.z > own) + (o.w > own);
-        same += (o.x == own) + (o.y == own) + (o.z == own) + (o.w == own);
       }
-      if (above < a.num_top && above + same >= a.num_top) s_bound = own;
+#pragma unroll
+      for (int o = kShare / 2; o > 0; o >>= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+      if (th % kShare == 0 && above < a.num_top) atomicMin(&s_bound, order_of(own));
     }
     __syncthreads();
-    const float bound = s_bound;
+    const float bound = of_order(s_bound);
     bool all = s_odd != 0 || bound == ninf;
     if (!all) {
       auto offer = [&](float x, int i) {
@@ -404,10 +407,17 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
       __syncthreads();
       const int count = s_count;
       all = count > kCandidates;
-      if (!all && warp == 0) {
-        Key k = warp_sort(lane < count ? s_keys[lane] : 0);
-        for (int i = 32; i < count; i += 32) k = warp_merge(k, warp_sort(i + lane < count ? s_keys[i + lane] : 0));
-        cluster.map_shared_rank(&c_keys[part][0], 0)[lane] = k;
+      if (!all) {
+        Key* const list = cluster.map_shared_rank(&c_keys[part][0], 0);
+        for (int i = th; i < max(count, 32); i += kThreads) {
+          const Key k = i < count ? s_keys[i] : 0;
+          int rank = i;
+          if (i < count) {
+            rank = 0;
+            for (int j = 0; j < count; ++j) rank += s_keys[j] > k;
+          }
+          if (rank < 32) list[rank] = k;
+        }
       }
     }
     if (all) {  // the same for the whole CTA
@@ -432,10 +442,10 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
   if (part != 0 || warp != 0) return;
   const Stat b = warp_join<kMaxCluster>(lane < parts ? c_stat[lane] : Stat{0.0f, 0.0f, 0.0f});
   // no distribution: all -inf, or a NaN or +inf in the row
-  const float log_s = b.s > 0.0f ? log2f(b.s) : __int_as_float(0x7fc00000);
-  if (lane == 0) {
-    a.logprobs[row] = x_t - b.m - log_s * kLn2;
-    if (a.entropy != nullptr) a.entropy[row] = (log_s - b.t / b.s) * kLn2;
+  const float log_s = (b.s > 0.0f ? log2f(b.s) : __int_as_float(0x7fc00000)) * kLn2;
+  if (th == 0) {
+    a.logprobs[row] = x_t - b.m - log_s;
+    if (a.entropy != nullptr) a.entropy[row] = log_s - b.t / b.s * kLn2;
   }
   if (a.num_top > 0) {
     const float ref = __shfl_sync(0xffffffffu, b.m, 0), ls = __shfl_sync(0xffffffffu, log_s, 0);
@@ -443,14 +453,14 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
     for (int q = 1; q < parts; ++q) k = warp_merge(k, c_keys[q][lane]);
     if (lane < a.num_top) {
       a.top_tokens[(size_t)row * a.num_top + lane] = index_of(k);
-      a.top_logprobs[(size_t)row * a.num_top + lane] = value_of(k) - ref - ls * kLn2;
+      a.top_logprobs[(size_t)row * a.num_top + lane] = value_of(k) - ref - ls;
     }
   }
 }
 
 template <typename T, int kThreads>
 int launch(const LogprobArgs& a, int num_rows, int sms, cudaStream_t stream) {
-  // CTAs per row: enough that every SM has its two of 512 threads, and no less than two rounds of loads for a thread
+  // CTAs per row: two for every SM, and no less than two rounds of loads for a thread
   int parts = 1;
   while (parts < kMaxCluster && (long long)num_rows * parts < 2LL * sms &&
          a.vocab > 2LL * parts * kThreads * Elem<T>::kUnroll * Elem<T>::kVec)
