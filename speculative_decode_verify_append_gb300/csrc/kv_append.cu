@@ -33,10 +33,7 @@ struct AppendArgs {
   const int32_t* seq_lens;
   int32_t* status;
   const int32_t* n_lane;  // nullable [B]: tokens lane b writes (<= n_new); NULL: n_new each
-  const int32_t* cu;      // packed rows: [B + 1] row offsets of the lanes
-  long long k_stride, v_stride;  // elements between token rows
   int num_pages, num_kv_heads, n_new, max_pages;
-  int num_lanes, total;  // packed rows
 };
 
 constexpr int kAppendThreads = 256;
@@ -90,84 +87,26 @@ __device__ __forceinline__ float block_max(float v) {
   return r;
 }
 
-// The page one CTA works on: tokens [t0, t0 + count) of lane b go to offsets
-// [start, start + count) of physical page pid; `row` is the first one's input
-// row.
-struct PageJob {
-  int pid, start, count;
-  size_t row;
-};
-
-// Packed rows: first slot of lane b in the flat grid of page slots.  A lane
-// of n tokens touches at most n / 64 + 2 pages wherever it starts, and
-// cu[b + 1] / 64 - cu[b] / 64 >= n / 64, so consecutive bases leave room
-// without a prefix sum over the lanes.
-__device__ __forceinline__ int slot_base(const int32_t* cu, int b) { return cu[b] / kPage + 2 * b; }
-
-// Which page this CTA writes, false if none: slot blockIdx.x of lane
-// blockIdx.y of a padded window, or flat slot blockIdx.x of packed rows.
-// Flags a bad count, length or page id once (`first`: the CTA is the first of
-// its page's along the grid's other axes).
-template <bool kPacked>
-__device__ bool page_job(const AppendArgs& a, bool first, PageJob* j) {
-  int b, slot, n;
-  size_t row0;
-  bool report;
-  if constexpr (kPacked) {
-    int bad = 0;
-    for (int i = threadIdx.x; i < a.num_lanes; i += blockDim.x) {
-      const int lo = a.cu[i], hi = a.cu[i + 1];
-      bad |= lo < 0 || hi < lo || hi > a.total;
-    }
-    if (__syncthreads_or(bad)) {
-      if (first && blockIdx.x == 0 && threadIdx.x == 0) raise_status(a.status, SDVA_STATUS_BAD_COUNT);
-      return false;
-    }
-    int lo = 0, hi = a.num_lanes;  // the last lane whose base is at or before this slot
-    if (slot_base(a.cu, 0) > (int)blockIdx.x) return false;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (slot_base(a.cu, mid) <= (int)blockIdx.x) lo = mid;
-      else hi = mid;
-    }
-    b = lo;
-    slot = (int)blockIdx.x - slot_base(a.cu, b);
-    n = a.cu[b + 1] - a.cu[b];
-    row0 = a.cu[b];
-    report = first && slot == 0;
-  } else {
-    b = blockIdx.y;
-    slot = blockIdx.x;
-    report = first && slot == 0;
-    n = lane_tokens(a, b, report);
-    row0 = (size_t)b * a.n_new;
-  }
-  if (n == 0) return false;  // nothing to write: the lane is not examined
-  const int L = a.seq_lens[b];
-  if (!lane_admitted(a, b, L, n, report)) return false;
-  const int lp = L / kPage + slot;
-  if ((long long)lp * kPage >= (long long)L + n) return false;
-  const int t0 = max(L, lp * kPage), t1 = (int)min((long long)L + n, (long long)lp * kPage + kPage);
-  j->pid = a.page_table[(size_t)b * a.max_pages + lp];
-  j->start = t0 - lp * kPage;
-  j->count = t1 - t0;
-  j->row = row0 + (t0 - L);
-  return true;
-}
-
-// grid: (touched-page slot, lane, kv_head * 2 + {0: K, 1: V}); packed rows:
-// (flat page slot, 1, kv_head * 2 + {0: K, 1: V})
-template <bool kPacked>
+// grid: (touched-page slot, lane, kv_head * 2 + {0: K, 1: V})
 __global__ void __launch_bounds__(kAppendThreads) append_fp8_kernel(AppendArgs a) {
   // a kernel launched as this one's programmatic dependent may be scheduled
   // now; it waits (griddepcontrol.wait) before it reads the cache
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  const int slot = blockIdx.x, b = blockIdx.y;
   const int hk = blockIdx.z >> 1, is_v = blockIdx.z & 1;
-  PageJob job;
-  if (!page_job<kPacked>(a, blockIdx.z == 0, &job)) return;
-  const int pid = job.pid, start = job.start, count = job.count;
-  const size_t token_stride = (size_t)(is_v ? a.v_stride : a.k_stride);
-  const uint16_t* src = (is_v ? a.v_new : a.k_new) + job.row * token_stride + (size_t)hk * kHeadDim;
+  const bool report = slot == 0 && blockIdx.z == 0;
+  const int n = lane_tokens(a, b, report);
+  if (n == 0) return;  // nothing to write: the lane is not examined
+  const int L = a.seq_lens[b];
+  if (!lane_admitted(a, b, L, n, report)) return;
+  const int lp = L / kPage + slot;
+  if ((long long)lp * kPage >= (long long)L + n) return;
+  const int pid = a.page_table[(size_t)b * a.max_pages + lp];
+  const int t0 = max(L, lp * kPage), t1 = min(L + n, lp * kPage + kPage);
+  const int start = t0 - lp * kPage, count = t1 - t0;
+  const size_t token_stride = (size_t)a.num_kv_heads * kHeadDim;
+  const uint16_t* src = (is_v ? a.v_new : a.k_new) + ((size_t)b * a.n_new + (t0 - L)) * token_stride +
+                        (size_t)hk * kHeadDim;
   uint8_t* codes = (is_v ? a.v_codes : a.k_codes) + ((size_t)pid * a.num_kv_heads + hk) * kPage * kHeadDim;
   float* scale = reinterpret_cast<float*>(is_v ? a.v_scales : a.k_scales) + (size_t)pid * a.num_kv_heads + hk;
 
@@ -224,23 +163,29 @@ __global__ void __launch_bounds__(kAppendThreads) append_fp8_kernel(AppendArgs a
   if (threadIdx.x == 0) *scale = s_new;
 }
 
-// grid: (touched-page slot, lane), packed rows: (flat page slot).  One thread
-// per (token, kv head, K|V, group of 32 dims): 64 bytes in, 16 bytes of codes
-// and one fp16 scale out.
-template <bool kPacked>
+// grid: (touched-page slot, lane).  One thread per (token, kv head, K|V,
+// group of 32 dims): 64 bytes in, 16 bytes of codes and one fp16 scale out.
 __global__ void __launch_bounds__(kAppendThreads) append_int4_kernel(AppendArgs a) {
   // a kernel launched as this one's programmatic dependent may be scheduled
   // now; it waits (griddepcontrol.wait) before it reads the cache
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  PageJob job;
-  if (!page_job<kPacked>(a, true, &job)) return;
-  const int pid = job.pid, count = job.count;
+  const int slot = blockIdx.x, b = blockIdx.y;
+  const int n = lane_tokens(a, b, slot == 0);
+  if (n == 0) return;  // nothing to write: the lane is not examined
+  const int L = a.seq_lens[b];
+  if (!lane_admitted(a, b, L, n, slot == 0)) return;
+  const int lp = L / kPage + slot;
+  if ((long long)lp * kPage >= (long long)L + n) return;
+  const int pid = a.page_table[(size_t)b * a.max_pages + lp];
+  const int t0 = max(L, lp * kPage), t1 = min(L + n, lp * kPage + kPage);
+  const int count = t1 - t0;
   const int H = a.num_kv_heads;
+  const size_t token_stride = (size_t)H * kHeadDim;
   for (int it = threadIdx.x; it < count * H * 8; it += blockDim.x) {
     const int g = it & 3, is_v = (it >> 2) & 1, rest = it >> 3;
     const int hk = rest % H, t = rest / H;
-    const int off = job.start + t;
-    const uint16_t* src = (is_v ? a.v_new + (job.row + t) * (size_t)a.v_stride : a.k_new + (job.row + t) * (size_t)a.k_stride) +
+    const int off = t0 + t - lp * kPage;
+    const uint16_t* src = (is_v ? a.v_new : a.k_new) + ((size_t)b * a.n_new + (t0 - L + t)) * token_stride +
                           (size_t)hk * kHeadDim + g * 32;
     float x[32];
     float amax = 0.0f;
@@ -275,28 +220,36 @@ __global__ void __launch_bounds__(kAppendThreads) append_int4_kernel(AppendArgs 
   }
 }
 
-// grid: (touched-page slot, lane), packed rows: (flat page slot).  INT8
-// group-64 and FP8 row formats: every token carries its own scales, so each row is quantised on its own.  Eight
+// grid: (touched-page slot, lane).  INT8 group-64 and FP8 row formats: every
+// token carries its own scales, so each row is quantised on its own.  Eight
 // threads per (token, kv head, K|V) row, 16 dims each (two 16-byte loads, one
 // 16-byte store of codes); the amax of the row (FP8 row) or of each 64-dim
 // group (INT8) is reduced over the row's threads with shuffles.
-template <bool kFp8Row, bool kPacked>
+template <bool kFp8Row>
 __global__ void __launch_bounds__(kAppendThreads) append_rowscaled_kernel(AppendArgs a) {
   // a kernel launched as this one's programmatic dependent may be scheduled
   // now; it waits (griddepcontrol.wait) before it reads the cache
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  PageJob job;
-  if (!page_job<kPacked>(a, true, &job)) return;
-  const int pid = job.pid, count = job.count;
+  const int slot = blockIdx.x, b = blockIdx.y;
+  const int n = lane_tokens(a, b, slot == 0);
+  if (n == 0) return;  // nothing to write: the lane is not examined
+  const int L = a.seq_lens[b];
+  if (!lane_admitted(a, b, L, n, slot == 0)) return;
+  const int lp = L / kPage + slot;
+  if ((long long)lp * kPage >= (long long)L + n) return;
+  const int pid = a.page_table[(size_t)b * a.max_pages + lp];
+  const int t0 = max(L, lp * kPage), t1 = min(L + n, lp * kPage + kPage);
+  const int count = t1 - t0;
   const int H = a.num_kv_heads;
+  const size_t token_stride = (size_t)H * kHeadDim;
   // The item count is a multiple of 8 and a row's 8 items are 8 aligned
   // lanes of one warp, so a row's threads enter and leave the loop together.
   const unsigned row_mask = 0xFFu << (threadIdx.x & 24);
   for (int it = threadIdx.x; it < count * H * 16; it += blockDim.x) {
     const int sub = it & 7, is_v = (it >> 3) & 1, rest = it >> 4;
     const int hk = rest % H, t = rest / H;
-    const int off = job.start + t;
-    const uint16_t* src = (is_v ? a.v_new + (job.row + t) * (size_t)a.v_stride : a.k_new + (job.row + t) * (size_t)a.k_stride) +
+    const int off = t0 + t - lp * kPage;
+    const uint16_t* src = (is_v ? a.v_new : a.k_new) + ((size_t)b * a.n_new + (t0 - L + t)) * token_stride +
                           (size_t)hk * kHeadDim + sub * 16;
     float x[16];
 #pragma unroll
@@ -350,24 +303,23 @@ __global__ void __launch_bounds__(kAppendThreads) append_rowscaled_kernel(Append
 
 using namespace sdva;
 
-namespace {
-
-int check_cache(const sdva_kv_cache* cache, int num_lanes, int max_pages_per_lane) {
+int sdva::append_launch(const sdva_kv_cache* cache, const void* k_new, const void* v_new, int num_lanes, int n_new,
+                       const int32_t* n_lane, const int32_t* page_table, int max_pages_per_lane,
+                       const int32_t* seq_lens, int32_t* status, sdva_stream_t stream, bool check_only) {
+  if (cache == nullptr || k_new == nullptr || v_new == nullptr || page_table == nullptr || seq_lens == nullptr)
+    return SDVA_ERR_INVALID;
   if (cache->k_codes == nullptr || cache->v_codes == nullptr || cache->k_scales == nullptr ||
       cache->v_scales == nullptr)
     return SDVA_ERR_INVALID;
-  if (num_lanes <= 0 || max_pages_per_lane <= 0 || cache->num_pages <= 0 || cache->num_kv_heads <= 0)
+  if (num_lanes <= 0 || n_new <= 0 || max_pages_per_lane <= 0 || cache->num_pages <= 0 ||
+      cache->num_kv_heads <= 0)
     return SDVA_ERR_INVALID;
   if (cache->page_size != kPage || cache->head_dim != kHeadDim) return SDVA_ERR_UNSUPPORTED;
   if (cache->dtype < SDVA_KV_FP8_E4M3 || cache->dtype > SDVA_KV_FP8_ROW) return SDVA_ERR_UNSUPPORTED;
   if (!cache_aligned(cache)) return SDVA_ERR_INVALID;
   if (num_lanes > 65535 || cache->num_kv_heads > 32767) return SDVA_ERR_UNSUPPORTED;
-  return SDVA_OK;
-}
-
-AppendArgs append_args(const sdva_kv_cache* cache, const void* k_new, const void* v_new, const int32_t* page_table,
-                       int max_pages_per_lane, const int32_t* seq_lens, int num_lanes, int32_t* status) {
-  AppendArgs a = {};
+  if (check_only) return SDVA_OK;
+  AppendArgs a;
   a.k_new = static_cast<const uint16_t*>(k_new);
   a.v_new = static_cast<const uint16_t*>(v_new);
   a.k_codes = static_cast<uint8_t*>(cache->k_codes);
@@ -377,66 +329,23 @@ AppendArgs append_args(const sdva_kv_cache* cache, const void* k_new, const void
   a.page_table = page_table;
   a.seq_lens = seq_lens;
   a.status = status;
+  a.n_lane = n_lane;
   a.num_pages = cache->num_pages;
   a.num_kv_heads = cache->num_kv_heads;
+  a.n_new = n_new;
   a.max_pages = max_pages_per_lane;
-  a.num_lanes = num_lanes;
-  return a;
-}
-
-// slots: page slots along x; lanes: along y (1 for packed rows)
-template <bool kPacked>
-int enqueue_append(const AppendArgs& a, int dtype, int slots, int lanes, cudaStream_t s) {
-  if (dtype == SDVA_KV_FP8_E4M3) {
-    append_fp8_kernel<kPacked><<<dim3(slots, lanes, a.num_kv_heads * 2), kAppendThreads, 0, s>>>(a);
-  } else if (dtype == SDVA_KV_INT4_G32) {
-    append_int4_kernel<kPacked><<<dim3(slots, lanes), kAppendThreads, 0, s>>>(a);
-  } else if (dtype == SDVA_KV_INT8_G64) {
-    append_rowscaled_kernel<false, kPacked><<<dim3(slots, lanes), kAppendThreads, 0, s>>>(a);
+  const int slots = (n_new + kPage - 1) / kPage + 1;  // pages a range of n_new tokens can touch
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (cache->dtype == SDVA_KV_FP8_E4M3) {
+    append_fp8_kernel<<<dim3(slots, num_lanes, cache->num_kv_heads * 2), kAppendThreads, 0, s>>>(a);
+  } else if (cache->dtype == SDVA_KV_INT4_G32) {
+    append_int4_kernel<<<dim3(slots, num_lanes), kAppendThreads, 0, s>>>(a);
+  } else if (cache->dtype == SDVA_KV_INT8_G64) {
+    append_rowscaled_kernel<false><<<dim3(slots, num_lanes), kAppendThreads, 0, s>>>(a);
   } else {
-    append_rowscaled_kernel<true, kPacked><<<dim3(slots, lanes), kAppendThreads, 0, s>>>(a);
+    append_rowscaled_kernel<true><<<dim3(slots, num_lanes), kAppendThreads, 0, s>>>(a);
   }
   return cudaGetLastError() == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
-}
-
-}  // namespace
-
-int sdva::append_launch(const sdva_kv_cache* cache, const void* k_new, const void* v_new, int num_lanes, int n_new,
-                       const int32_t* n_lane, const int32_t* page_table, int max_pages_per_lane,
-                       const int32_t* seq_lens, int32_t* status, sdva_stream_t stream, bool check_only) {
-  if (cache == nullptr || k_new == nullptr || v_new == nullptr || page_table == nullptr || seq_lens == nullptr)
-    return SDVA_ERR_INVALID;
-  if (n_new <= 0) return SDVA_ERR_INVALID;
-  if (const int rc = check_cache(cache, num_lanes, max_pages_per_lane)) return rc;
-  if (check_only) return SDVA_OK;
-  AppendArgs a = append_args(cache, k_new, v_new, page_table, max_pages_per_lane, seq_lens, num_lanes, status);
-  a.n_lane = n_lane;
-  a.n_new = n_new;
-  a.k_stride = a.v_stride = (long long)cache->num_kv_heads * kHeadDim;
-  const int slots = (n_new + kPage - 1) / kPage + 1;  // pages a range of n_new tokens can touch
-  return enqueue_append<false>(a, cache->dtype, slots, num_lanes, reinterpret_cast<cudaStream_t>(stream));
-}
-
-extern "C" int kv_append_packed(const sdva_kv_cache* cache, const void* k_new, const void* v_new, int64_t k_stride,
-                                int64_t v_stride, int total_tokens, const int32_t* cu_tokens, int num_lanes,
-                                const int32_t* page_table, int max_pages_per_lane, const int32_t* seq_lens,
-                                int32_t* status, sdva_stream_t stream) {
-  if (total_tokens == 0) return SDVA_OK;
-  if (cache == nullptr || k_new == nullptr || v_new == nullptr || cu_tokens == nullptr || page_table == nullptr ||
-      seq_lens == nullptr || total_tokens < 0)
-    return SDVA_ERR_INVALID;
-  if (const int rc = check_cache(cache, num_lanes, max_pages_per_lane)) return rc;
-  const int64_t width = (int64_t)cache->num_kv_heads * kHeadDim;
-  if (k_stride < width || v_stride < width || ((k_stride | v_stride) & 7) ||
-      ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15u))
-    return SDVA_ERR_INVALID;
-  AppendArgs a = append_args(cache, k_new, v_new, page_table, max_pages_per_lane, seq_lens, num_lanes, status);
-  a.cu = cu_tokens;
-  a.total = total_tokens;
-  a.k_stride = k_stride;
-  a.v_stride = v_stride;
-  return enqueue_append<true>(a, cache->dtype, total_tokens / kPage + 2 * num_lanes, 1,
-                              reinterpret_cast<cudaStream_t>(stream));
 }
 
 extern "C" int kv_append_quant(const sdva_kv_cache* cache, const void* k_new, const void* v_new, int num_lanes,

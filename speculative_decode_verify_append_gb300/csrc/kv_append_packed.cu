@@ -1,0 +1,287 @@
+// kv_append_packed.cu -- kv_append_quant for lanes packed one behind the
+// other: a prompt batch's K/V into the paged, quantised cache.
+//
+// What is written is what kv_append_quant writes (sdva.h).  The call is bound
+// by memory: 512 bytes in and 128 to 264 out per token and kv head.  One CTA
+// per (touched page, kv head) takes K and V together: eight threads per token
+// row, each with dims [8 t, 8 t + 8) of both 64-dim halves, so that a row's
+// loads and stores are whole 128- and 64-byte runs; all of a thread's loads
+// are issued before the lane's page ids are checked.  The grid is flat over
+// page slots, found from the offsets alone (slot_base).
+//
+// Division.  A code comes from fp32 x / s, rounded to nearest.  With r = 1 / s
+// rounded, q = x r, the remainder e = x - q s by one fused multiply-add is
+// exact and q + e r, rounded once, is the rounded quotient (Markstein, IBM
+// Journal of Research and Development 34, 1990).  That holds for every bf16
+// significand over every fp32 one (all 2^30 pairs compared with the division)
+// while nothing under- or overflows; outside s in [2^-80, 2^80] the division
+// itself is used.  Quotients that matter (2^-10 and more for E4M3, 1/2 for
+// the integers) have exact remainders there.  Five instructions against ten.
+#include "sdva_common.cuh"
+#include "sdva_internal.cuh"
+
+namespace sdva {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kRowThreads = 8;  // threads per token row
+constexpr int kItems = kPage * 2 * kRowThreads / kThreads;  // (token, K|V) rows per thread
+
+struct PackedArgs {
+  const uint16_t* k_new;
+  const uint16_t* v_new;
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  void* k_scales;
+  void* v_scales;
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const int32_t* cu;
+  int32_t* status;
+  long long k_stride, v_stride;
+  int num_pages, num_kv_heads, max_pages, num_lanes, total;
+};
+
+// First page slot of a lane whose rows start at row `at`.  A lane of n tokens
+// touches at most n / 64 + 2 pages wherever it starts in a page, and the next
+// lane's base is at least n / 64 + 2 further, so no prefix sum is needed.
+__device__ __forceinline__ int slot_base(int at, int lane) { return at / kPage + 2 * lane; }
+
+// x / s, rounded to nearest, by one divisor.
+struct Divisor {
+  float s, r;
+  bool plain;  // out of the range where the short form holds
+  __device__ explicit Divisor(float s_) : s(s_) {
+    plain = !(s >= 0x1p-80f && s <= 0x1p80f);
+    r = plain ? 0.0f : __frcp_rn(s);
+  }
+  __device__ float operator()(float x) const {
+    if (plain) return __fdiv_rn(x, s);
+    const float q = __fmul_rn(x, r);
+    return copysignf(__fmaf_rn(__fmaf_rn(-q, s, x), r, q), x);  // the sign of a zero
+  }
+};
+
+__device__ __forceinline__ float amax8(uint4 w) {
+  // the largest magnitude of eight bf16: their bits without the sign order as integers
+  const uint32_t a = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+  return __uint_as_float(max(a & 0xFFFF0000u, a << 16));
+}
+template <int kLanes>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int o = kLanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+__device__ __forceinline__ uint2 e4m3x8(uint4 w, const Divisor& d) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  uint32_t p[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) p[j] = e4m3x2_from_f32(d(bf16_lo(u[j])), d(bf16_hi(u[j])));
+  return make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
+}
+template <int kMax>
+__device__ __forceinline__ int code_of(float y) {
+  return max(-kMax, min(kMax, __float2int_rn(y)));
+}
+
+template <int KVT>
+__global__ void __launch_bounds__(kThreads, 4) append_packed_kernel(PackedArgs a) {
+  const int slot = blockIdx.x, hk = blockIdx.y, th = threadIdx.x;
+  // the slot's lane: the last whose base is at or before it
+  int below = 0, bad = 0;
+  for (int b0 = 0; b0 < a.num_lanes; b0 += kThreads) {
+    const int b = b0 + th;
+    bool at = false;
+    if (b < a.num_lanes) {
+      const int lo = a.cu[b], hi = a.cu[b + 1];
+      bad |= lo < 0 || hi < lo || hi > a.total;
+      at = slot_base(lo, b) <= slot;
+    }
+    below += __syncthreads_count(at);
+  }
+  if (__syncthreads_or(bad)) {
+    if (slot == 0 && hk == 0 && th == 0) raise_status(a.status, SDVA_STATUS_BAD_COUNT);
+    return;
+  }
+  if (below == 0) return;
+  const int b = below - 1, row0 = a.cu[b], n = a.cu[b + 1] - row0, page = slot - slot_base(row0, b);
+  if (n == 0) return;  // nothing to write: the lane is not examined
+  const int L = a.seq_lens[b];
+  const long long end = (long long)L + n;
+  const bool report = page == 0 && hk == 0 && th == 0;
+  if (L < 0 || end > (long long)a.max_pages * kPage) {
+    if (report) raise_status(a.status, SDVA_STATUS_OVERFLOW);
+    return;
+  }
+  const int lp = L / kPage + page;
+  if ((long long)lp * kPage >= end) return;
+  const int t0 = max(L, lp * kPage), start = t0 - lp * kPage;
+  const int count = (int)(min(end, (long long)lp * kPage + kPage) - t0);
+
+  // rows (token, K|V) it / 8 of items it = th, th + 256, ...; dims 8 sub .. and 64 + 8 sub ..
+  const int sub = th & (kRowThreads - 1), is_v = (th >> 3) & 1;
+  const uint16_t* const src = (is_v ? a.v_new : a.k_new) + (size_t)hk * kHeadDim + sub * 8;
+  const size_t stride = (size_t)(is_v ? a.v_stride : a.k_stride);
+  uint4 x[kItems][2];
+#pragma unroll
+  for (int i = 0; i < kItems; ++i) {
+    const int t = (th >> 4) + i * (kThreads / 16);
+    x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);
+    if (t < count) {
+      const uint16_t* r = src + ((size_t)row0 + (t0 - L) + t) * stride;
+      x[i][0] = __ldcs(reinterpret_cast<const uint4*>(r));
+      x[i][1] = __ldcs(reinterpret_cast<const uint4*>(r + 64));
+    }
+  }
+  // every page of the lane's range has to be valid before one is written
+  const int32_t* const row = a.page_table + (size_t)b * a.max_pages;
+  const int last = (int)((end - 1) / kPage), pid = row[lp];
+  for (int p = L / kPage + th; p <= last; p += kThreads) {
+    const int id = row[p];
+    bad |= id < 0 || id >= a.num_pages;
+  }
+  if (__syncthreads_or(bad)) {
+    if (report) raise_status(a.status, SDVA_STATUS_BAD_PAGE);
+    return;
+  }
+  const size_t ph = (size_t)pid * a.num_kv_heads + hk;
+  uint8_t* const codes = is_v ? a.v_codes : a.k_codes;
+  void* const scales = is_v ? a.v_scales : a.k_scales;
+
+  if constexpr (KVT == SDVA_KV_FP8_E4M3) {
+    // one scale for the page's K and one for its V
+    __shared__ float s_amax[2][kThreads / 32];
+    float m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) m = fmaxf(m, fmaxf(amax8(x[i][0]), amax8(x[i][1])));
+    // over the lanes of a warp with the same K|V (lane bit 3)
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (o != 8) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((th & 0x17) == 0) s_amax[is_v][th >> 5] = m;
+    float* const scale = static_cast<float*>(scales) + ph;
+    const float s_old = *scale;  // read by every thread before the barrier below
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, s_amax[is_v][w]);
+    const float s_cand = __fdiv_rn(m, 448.0f);
+    const float s_new = start == 0 ? s_cand : (s_cand > s_old ? s_cand : s_old);
+    uint8_t* const page_codes = codes + ph * kPage * kHeadDim;
+    if (start > 0 && s_new > s_old) {
+      // earlier tokens of the page move to the larger scale: 4 codes per item, by the threads of their half
+      uint32_t* const old = reinterpret_cast<uint32_t*>(page_codes);
+      for (int it = (th >> 4) * 8 + sub; it < start * (kHeadDim / 4); it += kThreads / 2) {
+        const uint32_t c = old[it];
+        float v[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = __fdiv_rn(__fmul_rn(e4m3_to_f32((c >> (8 * j)) & 0xFFu), s_old), s_new);
+        old[it] = (uint32_t)e4m3x2_from_f32(v[0], v[1]) | ((uint32_t)e4m3x2_from_f32(v[2], v[3]) << 16);
+      }
+    }
+    const Divisor d(s_new);
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int t = (th >> 4) + i * (kThreads / 16);
+      if (t < count) {
+        uint8_t* const out = page_codes + (size_t)(start + t) * kHeadDim + sub * 8;
+        const bool zero = s_new == 0.0f;
+        *reinterpret_cast<uint2*>(out) = zero ? make_uint2(0u, 0u) : e4m3x8(x[i][0], d);
+        *reinterpret_cast<uint2*>(out + 64) = zero ? make_uint2(0u, 0u) : e4m3x8(x[i][1], d);
+      }
+    }
+    if ((th & ~8) == 0) *scale = s_new;
+  } else {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int t = (th >> 4) + i * (kThreads / 16);
+      const size_t at = ph * kPage + start + t;  // (page, kv head, token) row
+      float m[2] = {amax8(x[i][0]), amax8(x[i][1])};
+      if constexpr (KVT == SDVA_KV_FP8_ROW) {
+        const float s = __fdiv_rn(lanes_max<8>(fmaxf(m[0], m[1])), 448.0f);
+        if (t < count) {
+          const Divisor d(s);
+          uint8_t* const out = codes + at * kHeadDim + sub * 8;
+          *reinterpret_cast<uint2*>(out) = s == 0.0f ? make_uint2(0u, 0u) : e4m3x8(x[i][0], d);
+          *reinterpret_cast<uint2*>(out + 64) = s == 0.0f ? make_uint2(0u, 0u) : e4m3x8(x[i][1], d);
+          if (sub == 0) static_cast<float*>(scales)[at] = s;
+        }
+      } else {
+        // a 64-dim half is one group of INT8 and, by four threads each, two of INT4
+        constexpr bool kInt4 = KVT == SDVA_KV_INT4_G32;
+        constexpr int kTop = kInt4 ? 7 : 127;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const __half s16 = __float2half_rn(fminf(__fdiv_rn(lanes_max<kInt4 ? 4 : 8>(m[h]), (float)kTop), 65504.0f));
+          if (t < count) {
+            const float s = __half2float(s16);
+            const Divisor d(s);
+            const uint32_t u[4] = {x[i][h].x, x[i][h].y, x[i][h].z, x[i][h].w};
+            uint32_t p[2] = {0u, 0u};
+            if (s != 0.0f) {
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+                const int c = code_of<kTop>(d((j & 1) ? bf16_hi(u[j >> 1]) : bf16_lo(u[j >> 1])));
+                if (kInt4) p[0] |= (uint32_t)(c & 0xF) << (4 * j);
+                else p[j >> 2] |= (uint32_t)(c & 0xFF) << (8 * (j & 3));
+              }
+            }
+            __half* const sc = static_cast<__half*>(scales);
+            if constexpr (kInt4) {
+              *reinterpret_cast<uint32_t*>(codes + at * (kHeadDim / 2) + 32 * h + 4 * sub) = p[0];
+              if ((sub & 3) == 0) sc[at * 4 + 2 * h + (sub >> 2)] = s16;
+            } else {
+              *reinterpret_cast<uint2*>(codes + at * kHeadDim + 64 * h + 8 * sub) = make_uint2(p[0], p[1]);
+              if (sub == 0) sc[at * 2 + h] = s16;
+            }
+          }
+        }
+      }
+    }
+  }
+}
+
+}  // namespace
+}  // namespace sdva
+
+using namespace sdva;
+
+extern "C" int kv_append_packed(const sdva_kv_cache* cache, const void* k_new, const void* v_new, int64_t k_stride,
+                                int64_t v_stride, int total_tokens, const int32_t* cu_tokens, int num_lanes,
+                                const int32_t* page_table, int max_pages_per_lane, const int32_t* seq_lens,
+                                int32_t* status, sdva_stream_t stream) {
+  if (total_tokens == 0) return SDVA_OK;
+  if (cu_tokens == nullptr || total_tokens < 0) return SDVA_ERR_INVALID;
+  if (const int rc = append_launch(cache, k_new, v_new, num_lanes, 1, nullptr, page_table, max_pages_per_lane,
+                                   seq_lens, status, stream, true))
+    return rc;
+  const int64_t width = (int64_t)cache->num_kv_heads * kHeadDim;
+  if (k_stride < width || v_stride < width || ((k_stride | v_stride) & 7) ||
+      ((reinterpret_cast<uintptr_t>(k_new) | reinterpret_cast<uintptr_t>(v_new)) & 15u))
+    return SDVA_ERR_INVALID;
+  PackedArgs a;
+  a.k_new = static_cast<const uint16_t*>(k_new);
+  a.v_new = static_cast<const uint16_t*>(v_new);
+  a.k_codes = static_cast<uint8_t*>(cache->k_codes);
+  a.v_codes = static_cast<uint8_t*>(cache->v_codes);
+  a.k_scales = cache->k_scales;
+  a.v_scales = cache->v_scales;
+  a.page_table = page_table;
+  a.seq_lens = seq_lens;
+  a.cu = cu_tokens;
+  a.status = status;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.num_pages = cache->num_pages;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.max_pages = max_pages_per_lane;
+  a.num_lanes = num_lanes;
+  a.total = total_tokens;
+  const dim3 grid(total_tokens / kPage + 2 * num_lanes, cache->num_kv_heads);
+  const auto kernel = cache->dtype == SDVA_KV_FP8_E4M3   ? append_packed_kernel<SDVA_KV_FP8_E4M3>
+                      : cache->dtype == SDVA_KV_INT4_G32 ? append_packed_kernel<SDVA_KV_INT4_G32>
+                      : cache->dtype == SDVA_KV_INT8_G64 ? append_packed_kernel<SDVA_KV_INT8_G64>
+                                                         : append_packed_kernel<SDVA_KV_FP8_ROW>;
+  kernel<<<grid, kThreads, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  return cudaGetLastError() == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
+}
