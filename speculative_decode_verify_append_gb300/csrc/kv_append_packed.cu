@@ -16,9 +16,11 @@
 // significand over every fp32 one (all 2^30 pairs compared with the division)
 // while nothing under- or overflows; outside s in [2^-80, 2^80] the division
 // itself is used.  Quotients that matter (2^-10 and more for E4M3, 1/2 for
-// the integers) have exact remainders there.  Five instructions against ten.
-#include "sdva_common.cuh"
+// the integers) have exact remainders there.  With -r for r the same three
+// steps give the negative quotient, and a zero keeps its sign; two at a time
+// they are one and a half instructions an element.
 #include "sdva_internal.cuh"
+#include "tc_primitives.cuh"
 
 namespace sdva {
 namespace {
@@ -47,18 +49,25 @@ struct PackedArgs {
 // lane's base is at least n / 64 + 2 further, so no prefix sum is needed.
 __device__ __forceinline__ int slot_base(int at, int lane) { return at / kPage + 2 * lane; }
 
-// x / s, rounded to nearest, by one divisor.
+using tc::f2_pack;
+using tc::f2_unpack;
+using tc::ffma2;
+using tc::fmul2;
+
+// Quotients by one divisor, rounded to nearest.
 struct Divisor {
-  float s, r;
+  float s, nr;
   bool plain;  // out of the range where the short form holds
   __device__ explicit Divisor(float s_) : s(s_) {
     plain = !(s >= 0x1p-80f && s <= 0x1p80f);
-    r = plain ? 0.0f : __frcp_rn(s);
+    nr = plain ? 0.0f : -__frcp_rn(s);
   }
-  __device__ float operator()(float x) const {
-    if (plain) return __fdiv_rn(x, s);
-    const float q = __fmul_rn(x, r);
-    return copysignf(__fmaf_rn(__fmaf_rn(-q, s, x), r, q), x);  // the sign of a zero
+  // -(x / s) of the two bf16 of a word
+  __device__ float2 minus(uint32_t w) const {
+    if (plain) return make_float2(-__fdiv_rn(bf16_lo(w), s), -__fdiv_rn(bf16_hi(w), s));
+    const unsigned long long x = f2_pack(bf16_lo(w), bf16_hi(w)), n = f2_pack(nr, nr);
+    const unsigned long long q = fmul2(x, n);
+    return f2_unpack(ffma2(ffma2(q, f2_pack(s, s), x), n, q));
   }
 };
 
@@ -77,12 +86,30 @@ __device__ __forceinline__ uint2 e4m3x8(uint4 w, const Divisor& d) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   uint32_t p[4];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) p[j] = e4m3x2_from_f32(d(bf16_lo(u[j])), d(bf16_hi(u[j])));
-  return make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
+  for (int j = 0; j < 4; ++j) {
+    const float2 y = d.minus(u[j]);
+    p[j] = e4m3x2_from_f32(y.x, y.y);
+  }
+  // the sign bits back
+  return make_uint2((p[0] | (p[1] << 16)) ^ 0x80808080u, (p[2] | (p[3] << 16)) ^ 0x80808080u);
 }
-template <int kMax>
-__device__ __forceinline__ int code_of(float y) {
-  return max(-kMax, min(kMax, __float2int_rn(y)));
+// Eight integer codes of x / s, halves to even, in [-top, top], as two's
+// complement in the low bits of each int.  `near`: no quotient rounds beyond
+// top, so that adding 1.5 * 2^23 rounds and nothing is left to clamp.
+template <int kTop>
+__device__ __forceinline__ void int_codes(uint4 w, const Divisor& d, bool near, uint32_t (&c)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float2 y = d.minus(u[j]);
+    if (near) {
+      c[2 * j] = __float_as_uint(12582912.0f - y.x);
+      c[2 * j + 1] = __float_as_uint(12582912.0f - y.y);
+    } else {
+      c[2 * j] = (uint32_t)max(-kTop, min(kTop, __float2int_rn(-y.x)));
+      c[2 * j + 1] = (uint32_t)max(-kTop, min(kTop, __float2int_rn(-y.y)));
+    }
+  }
 }
 
 template <int KVT>
@@ -212,18 +239,20 @@ __global__ void __launch_bounds__(kThreads, 4) append_packed_kernel(PackedArgs a
         constexpr int kTop = kInt4 ? 7 : 127;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const __half s16 = __float2half_rn(fminf(__fdiv_rn(lanes_max<kInt4 ? 4 : 8>(m[h]), (float)kTop), 65504.0f));
+          const float wide = __fdiv_rn(lanes_max<kInt4 ? 4 : 8>(m[h]), (float)kTop);
+          const __half s16 = __float2half_rn(fminf(wide, 65504.0f));
           if (t < count) {
             const float s = __half2float(s16);
-            const Divisor d(s);
-            const uint32_t u[4] = {x[i][h].x, x[i][h].y, x[i][h].z, x[i][h].w};
-            uint32_t p[2] = {0u, 0u};
+            uint32_t c[8], p[2] = {0u, 0u};
             if (s != 0.0f) {
+              // a normal scale is within 2^-11 of wide: quotients up to top (1 + 2^-11), which rounds to top
+              int_codes<kTop>(x[i][h], Divisor(s), s >= 0x1p-14f && wide <= 65504.0f, c);
 #pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                const int c = code_of<kTop>(d((j & 1) ? bf16_hi(u[j >> 1]) : bf16_lo(u[j >> 1])));
-                if (kInt4) p[0] |= (uint32_t)(c & 0xF) << (4 * j);
-                else p[j >> 2] |= (uint32_t)(c & 0xFF) << (8 * (j & 3));
+              for (int j = 0; j < 8; ++j)
+                if (kInt4) p[0] |= (c[j] & 0xFu) << (4 * j);
+              if (!kInt4) {
+                p[0] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+                p[1] = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
               }
             }
             __half* const sc = static_cast<__half*>(scales);
