@@ -34,6 +34,7 @@ The calls mirror ``include/sdva.h``:
 from __future__ import annotations
 
 import ctypes
+import math
 import os
 
 import torch
@@ -175,8 +176,8 @@ def _dptr(t: torch.Tensor | None, dtype: torch.dtype | None = None, name: str = 
 
 
 def _stream(stream) -> int | None:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:  # the handle itself: a torch.cuda.Stream object costs a few microseconds
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -422,30 +423,35 @@ def spec_accept_sampled(logits: torch.Tensor, draft_probs: torch.Tensor | None, 
     _check("spec_accept_sampled", rc)
 
 
-def _rows(t: torch.Tensor, name: str) -> int:
+def _refuse(t, dtype, shape, device: int, name: str) -> None:
+    if t.get_device() != device:
+        raise ValueError(f"{name} is on {t.device}; the tensors of a call are all on the current device, cuda:{device}")
+    if t.dtype is not dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _arg(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, device: int, name: str):
+    """The address of a contiguous tensor of this type and shape on the current device (None: not given)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != device or not t.is_contiguous():
+        _refuse(t, dtype, shape, device, name)
+    return t.data_ptr()
+
+
+def _rows(t: torch.Tensor, shape: tuple, device: int, name: str) -> int:
     """Elements between the token rows of a bf16 [T][H][128] tensor whose rows
     are contiguous inside (a tensor of its own, or a slice of a fused projection)."""
-    if t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3 or t.shape[2] != HEAD_DIM:
-        raise ValueError(f"{name} must be a bf16 CUDA tensor [T][H][{HEAD_DIM}]")
     st = t.stride()
-    if st[2] != 1 or (st[1] != HEAD_DIM and t.shape[1] > 1):
-        raise ValueError(f"{name} must be contiguous inside a token row")
-    return st[0] if t.shape[0] > 1 else max(st[0], t.shape[1] * HEAD_DIM)
-
-
-def _expect(t: torch.Tensor, shape: tuple, name: str) -> None:
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-
-
-def _same_device(first: torch.Tensor, **others) -> None:
-    """Every tensor on the first one's device, which must be the current one
-    (the library enqueues on the current device)."""
-    if first.device.index != torch.cuda.current_device():
-        raise ValueError(f"the tensors are on {first.device}, the current device is {torch.cuda.current_device()}")
-    for name, t in others.items():
-        if t is not None and t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, not on {first.device}")
+    if (t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != device or st[2] != 1 or
+            (st[1] != HEAD_DIM and shape[1] > 1)):
+        if t.shape == shape and t.dtype is torch.bfloat16 and t.get_device() == device:
+            raise ValueError(f"{name} must be contiguous inside a token row")
+        _refuse(t, torch.bfloat16, shape, device, name)
+    return st[0] if shape[0] > 1 else max(st[0], shape[1] * HEAD_DIM)
 
 
 def kv_append_packed(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, cu_tokens: torch.Tensor,
@@ -454,20 +460,19 @@ def kv_append_packed(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, c
     """k_new, v_new: bf16 [T][Hkv][128], token rows of any stride; cu_tokens int32
     [B + 1]: lane b appends rows cu_tokens[b] .. cu_tokens[b + 1] - 1; page_table
     int32 [B][max_pages]; seq_lens int32 [B]."""
+    dev = torch.cuda.current_device()
     T, B = k_new.shape[0], seq_lens.shape[0]
-    ks, vs = _rows(k_new, "k_new"), _rows(v_new, "v_new")
-    _expect(k_new, (T, cache.num_kv_heads, HEAD_DIM), "k_new")
-    _expect(v_new, (T, cache.num_kv_heads, HEAD_DIM), "v_new")
-    _expect(cu_tokens, (B + 1,), "cu_tokens")
-    _expect(page_table, (B, page_table.shape[-1]), "page_table")
-    _same_device(k_new, v_new=v_new, cu_tokens=cu_tokens, page_table=page_table, seq_lens=seq_lens,
-                 cache=cache.k_codes, status=status)
+    shape = (T, cache.num_kv_heads, HEAD_DIM)
+    ks, vs = _rows(k_new, shape, dev, "k_new"), _rows(v_new, shape, dev, "v_new")
+    pages = page_table.shape[-1]
+    if cache.k_codes.get_device() != dev:
+        raise ValueError(f"the cache is on {cache.k_codes.device}, the current device is cuda:{dev}")
     s = cache.struct()
     rc = _lib.kv_append_packed(ctypes.byref(s), k_new.data_ptr(), v_new.data_ptr(), ks, vs, T,
-                               _dptr(cu_tokens, torch.int32, "cu_tokens"), B,
-                               _dptr(page_table, torch.int32, "page_table"), page_table.shape[1],
-                               _dptr(seq_lens, torch.int32, "seq_lens"), _dptr(status, torch.int32, "status"),
-                               _stream(stream))
+                               _arg(cu_tokens, torch.int32, (B + 1,), dev, "cu_tokens"), B,
+                               _arg(page_table, torch.int32, (B, pages), dev, "page_table"), pages,
+                               _arg(seq_lens, torch.int32, (B,), dev, "seq_lens"),
+                               _dptr(status, torch.int32, "status"), _stream(stream))
     _check("kv_append_packed", rc)
 
 
@@ -476,19 +481,16 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_tokens: to
                 stream=None) -> None:
     """q bf16 [T][Hq][128], k, v bf16 [T][Hkv][128], token rows of any stride;
     cu_tokens int32 [B + 1]; out bf16 [T][Hq][128]; lse fp32 [T][Hq]."""
-    qs, ks, vs = _rows(q, "q"), _rows(k, "k"), _rows(v, "v")
-    T, Hq, Hkv = q.shape[0], q.shape[1], k.shape[1]
-    _expect(k, (T, Hkv, HEAD_DIM), "k")
-    _expect(v, (T, Hkv, HEAD_DIM), "v")
-    _expect(out, (T, Hq, HEAD_DIM), "out")
-    if lse is not None:
-        _expect(lse, (T, Hq), "lse")
-    if cu_tokens.dim() != 1:
-        raise ValueError("cu_tokens must be [B + 1]")
-    _same_device(q, k=k, v=v, cu_tokens=cu_tokens, out=out, lse=lse, status=status)
+    dev = torch.cuda.current_device()
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"q, k and v must be [T][H][{HEAD_DIM}]")
+    T, Hq, Hkv, B = q.shape[0], q.shape[1], k.shape[1], cu_tokens.shape[0] - 1
+    kv = (T, Hkv, HEAD_DIM)
+    qs, ks, vs = _rows(q, (T, Hq, HEAD_DIM), dev, "q"), _rows(k, kv, dev, "k"), _rows(v, kv, dev, "v")
     rc = _lib.prompt_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, Hq, Hkv, T,
-                          _dptr(cu_tokens, torch.int32, "cu_tokens"), cu_tokens.shape[0] - 1, float(sm_scale),
-                          _dptr(out, torch.bfloat16, "out"), _dptr(lse, torch.float32, "lse"),
+                          _arg(cu_tokens, torch.int32, (B + 1,), dev, "cu_tokens"), B, sm_scale,
+                          _arg(out, torch.bfloat16, (T, Hq, HEAD_DIM), dev, "out"),
+                          _arg(lse, torch.float32, (T, Hq), dev, "lse"),
                           _dptr(status, torch.int32, "status"), _stream(stream))
     _check("prompt_attn", rc)
 
@@ -503,33 +505,30 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: torch.T
     [B][W][V]; tokens int32 [N] or [B][W] (-1: row not scored); logprobs,
     entropy fp32 like tokens; top_tokens int32, top_logprobs fp32 with a last
     axis of the number of tokens to list (both or neither)."""
-    if logits.dtype not in _LOGITS or not logits.is_cuda:
-        raise ValueError("logits must be a float32, bfloat16 or float16 CUDA tensor")
-    lead, V = tuple(logits.shape[:-1]), logits.shape[-1]
+    dev = torch.cuda.current_device()
+    kind = _LOGITS.get(logits.dtype)
+    if kind is None or logits.get_device() != dev:
+        raise ValueError(f"logits must be float32, bfloat16 or float16 on the current device, cuda:{dev}")
+    shape = tuple(logits.shape)
+    lead, V = shape[:-1], shape[-1]
     if len(lead) == 1:
-        if logits.stride(1) != 1 and V > 1:
+        st = logits.stride()
+        if st[1] != 1 and V > 1:
             raise ValueError("logits must be contiguous inside a row")
-        stride = logits.stride(0) if lead[0] > 1 else max(logits.stride(0), V)
-    else:
-        if not logits.is_contiguous():
-            raise ValueError("logits must be [N][V] or contiguous")
+        stride = st[0] if lead[0] > 1 else max(st[0], V)
+    elif logits.is_contiguous():
         stride = V
-    _expect(tokens, lead, "tokens")
-    _expect(logprobs, lead, "logprobs")
-    if entropy is not None:
-        _expect(entropy, lead, "entropy")
+    else:
+        raise ValueError("logits must be [N][V] or contiguous")
     if (top_tokens is None) != (top_logprobs is None):
         raise ValueError("top_tokens and top_logprobs go together")
     top = 0 if top_tokens is None else top_tokens.shape[-1]
-    if top_tokens is not None:
-        _expect(top_tokens, lead + (top,), "top_tokens")
-        _expect(top_logprobs, lead + (top,), "top_logprobs")
-    _same_device(logits, tokens=tokens, logprobs=logprobs, entropy=entropy, top_tokens=top_tokens,
-                 top_logprobs=top_logprobs, status=status)
-    rc = _lib.token_logprobs(logits.data_ptr(), _LOGITS[logits.dtype], stride, tokens.numel(), V,
-                             _dptr(tokens, torch.int32, "tokens"), top, _dptr(logprobs, torch.float32, "logprobs"),
-                             _dptr(entropy, torch.float32, "entropy"), _dptr(top_tokens, torch.int32, "top_tokens"),
-                             _dptr(top_logprobs, torch.float32, "top_logprobs"),
+    rc = _lib.token_logprobs(logits.data_ptr(), kind, stride, math.prod(lead), V,
+                             _arg(tokens, torch.int32, lead, dev, "tokens"), top,
+                             _arg(logprobs, torch.float32, lead, dev, "logprobs"),
+                             _arg(entropy, torch.float32, lead, dev, "entropy"),
+                             _arg(top_tokens, torch.int32, lead + (top,), dev, "top_tokens"),
+                             _arg(top_logprobs, torch.float32, lead + (top,), dev, "top_logprobs"),
                              _dptr(status, torch.int32, "status"), _stream(stream))
     _check("token_logprobs", rc)
 

@@ -218,29 +218,6 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, i
                : "memory");
 }
 
-// Ask for the place of a CTA of this grid that has not started: 16 bytes at
-// `dst`, completion on `bar`.
-__device__ __forceinline__ void take_over_next(uint32_t dst, uint32_t bar) {
-  mbar_arrive_expect_tx(bar, 16);
-  asm volatile(
-      "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
-      "r"(bar)
-      : "memory");
-}
-// Whether the answer at `src` grants one, and its block index.
-__device__ __forceinline__ bool taken_over(uint32_t src, uint32_t* cta) {
-  uint32_t ok, x;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\tld.shared.b128 h, [%2];\n\t"
-      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
-      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
-      : "=r"(ok), "=r"(x)
-      : "r"(src)
-      : "memory");
-  *cta = x;
-  return ok != 0;
-}
-
 // Bits 15 and 31 of the result: whether some bf16 of the words has an exponent
 // of all ones (the addition carries into those bits).
 __device__ __forceinline__ uint32_t nonfinite_bits(uint4 w) {
