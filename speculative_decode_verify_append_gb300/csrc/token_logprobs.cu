@@ -22,8 +22,10 @@
 #include <cuda_fp16.h>
 #include <math.h>
 
+#include <algorithm>
 #include <utility>
 
+#include "sdva_internal.cuh"
 #include "tc_primitives.cuh"
 
 namespace cg = cooperative_groups;
@@ -38,7 +40,6 @@ using tc::ffma2;
 using tc::fmul2;
 
 constexpr int kMaxCluster = 8;
-constexpr int kBig = 512;       // threads per CTA (128 for short rows)
 constexpr int kGroups = 128;    // groups of threads whose maxima bound the list
 constexpr int kCandidates = 512;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
@@ -175,7 +176,7 @@ __device__ Key block_merge(Key k, Key (*buf)[32]) {
 // The part of a row that one CTA reads.  Vectors start at the row's first
 // 16-byte boundary; the few elements before it and behind the last whole
 // vector go one each to the first threads of CTA 0.
-template <typename T, int kThreads>
+template <typename T>
 struct Part {
   static constexpr int kVec = Elem<T>::kVec;
   const T* x;
@@ -244,9 +245,37 @@ __device__ __forceinline__ Stat warp_join(Stat a) {
   return b;
 }
 
-// kThreads: 512, or 128 for short rows.
-template <typename T, int kThreads>
-__global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kernel(LogprobArgs a, int parts) {
+// The statistics of a cluster's CTAs, in every lane.
+__device__ __forceinline__ Stat cluster_join(const Stat* c, int parts) {
+  const int i = threadIdx.x % kMaxCluster;
+  return warp_join<kMaxCluster>(i < parts ? c[i] : Stat{0.0f, 0.0f, 0.0f});
+}
+
+// A row's outputs, by one warp: b in every lane, x_t in lane 0, the sorted
+// lists of `parts` CTAs.
+__device__ __forceinline__ void write_row(const LogprobArgs& a, int row, float x_t, const Stat& b,
+                                          const Key (*lists)[32], int parts) {
+  const int lane = threadIdx.x & 31;
+  // no distribution: all -inf, or a NaN or +inf in the row
+  const float log_s = (b.s > 0.0f ? log2f(b.s) : __int_as_float(0x7fc00000)) * kLn2;
+  if (lane == 0) {
+    a.logprobs[row] = x_t - b.m - log_s;
+    if (a.entropy != nullptr) a.entropy[row] = log_s - b.t / b.s * kLn2;
+  }
+  if (a.num_top > 0) {
+    Key k = lists[0][lane];
+    for (int q = 1; q < parts; ++q) k = warp_merge(k, lists[q][lane]);
+    if (lane < a.num_top) {
+      a.top_tokens[(size_t)row * a.num_top + lane] = index_of(k);
+      a.top_logprobs[(size_t)row * a.num_top + lane] = value_of(k) - b.m - log_s;
+    }
+  }
+}
+
+// Short rows: 128 threads, a thread's rounds of loads in registers.
+template <typename T>
+__global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, int parts) {
+  constexpr int kThreads = 128;
   constexpr int kVec = Elem<T>::kVec, kPer = 16 / kVec, kUnroll = Elem<T>::kUnroll, kWarps = kThreads / 32;
   __shared__ Stat s_stat[kWarps];
   __shared__ float4 s_group4[kGroups / 4];  // read four at a time
@@ -277,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
   cg::cluster_group cluster = cg::this_cluster();
   auto started = cluster.barrier_arrive();
   const float ninf = __int_as_float(0xff800000);
-  const Part<T, kThreads> p(static_cast<const T*>(a.logits) + (size_t)row * a.row_stride, a.vocab, part, parts);
+  const Part<T> p(static_cast<const T*>(a.logits) + (size_t)row * a.row_stride, a.vocab, part, parts);
   float x_t = 0.0f;
   if (part == 0 && th == 0) x_t = Elem<T>::one(p.x[token]);
 
@@ -440,34 +469,411 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) token_logprobs_kern
   }
   cluster.sync();
   if (part != 0 || warp != 0) return;
-  const Stat b = warp_join<kMaxCluster>(lane < parts ? c_stat[lane] : Stat{0.0f, 0.0f, 0.0f});
-  // no distribution: all -inf, or a NaN or +inf in the row
-  const float log_s = (b.s > 0.0f ? log2f(b.s) : __int_as_float(0x7fc00000)) * kLn2;
-  if (th == 0) {
-    a.logprobs[row] = x_t - b.m - log_s;
-    if (a.entropy != nullptr) a.entropy[row] = log_s - b.t / b.s * kLn2;
-  }
-  if (a.num_top > 0) {
-    const float ref = __shfl_sync(0xffffffffu, b.m, 0), ls = __shfl_sync(0xffffffffu, log_s, 0);
-    Key k = c_keys[0][lane];
-    for (int q = 1; q < parts; ++q) k = warp_merge(k, c_keys[q][lane]);
+  const Stat b = cluster_join(c_stat, parts);
+  write_row(a, row, x_t, b, c_keys, parts);
+}
+
+// Long rows.  Warps 0-7 stream: they add up what a ring of 16 KB stages
+// brings and hand their sums and maxima to warps 8-11 (the team), which
+// finish the row while the next one streams; warp 12 fills the ring with bulk
+// copies.  The reading of one row after the other never stops for the end of
+// a row, and the copies leave the load path to the team: with one kind of
+// warps that loads through registers, a row's end costs 3,000 cycles of
+// shuffles and shared-memory reads queued behind the loads (4,096 bf16 rows
+// 251 us against KEPTA).  Many rows: a CTA takes units of consecutive rows
+// and, when one is on its way, the next one's CTA's place.  Few rows
+// (kCluster): one cluster of `parts` CTAs per row.
+constexpr int kStreamThreads = 256, kTeamThreads = 128, kLongThreads = kStreamThreads + kTeamThreads + 32;
+constexpr int kStages = 6, kStageVecs = 4 * kStreamThreads;  // 16-byte vectors per stage
+constexpr uint32_t kStageBytes = kStageVecs * 16;
+constexpr int kRowRing = 4;
+constexpr int kTeamWarps = kTeamThreads / 32, kStreamWarps = kStreamThreads / 32;
+static_assert(kGroups == kTeamThreads && kStreamThreads == 2 * kGroups, "a group is a team thread's two stream threads");
+
+struct LongCtl {
+  uint64_t full[kStages], empty[kStages], row_full[kRowRing], row_free[kRowRing], sums_full[2], sums_free[2], next_full;
+  alignas(16) uint32_t next_cta[4];
+  float4 group4[kGroups / 4];
+  Key keys[kCandidates];  // candidates, or the warps' lists
+  Key c_keys[kMaxCluster][32];
+  Stat c_stat[kMaxCluster];
+  Stat stat[kTeamWarps];
+  float top[2][kStreamThreads], s[2][kStreamThreads], t[2][kStreamThreads];
+  int hot[kStreamThreads];
+  int row[kRowRing];  // -1: no more
+  float x_t;       // of the given token, across the cluster's barrier
+  uint32_t bound;
+  int count, hots, abort;
+};
+constexpr size_t kLongSmem = kStages * kStageBytes + sizeof(LongCtl);
+static_assert(2 * (kLongSmem + 1024) <= 233472, "two CTAs per SM");
+
+__device__ __forceinline__ void team_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kTeamThreads) : "memory"); }
+// whether every thread of the team says so, the same for all
+__device__ __forceinline__ bool team_all(bool ok) {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(r)
+               : "r"((uint32_t)ok), "n"(kTeamThreads)
+               : "memory");
+  return r != 0;
+}
+
+template <typename T, bool kCluster>
+__global__ void __launch_bounds__(kLongThreads, 2)
+    long_logprobs_kernel(LogprobArgs a, int num_rows, int unit, int parts, long long limit) {
+  constexpr int kVec = Elem<T>::kVec, kPer = 16 / kVec;
+  extern __shared__ __align__(16) uint8_t smem[];
+  LongCtl* const ctl = reinterpret_cast<LongCtl*>(smem + kStages * kStageBytes);
+  const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, th = threadIdx.x;
+  const int part = kCluster ? blockIdx.x % parts : 0;
+  const float ninf = __int_as_float(0xff800000);
+  auto scored = [&](int row) {
+    const int token = a.tokens[row];
+    return token >= 0 && token < a.vocab;
+  };
+  auto leave_row = [&](int row) {  // by one warp: a row that is not scored
+    if (lane == 0) {
+      if (a.tokens[row] != -1) raise_status(a.status, SDVA_STATUS_BAD_DRAFT);
+      a.logprobs[row] = 0.0f;
+      if (a.entropy != nullptr) a.entropy[row] = 0.0f;
+    }
     if (lane < a.num_top) {
-      a.top_tokens[(size_t)row * a.num_top + lane] = index_of(k);
-      a.top_logprobs[(size_t)row * a.num_top + lane] = value_of(k) - ref - ls;
+      a.top_tokens[(size_t)row * a.num_top + lane] = -1;
+      a.top_logprobs[(size_t)row * a.num_top + lane] = 0.0f;
+    }
+  };
+  if (kCluster && !scored(blockIdx.x / parts)) {  // the same for the whole cluster
+    if (part == 0 && warp == 0) leave_row(blockIdx.x / parts);
+    return;
+  }
+  if (th == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      tc::mbar_init(smem_u32(&ctl->full[i]), 1);
+      tc::mbar_init(smem_u32(&ctl->empty[i]), kStreamWarps);
+    }
+    for (int i = 0; i < kRowRing; ++i) {
+      tc::mbar_init(smem_u32(&ctl->row_full[i]), 1);
+      tc::mbar_init(smem_u32(&ctl->row_free[i]), kStreamWarps + kTeamWarps);
+    }
+    for (int i = 0; i < 2; ++i) {
+      tc::mbar_init(smem_u32(&ctl->sums_full[i]), kStreamWarps);
+      tc::mbar_init(smem_u32(&ctl->sums_free[i]), kTeamWarps);
+    }
+    tc::mbar_init(smem_u32(&ctl->next_full), 1);
+    ctl->abort = 0;
+    tc::mbar_fence_init();
+  }
+  __syncthreads();
+  cg::cluster_group cluster = cg::this_cluster();
+  // CTA 0's shared memory is written to once every CTA of the cluster runs
+  if (kCluster) cluster.sync();
+  volatile int* const abort_flag = &ctl->abort;
+  auto wait = [&](uint64_t& bar, uint32_t parity) {
+    return tc::mbar_wait<false>(smem_u32(&bar), parity & 1u, abort_flag, limit);
+  };
+  auto arrive = [&](uint64_t& bar) {
+    __syncwarp();
+    if (lane == 0) tc::mbar_arrive(smem_u32(&bar));
+  };
+  auto give_up = [&]() {
+    if (lane == 0) {
+      ctl->abort = 1;
+      raise_status(a.status, SDVA_STATUS_TIMEOUT);
+    }
+  };
+  auto part_of = [&](int row) {
+    return Part<T>(static_cast<const T*>(a.logits) + (size_t)row * a.row_stride, a.vocab, part, parts);
+  };
+  bool ok = true;
+
+  if (warp == kStreamWarps + kTeamWarps) {
+    // ---- the copies ----
+    uint32_t fills = 0, rows = 0, asks = 0;
+    auto publish = [&](int row) {
+      const uint32_t slot = rows % kRowRing;
+      if (rows >= kRowRing && !wait(ctl->row_free[slot], rows / kRowRing - 1)) return false;
+      if (lane == 0) {
+        ctl->row[slot] = row;
+        tc::mbar_arrive(smem_u32(&ctl->row_full[slot]));
+      }
+      __syncwarp();
+      ++rows;
+      return true;
+    };
+    uint32_t next = kCluster ? blockIdx.x / parts : blockIdx.x;
+    for (bool more = true; more && ok;) {
+      const int first = (int)next * unit, end = (int)min((long long)num_rows, (long long)first + unit);
+      for (int row = first; row < end && ok; ++row) {
+        if (!kCluster && !scored(row)) {
+          leave_row(row);
+          continue;
+        }
+        if (!(ok = publish(row))) break;
+        const Part<T> p = part_of(row);
+        for (int v = 0; v < p.vectors && ok; v += kStageVecs, ++fills) {
+          const uint32_t st = fills % kStages;
+          if (fills >= kStages && !(ok = wait(ctl->empty[st], fills / kStages - 1))) break;
+          if (lane == 0) {
+            const uint32_t bytes = 16u * (uint32_t)min(kStageVecs, p.vectors - v), bar = smem_u32(&ctl->full[st]);
+            tc::mbar_arrive_expect_tx(bar, bytes);
+            tc::bulk_load(smem_u32(smem) + st * kStageBytes, reinterpret_cast<const uint4*>(p.x + p.first) + v, bytes, bar);
+          }
+          __syncwarp();
+        }
+      }
+      more = false;
+      if (!kCluster && ok) {
+        if (lane == 0) tc::take_over_next(smem_u32(ctl->next_cta), smem_u32(&ctl->next_full));
+        __syncwarp();
+        if ((ok = wait(ctl->next_full, asks++))) {
+          more = tc::taken_over(smem_u32(ctl->next_cta), &next);
+          tc::fence_proxy_async_smem();  // the answer is read before the next one is written
+          __syncwarp();
+        }
+      }
+    }
+    if (ok) ok = publish(-1);
+    if (!ok) {
+      give_up();
+      // this warp's copies still in flight (bounded)
+      int none = 0;
+      for (uint32_t f = fills > kStages ? fills - kStages : 0; f < fills; ++f)
+        tc::mbar_wait<false>(smem_u32(&ctl->full[f % kStages]), (f / kStages) & 1u, &none, 400000000LL);
+      if (asks > 0) tc::mbar_wait<false>(smem_u32(&ctl->next_full), (asks - 1) & 1u, &none, 400000000LL);
+    }
+  } else if (warp < kStreamWarps) {
+    // ---- the sums ----
+    uint32_t st = 0, phase = 0;
+    for (uint32_t r = 0;; ++r) {
+      const uint32_t slot = r % kRowRing;
+      if (!(ok = wait(ctl->row_full[slot], r / kRowRing))) break;
+      const int row = ctl->row[slot];
+      if (row < 0) break;
+      const Part<T> p = part_of(row);
+      float x0 = ninf;
+      if (th < p.extra) x0 = Elem<T>::one(p.x[p.extra_index(th)]);
+      Stat sum = {0.0f, 0.0f, 0.0f};
+      float top = ninf;
+      for (int v0 = 0; v0 < p.vectors && ok; v0 += kStageVecs) {
+        if (!(ok = wait(ctl->full[st], phase))) break;
+        const uint4* const stage = reinterpret_cast<const uint4*>(smem + st * kStageBytes);
+        uint4 w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int at = u * kStreamThreads + th;
+          // what a last, shorter stage lacks has no part in anything
+          w[u] = v0 + at < p.vectors ? stage[at]
+                                     : make_uint4(Elem<T>::kNone, Elem<T>::kNone, Elem<T>::kNone, Elem<T>::kNone);
+        }
+        arrive(ctl->empty[st]);
+        if (++st == kStages) {
+          st = 0;
+          phase ^= 1u;
+        }
+#pragma unroll
+        for (int u = 0; u < 4; u += kPer) {
+          float x[16], m = ninf;
+#pragma unroll
+          for (int k = 0; k < kPer; ++k) {
+            Elem<T>::unpack(w[u + k], x + k * kVec);
+            m = fmaxf(m, Elem<T>::largest(w[u + k]));
+          }
+          add16(sum, top, m, x);
+        }
+      }
+      if (!ok) break;
+      if (th < p.extra) {
+        float x[16];
+        x[0] = x0;
+#pragma unroll
+        for (int j = 1; j < 16; ++j) x[j] = ninf;
+        add16(sum, top, x0, x);
+      }
+      const uint32_t d = r & 1u;
+      if (r >= 2 && !(ok = wait(ctl->sums_free[d], r / 2 - 1))) break;
+      ctl->top[d][th] = top;
+      ctl->s[d][th] = sum.s;
+      ctl->t[d][th] = sum.t;
+      arrive(ctl->sums_full[d]);
+      if (lane == 0) tc::mbar_arrive(smem_u32(&ctl->row_free[slot]));
+    }
+    if (!ok) give_up();
+  } else {
+    // ---- the end of a row ----
+    const int tt = th - kStreamThreads, tw = warp - kStreamWarps;
+    float* const group = reinterpret_cast<float*>(ctl->group4);
+    for (uint32_t r = 0;; ++r) {
+      const uint32_t slot = r % kRowRing, d = r & 1u;
+      if (!team_all(ok = wait(ctl->row_full[slot], r / kRowRing))) break;
+      const int row = ctl->row[slot];
+      if (row < 0) break;
+      const Part<T> p = part_of(row);
+      float x_t = 0.0f;
+      if (part == 0 && tt == 0) x_t = Elem<T>::one(p.x[a.tokens[row]]);
+      if (!team_all(ok = wait(ctl->sums_full[d], r / 2))) break;
+      // this thread's two stream threads
+      float top[2];
+      Stat own[2];
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        const int who = tt + k * kTeamThreads;
+        top[k] = ctl->top[d][who];
+        own[k] = {top[k] == ninf ? 0.0f : top[k], ctl->s[d][who], ctl->t[d][who]};
+      }
+      arrive(ctl->sums_free[d]);
+      {
+        const float m = fmaxf(own[0].s == 0.0f ? ninf : own[0].m, own[1].s == 0.0f ? ninf : own[1].m);
+        const Stat u = moved(own[0], m == ninf ? 0.0f : m), w = moved(own[1], m == ninf ? 0.0f : m);
+        const Stat j = warp_join<32>(Stat{u.m, u.s + w.s, u.t + w.t});
+        if (lane == 0) ctl->stat[tw] = j;
+        group[tt] = fmaxf(top[0], top[1]);
+        if (tt == 0) {
+          ctl->count = ctl->hots = 0;
+          ctl->bound = 0xffffffffu;
+        }
+      }
+      team_sync();
+      const Stat b = warp_join<kTeamWarps>(ctl->stat[lane % kTeamWarps]);
+      if (a.num_top > 0) {
+        // the bound: the smallest group maximum with fewer than num_top above it
+        {
+          const float mine = group[tt];
+          int above = 0;
+#pragma unroll 8
+          for (int i = 0; i < kGroups / 4; ++i) {
+            const float4 o = ctl->group4[i];
+            above += (o.x > mine) + (o.y > mine) + (o.z > mine) + (o.w > mine);
+          }
+          if (above < a.num_top) atomicMin(&ctl->bound, order_of(mine));
+        }
+        team_sync();
+        const float bound = of_order(ctl->bound);
+        Key* list = &ctl->c_keys[part][0];
+        if (kCluster) list = cluster.map_shared_rank(list, 0);
+        // a NaN (or +inf, which makes one) hides its thread's maximum
+        bool all = b.s != b.s || bound == ninf;
+        if (!all) {
+          auto offer = [&](float x, int i) {
+            if (x >= bound) {
+              const int at = atomicAdd(&ctl->count, 1);
+              if (at < kCandidates) ctl->keys[at] = key_of(x, i);
+            }
+          };
+#pragma unroll
+          for (int k = 0; k < 2; ++k)
+            if (top[k] >= bound) {
+              const int who = tt + k * kTeamThreads;
+              ctl->hot[atomicAdd(&ctl->hots, 1)] = who;
+              if (who < p.extra) offer(Elem<T>::one(p.x[p.extra_index(who)]), p.extra_index(who));
+            }
+          team_sync();
+          // their vectors, dealt to the team
+          const int each = (p.vectors + kStreamThreads - 1) / kStreamThreads, items = ctl->hots * each;
+          for (int i0 = tt; i0 < items; i0 += 4 * kTeamThreads) {
+            uint4 w[4];
+            int v[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int i = i0 + u * kTeamThreads;
+              v[u] = i < items ? ctl->hot[i / each] + i % each * kStreamThreads : p.vectors;
+              if (v[u] < p.vectors) w[u] = p.load(v[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              if (v[u] < p.vectors && Elem<T>::largest(w[u]) >= bound) {
+                float x[kVec];
+                Elem<T>::unpack(w[u], x);
+#pragma unroll
+                for (int j = 0; j < kVec; ++j) offer(x[j], p.first + v[u] * kVec + j);
+              }
+          }
+          team_sync();
+          const int count = ctl->count;
+          all = count > kCandidates;
+          if (!all)
+            for (int i = tt; i < max(count, 32); i += kTeamThreads) {
+              const Key k = i < count ? ctl->keys[i] : 0;
+              int rank = i;
+              if (i < count) {
+                rank = 0;
+                for (int j = 0; j < count; ++j) rank += ctl->keys[j] > k;
+              }
+              if (rank < 32) list[rank] = k;
+            }
+        }
+        if (all) {  // the same for the whole team
+          team_sync();
+          Key mine = 0;
+          auto take = [&](Key k) {
+            const Key last = __shfl_sync(0xffffffffu, mine, a.num_top - 1);
+            if (__any_sync(0xffffffffu, k > last)) mine = warp_merge(mine, warp_sort(k));
+          };
+          if (tw == 0) take(lane < p.extra ? key_of(Elem<T>::one(p.x[p.extra_index(lane)]), p.extra_index(lane)) : 0);
+          for (int v0 = tw * 32; v0 < p.vectors; v0 += 4 * kTeamThreads) {
+            uint4 w[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int v = v0 + u * kTeamThreads + lane;
+              w[u] = v < p.vectors ? p.load(v) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+              const int v = v0 + u * kTeamThreads + lane;
+              float x[kVec];
+              Elem<T>::unpack(w[u], x);
+#pragma unroll
+              for (int j = 0; j < kVec; ++j) take(v < p.vectors ? key_of(x[j], p.first + v * kVec + j) : 0);
+            }
+          }
+          // the warps' lists into one
+          ctl->keys[tw * 32 + lane] = mine;
+          team_sync();
+          if (tw == 0) {
+#pragma unroll
+            for (int o = 1; o < kTeamWarps; ++o) mine = warp_merge(mine, ctl->keys[o * 32 + lane]);
+            list[lane] = mine;
+          }
+        }
+      }
+      if (kCluster) {
+        if (tt == 0) {
+          *cluster.map_shared_rank(&ctl->c_stat[part], 0) = b;
+          ctl->x_t = x_t;
+        }
+      } else {
+        team_sync();
+        if (tw == 0) write_row(a, row, x_t, b, ctl->c_keys, 1);
+      }
+      arrive(ctl->row_free[slot]);
+    }
+    if (!ok) give_up();
+  }
+  if (kCluster) {
+    cluster.sync();
+    if (part == 0 && warp == 0) {
+      const Stat b = cluster_join(ctl->c_stat, parts);
+      write_row(a, blockIdx.x / parts, ctl->x_t, b, ctl->c_keys, parts);
     }
   }
 }
 
-template <typename T, int kThreads>
-int launch(const LogprobArgs& a, int num_rows, int sms, cudaStream_t stream) {
-  // CTAs per row: two for every SM, and no less than two rounds of loads for a thread
+template <typename T>
+int launch(const LogprobArgs& a, int num_rows, cudaStream_t stream) {
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SDVA_ERR_CUDA;
+  constexpr int kVec = Elem<T>::kVec;
+  // Rows of fewer than four stages go to the small blocks: the team's time on
+  // a row is that of about as many.  (KEPTB)
+  const bool is_short = a.vocab < 4 * kStageVecs * kVec;
+  // CTAs per row: while every SM would not have one, and each has two rounds of loads
+  const long long round = is_short ? 128LL * Elem<T>::kUnroll * kVec : (long long)kStageVecs * kVec;
+  const long long wanted = is_short ? 2LL * sms : sms;
   int parts = 1;
-  while (parts < kMaxCluster && (long long)num_rows * parts < 2LL * sms &&
-         a.vocab > 2LL * parts * kThreads * Elem<T>::kUnroll * Elem<T>::kVec)
-    parts *= 2;
+  while (parts < kMaxCluster && (long long)num_rows * parts < wanted && a.vocab > 2 * parts * round) parts *= 2;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)num_rows * parts, 1, 1);
-  cfg.blockDim = dim3(kThreads, 1, 1);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -475,15 +881,25 @@ int launch(const LogprobArgs& a, int num_rows, int sms, cudaStream_t stream) {
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, token_logprobs_kernel<T, kThreads>, a, parts) == cudaSuccess ? SDVA_OK
-                                                                                              : SDVA_ERR_CUDA;
-}
-
-template <typename T>
-int launch(const LogprobArgs& a, int num_rows, int sms, cudaStream_t stream) {
-  return a.vocab < 8 * kBig * Elem<T>::kVec ? launch<T, 128>(a, num_rows, sms, stream)
-                                            : launch<T, kBig>(a, num_rows, sms, stream);
+  cudaError_t e;
+  if (is_short) {
+    cfg.gridDim = dim3((unsigned)num_rows * parts, 1, 1);
+    cfg.blockDim = dim3(128, 1, 1);
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, short_logprobs_kernel<T>, a, parts);
+  } else {
+    const auto kernel = parts > 1 ? long_logprobs_kernel<T, true> : long_logprobs_kernel<T, false>;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLongSmem) != cudaSuccess)
+      return SDVA_ERR_CUDA;
+    // consecutive rows per unit of work: more than one only where units stay many for each SM
+    const int unit = parts > 1 ? 1 : (int)std::min(8LL, std::max(1LL, num_rows / (32LL * sms)));
+    cfg.gridDim = dim3(parts > 1 ? (unsigned)num_rows * parts : (unsigned)((num_rows + unit - 1) / unit), 1, 1);
+    cfg.blockDim = dim3(kLongThreads, 1, 1);
+    cfg.dynamicSmemBytes = kLongSmem;
+    cfg.numAttrs = parts > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, kernel, a, num_rows, unit, parts, wait_limit());
+  }
+  return e == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
 }
 
 }  // namespace
@@ -502,13 +918,9 @@ extern "C" int token_logprobs(const void* logits, int logits_dtype, int64_t row_
   if (num_top > SDVA_MAX_TOP || logits_dtype < SDVA_LOGITS_F32 || logits_dtype > SDVA_LOGITS_F16)
     return SDVA_ERR_UNSUPPORTED;
   if (reinterpret_cast<uintptr_t>(logits) & (logits_dtype == SDVA_LOGITS_F32 ? 3u : 1u)) return SDVA_ERR_INVALID;
-  int dev = 0, sms = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-    return SDVA_ERR_CUDA;
   const LogprobArgs a = {logits, row_stride, tokens, logprobs, entropy, top_tokens, top_logprobs, status, vocab, num_top};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  return logits_dtype == SDVA_LOGITS_F32    ? launch<float>(a, num_rows, sms, s)
-         : logits_dtype == SDVA_LOGITS_BF16 ? launch<__nv_bfloat16>(a, num_rows, sms, s)
-                                            : launch<__half>(a, num_rows, sms, s);
+  return logits_dtype == SDVA_LOGITS_F32    ? launch<float>(a, num_rows, s)
+         : logits_dtype == SDVA_LOGITS_BF16 ? launch<__nv_bfloat16>(a, num_rows, s)
+                                            : launch<__half>(a, num_rows, s);
 }
