@@ -480,7 +480,7 @@ __global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, i
 // a row, and the copies leave the load path to the team: with one kind of
 // warps that loads through registers, a row's end costs 3,000 cycles of
 // shuffles and shared-memory reads queued behind the loads (4,096 bf16 rows
-// 251 us against KEPTA).  Many rows: a CTA takes units of consecutive rows
+// 251 us against 198).  Many rows: a CTA takes units of consecutive rows
 // and, when one is on its way, the next one's CTA's place.  Few rows
 // (kCluster): one cluster of `parts` CTAs per row.
 constexpr int kStreamThreads = 256, kTeamThreads = 128, kLongThreads = kStreamThreads + kTeamThreads + 32;
@@ -497,13 +497,16 @@ struct LongCtl {
   Key keys[kCandidates];  // candidates, or the warps' lists
   Key c_keys[kMaxCluster][32];
   Stat c_stat[kMaxCluster];
-  Stat stat[kTeamWarps];
-  float top[2][kStreamThreads], s[2][kStreamThreads], t[2][kStreamThreads];
-  int hot[kStreamThreads];
+  Stat stat[2][kStreamWarps];
+  // of each stream thread: its maximum, the stage of the row that holds the
+  // largest vectors' maximum, and the largest of the other stages'
+  float top[2][kStreamThreads], second[2][kStreamThreads];
+  int stage[2][kStreamThreads];
+  int hot[kStreamThreads], wide[kStreamThreads];
   int row[kRowRing];  // -1: no more
   float x_t;       // of the given token, across the cluster's barrier
   uint32_t bound;
-  int count, hots, abort;
+  int count, hots, wides, abort;
 };
 constexpr size_t kLongSmem = kStages * kStageBytes + sizeof(LongCtl);
 static_assert(2 * (kLongSmem + 1024) <= 233472, "two CTAs per SM");
@@ -654,9 +657,11 @@ __global__ void __launch_bounds__(kLongThreads, 2)
       float x0 = ninf;
       if (th < p.extra) x0 = Elem<T>::one(p.x[p.extra_index(th)]);
       Stat sum = {0.0f, 0.0f, 0.0f};
-      float top = ninf;
+      float top = ninf, best = ninf, second = ninf;
+      int at_best = 0;
       for (int v0 = 0; v0 < p.vectors && ok; v0 += kStageVecs) {
         if (!(ok = wait(ctl->full[st], phase))) break;
+        float here = ninf;
         const uint4* const stage = reinterpret_cast<const uint4*>(smem + st * kStageBytes);
         uint4 w[4];
 #pragma unroll
@@ -679,7 +684,13 @@ __global__ void __launch_bounds__(kLongThreads, 2)
             Elem<T>::unpack(w[u + k], x + k * kVec);
             m = fmaxf(m, Elem<T>::largest(w[u + k]));
           }
+          here = fmaxf(here, m);
           add16(sum, top, m, x);
+        }
+        second = fmaxf(second, fminf(best, here));
+        if (here > best) {
+          best = here;
+          at_best = v0 / kStageVecs;
         }
       }
       if (!ok) break;
@@ -692,9 +703,11 @@ __global__ void __launch_bounds__(kLongThreads, 2)
       }
       const uint32_t d = r & 1u;
       if (r >= 2 && !(ok = wait(ctl->sums_free[d], r / 2 - 1))) break;
+      const Stat joined = warp_join<32>(sum);
+      if (lane == 0) ctl->stat[d][warp] = joined;
       ctl->top[d][th] = top;
-      ctl->s[d][th] = sum.s;
-      ctl->t[d][th] = sum.t;
+      ctl->second[d][th] = second;
+      ctl->stage[d][th] = at_best;
       arrive(ctl->sums_full[d]);
       if (lane == 0) tc::mbar_arrive(smem_u32(&ctl->row_free[slot]));
     }
@@ -713,28 +726,23 @@ __global__ void __launch_bounds__(kLongThreads, 2)
       if (part == 0 && tt == 0) x_t = Elem<T>::one(p.x[a.tokens[row]]);
       if (!team_all(ok = wait(ctl->sums_full[d], r / 2))) break;
       // this thread's two stream threads
-      float top[2];
-      Stat own[2];
+      float top[2], second[2];
+      int at_best[2];
 #pragma unroll
       for (int k = 0; k < 2; ++k) {
         const int who = tt + k * kTeamThreads;
         top[k] = ctl->top[d][who];
-        own[k] = {top[k] == ninf ? 0.0f : top[k], ctl->s[d][who], ctl->t[d][who]};
+        second[k] = ctl->second[d][who];
+        at_best[k] = ctl->stage[d][who];
       }
+      const Stat b = warp_join<kStreamWarps>(ctl->stat[d][lane % kStreamWarps]);
       arrive(ctl->sums_free[d]);
-      {
-        const float m = fmaxf(own[0].s == 0.0f ? ninf : own[0].m, own[1].s == 0.0f ? ninf : own[1].m);
-        const Stat u = moved(own[0], m == ninf ? 0.0f : m), w = moved(own[1], m == ninf ? 0.0f : m);
-        const Stat j = warp_join<32>(Stat{u.m, u.s + w.s, u.t + w.t});
-        if (lane == 0) ctl->stat[tw] = j;
-        group[tt] = fmaxf(top[0], top[1]);
-        if (tt == 0) {
-          ctl->count = ctl->hots = 0;
-          ctl->bound = 0xffffffffu;
-        }
+      group[tt] = fmaxf(top[0], top[1]);
+      if (tt == 0) {
+        ctl->count = ctl->hots = ctl->wides = 0;
+        ctl->bound = 0xffffffffu;
       }
       team_sync();
-      const Stat b = warp_join<kTeamWarps>(ctl->stat[lane % kTeamWarps]);
       if (a.num_top > 0) {
         // the bound: the smallest group maximum with fewer than num_top above it
         {
@@ -764,29 +772,37 @@ __global__ void __launch_bounds__(kLongThreads, 2)
           for (int k = 0; k < 2; ++k)
             if (top[k] >= bound) {
               const int who = tt + k * kTeamThreads;
-              ctl->hot[atomicAdd(&ctl->hots, 1)] = who;
+              if (second[k] >= bound) ctl->wide[atomicAdd(&ctl->wides, 1)] = who;
+              else ctl->hot[atomicAdd(&ctl->hots, 1)] = at_best[k] * kStageVecs + who;
               if (who < p.extra) offer(Elem<T>::one(p.x[p.extra_index(who)]), p.extra_index(who));
             }
           team_sync();
-          // their vectors, dealt to the team
-          const int each = (p.vectors + kStreamThreads - 1) / kStreamThreads, items = ctl->hots * each;
+          auto look = [&](uint4 w, int v) {
+            if (Elem<T>::largest(w) >= bound) {
+              float x[kVec];
+              Elem<T>::unpack(w, x);
+#pragma unroll
+              for (int j = 0; j < kVec; ++j) offer(x[j], p.first + v * kVec + j);
+            }
+          };
+          // their vectors, dealt to the team: of the one stage that reaches the bound, or of all
+          for (int i = tt; i < 4 * ctl->hots; i += kTeamThreads) {
+            const int v = ctl->hot[i >> 2] + (i & 3) * kStreamThreads;
+            if (v < p.vectors) look(p.load(v), v);
+          }
+          const int each = (p.vectors + kStreamThreads - 1) / kStreamThreads, items = ctl->wides * each;
           for (int i0 = tt; i0 < items; i0 += 4 * kTeamThreads) {
             uint4 w[4];
             int v[4];
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
               const int i = i0 + u * kTeamThreads;
-              v[u] = i < items ? ctl->hot[i / each] + i % each * kStreamThreads : p.vectors;
-              if (v[u] < p.vectors) w[u] = p.load(v[u]);
+              v[u] = i < items ? ctl->wide[i / each] + i % each * kStreamThreads : p.vectors;
+              w[u] = v[u] < p.vectors ? p.load(v[u]) : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u)
-              if (v[u] < p.vectors && Elem<T>::largest(w[u]) >= bound) {
-                float x[kVec];
-                Elem<T>::unpack(w[u], x);
-#pragma unroll
-                for (int j = 0; j < kVec; ++j) offer(x[j], p.first + v[u] * kVec + j);
-              }
+              if (v[u] < p.vectors) look(w[u], v[u]);
           }
           team_sync();
           const int count = ctl->count;
