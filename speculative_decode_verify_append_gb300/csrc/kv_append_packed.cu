@@ -9,16 +9,20 @@
 // are issued before the lane's page ids are checked.  The grid is flat over
 // page slots, found from the offsets alone (slot_base).
 //
-// Division.  A code comes from fp32 x / s, rounded to nearest.  With r = 1 / s
-// rounded, q = x r, the remainder e = x - q s by one fused multiply-add is
-// exact and q + e r, rounded once, is the rounded quotient (Markstein, IBM
-// Journal of Research and Development 34, 1990).  That holds for every bf16
-// significand over every fp32 one (all 2^30 pairs compared with the division)
-// while nothing under- or overflows; outside s in [2^-80, 2^80] the division
-// itself is used.  Quotients that matter (2^-10 and more for E4M3, 1/2 for
-// the integers) have exact remainders there.  With -r for r the same three
-// steps give the negative quotient, and a zero keeps its sign; two at a time
-// they are one and a half instructions an element.
+// Division.  A code comes from fp32 x / s, rounded to nearest, and a scale
+// from amax / 448, / 127 or / 7.  With r = 1 / s rounded, q = x r, the
+// remainder e = x - q s by one fused multiply-add is exact and q + e r,
+// rounded once, is the rounded quotient (Markstein, IBM Journal of Research
+// and Development 34, 1990).  r comes from the hardware's approximation by one
+// such step.  For every bf16 significand over every fp32 one but all ones, and
+// an approximation within two units in the last place, the result was
+// compared with the division (all 2^30 pairs), while nothing under- or
+// overflows: with s in [2^-80, 2^80] the quotients that matter (2^-10 and more
+// for E4M3, 1/2 for the integers) have exact remainders.  Elsewhere the
+// division itself is used.  With -r for r the same steps give the negative
+// quotient, and a zero keeps its sign; two at a time they are one and a half
+// instructions an element, where the encoding of a row by divisions and
+// conversions made the call bound by instructions (19 an element for INT8).
 #include "sdva_internal.cuh"
 #include "tc_primitives.cuh"
 
@@ -54,22 +58,28 @@ using tc::f2_unpack;
 using tc::ffma2;
 using tc::fmul2;
 
-// Quotients by one divisor, rounded to nearest.
+// -(x / s) of two values, nr = -1 / s (see above)
+__device__ __forceinline__ float2 minus_quotients(float x0, float x1, float s, float nr) {
+  const unsigned long long x = f2_pack(x0, x1), n = f2_pack(nr, nr), q = fmul2(x, n);
+  return f2_unpack(ffma2(ffma2(q, f2_pack(s, s), x), n, q));
+}
 struct Divisor {
   float s, nr;
-  bool plain;  // out of the range where the short form holds
+  bool plain;  // not for the short form
   __device__ explicit Divisor(float s_) : s(s_) {
-    plain = !(s >= 0x1p-80f && s <= 0x1p80f);
-    nr = plain ? 0.0f : -__frcp_rn(s);
-  }
-  // -(x / s) of the two bf16 of a word
-  __device__ float2 minus(uint32_t w) const {
-    if (plain) return make_float2(-__fdiv_rn(bf16_lo(w), s), -__fdiv_rn(bf16_hi(w), s));
-    const unsigned long long x = f2_pack(bf16_lo(w), bf16_hi(w)), n = f2_pack(nr, nr);
-    const unsigned long long q = fmul2(x, n);
-    return f2_unpack(ffma2(ffma2(q, f2_pack(s, s), x), n, q));
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    nr = -__fmaf_rn(r, __fmaf_rn(-s, r, 1.0f), r);
+    plain = !(s >= 0x1p-80f && s <= 0x1p80f) || (~__float_as_uint(s) & 0x7FFFFFu) == 0;
   }
 };
+// amax / kTop of a bf16 amax >= 0
+template <int kTop>
+__device__ __forceinline__ float scale_of(float amax) {
+  if (amax < 0x1p-70f) return __fdiv_rn(amax, (float)kTop);
+  const float n = -1.0f / kTop, q = __fmul_rn(amax, n);
+  return -__fmaf_rn(__fmaf_rn(q, (float)kTop, amax), n, q);
+}
 
 __device__ __forceinline__ float amax8(uint4 w) {
   // the largest magnitude of eight bf16: their bits without the sign order as integers
@@ -82,33 +92,46 @@ __device__ __forceinline__ float lanes_max(float v) {
   for (int o = kLanes / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
   return v;
 }
+// The E4M3 codes of eight x / s; zeros for s = 0.
 __device__ __forceinline__ uint2 e4m3x8(uint4 w, const Divisor& d) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
   uint32_t p[4];
+  if (!d.plain) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 y = d.minus(u[j]);
-    p[j] = e4m3x2_from_f32(y.x, y.y);
+    for (int j = 0; j < 4; ++j) {
+      const float2 y = minus_quotients(bf16_lo(u[j]), bf16_hi(u[j]), d.s, d.nr);
+      p[j] = e4m3x2_from_f32(y.x, y.y);
+    }
+    // the sign bits back
+    return make_uint2((p[0] | (p[1] << 16)) ^ 0x80808080u, (p[2] | (p[3] << 16)) ^ 0x80808080u);
   }
-  // the sign bits back
-  return make_uint2((p[0] | (p[1] << 16)) ^ 0x80808080u, (p[2] | (p[3] << 16)) ^ 0x80808080u);
-}
-// Eight integer codes of x / s, halves to even, in [-top, top], as two's
-// complement in the low bits of each int.  `near`: no quotient rounds beyond
-// top, so that adding 1.5 * 2^23 rounds and nothing is left to clamp.
-template <int kTop>
-__device__ __forceinline__ void int_codes(uint4 w, const Divisor& d, bool near, uint32_t (&c)[8]) {
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  if (d.s == 0.0f) return make_uint2(0u, 0u);
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float2 y = d.minus(u[j]);
-    if (near) {
+  for (int j = 0; j < 4; ++j) p[j] = e4m3x2_from_f32(__fdiv_rn(bf16_lo(u[j]), d.s), __fdiv_rn(bf16_hi(u[j]), d.s));
+  return make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
+}
+// Eight integer codes of x / s, halves to even, in [-kTop, kTop], as two's
+// complement in the low bits of each; zeros for s = 0.  wide is the scale
+// before it was rounded to fp16: a normal one is within 2^-11 of it, so that
+// quotients reach kTop (1 + 2^-11) at most, which rounds to kTop; adding
+// 1.5 * 2^23 rounds them and nothing is left to clamp.
+template <int kTop>
+__device__ __forceinline__ void int_codes(uint4 w, float s, float wide, uint32_t (&c)[8]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+  const Divisor d(s);
+  if (s >= 0x1p-14f && wide <= 65504.0f) {  // fp16 significands are never all ones
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 y = minus_quotients(bf16_lo(u[j]), bf16_hi(u[j]), s, d.nr);
       c[2 * j] = __float_as_uint(12582912.0f - y.x);
       c[2 * j + 1] = __float_as_uint(12582912.0f - y.y);
-    } else {
-      c[2 * j] = (uint32_t)max(-kTop, min(kTop, __float2int_rn(-y.x)));
-      c[2 * j + 1] = (uint32_t)max(-kTop, min(kTop, __float2int_rn(-y.y)));
     }
+    return;
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = (j & 1) ? bf16_hi(u[j >> 1]) : bf16_lo(u[j >> 1]);
+    c[j] = s == 0.0f ? 0u : (uint32_t)max(-kTop, min(kTop, __float2int_rn(__fdiv_rn(x, s))));
   }
 }
 
@@ -192,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_packed_kernel(PackedArgs a
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) m = fmaxf(m, s_amax[is_v][w]);
-    const float s_cand = __fdiv_rn(m, 448.0f);
+    const float s_cand = scale_of<448>(m);
     const float s_new = start == 0 ? s_cand : (s_cand > s_old ? s_cand : s_old);
     uint8_t* const page_codes = codes + ph * kPage * kHeadDim;
     if (start > 0 && s_new > s_old) {
@@ -212,9 +235,8 @@ __global__ void __launch_bounds__(kThreads, 4) append_packed_kernel(PackedArgs a
       const int t = (th >> 4) + i * (kThreads / 16);
       if (t < count) {
         uint8_t* const out = page_codes + (size_t)(start + t) * kHeadDim + sub * 8;
-        const bool zero = s_new == 0.0f;
-        *reinterpret_cast<uint2*>(out) = zero ? make_uint2(0u, 0u) : e4m3x8(x[i][0], d);
-        *reinterpret_cast<uint2*>(out + 64) = zero ? make_uint2(0u, 0u) : e4m3x8(x[i][1], d);
+          *reinterpret_cast<uint2*>(out) = e4m3x8(x[i][0], d);
+        *reinterpret_cast<uint2*>(out + 64) = e4m3x8(x[i][1], d);
       }
     }
     if ((th & ~8) == 0) *scale = s_new;
@@ -225,12 +247,12 @@ __global__ void __launch_bounds__(kThreads, 4) append_packed_kernel(PackedArgs a
       const size_t at = ph * kPage + start + t;  // (page, kv head, token) row
       float m[2] = {amax8(x[i][0]), amax8(x[i][1])};
       if constexpr (KVT == SDVA_KV_FP8_ROW) {
-        const float s = __fdiv_rn(lanes_max<8>(fmaxf(m[0], m[1])), 448.0f);
+        const float s = scale_of<448>(lanes_max<8>(fmaxf(m[0], m[1])));
         if (t < count) {
           const Divisor d(s);
           uint8_t* const out = codes + at * kHeadDim + sub * 8;
-          *reinterpret_cast<uint2*>(out) = s == 0.0f ? make_uint2(0u, 0u) : e4m3x8(x[i][0], d);
-          *reinterpret_cast<uint2*>(out + 64) = s == 0.0f ? make_uint2(0u, 0u) : e4m3x8(x[i][1], d);
+            *reinterpret_cast<uint2*>(out) = e4m3x8(x[i][0], d);
+          *reinterpret_cast<uint2*>(out + 64) = e4m3x8(x[i][1], d);
           if (sub == 0) static_cast<float*>(scales)[at] = s;
         }
       } else {
@@ -239,21 +261,17 @@ __global__ void __launch_bounds__(kThreads, 4) append_packed_kernel(PackedArgs a
         constexpr int kTop = kInt4 ? 7 : 127;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          const float wide = __fdiv_rn(lanes_max<kInt4 ? 4 : 8>(m[h]), (float)kTop);
+            const float wide = scale_of<kTop>(lanes_max<kInt4 ? 4 : 8>(m[h]));
           const __half s16 = __float2half_rn(fminf(wide, 65504.0f));
           if (t < count) {
-            const float s = __half2float(s16);
-            uint32_t c[8], p[2] = {0u, 0u};
-            if (s != 0.0f) {
-              // a normal scale is within 2^-11 of wide: quotients up to top (1 + 2^-11), which rounds to top
-              int_codes<kTop>(x[i][h], Divisor(s), s >= 0x1p-14f && wide <= 65504.0f, c);
+              uint32_t c[8], p[2] = {0u, 0u};
+            int_codes<kTop>(x[i][h], __half2float(s16), wide, c);
+            if constexpr (kInt4) {
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (kInt4) p[0] |= (c[j] & 0xFu) << (4 * j);
-              if (!kInt4) {
-                p[0] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
-                p[1] = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
-              }
+              for (int j = 0; j < 8; ++j) p[0] |= (c[j] & 0xFu) << (4 * j);
+            } else {
+              p[0] = __byte_perm(__byte_perm(c[0], c[1], 0x0040), __byte_perm(c[2], c[3], 0x0040), 0x5410);
+              p[1] = __byte_perm(__byte_perm(c[4], c[5], 0x0040), __byte_perm(c[6], c[7], 0x0040), 0x5410);
             }
             __half* const sc = static_cast<__half*>(scales);
             if constexpr (kInt4) {

@@ -882,7 +882,8 @@ int launch(const LogprobArgs& a, int num_rows, cudaStream_t stream) {
     return SDVA_ERR_CUDA;
   constexpr int kVec = Elem<T>::kVec;
   // Rows of fewer than four stages go to the small blocks: the team's time on
-  // a row is that of about as many.  (KEPTB)
+  // a row is that of about as many (4,000 rows of 10,000 fp32 47 us in small
+  // blocks, 56 streamed; 2,000 of 30,000 bf16 38 and 40).
   const bool is_short = a.vocab < 4 * kStageVecs * kVec;
   // CTAs per row: while every SM would not have one, and each has two rounds of loads
   const long long round = is_short ? 128LL * Elem<T>::kUnroll * kVec : (long long)kStageVecs * kVec;

@@ -347,6 +347,36 @@ def test_packed_append_hostile_values():
                 KV_NAMES[kind], name)
 
 
+@pytest.mark.parametrize("exponent", [127, 127 - 75, 127 + 100])
+@pytest.mark.parametrize("kind", ALL_KV, ids=[KV_NAMES[k] for k in ALL_KV])
+def test_packed_append_every_significand(kind, exponent):
+    """Every bf16 significand under every scale significand (a scale comes from
+    a bf16 maximum), the values 0 .. 13 binades below it: the codes' quotients
+    are exact where the kernel replaces the division, and where it does not."""
+    import speculative_decode_verify_append_gb300 as sdva
+    m = np.arange(128, dtype=np.uint32)
+    a, e = np.repeat(m, 14), np.tile(np.arange(14, dtype=np.uint32), 128)
+    top = (exponent << 7) | a
+    x = ((exponent - e[:, None]) << 7) | m[None, :]
+    x = np.minimum(x, top[:, None])
+    x[:, ::32] = top[:, None]
+    x = (x | ((m & 1) << 15)[None, :]).astype(np.uint16)[:, None, :]
+    n = x.shape[0]
+    pages = n // 64
+    # page scales: one maximum to a page, so the pages' rows share theirs
+    if kind == synth.KV_FP8:
+        x = np.sort(x.view(np.int16), axis=0).view(np.uint16)
+    table = np.arange(pages, dtype=np.int32)[None]
+    gc, oc = sdva.KVCache(kind, pages, 1), oracle.Cache(kind, pages, 1)
+    st = _status()
+    sdva.kv_append_packed(gc, bf16_dev(x), bf16_dev(x[:, :, ::-1]), _cu([n]), i32_dev(table), i32_dev(np.array([0])), st)
+    assert oracle.append(oc, x[None], x[None, :, :, ::-1].copy(), table, np.array([0], np.int32)) == 0
+    assert int(st.item()) == 0
+    host = cache_to_host(gc)
+    for name in ("k_codes", "v_codes", "k_scales", "v_scales"):
+        assert np.array_equal(host[name].view(np.uint8), np.ascontiguousarray(getattr(oc, name)).view(np.uint8)), name
+
+
 # ---------------------------------------------------------------------------
 # token_logprobs
 # ---------------------------------------------------------------------------
