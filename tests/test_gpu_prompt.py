@@ -175,6 +175,29 @@ def test_prompt_attn_infinities_and_nan_stay_behind_the_mask():
             assert got.isnan().all() and lse[rows, heads].isnan().all()
 
 
+def test_prompt_attn_first_keys_without_weight():
+    """Scores of -inf over the whole first block of keys and more: the rows
+    behind them weigh the other keys alone; rows that see nothing else are NaN
+    with lse -inf, as the formula's 0 / 0."""
+    q, k, v = _qkv(_gen(12), 400, 4, 2)
+    q[:, :, 0] = 1.0
+    k[:150, :, 0] = -INF
+    out, lse = _run_attn(q, k, v, _cu([400]))
+    assert out[:150].isnan().all() and (lse[:150] == -INF).all()
+    for t in (150, 151, 260, 399):
+        want, wl, to, tl = _attn_ref(q[150:t + 1], k[150:t + 1], v[150:t + 1], [t - 149], float(SM_SCALE))
+        assert ((out[t].double() - want[-1]).abs() <= to[-1]).all()
+        assert ((lse[t].double() - wl[-1]).abs() <= tl[-1]).all()
+
+
+@pytest.mark.parametrize("lens", [[1501, 999, 2047, 3], [4000]])
+def test_prompt_attn_outlier_channels(lens):
+    """A few key channels eight times the rest, as real models have them."""
+    q, k, v = _qkv(_gen(13), sum(lens), 8, 4)
+    k[:, :, ::32] *= 8.0
+    _check_attn(q, k, v, lens)
+
+
 def test_prompt_attn_opposite_infinities():
     q, k, v = _qkv(_gen(7), 100, 2, 1)
     v[40, 0, 3], v[45, 0, 3] = INF, -INF
