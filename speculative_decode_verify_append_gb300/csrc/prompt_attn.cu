@@ -124,10 +124,14 @@ __device__ __forceinline__ int guard_from(const Tile& t) { return (t.t0 + 1) / k
 // Which tile comes r-th.  Tiles are ordered with the longest rows first over
 // all lanes (a tile's work grows with its position); the grid has a CTA per
 // tile, and a CTA that runs takes over the next one that has not started, so
-// that the work is dealt as it is done and ends with the shortest tiles.  A lane with n tiles has one at each position below n; between
-// two successive tile counts of the batch the number of lanes that reach a
-// position stays the same, which turns a rank into a position by one division
-// per distinct count.  The ranks a CTA gets grow, so it keeps its place.
+// that the work is dealt as it is done and ends with the shortest tiles.  A
+// lane with n tiles has one at each position below n; between two successive
+// tile counts of the batch the number of lanes that reach a position stays the
+// same, which turns a rank into a position by one division per distinct count.
+// The ranks a CTA gets grow, so it keeps its place.  (Where the longest chain
+// of blocks outlasts the rest, halves that share T rows and take every other
+// block would halve it, but each block then serves half as many rows: 2,048
+// tokens 37.5 against 26.8 us.)
 struct Order {
   const int32_t* cu;
   int B, span, lane;

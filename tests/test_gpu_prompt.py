@@ -110,6 +110,16 @@ def test_prompt_attn_head_layouts(hq, hkv):
     _check_attn(q, k, v, lens)
 
 
+@pytest.mark.parametrize("lens", [[256], [257], [383], [384], [385], [511, 130], [640, 1, 900], [2048], [3001]])
+@pytest.mark.parametrize("hq,hkv", [(4, 1), (1, 1), (12, 2), (7, 1)])
+def test_prompt_attn_few_long_tiles(lens, hq, hkv):
+    """Fewer tiles than SMs, of every number of blocks; flat and peaked scores."""
+    q, k, v = _qkv(_gen(len(lens) + 10 * hq), sum(lens), hq, hkv)
+    _check_attn(q, k, v, lens)
+    k[:, :, ::32] *= 16.0
+    _check_attn(q, k, v, lens)
+
+
 def test_prompt_attn_rows_outside_the_lanes_are_left():
     """Lanes that start behind row 0 and end before the last row; the rows
     around them hold NaN, which reaches nothing."""
