@@ -83,7 +83,8 @@ __device__ __forceinline__ float scale_of(float amax) {
 
 __device__ __forceinline__ float amax8(uint4 w) {
   // the largest magnitude of eight bf16: their bits without the sign order as integers
-  const uint32_t a = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu), __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
+  const uint32_t a = __vmaxu2(__vmaxu2(w.x & 0x7FFF7FFFu, w.y & 0x7FFF7FFFu),
+                              __vmaxu2(w.z & 0x7FFF7FFFu, w.w & 0x7FFF7FFFu));
   return __uint_as_float(max(a & 0xFFFF0000u, a << 16));
 }
 template <int kLanes>

@@ -280,7 +280,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const long long limit = a.wait_limit;
   // (spinning instead of sleeping takes issue slots from the softmax: 1,496
   // against 1,524 TFLOP/s at 32,768 tokens)
-  auto wait = [&](uint64_t& bar, uint32_t parity) { return mbar_wait<false>(smem_u32(&bar), parity, abort_flag, limit); };
+  auto wait = [&](uint64_t& bar, uint32_t parity) {
+    return mbar_wait<false>(smem_u32(&bar), parity, abort_flag, limit);
+  };
 
   if (bad) {  // the same for the whole CTA
     if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(a.status, SDVA_STATUS_BAD_COUNT);

@@ -8,15 +8,16 @@
 // reading the logits (16-bit logits also by the work per element, about four
 // instructions).
 //
-// One cluster of up to 8 CTAs per row, joined through distributed shared
-// memory: no workspace, no second launch.  A thread reads 16-byte vectors at
-// a stride of the block and keeps its maximum, S and T.  The listed tokens come out of these maxima: the k-th largest of the
-// maxima of 128 groups of threads is a bound that k elements reach, so only
-// threads whose maximum reaches it read their elements again (a few more
-// than k), and what reaches it is put in order by counting.  Comparing a list on every element
+// Few rows: a cluster of up to 8 CTAs per row, joined through distributed
+// shared memory; no workspace, no second launch.  A thread reads 16-byte
+// vectors at a stride of the block and keeps its maximum, S and T.  The listed
+// tokens come out of these maxima: the k-th largest of the maxima of 128
+// groups of threads is a bound that k elements reach, so only threads whose
+// maximum reaches it read their elements again (a few more than k), and what
+// reaches it is put in order by counting.  Comparing a list on every element
 // instead would cost more than the sums.  Where that bound says little (fewer
-// than k finite values, long ties, NaN), every element is looked at again in
-// index order against sorted lists of the warps.
+// than k finite values, long ties, NaN), every element is looked at again
+// against sorted lists of the warps.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -488,7 +489,8 @@ constexpr int kStages = 6, kStageVecs = 4 * kStreamThreads;  // 16-byte vectors 
 constexpr uint32_t kStageBytes = kStageVecs * 16;
 constexpr int kRowRing = 4;
 constexpr int kTeamWarps = kTeamThreads / 32, kStreamWarps = kStreamThreads / 32;
-static_assert(kGroups == kTeamThreads && kStreamThreads == 2 * kGroups, "a group is a team thread's two stream threads");
+static_assert(kGroups == kTeamThreads && kStreamThreads == 2 * kGroups,
+              "a group is a team thread's two stream threads");
 
 struct LongCtl {
   uint64_t full[kStages], empty[kStages], row_full[kRowRing], row_free[kRowRing], sums_full[2], sums_free[2], next_full;
@@ -515,10 +517,11 @@ __device__ __forceinline__ void team_sync() { asm volatile("bar.sync 1, %0;" ::"
 // whether every thread of the team says so, the same for all
 __device__ __forceinline__ bool team_all(bool ok) {
   uint32_t r;
-  asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-               : "=r"(r)
-               : "r"((uint32_t)ok), "n"(kTeamThreads)
-               : "memory");
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.and.pred q, 1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "n"(kTeamThreads)
+      : "memory");
   return r != 0;
 }
 
@@ -620,7 +623,8 @@ __global__ void __launch_bounds__(kLongThreads, 2)
           if (lane == 0) {
             const uint32_t bytes = 16u * (uint32_t)min(kStageVecs, p.vectors - v), bar = smem_u32(&ctl->full[st]);
             tc::mbar_arrive_expect_tx(bar, bytes);
-            tc::bulk_load(smem_u32(smem) + st * kStageBytes, reinterpret_cast<const uint4*>(p.x + p.first) + v, bytes, bar);
+            tc::bulk_load(smem_u32(smem) + st * kStageBytes, reinterpret_cast<const uint4*>(p.x + p.first) + v, bytes,
+                          bar);
           }
           __syncwarp();
         }
@@ -935,7 +939,8 @@ extern "C" int token_logprobs(const void* logits, int logits_dtype, int64_t row_
   if (num_top > SDVA_MAX_TOP || logits_dtype < SDVA_LOGITS_F32 || logits_dtype > SDVA_LOGITS_F16)
     return SDVA_ERR_UNSUPPORTED;
   if (reinterpret_cast<uintptr_t>(logits) & (logits_dtype == SDVA_LOGITS_F32 ? 3u : 1u)) return SDVA_ERR_INVALID;
-  const LogprobArgs a = {logits, row_stride, tokens, logprobs, entropy, top_tokens, top_logprobs, status, vocab, num_top};
+  const LogprobArgs a = {logits,     row_stride,   tokens, logprobs, entropy,
+                         top_tokens, top_logprobs, status, vocab,    num_top};
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   return logits_dtype == SDVA_LOGITS_F32    ? launch<float>(a, num_rows, s)
          : logits_dtype == SDVA_LOGITS_BF16 ? launch<__nv_bfloat16>(a, num_rows, s)

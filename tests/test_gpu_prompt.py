@@ -594,6 +594,116 @@ def test_token_logprobs_without_the_optional_outputs_and_replayed(n):
 
 
 # ---------------------------------------------------------------------------
+# together
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("kind", ALL_KV, ids=[KV_NAMES[k] for k in ALL_KV])
+def test_prompts_into_verify_steps(kind):
+    """Prompts packed into the cache in one pass, then a verify step and the
+    scores of its tokens, all in one captured graph: the cache and the step's
+    results are those of lane-by-lane appends, byte for byte."""
+    import speculative_decode_verify_append_gb300 as sdva
+    from speculative_decode_verify_append_gb300.step import PromptStep, VerifyStep, fill_context
+    lens, hq, hkv, W, V = [300, 1, 64, 129], 12, 2, 4, 5003
+    B, T = len(lens), sum(lens)
+    g = _gen(21)
+    q, k, v = _qkv(g, T, hq, hkv, fused=True)
+    rows = 8
+    table = torch.randperm(B * rows, generator=g, device="cuda").to(torch.int32).view(B, rows)
+    win = [torch.randn((B, W, n, D), generator=g, device="cuda").to(torch.bfloat16) for n in (hq, hkv, hkv)]
+    logits = torch.randn((B, W, V), generator=g, device="cuda") * 3
+    drafts = logits[:, :-1].argmax(-1).to(torch.int32)
+    drafts[0, 1] = drafts[2, 0] = 7
+    caches = [sdva.KVCache(kind, B * rows, hkv) for _ in range(2)]
+    prompt = PromptStep(T + 50, hq)
+    steps = [VerifyStep(B, W, hq, hkv, 512, V, num_top=6) for _ in range(2)]
+    zero, cu = torch.zeros(B, dtype=torch.int32, device="cuda"), _cu(lens)
+    seq = [torch.tensor(lens, dtype=torch.int32, device="cuda") for _ in range(2)]
+
+    def one_pass():
+        out, lse = prompt.run(caches[0], q, k, v, cu, table, zero)
+        steps[0].append(caches[0], win[1], win[2], table, seq[0])
+        steps[0].attend(caches[0], win[0], table, seq[0])
+        steps[0].accept_lazy(logits, drafts)
+        steps[0].score(logits)
+        return out, lse
+
+    one_pass()  # eager, also before a capture loads the code
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out, lse = one_pass()
+    out.fill_(7.0)
+    steps[0].out.fill_(7.0)
+    steps[0].logprobs.fill_(7.0)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert int(prompt.status.item()) == 0 and int(steps[0].status.item()) == 0
+
+    a = 0
+    for b, n in enumerate(lens):
+        fill_context(caches[1], k[a:a + n].contiguous(), v[a:a + n].contiguous(), table[b])
+        a += n
+    steps[1].append(caches[1], win[1], win[2], table, seq[1])
+    steps[1].attend(caches[1], win[0], table, seq[1])
+    steps[1].accept_lazy(logits, drafts)
+    for name in ("k_codes", "v_codes", "k_scales", "v_scales"):
+        x, y = (getattr(c, name)[table.long()[torch.arange(B), [n // 64 for n in lens]]] for c in caches)
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)), name
+    assert torch.equal(steps[0].out, steps[1].out)
+    assert torch.equal(steps[0].out_tokens, steps[1].out_tokens)
+    assert torch.equal(steps[0].accept_len, steps[1].accept_len)
+    ro, rl, to, tl = _attn_ref(q, k, v, lens, float(SM_SCALE))
+    assert ((out.double() - ro).abs() <= to).all() and ((lse.double() - rl).abs() <= tl).all()
+    tok = steps[0].out_tokens
+    on = tok >= 0
+    assert on.sum(-1).tolist() == (steps[0].accept_len + 1).tolist()
+    lp = logits.double().log_softmax(-1)
+    want = lp.gather(-1, tok.clamp(min=0).long()[..., None]).squeeze(-1)
+    # 2^-22 (V / 512 + 32) of the sum, as in _check_scores, with E|d| below 64 here
+    assert ((steps[0].logprobs.double() - want).abs()[on] <= 2.0 ** -22 * (V / 512 + 32) * 65).all()
+    assert not steps[0].logprobs[~on].any() and (steps[0].top_tokens[~on] == -1).all()
+    assert torch.equal(steps[0].top_tokens[on], _order(logits, 6)[on].to(torch.int32))
+
+
+def test_prompt_rows_agree_with_the_cache():
+    """The last rows of a prompt by prompt_attn, and by verify_attn as a window
+    over the INT8 cache that kv_append_packed filled.
+
+    Bounds.  A cached element is off by at most half a step of its group's
+    scale, s / 2 <= amax / 254 (1 + 2^-11), and once more by 2^-11 of itself
+    when it is widened to fp16; a score then by e = scale * sum |q| (amax_K / 253 +
+    2^-11 amax_K), a weight by a factor within exp(+-2e), an output by
+    amax_V (1 / 253 + 2^-11) more.  Weights and outputs are rounded on both
+    sides (2^-8 of sum p |v| and of the output each; q to fp16, 2^-11, on one)."""
+    import speculative_decode_verify_append_gb300 as sdva
+    from speculative_decode_verify_append_gb300.step import PromptStep, VerifyStep
+    lens, hq, hkv, W = [500, 77], 6, 2, 5
+    q, k, v = _qkv(_gen(31), sum(lens), hq, hkv)
+    cache = sdva.KVCache(sdva.KV_INT8_G64, 20, hkv)
+    table = torch.arange(20, dtype=torch.int32, device="cuda").view(2, 10)
+    prompt = PromptStep(sum(lens), hq)
+    out, _ = prompt.run(cache, q, k, v, _cu(lens), table, torch.zeros(2, dtype=torch.int32, device="cuda"))
+    step = VerifyStep(2, W, hq, hkv, 512, None)
+    last = torch.tensor([list(range(n - W, n)) for n in (500, 577)], device="cuda")
+    step.attend(cache, q[last].contiguous(), table, torch.tensor([n - W for n in lens], dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert int(prompt.status.item()) == 0 and int(step.status.item()) == 0
+    scale = float(SM_SCALE)
+    for b, (start, n) in enumerate(((0, 500), (500, 77))):
+        for i in range(W):
+            t = start + n - W + i
+            for h in range(hq):
+                kk, vv = k[start:t + 1, h // 3].double(), v[start:t + 1, h // 3].double()
+                qq = q[t, h].double()
+                p = (kk @ qq * scale).softmax(0)
+                e = scale * float(qq.abs().sum()) * float(kk.abs().max()) * (1 / 253 + 2.0 ** -11 + 2.0 ** -11)
+                av = p @ vv.abs()
+                tol = (math.expm1(2 * e) + 2 * 2.0 ** -8) * av + float(vv.abs().max()) * (1 / 253 + 2.0 ** -11) + \
+                    2 * 2.0 ** -8 * (p @ vv).abs()
+                err = (out[t, h].double() - step.out[b, i, h].double()).abs()
+                assert (err <= tol).all(), (b, i, h, float((err / tol).max()))
+
+
+# ---------------------------------------------------------------------------
 # arguments
 # ---------------------------------------------------------------------------
 def test_refusals_of_the_binding():
@@ -639,6 +749,9 @@ def test_refusals_of_the_binding():
         sdva.token_logprobs(x.T.contiguous().T, t, lp)
     with pytest.raises(ValueError):
         sdva.token_logprobs(x, t, lp, None, torch.empty((3, 2), dtype=torch.int32, device="cuda"))
+    from speculative_decode_verify_append_gb300.step import VerifyStep
+    with pytest.raises(ValueError):
+        VerifyStep(1, 1, 4, 2, 64, 50).score(x[:1].view(1, 1, 50))
     for top, code in ((33, sdva.ERR_UNSUPPORTED), (51, sdva.ERR_INVALID)):
         with pytest.raises(sdva.SdvaError) as e:
             sdva.token_logprobs(x, t, lp, None, torch.empty((3, top), dtype=torch.int32, device="cuda"),
