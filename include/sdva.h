@@ -549,7 +549,7 @@ typedef enum {
  * A token at -inf has log probability -inf and no part in the entropy.  A
  * row without a distribution (all -inf, or holding +inf or NaN) gets NaN in
  * logprobs, entropy and top_logprobs; its top_tokens still follow the order.
- * Sums are fp32.  num_rows >= 0 (0 enqueues nothing and returns SDVA_OK).
+ * Sums are fp32, in an order that the sizes alone fix.  num_rows >= 0 (0 enqueues nothing and returns SDVA_OK).
  * Returns SDVA_OK, SDVA_ERR_INVALID, SDVA_ERR_UNSUPPORTED or SDVA_ERR_CUDA.
  */
 int token_logprobs(const void* logits, int logits_dtype, int64_t row_stride, int num_rows, int vocab,
@@ -558,7 +558,8 @@ int token_logprobs(const void* logits, int logits_dtype, int64_t row_stride, int
 
 /*
  * sdva_debug_set_wait_limit -- diagnostic hook (no counterpart in the pages).
- * Every device-side wait of verify_attn's and prompt_attn's tensor-core kernels gives up after
+ * Every device-side wait of the tensor-core kernels of verify_attn and
+ * prompt_attn and of token_logprobs' kernel for long rows gives up after
  * `cycles` clock cycles (default about 4e9, two seconds); the CTA then
  * raises SDVA_STATUS_TIMEOUT, waits (with its own bound) for the copies and
  * tensor-core work it issued, frees its tensor memory and returns, leaving

@@ -136,8 +136,8 @@ _lib.sdva_status_string.argtypes = [_I]
 
 EXPORTED = ("kv_append_quant", "kv_append_quant_ragged", "verify_attn_workspace_size", "verify_attn",
             "verify_attn_tree", "verify_attn_ragged", "verify_step", "verify_attn_noalloc", "spec_accept", "spec_accept_lazy", "spec_accept_tree",
-            "spec_accept_sampled_workspace_size", "spec_accept_sampled", "kv_append_packed", "prompt_attn", "token_logprobs", "sdva_debug_set_wait_limit",
-            "sdva_status_string")
+            "spec_accept_sampled_workspace_size", "spec_accept_sampled", "kv_append_packed", "prompt_attn",
+            "token_logprobs", "sdva_debug_set_wait_limit", "sdva_status_string")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -451,7 +451,7 @@ def _rows(t: torch.Tensor, shape: tuple, device: int, name: str) -> int:
         if t.shape == shape and t.dtype is torch.bfloat16 and t.get_device() == device:
             raise ValueError(f"{name} must be contiguous inside a token row")
         _refuse(t, torch.bfloat16, shape, device, name)
-    return st[0] if shape[0] > 1 else max(st[0], shape[1] * HEAD_DIM)
+    return st[0] if shape[0] > 1 else shape[1] * HEAD_DIM  # of one row the stride means nothing
 
 
 def kv_append_packed(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, cu_tokens: torch.Tensor,
@@ -461,10 +461,12 @@ def kv_append_packed(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, c
     [B + 1]: lane b appends rows cu_tokens[b] .. cu_tokens[b + 1] - 1; page_table
     int32 [B][max_pages]; seq_lens int32 [B]."""
     dev = torch.cuda.current_device()
-    T, B = k_new.shape[0], seq_lens.shape[0]
+    if k_new.dim() != 3 or v_new.dim() != 3 or page_table.dim() != 2:
+        raise ValueError(f"k_new and v_new must be [T][Hkv][{HEAD_DIM}], page_table [B][max_pages]")
+    T, B = k_new.shape[0], seq_lens.numel()
     shape = (T, cache.num_kv_heads, HEAD_DIM)
     ks, vs = _rows(k_new, shape, dev, "k_new"), _rows(v_new, shape, dev, "v_new")
-    pages = page_table.shape[-1]
+    pages = page_table.shape[1]
     if cache.k_codes.get_device() != dev:
         raise ValueError(f"the cache is on {cache.k_codes.device}, the current device is cuda:{dev}")
     s = cache.struct()
@@ -484,11 +486,11 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_tokens: to
     dev = torch.cuda.current_device()
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError(f"q, k and v must be [T][H][{HEAD_DIM}]")
-    T, Hq, Hkv, B = q.shape[0], q.shape[1], k.shape[1], cu_tokens.shape[0] - 1
+    T, Hq, Hkv, B = q.shape[0], q.shape[1], k.shape[1], cu_tokens.numel() - 1
     kv = (T, Hkv, HEAD_DIM)
     qs, ks, vs = _rows(q, (T, Hq, HEAD_DIM), dev, "q"), _rows(k, kv, dev, "k"), _rows(v, kv, dev, "v")
     rc = _lib.prompt_attn(q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs, Hq, Hkv, T,
-                          _arg(cu_tokens, torch.int32, (B + 1,), dev, "cu_tokens"), B, sm_scale,
+                          _arg(cu_tokens, torch.int32, (B + 1,), dev, "cu_tokens"), B, float(sm_scale),
                           _arg(out, torch.bfloat16, (T, Hq, HEAD_DIM), dev, "out"),
                           _arg(lse, torch.float32, (T, Hq), dev, "lse"),
                           _dptr(status, torch.int32, "status"), _stream(stream))
@@ -510,16 +512,18 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: torch.T
     if kind is None or logits.get_device() != dev:
         raise ValueError(f"logits must be float32, bfloat16 or float16 on the current device, cuda:{dev}")
     shape = tuple(logits.shape)
+    if len(shape) < 2:
+        raise ValueError("logits must be [N][V] or contiguous [B][W][V]")
     lead, V = shape[:-1], shape[-1]
     if len(lead) == 1:
         st = logits.stride()
         if st[1] != 1 and V > 1:
             raise ValueError("logits must be contiguous inside a row")
-        stride = st[0] if lead[0] > 1 else max(st[0], V)
+        stride = st[0] if lead[0] > 1 else V
     elif logits.is_contiguous():
         stride = V
     else:
-        raise ValueError("logits must be [N][V] or contiguous")
+        raise ValueError("logits must be [N][V] or contiguous [B][W][V]")
     if (top_tokens is None) != (top_logprobs is None):
         raise ValueError("top_tokens and top_logprobs go together")
     top = 0 if top_tokens is None else top_tokens.shape[-1]

@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_packed_kernel(PackedArgs a
       const int t = (th >> 4) + i * (kThreads / 16);
       if (t < count) {
         uint8_t* const out = page_codes + (size_t)(start + t) * kHeadDim + sub * 8;
-          *reinterpret_cast<uint2*>(out) = e4m3x8(x[i][0], d);
+        *reinterpret_cast<uint2*>(out) = e4m3x8(x[i][0], d);
         *reinterpret_cast<uint2*>(out + 64) = e4m3x8(x[i][1], d);
       }
     }
@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_packed_kernel(PackedArgs a
         if (t < count) {
           const Divisor d(s);
           uint8_t* const out = codes + at * kHeadDim + sub * 8;
-            *reinterpret_cast<uint2*>(out) = e4m3x8(x[i][0], d);
+          *reinterpret_cast<uint2*>(out) = e4m3x8(x[i][0], d);
           *reinterpret_cast<uint2*>(out + 64) = e4m3x8(x[i][1], d);
           if (sub == 0) static_cast<float*>(scales)[at] = s;
         }
@@ -262,10 +262,10 @@ __global__ void __launch_bounds__(kThreads, 4) append_packed_kernel(PackedArgs a
         constexpr int kTop = kInt4 ? 7 : 127;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float wide = scale_of<kTop>(lanes_max<kInt4 ? 4 : 8>(m[h]));
+          const float wide = scale_of<kTop>(lanes_max<kInt4 ? 4 : 8>(m[h]));
           const __half s16 = __float2half_rn(fminf(wide, 65504.0f));
           if (t < count) {
-              uint32_t c[8], p[2] = {0u, 0u};
+            uint32_t c[8], p[2] = {0u, 0u};
             int_codes<kTop>(x[i][h], __half2float(s16), wide, c);
             if constexpr (kInt4) {
 #pragma unroll

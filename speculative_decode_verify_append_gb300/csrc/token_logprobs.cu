@@ -914,7 +914,7 @@ int launch(const LogprobArgs& a, int num_rows, cudaStream_t stream) {
       return SDVA_ERR_CUDA;
     // consecutive rows per unit of work: more than one only where units stay many for each SM
     const int unit = parts > 1 ? 1 : (int)std::min(8LL, std::max(1LL, num_rows / (32LL * sms)));
-    cfg.gridDim = dim3(parts > 1 ? (unsigned)num_rows * parts : (unsigned)((num_rows + unit - 1) / unit), 1, 1);
+    cfg.gridDim = dim3(parts > 1 ? (unsigned)num_rows * parts : ((unsigned)num_rows + unit - 1) / unit, 1, 1);
     cfg.blockDim = dim3(kLongThreads, 1, 1);
     cfg.dynamicSmemBytes = kLongSmem;
     cfg.numAttrs = parts > 1 ? 1 : 0;

@@ -66,7 +66,8 @@ def _attn_ref(q, k, v, lens, scale, start=0):
             o = p @ vv
             out[a:a + n], lse[a:a + n] = o.transpose(0, 1), z.transpose(0, 1)
             av = p @ vv.abs()
-            tol_o[a:a + n] = (2.0 ** -8 * o.abs() + (2.0 ** -8 + 4 * e[..., None] + 2.0 ** -18) * av * 1.01).transpose(0, 1)
+            near = (2.0 ** -8 + 4 * e[..., None] + 2.0 ** -18) * av * 1.01
+            tol_o[a:a + n] = (2.0 ** -8 * o.abs() + near).transpose(0, 1)
             tol_l[a:a + n] = (e + 2.0 ** -20 * (1 + z.abs())).transpose(0, 1)
         a += n
     return out, lse, tol_o, tol_l
@@ -102,8 +103,8 @@ def test_prompt_attn_lengths(lens, hq, hkv):
     _check_attn(q, k, v, lens)
 
 
-@pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 1), (5, 1), (7, 1), (12, 1), (16, 2), (24, 1), (32, 2), (48, 1), (64, 1),
-                                    (100, 1), (128, 1), (8, 8), (40, 8)])
+@pytest.mark.parametrize("hq,hkv", [(1, 1), (3, 1), (5, 1), (7, 1), (12, 1), (16, 2), (24, 1), (32, 2), (48, 1),
+                                    (64, 1), (100, 1), (128, 1), (8, 8), (40, 8)])
 def test_prompt_attn_head_layouts(hq, hkv):
     lens = [150, 3, 260]
     q, k, v = _qkv(_gen(hq), sum(lens), hq, hkv, fused=True)
@@ -402,7 +403,8 @@ def test_packed_append_every_significand(kind, exponent):
     table = np.arange(pages, dtype=np.int32)[None]
     gc, oc = sdva.KVCache(kind, pages, 1), oracle.Cache(kind, pages, 1)
     st = _status()
-    sdva.kv_append_packed(gc, bf16_dev(x), bf16_dev(x[:, :, ::-1]), _cu([n]), i32_dev(table), i32_dev(np.array([0])), st)
+    sdva.kv_append_packed(gc, bf16_dev(x), bf16_dev(x[:, :, ::-1]), _cu([n]), i32_dev(table), i32_dev(np.array([0])),
+                          st)
     assert oracle.append(oc, x[None], x[None, :, :, ::-1].copy(), table, np.array([0], np.int32)) == 0
     assert int(st.item()) == 0
     host = cache_to_host(gc)
@@ -684,7 +686,8 @@ def test_prompt_rows_agree_with_the_cache():
     out, _ = prompt.run(cache, q, k, v, _cu(lens), table, torch.zeros(2, dtype=torch.int32, device="cuda"))
     step = VerifyStep(2, W, hq, hkv, 512, None)
     last = torch.tensor([list(range(n - W, n)) for n in (500, 577)], device="cuda")
-    step.attend(cache, q[last].contiguous(), table, torch.tensor([n - W for n in lens], dtype=torch.int32, device="cuda"))
+    step.attend(cache, q[last].contiguous(), table,
+                torch.tensor([n - W for n in lens], dtype=torch.int32, device="cuda"))
     torch.cuda.synchronize()
     assert int(prompt.status.item()) == 0 and int(step.status.item()) == 0
     scale = float(SM_SCALE)
@@ -730,7 +733,8 @@ def test_refusals_of_the_binding():
             sdva.prompt_attn(q, k, v, cu, scale, out)
         assert e.value.code == sdva.ERR_INVALID
     with pytest.raises(sdva.SdvaError) as e:  # 129 q heads to a kv head
-        sdva.prompt_attn(*_qkv(_gen(1), 2, 129, 1), cu, 0.1, torch.empty((2, 129, D), dtype=torch.bfloat16, device="cuda"))
+        sdva.prompt_attn(*_qkv(_gen(1), 2, 129, 1), cu, 0.1,
+                         torch.empty((2, 129, D), dtype=torch.bfloat16, device="cuda"))
     assert e.value.code == sdva.ERR_UNSUPPORTED
     cache = sdva.KVCache(sdva.KV_FP8_E4M3, 2, 2)
     table, lens = i32_dev(np.array([[0, 1]])), i32_dev(np.array([0]))
@@ -769,3 +773,136 @@ def test_empty_calls_do_nothing():
     e = torch.empty(0, device="cuda")
     sdva.token_logprobs(torch.empty((0, 9), device="cuda"), torch.empty(0, dtype=torch.int32, device="cuda"), e, e)
     torch.cuda.synchronize()
+
+
+def test_shapes_with_the_wrong_number_of_axes_are_refused():
+    import speculative_decode_verify_append_gb300 as sdva
+    q, k, v = _qkv(_gen(1), 10, 4, 2)
+    cu, out = _cu([10]), torch.empty_like(q)
+    cache = sdva.KVCache(sdva.KV_INT4_G32, 1, 2)
+    table, lens = i32_dev(np.array([[0]])), i32_dev(np.array([0]))
+    for bad in (k.view(10, -1), k[None]):
+        with pytest.raises(ValueError):
+            sdva.kv_append_packed(cache, bad, v, cu, table, lens)
+        with pytest.raises(ValueError):
+            sdva.kv_append_packed(cache, k, bad, cu, table, lens)
+        with pytest.raises(ValueError):
+            sdva.prompt_attn(q, bad, v, cu, 0.1, out)
+    with pytest.raises(ValueError):
+        sdva.kv_append_packed(cache, k, v, cu, table[0], lens)
+    with pytest.raises(ValueError):
+        sdva.kv_append_packed(cache, k, v, cu, table, lens[0])
+    with pytest.raises(ValueError):
+        sdva.prompt_attn(q, k, v, cu[0], 0.1, out)
+    with pytest.raises(ValueError):
+        sdva.token_logprobs(torch.zeros(9, device="cuda"), lens, torch.empty(1, device="cuda"))
+
+
+def test_one_row_of_any_stride():
+    """One token has no row stride that means anything: slices whose stride is
+    odd, shorter than the row or 0 are as good as a tensor of their own."""
+    import speculative_decode_verify_append_gb300 as sdva
+    q, k, v = _qkv(_gen(2), 1, 4, 2)
+
+    def odd(x, stride):
+        return x.as_strided(x.shape, (stride, D, 1))
+
+    cu = _cu([1])
+    want, got = torch.empty_like(q), torch.empty_like(q)
+    sdva.prompt_attn(q, k, v, cu, np.float32(0.1), want)
+    sdva.prompt_attn(odd(q, 0), odd(k, 13), odd(v, 1001), cu, 0.1, got)
+    table, lens = i32_dev(np.array([[0]])), i32_dev(np.array([0]))
+    a, b = sdva.KVCache(sdva.KV_INT8_G64, 1, 2), sdva.KVCache(sdva.KV_INT8_G64, 1, 2)
+    sdva.kv_append_packed(a, k, v, cu, table, lens)
+    sdva.kv_append_packed(b, odd(k, 13), odd(v, 0), cu, table, lens)
+    torch.cuda.synchronize()
+    assert torch.equal(want, got)
+    assert torch.equal(a.k_codes, b.k_codes) and torch.equal(a.v_codes, b.v_codes)
+    x = torch.randn((1, 40), device="cuda")
+    lp = [torch.empty(1, device="cuda") for _ in range(2)]
+    sdva.token_logprobs(x, lens, lp[0])
+    sdva.token_logprobs(x.as_strided((1, 40), (0, 1)), lens, lp[1])
+    torch.cuda.synchronize()
+    assert torch.equal(*lp)
+
+
+def test_calls_at_once_on_several_streams():
+    """Kernels of several calls, each on its own stream, share the GPU: what
+    they write is what they write one after the other."""
+    import speculative_decode_verify_append_gb300 as sdva
+    g = _gen(12)
+    lens = [900, 64, 2000, 1]
+    q, k, v = _qkv(g, sum(lens), 24, 4)
+    cu = _cu(lens)
+    pages = [n // 64 + 1 for n in lens]
+    table = torch.full((4, max(pages)), -1, dtype=torch.int32, device="cuda")
+    for b in range(4):
+        table[b, :pages[b]] = torch.arange(pages[b], dtype=torch.int32, device="cuda") + sum(pages[:b])
+    start = torch.zeros(4, dtype=torch.int32, device="cuda")
+    long, short = _logits(g, 200, 50000, torch.bfloat16), _logits(g, 300, 9000, torch.float32)
+    tokens = torch.randint(9000, (300,), generator=g, device="cuda", dtype=torch.int32)
+    status = _status()
+
+    def calls(streams):
+        results = []
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                if i % 4 == 0:
+                    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], device="cuda")
+                    sdva.prompt_attn(q, k, v, cu, float(SM_SCALE), out, lse, status)
+                    results += [out, lse]
+                elif i % 4 == 1:
+                    cache = sdva.KVCache(sdva.KV_FP8_E4M3, sum(pages), 4)
+                    sdva.kv_append_packed(cache, k, v, cu, table, start, status)
+                    results += [cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales]
+                else:
+                    x = long if i % 4 == 2 else short
+                    n = x.shape[0]
+                    lp, en = torch.zeros(n, device="cuda"), torch.zeros(n, device="cuda")
+                    tt, tl = torch.zeros((n, 9), dtype=torch.int32, device="cuda"), torch.zeros((n, 9), device="cuda")
+                    sdva.token_logprobs(x, tokens[:n], lp, en, tt, tl, status)
+                    results += [lp, en, tt, tl]
+        torch.cuda.synchronize()
+        return results
+
+    one = calls([torch.cuda.current_stream()] * 8)
+    streams = [torch.cuda.Stream() for _ in range(8)]
+    for _ in range(3):
+        for a, b in zip(one, calls(streams)):
+            assert torch.equal(a, b)
+    assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("what", ["prompt_attn", "rows", "few_rows"])
+def test_wait_that_runs_out_is_reported_and_recovered(what):
+    """With a limit of zero cycles a wait that is not over when its sleep ends
+    (some 200 us) gives up; the sizes have one warp wait through more of
+    another's work than that.  The call reports it and returns, and the next
+    one is right."""
+    import speculative_decode_verify_append_gb300 as sdva
+    g = _gen(13)
+    if what == "prompt_attn":
+        q, k, v = _qkv(g, 80000, 2, 1)
+
+        def run(st):
+            return _run_attn(q, k, v, _cu([80000]), status=st)
+    else:
+        n, V = (160, 3000000) if what == "rows" else (3, 30000000)
+        x = torch.randn((n, V), generator=g, device="cuda")
+        tokens = torch.zeros(n, dtype=torch.int32, device="cuda")
+
+        def run(st):
+            return _score(x, tokens, 4, st)
+    want = run(None)
+    st = _status()
+    prev = sdva.sdva_debug_set_wait_limit(0)
+    try:
+        run(st)
+    finally:
+        sdva.sdva_debug_set_wait_limit(prev)
+    assert int(st.item()) == sdva.STATUS_TIMEOUT
+    for _ in range(2):
+        st = _status()
+        got = run(st)
+        assert int(st.item()) == 0
+        assert all(torch.equal(a, b) for a, b in zip(got, want))
