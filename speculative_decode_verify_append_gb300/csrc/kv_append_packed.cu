@@ -139,22 +139,26 @@ __device__ __forceinline__ void int_codes(uint4 w, float s, float wide, uint32_t
 template <int KVT>
 __global__ void __launch_bounds__(kThreads, 4) append_packed_kernel(PackedArgs a) {
   const int slot = blockIdx.x, hk = blockIdx.y, th = threadIdx.x;
-  // the slot's lane: the last whose base is at or before it
-  int below = 0, bad = 0;
-  for (int b0 = 0; b0 < a.num_lanes; b0 += kThreads) {
-    const int b = b0 + th;
-    bool at = false;
-    if (b < a.num_lanes) {
-      const int lo = a.cu[b], hi = a.cu[b + 1];
-      bad |= lo < 0 || hi < lo || hi > a.total;
-      at = slot_base(lo, b) <= slot;
-    }
-    below += __syncthreads_count(at);
+  // the slot's lane, the last whose base is at or before it, and whether all offsets are in order
+  __shared__ uint32_t s_found[kThreads / 32];
+  constexpr uint32_t kBad = 1u << 20;  // above every count: the host refuses more lanes than 65,535
+  uint32_t found = 0, bad = 0;
+  for (int b = th; b < a.num_lanes; b += kThreads) {
+    const int lo = a.cu[b], hi = a.cu[b + 1];
+    bad |= lo < 0 || hi < lo || hi > a.total;
+    found += slot_base(lo, b) <= slot;
   }
-  if (__syncthreads_or(bad)) {
+  found = __reduce_add_sync(0xffffffffu, found + (bad ? kBad : 0u));
+  if ((th & 31) == 0) s_found[th >> 5] = found;
+  __syncthreads();
+  found = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) found += s_found[w];
+  if (found >= kBad) {
     if (slot == 0 && hk == 0 && th == 0) raise_status(a.status, SDVA_STATUS_BAD_COUNT);
     return;
   }
+  const int below = (int)found;
   if (below == 0) return;
   const int b = below - 1, row0 = a.cu[b], n = a.cu[b + 1] - row0, page = slot - slot_base(row0, b);
   if (n == 0) return;  // nothing to write: the lane is not examined
@@ -244,6 +248,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_packed_kernel(PackedArgs a
   } else {
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
+      if (i * (kThreads / 16) >= count) break;
       const int t = (th >> 4) + i * (kThreads / 16);
       const size_t at = ph * kPage + start + t;  // (page, kv head, token) row
       float m[2] = {amax8(x[i][0]), amax8(x[i][1])};
