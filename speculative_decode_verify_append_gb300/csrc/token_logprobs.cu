@@ -67,6 +67,7 @@ struct Elem<float> {
   static constexpr int kVec = 4, kUnroll = 4;  // elements per vector; vectors per thread and round
   static constexpr uint32_t kNone = 0xff800000u;  // -inf
   static __device__ float one(float x) { return x; }
+  static __device__ uint32_t word(float x) { return __float_as_uint(x); }
   static __device__ void unpack(uint4 w, float* f) {
     f[0] = __uint_as_float(w.x), f[1] = __uint_as_float(w.y), f[2] = __uint_as_float(w.z), f[3] = __uint_as_float(w.w);
   }
@@ -79,6 +80,7 @@ struct Elem<__nv_bfloat16> {
   static constexpr int kVec = 8, kUnroll = 4;
   static constexpr uint32_t kNone = 0xff80ff80u;
   static __device__ float one(__nv_bfloat16 x) { return __bfloat162float(x); }
+  static __device__ uint32_t word(__nv_bfloat16 x) { return (kNone & 0xffff0000u) | __bfloat16_as_ushort(x); }
   static __device__ void unpack(uint4 w, float* f) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -95,6 +97,7 @@ struct Elem<__half> {
   static constexpr int kVec = 8, kUnroll = 4;
   static constexpr uint32_t kNone = 0xfc00fc00u;
   static __device__ float one(__half x) { return __half2float(x); }
+  static __device__ uint32_t word(__half x) { return (kNone & 0xffff0000u) | __half_as_ushort(x); }
   static __device__ void unpack(uint4 w, float* f) {
     const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -200,26 +203,42 @@ struct Part {
   __device__ int extra_index(int e) const { return e < head ? e : tail0 + e - head; }
 };
 
-// 16 logits with maximum m into the thread's statistics; `top` is the
-// thread's maximum.
-__device__ __forceinline__ void add16(Stat& a, float& top, float m, const float (&x)[16]) {
+// 16 logits (w) into the thread's statistics; `top` is the thread's maximum.
+// Returns theirs.  0 * -inf, of a forbidden token, would make T a NaN: either y
+// is kept above kNothing, two instructions more for two logits, or the sum is
+// done again where it came out a NaN (of 4,096 bf16 rows of 151,936 the first
+// takes 207 us whatever they hold, the second 199 and, where nine tokens in ten
+// are forbidden, 282).
+template <typename T, bool kAbove>
+__device__ __forceinline__ float add16(Stat& a, float& top, const uint4 (&w)[16 / Elem<T>::kVec]) {
+  constexpr int kVec = Elem<T>::kVec, kPer = 16 / kVec;
+  float m = __int_as_float(0xff800000);
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) m = fmaxf(m, Elem<T>::largest(w[k]));
   if (m > top) {
     top = m;
     a = moved(a, m);
   }
+  float x[16];
+#pragma unroll
+  for (int k = 0; k < kPer; ++k) Elem<T>::unpack(w[k], x + k * kVec);
   const unsigned long long c2 = f2_pack(kLog2e, kLog2e), r2 = f2_pack(-a.m, -a.m);
   unsigned long long s[2] = {0ull, 0ull}, t[2] = {0ull, 0ull};
 #pragma unroll
   for (int j = 0; j < 16; j += 2) {
-    const unsigned long long y2 = fmul2(fadd2(f2_pack(x[j], x[j + 1]), r2), c2);
-    const float2 y = f2_unpack(y2);
+    unsigned long long y2 = fmul2(fadd2(f2_pack(x[j], x[j + 1]), r2), c2);
+    float2 y = f2_unpack(y2);
+    if (kAbove) {
+      y.x = max_nan(y.x, kNothing), y.y = max_nan(y.y, kNothing);
+      y2 = f2_pack(y.x, y.y);
+    }
     const unsigned long long e = f2_pack(fast_exp2(y.x), fast_exp2(y.y));
     s[(j >> 1) & 1] = fadd2(s[(j >> 1) & 1], e);
     t[(j >> 1) & 1] = ffma2(e, y2, t[(j >> 1) & 1]);
   }
   const float2 sum = f2_unpack(fadd2(s[0], s[1])), dot = f2_unpack(fadd2(t[0], t[1]));
   float d = dot.x + dot.y;
-  if (d != d) {  // 0 * -inf: forbidden tokens have no part
+  if (!kAbove && d != d) {
     d = 0.0f;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
@@ -229,6 +248,17 @@ __device__ __forceinline__ void add16(Stat& a, float& top, float m, const float 
   }
   a.s += sum.x + sum.y;
   a.t += d;
+  return m;
+}
+// one logit
+template <typename T>
+__device__ __forceinline__ void add1(Stat& a, float& top, T x) {
+  constexpr uint32_t none = Elem<T>::kNone;
+  uint4 w[16 / Elem<T>::kVec];
+#pragma unroll
+  for (int k = 0; k < 16 / Elem<T>::kVec; ++k) w[k] = make_uint4(none, none, none, none);
+  w[0].x = Elem<T>::word(x);
+  add16<T, true>(a, top, w);
 }
 
 // The statistics of n lanes' sets (a power of two), in every lane of them.
@@ -274,9 +304,11 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int row, float x
 }
 
 // Short rows: 128 threads, a thread's rounds of loads in registers.
+constexpr int kShortThreads = 128;
+constexpr int kShortVecs = 32 * kShortThreads;  // fewer vectors to a row: a warp reads a thread's at once
 template <typename T>
 __global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, int parts) {
-  constexpr int kThreads = 128;
+  constexpr int kThreads = kShortThreads;
   constexpr int kVec = Elem<T>::kVec, kPer = 16 / kVec, kUnroll = Elem<T>::kUnroll, kWarps = kThreads / 32;
   __shared__ Stat s_stat[kWarps];
   __shared__ float4 s_group4[kGroups / 4];  // read four at a time
@@ -314,15 +346,6 @@ __global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, i
   Stat st = {0.0f, 0.0f, 0.0f};
   float top = ninf;
   // rounds of whole vectors, the next one's loads in flight
-  auto add = [&](const uint4 (&w)[kPer]) {
-    float x[16], m = ninf;
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) {
-      Elem<T>::unpack(w[k], x + k * kVec);
-      m = fmaxf(m, Elem<T>::largest(w[k]));
-    }
-    add16(st, top, m, x);
-  };
   constexpr int kRound = kUnroll * kThreads;
   int v = th;
   if (v + (kUnroll - 1) * kThreads < p.vectors) {
@@ -343,7 +366,7 @@ __global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, i
         uint4 g[kPer];
 #pragma unroll
         for (int k = 0; k < kPer; ++k) g[k] = w[u + k];
-        add(g);
+        add16<T, true>(st, top, g);
       }
     } while (v + (kUnroll - 1) * kThreads < p.vectors);
   }
@@ -359,16 +382,10 @@ __global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, i
       uint4 g[kPer];
 #pragma unroll
       for (int k = 0; k < kPer; ++k) g[k] = w[u + k];
-      if (v + u * kThreads < p.vectors) add(g);
+      if (v + u * kThreads < p.vectors) add16<T, true>(st, top, g);
     }
   }
-  if (th < p.extra) {
-    float x[16];
-    x[0] = Elem<T>::one(p.x[p.extra_index(th)]);
-#pragma unroll
-    for (int j = 1; j < 16; ++j) x[j] = ninf;
-    add16(st, top, x[0], x);
-  }
+  if (th < p.extra) add1(st, top, p.x[p.extra_index(th)]);
 
   const Stat ws = warp_join<32>(st);
   if (lane == 0) s_stat[warp] = ws;
@@ -417,21 +434,26 @@ __global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, i
           if (at < kCandidates) s_keys[at] = key_of(x, i);
         }
       };
+      if (th < p.extra && top >= bound) offer(Elem<T>::one(p.x[p.extra_index(th)]), p.extra_index(th));
+      // the vectors of the threads that reach it, one a lane, of four threads at a time
       unsigned hot = __ballot_sync(0xffffffffu, top >= bound);
       while (hot != 0 && __all_sync(0xffffffffu, s_count <= kCandidates)) {  // a count beyond the place ends the search
-        const int who = warp * 32 + __ffs(hot) - 1;
-        hot &= hot - 1;
-#pragma unroll 3
-        for (int v = who + lane * kThreads; v < p.vectors; v += 32 * kThreads) {
-          const uint4 w = p.load(v);
-          if (Elem<T>::largest(w) >= bound) {
-            float x[kVec];
-            Elem<T>::unpack(w, x);
+        uint4 w[4];
+        int v[4];
 #pragma unroll
-            for (int j = 0; j < kVec; ++j) offer(x[j], p.first + v * kVec + j);
-          }
+        for (int u = 0; u < 4; ++u) {
+          v[u] = hot != 0 ? warp * 32 + __ffs(hot) - 1 + lane * kThreads : p.vectors;
+          hot &= hot - 1;
+          w[u] = v[u] < p.vectors ? p.load(v[u]) : make_uint4(0u, 0u, 0u, 0u);
         }
-        if (lane == 0 && who < p.extra) offer(Elem<T>::one(p.x[p.extra_index(who)]), p.extra_index(who));
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+          if (v[u] < p.vectors && Elem<T>::largest(w[u]) >= bound) {
+            float x[kVec];
+            Elem<T>::unpack(w[u], x);
+#pragma unroll
+            for (int j = 0; j < kVec; ++j) offer(x[j], p.first + v[u] * kVec + j);
+          }
         __syncwarp();
       }
       __syncthreads();
@@ -489,6 +511,7 @@ constexpr int kStages = 6, kStageVecs = 4 * kStreamThreads;  // 16-byte vectors 
 constexpr uint32_t kStageBytes = kStageVecs * 16;
 constexpr int kRowRing = 4;
 constexpr int kTeamWarps = kTeamThreads / 32, kStreamWarps = kStreamThreads / 32;
+static_assert(kShortVecs == 4 * kStageVecs, "rows of fewer than four stages are short");
 static_assert(kGroups == kTeamThreads && kStreamThreads == 2 * kGroups,
               "a group is a team thread's two stream threads");
 
@@ -529,6 +552,8 @@ template <typename T, bool kCluster>
 __global__ void __launch_bounds__(kLongThreads, 2)
     long_logprobs_kernel(LogprobArgs a, int num_rows, int unit, int parts, long long limit) {
   constexpr int kVec = Elem<T>::kVec, kPer = 16 / kVec;
+  // many rows of 16-bit logits (a prompt's, where nothing is forbidden) are bound by the work per element
+  constexpr bool kAbove = kCluster || sizeof(T) == 4;
   extern __shared__ __align__(16) uint8_t smem[];
   LongCtl* const ctl = reinterpret_cast<LongCtl*>(smem + kStages * kStageBytes);
   const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31, th = threadIdx.x;
@@ -658,8 +683,8 @@ __global__ void __launch_bounds__(kLongThreads, 2)
       const int row = ctl->row[slot];
       if (row < 0) break;
       const Part<T> p = part_of(row);
-      float x0 = ninf;
-      if (th < p.extra) x0 = Elem<T>::one(p.x[p.extra_index(th)]);
+      T x0;
+      if (th < p.extra) x0 = p.x[p.extra_index(th)];
       Stat sum = {0.0f, 0.0f, 0.0f};
       float top = ninf, best = ninf, second = ninf;
       int at_best = 0;
@@ -682,14 +707,10 @@ __global__ void __launch_bounds__(kLongThreads, 2)
         }
 #pragma unroll
         for (int u = 0; u < 4; u += kPer) {
-          float x[16], m = ninf;
+          uint4 g[kPer];
 #pragma unroll
-          for (int k = 0; k < kPer; ++k) {
-            Elem<T>::unpack(w[u + k], x + k * kVec);
-            m = fmaxf(m, Elem<T>::largest(w[u + k]));
-          }
-          here = fmaxf(here, m);
-          add16(sum, top, m, x);
+          for (int k = 0; k < kPer; ++k) g[k] = w[u + k];
+          here = fmaxf(here, add16<T, kAbove>(sum, top, g));
         }
         second = fmaxf(second, fminf(best, here));
         if (here > best) {
@@ -698,13 +719,7 @@ __global__ void __launch_bounds__(kLongThreads, 2)
         }
       }
       if (!ok) break;
-      if (th < p.extra) {
-        float x[16];
-        x[0] = x0;
-#pragma unroll
-        for (int j = 1; j < 16; ++j) x[j] = ninf;
-        add16(sum, top, x0, x);
-      }
+      if (th < p.extra) add1(sum, top, x0);
       const uint32_t d = r & 1u;
       if (r >= 2 && !(ok = wait(ctl->sums_free[d], r / 2 - 1))) break;
       const Stat joined = warp_join<32>(sum);
@@ -888,7 +903,7 @@ int launch(const LogprobArgs& a, int num_rows, cudaStream_t stream) {
   // Rows of fewer than four stages go to the small blocks: the team's time on
   // a row is that of about as many (4,000 rows of 10,000 fp32 47 us in small
   // blocks, 56 streamed; 2,000 of 30,000 bf16 38 and 40).
-  const bool is_short = a.vocab < 4 * kStageVecs * kVec;
+  const bool is_short = a.vocab < kShortVecs * kVec;
   // CTAs per row: while every SM would not have one, and each has two rounds of loads
   const long long round = is_short ? 128LL * Elem<T>::kUnroll * kVec : (long long)kStageVecs * kVec;
   const long long wanted = is_short ? 2LL * sms : sms;
