@@ -5,8 +5,8 @@
 // the lane's rows j <= t, out = sum_j exp(s_j - lse) v_j, lse = log sum exp s_j,
 // in one pass over the keys with the running maximum and sum.
 //
-// A tile is 2 x T consecutive rows of one kv head, T = 128 / G: each of its
-// two halves fills the 128 rows of a tensor-core tile with T tokens x G q
+// A tile is 2 x T consecutive rows of one kv head, T = 128 / G (T rows where
+// there are few): each of its two halves fills the 128 rows of a tensor-core tile with T tokens x G q
 // heads (row r = token r / G, head r % G), so that a group's heads share the
 // K/V tiles and few rows are empty whatever the group.  Twelve warps:
 //   * warp 8 (loader): takes the next tile, TMA-loads its Q and the K and V
@@ -32,6 +32,11 @@
 //     before it (one issuer, in order), so the thread may rescale its O in
 //     place when the reference moves.  At the end it divides by the sum and
 //     stores.
+// Bound by the tensor cores from some thousand tokens on (16,384 tokens of 24 /
+// 4 heads 985 us, 1,680 TFLOP/s of 1,865 that a library product reaches; 8,192
+// 236 us, 1,750), below by the chain of blocks of the longest tile, a few
+// hundred cycles each for the products, the scores' way to the softmax and the
+// weights' way back.
 // Every wait is bounded: on timeout the CTA raises SDVA_STATUS_TIMEOUT,
 // drains its copies and products, frees tensor memory and returns.
 #include <math.h>
@@ -80,7 +85,7 @@ struct PromptArgs {
   uint16_t* out;
   float* lse;
   int32_t* status;
-  int Hq, Hkv, G, T, total, num_lanes;
+  int Hq, Hkv, G, T, span, total, num_lanes;
   float scale, scale_log2;
   long long wait_limit;
 };
@@ -110,10 +115,10 @@ __device__ __forceinline__ int blocks_to(int end) { return (end + kBlock - 1) / 
 
 struct Shape {
   int end, n[2], total;  // the tile's last row + 1; blocks of each half; blocks loaded
-  __device__ Shape(const Tile& t, int T) {
-    end = (int)min((long long)t.t0 + 2 * T, (long long)t.len);
+  __device__ Shape(const Tile& t, int T, int span) {
+    end = (int)min((long long)t.t0 + span, (long long)t.len);
     n[0] = blocks_to(min(t.t0 + T, t.len));
-    n[1] = t.len - t.t0 > T ? blocks_to(end) : 0;
+    n[1] = end - t.t0 > T ? blocks_to(end) : 0;
     total = max(n[0], n[1]);
   }
 };
@@ -239,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   Order order;  // the loader's; safe to set up from offsets that turn out bad
   if (warp == kLoaderWarp) {
     if (lane < 3) prefetch_tmap(lane == 0 ? &mq : lane == 1 ? &mk : &mv);
-    order.init(a.cu, a.num_lanes, 2 * a.T, lane);
+    order.init(a.cu, a.num_lanes, a.span, lane);
   } else if (warp == kGuardWarp) {
     tmem_alloc(smem_u32(&ctl->tmem_base), kTmemCols);
   } else if (threadIdx.x == kIssueWarp * 32) {
@@ -321,7 +326,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!order.find(r / (uint32_t)a.Hkv, &b, &pos)) return false;
         t.row0 = a.cu[b];
         t.len = a.cu[b + 1] - t.row0;
-        t.t0 = pos * 2 * a.T;
+        t.t0 = pos * a.span;
         return true;
       };
       uint32_t asks = 0, answers = 0;
@@ -340,7 +345,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
         if (!more) break;
-        const Shape sh(t, a.T);
+        const Shape sh(t, a.T, a.span);
         const int halves = sh.n[1] ? 2 : 1;
         if (lane < 4 && (lane >> 1) < halves)  // Q waits for its place: into L2 meanwhile
           tma_prefetch_3d(&mq, 64 * (lane & 1), t.hk * a.G, t.row0 + t.t0 + (lane >> 1) * a.T);
@@ -439,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait(ctl->tile_full[slot], (uint32_t)((i / 2) & 1)))) break;
         const Tile t = ctl->tile[slot];
         if (t.len == 0) break;
-        const Shape sh(t, a.T);
+        const Shape sh(t, a.T, a.span);
         const int n = __shfl_sync(0xffffffffu, sh.n[s], 0), total = __shfl_sync(0xffffffffu, sh.total, 0);
         if (n > 0 && !(ok = wait(ctl->q_full[s], q_phase.take()) && wait(ctl->full[ring.st], ring.phase))) break;
         if (!(ok = take_turn())) break;
@@ -506,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!(ok = wait(ctl->tile_full[slot], (uint32_t)((i / 2) & 1)))) break;
         const Tile t = ctl->tile[slot];
         if (t.len == 0) break;
-        const Shape sh(t, a.T);
+        const Shape sh(t, a.T, a.span);
         for (int j = guard_from(t); j < sh.total; ++j, ++guard0) {
           const long long f = stage0 + 2 * j + 1;
           if (!(ok = wait(ctl->guard[guard0 % kGuardRing], (uint32_t)((guard0 / kGuardRing) & 1)))) break;
@@ -559,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait(ctl->tile_full[slot], (uint32_t)((i / 2) & 1)))) break;
       const Tile t = ctl->tile[slot];
       if (t.len == 0) break;
-      const Shape sh(t, a.T);
+      const Shape sh(t, a.T, a.span);
       const int n = sh.n[s], first = t.t0 + s * a.T;
       const int tok = first + r_tok;
       const bool valid = r_tok < a.T && tok < t.len;
@@ -766,8 +771,19 @@ extern "C" int prompt_attn(const void* q, const void* k, const void* v, int64_t 
   if (cudaFuncSetAttribute(prompt_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
       cudaSuccess)
     return SDVA_ERR_CUDA;
-  // at most this many tiles: one per 2 T rows and a ragged one per lane
-  const long long tiles = ((long long)total_tokens / (2 * a.T) + num_lanes) * num_kv_heads;
+  // At most this many tiles: one per span of rows and a ragged one per lane.
+  // Where tiles of one half leave the GPU not much over one each, the shorter
+  // chain of one half wins over the work that two halves share (40 tokens of
+  // 24 / 4 heads 7.6 against 9.7 us, 512 11.4 / 12.8, 1,024 16.5 / 18.1, 2,048
+  // of 8 / 8 24.1 / 25.7; from 272 half tiles on 152 SMs two halves win: 1,024
+  // of 32 / 8 17.8 / 18.4, 2,048 of 24 / 4 27.0 / 37.6).
+  int dev = 0, sms = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return SDVA_ERR_CUDA;
+  auto tiles_of = [&](int span) { return ((long long)total_tokens / span + num_lanes) * num_kv_heads; };
+  a.span = 3 * tiles_of(2 * a.T) <= 2 * sms ? a.T : 2 * a.T;
+  const long long tiles = tiles_of(a.span);
   if (tiles > 0x7fffffffLL) return SDVA_ERR_UNSUPPORTED;  // more rows of K and V than memory holds
   prompt_attn_kernel<<<(unsigned)tiles, kThreads, kSmemBytes,
                        reinterpret_cast<cudaStream_t>(stream)>>>(mq, mk, mv, a);
