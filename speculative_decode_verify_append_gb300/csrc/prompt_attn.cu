@@ -33,8 +33,9 @@
 //     place when the reference moves.  At the end it divides by the sum and
 //     stores.
 // Bound by the tensor cores from some thousand tokens on (16,384 tokens of 24 /
-// 4 heads 985 us, 1,680 TFLOP/s of 1,865 that a library product reaches; 8,192
-// 236 us, 1,750), below by the chain of blocks of the longest tile, a few
+// 4 heads 890 to 980 us with the clock that power leaves, 1,680 to 1,850 TFLOP/s,
+// where a library product reaches 1,690 sustained and 1,865 in a burst; 8,192
+// 229 us, 1,800), below by the chain of blocks of the longest tile, a few
 // hundred cycles each for the products, the scores' way to the softmax and the
 // weights' way back.
 // Every wait is bounded: on timeout the CTA raises SDVA_STATUS_TIMEOUT,
@@ -229,6 +230,25 @@ __device__ __forceinline__ void tma_prefetch_3d(const CUtensorMap* map, int x, i
 __device__ __forceinline__ uint32_t nonfinite_bits(uint4 w) {
   return ((w.x & 0x7F807F80u) + 0x00800080u) | ((w.y & 0x7F807F80u) + 0x00800080u) |
          ((w.z & 0x7F807F80u) + 0x00800080u) | ((w.w & 0x7F807F80u) + 0x00800080u);
+}
+
+// Lane q of four holds the 16-byte units 0 .. 3 of its row q and gets unit q of the four rows.
+__device__ __forceinline__ uint4 shfl_xor4(uint4 v, int m) {
+  return make_uint4(__shfl_xor_sync(0xffffffffu, v.x, m), __shfl_xor_sync(0xffffffffu, v.y, m),
+                    __shfl_xor_sync(0xffffffffu, v.z, m), __shfl_xor_sync(0xffffffffu, v.w, m));
+}
+__device__ __forceinline__ void quad_transpose(uint4 (&u)[4]) {
+#pragma unroll
+  for (int m = 1; m <= 2; m *= 2) {
+    const bool high = threadIdx.x & m;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (!(k & m)) {
+        const uint4 got = shfl_xor4(high ? u[k] : u[k + m], m);
+        if (high) u[k] = got;
+        else u[k + m] = got;
+      }
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -579,10 +599,13 @@ __global__ void __launch_bounds__(kThreads, 1)
         if ((j + 1) * kBlock > first + w_tok + 1) {  // some row of the warp does not see the whole block
           const int seen = tok - j * kBlock + 1;
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 4; ++c) {
+            const int left = min(max(seen - 32 * c, 0), 32);
+            const uint32_t hidden = left == 32 ? 0u : 0xffffffffu << left;
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              if (32 * c + k >= seen) x[c][k] = 0xff800000u;
+              if (hidden & (1u << k)) x[c][k] = 0xff800000u;
+          }
         }
         // The weights of the first 64 keys are taken about the reference that
         // the row has, beside this block's maximum (64 three-way maxima are a
@@ -661,17 +684,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!(ok = wait(ctl->o_full[s], o_phase.take()))) break;
       fence_after_sync();
       const float inv = 1.0f / l;
+      // where this lane's four rows of the tile lie behind its first (-1: nowhere)
+      const int own_at = valid ? r_tok * a.Hq + r_head : -1;
+      int at4[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) at4[k] = __shfl_sync(0xffffffffu, own_at, (lane & ~3) + k);
+      uint16_t* const tile_out = a.out + ((size_t)(t.row0 + first) * a.Hq + (size_t)t.hk * a.G) * kHeadDim;
       const size_t at = (size_t)(t.row0 + tok) * a.Hq + (size_t)t.hk * a.G + r_head;
+      uint32_t all[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tmem_ld32(t_o + 32 * c, all[c]);
+      tmem_wait_ld();
+      fence_before_sync();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&ctl->o_free[s]));
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        tmem_ld32(t_o + 32 * c, o);
-        tmem_wait_ld();
-        if (c == 3) {
-          fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ctl->o_free[s]));
-        }
+        uint32_t(&o)[32] = all[c];
 #pragma unroll
         for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * inv);
         if (dirty && valid) {
@@ -686,15 +715,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (valid) {
-          uint4* dst = reinterpret_cast<uint4*>(a.out + at * kHeadDim + 32 * c);
+        // A row's 64 bytes go out by four lanes: of its own row a lane would
+        // write 16 bytes into a line of its own each time, 32 lines to a store,
+        // and every shared-memory access of the SM queues behind them (228
+        // prompts of 42 rows, 24 / 4 heads, 45.5 against 36.4 us; three of 4,096
+        // with 32 / 8 heads 254 against 243).
+        uint4 u[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            dst[k] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * k]), __uint_as_float(o[8 * k + 1])),
-                                pack_bf16x2(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3])),
-                                pack_bf16x2(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5])),
-                                pack_bf16x2(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7])));
-        }
+        for (int k = 0; k < 4; ++k)
+          u[k] = make_uint4(pack_bf16x2(__uint_as_float(o[8 * k]), __uint_as_float(o[8 * k + 1])),
+                            pack_bf16x2(__uint_as_float(o[8 * k + 2]), __uint_as_float(o[8 * k + 3])),
+                            pack_bf16x2(__uint_as_float(o[8 * k + 4]), __uint_as_float(o[8 * k + 5])),
+                            pack_bf16x2(__uint_as_float(o[8 * k + 6]), __uint_as_float(o[8 * k + 7])));
+        quad_transpose(u);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          if (at4[k] >= 0) *reinterpret_cast<uint4*>(tile_out + at4[k] * kHeadDim + 32 * c + 8 * (lane & 3)) = u[k];
       }
       if (valid && a.lse != nullptr) a.lse[at] = m * a.scale + logf(l);
     }
