@@ -209,6 +209,22 @@ def test_prompt_attn_outlier_channels(lens):
     _check_attn(q, k, v, lens)
 
 
+@pytest.mark.parametrize("hq,hkv", [(24, 4), (8, 8), (16, 1)])
+def test_prompt_attn_rows_keep_their_bits(hq, hkv):
+    """A row's bits depend on its lane's rows up to it alone: not on the rows
+    behind them, nor on the other lanes.  Of one key the output is its value."""
+    q, k, v = _qkv(_gen(21), 1000, hq, hkv)
+    out, lse = _run_attn(q, k, v, _cu([1000]))
+    assert torch.equal(out[0], v[0].repeat_interleave(hq // hkv, 0))
+    for n in (1, 5, 127, 128, 129, 300, 999):
+        o, z = _run_attn(q[:n], k[:n], v[:n], _cu([n]))
+        assert torch.equal(o, out[:n]) and torch.equal(z, lse[:n]), n
+    junk = torch.randn_like(q[:700])
+    kv = torch.randn_like(k[:700])
+    o, z = _run_attn(torch.cat([junk, q]), torch.cat([kv, k]), torch.cat([kv, v]), _cu([1, 400, 299, 1000]))
+    assert torch.equal(o[700:], out) and torch.equal(z[700:], lse)
+
+
 def test_prompt_attn_opposite_infinities():
     q, k, v = _qkv(_gen(7), 100, 2, 1)
     v[40, 0, 3], v[45, 0, 3] = INF, -INF
