@@ -303,10 +303,13 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int row, float x
   }
 }
 
-// Short rows: 128 threads, a thread's rounds of loads in registers.
+// Short rows: 128 threads, a thread's rounds of loads in registers.  A row in
+// one block has nothing of a cluster: its barriers and launch take a
+// microsecond (333 fp16 rows of 32,003 14.0 against 13.0 us, 8,192 fp32 rows of
+// 5,000 59.6 against 52.0).
 constexpr int kShortThreads = 128;
 constexpr int kShortVecs = 32 * kShortThreads;  // fewer vectors to a row: a warp reads a thread's at once
-template <typename T>
+template <typename T, bool kCluster>
 __global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, int parts) {
   constexpr int kThreads = kShortThreads;
   constexpr int kVec = Elem<T>::kVec, kPer = 16 / kVec, kUnroll = Elem<T>::kUnroll, kWarps = kThreads / 32;
@@ -315,11 +318,12 @@ __global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, i
   __shared__ Key s_keys[kCandidates];  // candidates, or the warps' lists
   __shared__ uint32_t s_bound;
   __shared__ int s_count, s_odd;
-  __shared__ Stat c_stat[kMaxCluster];  // in CTA 0: one entry per CTA of the cluster
-  __shared__ Key c_keys[kMaxCluster][32];
+  constexpr int kLists = kCluster ? kMaxCluster : 1;
+  __shared__ Stat c_stat[kLists];  // in CTA 0: one entry per CTA of the cluster
+  __shared__ Key c_keys[kLists][32];
   float* const s_group = reinterpret_cast<float*>(s_group4);
   static_assert(kCandidates >= kWarps * 32, "the warps' lists share the candidates' place");
-  const int row = blockIdx.x / parts, part = blockIdx.x % parts;
+  const int row = kCluster ? blockIdx.x / parts : blockIdx.x, part = kCluster ? blockIdx.x % parts : 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, th = threadIdx.x;
   const int token = a.tokens[row];
   if (token < 0 || token >= a.vocab) {  // the same for the whole cluster
@@ -337,7 +341,14 @@ __global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, i
   }
   // CTA 0's shared memory is written to once every CTA of the cluster runs
   cg::cluster_group cluster = cg::this_cluster();
-  auto started = cluster.barrier_arrive();
+  cg::cluster_group::arrival_token started;
+  if (kCluster) started = cluster.barrier_arrive();
+  Stat* stat_out = &c_stat[part];
+  Key* list_out = &c_keys[part][0];
+  if (kCluster) {
+    stat_out = cluster.map_shared_rank(stat_out, 0);
+    list_out = cluster.map_shared_rank(list_out, 0);
+  }
   const float ninf = __int_as_float(0xff800000);
   const Part<T> p(static_cast<const T*>(a.logits) + (size_t)row * a.row_stride, a.vocab, part, parts);
   float x_t = 0.0f;
@@ -400,12 +411,12 @@ __global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, i
     }
   }
   __syncthreads();
-  cluster.barrier_wait(std::move(started));
+  if (kCluster) cluster.barrier_wait(std::move(started));
   if (warp == kWarps - 1) {
     const Stat b = warp_join<kWarps>(lane < kWarps ? s_stat[lane] : Stat{0.0f, 0.0f, 0.0f});
     if (lane == 0) {
       s_odd = b.s != b.s;  // a NaN, or +inf, which makes one
-      *cluster.map_shared_rank(&c_stat[part], 0) = b;
+      *stat_out = b;
     }
   }
   if (a.num_top > 0) {
@@ -460,7 +471,6 @@ __global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, i
       const int count = s_count;
       all = count > kCandidates;
       if (!all) {
-        Key* const list = cluster.map_shared_rank(&c_keys[part][0], 0);
         for (int i = th; i < max(count, 32); i += kThreads) {
           const Key k = i < count ? s_keys[i] : 0;
           int rank = i;
@@ -468,7 +478,7 @@ __global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, i
             rank = 0;
             for (int j = 0; j < count; ++j) rank += s_keys[j] > k;
           }
-          if (rank < 32) list[rank] = k;
+          if (rank < 32) list_out[rank] = k;
         }
       }
     }
@@ -487,13 +497,14 @@ __global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, i
         if (__any_sync(0xffffffffu, k > last)) list = warp_merge(list, warp_sort(k));
       }
       list = block_merge<kWarps>(list, reinterpret_cast<Key(*)[32]>(s_keys));
-      if (warp == 0) cluster.map_shared_rank(&c_keys[part][0], 0)[lane] = list;
+      if (warp == 0) list_out[lane] = list;
     }
   }
-  cluster.sync();
+  if (kCluster) cluster.sync();
+  else __syncthreads();
   if (part != 0 || warp != 0) return;
-  const Stat b = cluster_join(c_stat, parts);
-  write_row(a, row, x_t, b, c_keys, parts);
+  const Stat b = kCluster ? cluster_join(c_stat, parts) : c_stat[0];
+  write_row(a, row, x_t, b, c_keys, kCluster ? parts : 1);
 }
 
 // Long rows.  Warps 0-7 stream: they add up what a ring of 16 KB stages
@@ -921,8 +932,8 @@ int launch(const LogprobArgs& a, int num_rows, cudaStream_t stream) {
   if (is_short) {
     cfg.gridDim = dim3((unsigned)num_rows * parts, 1, 1);
     cfg.blockDim = dim3(128, 1, 1);
-    cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, short_logprobs_kernel<T>, a, parts);
+    cfg.numAttrs = parts > 1 ? 1 : 0;
+    e = cudaLaunchKernelEx(&cfg, parts > 1 ? short_logprobs_kernel<T, true> : short_logprobs_kernel<T, false>, a, parts);
   } else {
     const auto kernel = parts > 1 ? long_logprobs_kernel<T, true> : long_logprobs_kernel<T, false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLongSmem) != cudaSuccess)
