@@ -64,7 +64,7 @@ template <typename T>
 struct Elem;
 template <>
 struct Elem<float> {
-  static constexpr int kVec = 4, kUnroll = 4;  // elements per vector; vectors per thread and round
+  static constexpr int kVec = 4;  // elements per vector
   static constexpr uint32_t kNone = 0xff800000u;  // -inf
   static __device__ float one(float x) { return x; }
   static __device__ uint32_t word(float x) { return __float_as_uint(x); }
@@ -77,7 +77,7 @@ struct Elem<float> {
 };
 template <>
 struct Elem<__nv_bfloat16> {
-  static constexpr int kVec = 8, kUnroll = 4;
+  static constexpr int kVec = 8;
   static constexpr uint32_t kNone = 0xff80ff80u;
   static __device__ float one(__nv_bfloat16 x) { return __bfloat162float(x); }
   static __device__ uint32_t word(__nv_bfloat16 x) { return (kNone & 0xffff0000u) | __bfloat16_as_ushort(x); }
@@ -94,7 +94,7 @@ struct Elem<__nv_bfloat16> {
 };
 template <>
 struct Elem<__half> {
-  static constexpr int kVec = 8, kUnroll = 4;
+  static constexpr int kVec = 8;
   static constexpr uint32_t kNone = 0xfc00fc00u;
   static __device__ float one(__half x) { return __half2float(x); }
   static __device__ uint32_t word(__half x) { return (kNone & 0xffff0000u) | __half_as_ushort(x); }
@@ -309,10 +309,10 @@ __device__ __forceinline__ void write_row(const LogprobArgs& a, int row, float x
 // 5,000 59.6 against 52.0).
 constexpr int kShortThreads = 128;
 constexpr int kShortVecs = 32 * kShortThreads;  // fewer vectors to a row: a warp reads a thread's at once
-template <typename T, bool kCluster>
-__global__ void __launch_bounds__(128, 8) short_logprobs_kernel(LogprobArgs a, int parts) {
+template <typename T, bool kCluster, int kUnroll>
+__global__ void __launch_bounds__(128, 32 / kUnroll) short_logprobs_kernel(LogprobArgs a, int parts) {
   constexpr int kThreads = kShortThreads;
-  constexpr int kVec = Elem<T>::kVec, kPer = 16 / kVec, kUnroll = Elem<T>::kUnroll, kWarps = kThreads / 32;
+  constexpr int kVec = Elem<T>::kVec, kPer = 16 / kVec, kWarps = kThreads / 32;
   __shared__ Stat s_stat[kWarps];
   __shared__ float4 s_group4[kGroups / 4];  // read four at a time
   __shared__ Key s_keys[kCandidates];  // candidates, or the warps' lists
@@ -916,7 +916,7 @@ int launch(const LogprobArgs& a, int num_rows, cudaStream_t stream) {
   // blocks, 56 streamed; 2,000 of 30,000 bf16 38 and 40).
   const bool is_short = a.vocab < kShortVecs * kVec;
   // CTAs per row: while every SM would not have one, and each has two rounds of loads
-  const long long round = is_short ? 128LL * Elem<T>::kUnroll * kVec : (long long)kStageVecs * kVec;
+  const long long round = is_short ? kShortThreads * 4LL * kVec : (long long)kStageVecs * kVec;
   const long long wanted = is_short ? 2LL * sms : sms;
   int parts = 1;
   while (parts < kMaxCluster && (long long)num_rows * parts < wanted && a.vocab > 2 * parts * round) parts *= 2;
@@ -933,7 +933,15 @@ int launch(const LogprobArgs& a, int num_rows, cudaStream_t stream) {
     cfg.gridDim = dim3((unsigned)num_rows * parts, 1, 1);
     cfg.blockDim = dim3(128, 1, 1);
     cfg.numAttrs = parts > 1 ? 1 : 0;
-    e = cudaLaunchKernelEx(&cfg, parts > 1 ? short_logprobs_kernel<T, true> : short_logprobs_kernel<T, false>, a, parts);
+    // Up to four blocks per SM have eight vectors of a thread in flight, and as
+    // many again, where a thread has as many; more blocks four, which leaves
+    // registers for eight of them (333 fp16 rows of 32,003 11.9 against 12.7 us,
+    // 333 fp32 rows of 15,000 9.4 / 10.9; one row of 32,000 bf16 8.9 / 8.5, 1,000
+    // of 32,003 23.7 / 22.1, 8,192 of 5,000 62.6 / 50.6).
+    const bool deep = (long long)num_rows * parts <= 4 * sms && a.vocab >= 8LL * kShortThreads * kVec * parts;
+    const auto kernel = parts > 1 ? (deep ? short_logprobs_kernel<T, true, 8> : short_logprobs_kernel<T, true, 4>)
+                                  : (deep ? short_logprobs_kernel<T, false, 8> : short_logprobs_kernel<T, false, 4>);
+    e = cudaLaunchKernelEx(&cfg, kernel, a, parts);
   } else {
     const auto kernel = parts > 1 ? long_logprobs_kernel<T, true> : long_logprobs_kernel<T, false>;
     if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kLongSmem) != cudaSuccess)

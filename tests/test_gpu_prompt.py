@@ -509,6 +509,18 @@ def test_token_logprobs_sizes(dtype, n, V, top):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("n,V,top", [(330, 9999, 4), (400, 16003, 32), (160, 32001, 5), (609, 16003, 5), (20, 8195, 1),
+                                     (300, 16383, 0)])
+def test_token_logprobs_short_rows_few_and_many(dtype, n, V, top):
+    """Blocks with eight and with four vectors in flight, alone and in clusters."""
+    g = _gen(V + n)
+    x = _logits(g, n, V, dtype)
+    x[::7, ::3] = -INF
+    tokens = torch.randint(V, (n,), generator=g, device="cuda", dtype=torch.int32)
+    _check_scores(x, tokens, top)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_token_logprobs_strided_and_unaligned_rows(dtype):
     """Rows behind one another with a gap, starting at an odd element."""
     g = _gen(4)
