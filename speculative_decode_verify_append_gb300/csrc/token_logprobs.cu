@@ -815,23 +815,26 @@ __global__ void __launch_bounds__(kLongThreads, 2)
               for (int j = 0; j < kVec; ++j) offer(x[j], p.first + v * kVec + j);
             }
           };
-          // their vectors, dealt to the team: of the one stage that reaches the bound, or of all
-          for (int i = tt; i < 4 * ctl->hots; i += kTeamThreads) {
-            const int v = ctl->hot[i >> 2] + (i & 3) * kStreamThreads;
-            if (v < p.vectors) look(p.load(v), v);
-          }
-          const int each = (p.vectors + kStreamThreads - 1) / kStreamThreads, items = ctl->wides * each;
-          for (int i0 = tt; i0 < items; i0 += 4 * kTeamThreads) {
-            uint4 w[4];
-            int v[4];
+          // Their vectors, dealt to the team: of the one stage that reaches the
+          // bound, or of all; in a cluster's short parts mostly one to a thread,
+          // where less code to fetch is worth more (one row 8.4 against 9.1 us).
+          constexpr int kBatch = kCluster ? 1 : 4;
+          const int single = 4 * ctl->hots, each = (p.vectors + kStreamThreads - 1) / kStreamThreads;
+          const int items = single + ctl->wides * each;
+#pragma unroll 1
+          for (int i0 = tt; i0 < items; i0 += kBatch * kTeamThreads) {
+            uint4 w[kBatch];
+            int v[kBatch];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-              const int i = i0 + u * kTeamThreads;
-              v[u] = i < items ? ctl->wide[i / each] + i % each * kStreamThreads : p.vectors;
+            for (int u = 0; u < kBatch; ++u) {
+              const int i = i0 + u * kTeamThreads, k = i - single;
+              v[u] = i < single  ? ctl->hot[i >> 2] + (i & 3) * kStreamThreads
+                     : i < items ? ctl->wide[k / each] + k % each * kStreamThreads
+                                 : p.vectors;
               w[u] = v[u] < p.vectors ? p.load(v[u]) : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
-            for (int u = 0; u < 4; ++u)
+            for (int u = 0; u < kBatch; ++u)
               if (v[u] < p.vectors) look(w[u], v[u]);
           }
           team_sync();
