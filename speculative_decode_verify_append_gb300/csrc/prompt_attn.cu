@@ -5,8 +5,8 @@
 // the lane's rows j <= t, out = sum_j exp(s_j - lse) v_j, lse = log sum exp s_j,
 // in one pass over the keys with the running maximum and sum.
 //
-// A tile is 2 x T consecutive rows of one kv head, T = 128 / G (T rows where
-// there are few): each of its two halves fills the 128 rows of a tensor-core tile with T tokens x G q
+// A tile is 2 x T consecutive rows of one kv head, T = 128 / G: each of its
+// two halves fills the 128 rows of a tensor-core tile with T tokens x G q
 // heads (row r = token r / G, head r % G), so that a group's heads share the
 // K/V tiles and few rows are empty whatever the group.  Twelve warps:
 //   * warp 8 (loader): takes the next tile, TMA-loads its Q and the K and V
@@ -32,6 +32,9 @@
 //     before it (one issuer, in order), so the thread may rescale its O in
 //     place when the reference moves.  At the end it divides by the sum and
 //     stores.
+// Where there are few tiles, one of T rows has the CTA alone (kOne): one
+// issuer and one softmax warpgroup, the scores in the places of both halves in
+// turns, so that a block's products run under the softmax of the one before.
 // Bound by the tensor cores from some thousand tokens on (16,384 tokens of 24 /
 // 4 heads 890 to 980 us with the clock that power leaves, 1,680 to 1,850 TFLOP/s,
 // where a library product reaches 1,690 sustained and 1,865 in a burst; 8,192
@@ -251,6 +254,7 @@ __device__ __forceinline__ void quad_transpose(uint4 (&u)[4]) {
   }
 }
 
+template <bool kOne>
 __global__ void __launch_bounds__(kThreads, 1)
     prompt_attn_kernel(const __grid_constant__ CUtensorMap mq, const __grid_constant__ CUtensorMap mk,
                        const __grid_constant__ CUtensorMap mv, const PromptArgs a) {
@@ -271,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&ctl->next_full), 1);
     for (int i = 0; i < kStages; ++i) {
       mbar_init(smem_u32(&ctl->full[i]), 1);
-      mbar_init(smem_u32(&ctl->empty[i]), 2);
+      mbar_init(smem_u32(&ctl->empty[i]), kOne ? 1 : 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&ctl->q_full[i]), 1);
@@ -284,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(smem_u32(&ctl->o_full[i]), 1);
       mbar_init(smem_u32(&ctl->o_free[i]), 4);
       mbar_init(smem_u32(&ctl->tile_full[i]), 1);
-      mbar_init(smem_u32(&ctl->tile_free[i]), 11);  // both issuers, the guard, eight softmax warps
+      mbar_init(smem_u32(&ctl->tile_free[i]), kOne ? 6 : 11);  // the issuers, the guard, the softmax warps
       mbar_init(smem_u32(&ctl->tile_guarded[i]), 1);
     }
     for (int i = 0; i < kGuardRing; ++i) mbar_init(smem_u32(&ctl->guard[i]), 1);
@@ -417,7 +421,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < 2; ++s)
           if (q_loads[s]) mbar_wait<false>(smem_u32(&ctl->q_full[s]), (q_loads[s] - 1) & 1u, &none, 400000000LL);
       }
-    } else if (warp == kIssueWarp || warp == kIssueWarp + 1) {
+    } else if (kOne ? warp == kIssueWarp : warp == kIssueWarp || warp == kIssueWarp + 1) {
       const int s = warp - kIssueWarp;
       // Descriptors differ in their start address alone: the low words are
       // added up from constants, so that a product costs few instructions
@@ -427,22 +431,24 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t k_desc = sdesc_sw128(base + kOffKv, 1024, 1024);
       const uint64_t v_desc = sdesc_sw128(base + kOffKv, kPanel, 1024);
       constexpr uint64_t kStage16 = kStageBytes >> 4, kPanel16 = kPanel >> 4;
-      const uint32_t d_s = tmem + col_s(s), d_o = tmem + col_o(s);
+      const uint32_t d_o = tmem + col_o(s);
       Ring ring;
       Phase p_phase, o_phase, q_phase, turn_phase;
       bool used = false;
-      // S = Q K^T with the K block of stage st
-      auto qk = [&](uint32_t st) {
+      // S of place b = Q K^T with the K block of stage st
+      auto qk = [&](uint32_t st, int b) {
+        const uint32_t d_s = tmem + col_s(b);
         const uint64_t kd = k_desc + st * kStage16;
 #pragma unroll
         for (int k = 0; k < 8; ++k)
           mma_f16_ss(d_s, q_desc + kPanel16 * (k >> 2) + 2 * (k & 3), kd + kPanel16 * (k >> 2) + 2 * (k & 3), kIdescQK,
                      k != 0);
-        mma_commit(smem_u32(&ctl->s_full[s]));
+        mma_commit(smem_u32(&ctl->s_full[b]));
         mma_commit(smem_u32(&ctl->empty[st]));
       };
       // O (+)= P V with keys 64 part .. + 63 of the V block of stage st
-      auto pv = [&](uint32_t st, int part, bool add) {
+      auto pv = [&](uint32_t st, int b, int part, bool add) {
+        const uint32_t d_s = tmem + col_s(b);
         const uint64_t vd = v_desc + st * kStage16;
 #pragma unroll
         for (int k = 0; k < 4; ++k)
@@ -459,7 +465,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(smem_u32(&ctl->empty[r.st]));
         return true;
       };
-      for (int i = 0; ok; ++i) {
+      // One half: its scores go to the places of both halves in turns, so that
+      // the next ones are there when a block's weights are.
+      uint32_t places = 0;  // bit b: the parity of place b's next weights
+      for (int i = 0; kOne && ok; ++i) {
+        const int slot = i & 1;
+        if (!(ok = wait(ctl->tile_full[slot], (uint32_t)((i / 2) & 1)))) break;
+        const Tile t = ctl->tile[slot];
+        if (t.len == 0) break;
+        const Shape sh(t, a.T, a.span);
+        const int n = __shfl_sync(0xffffffffu, sh.n[0], 0);
+        Ring k = ring, v = ring;
+        v.next();
+        // the scores of block j
+        auto scores = [&](int j) {
+          if (!wait(ctl->full[k.st], k.phase)) return false;
+          fence_after_sync();
+          if (elect_one()) {
+            qk(k.st, j & 1);
+            if (j + 1 == n) mma_commit(smem_u32(&ctl->q_free[0]));
+          }
+          __syncwarp();
+          k.next();
+          k.next();
+          return true;
+        };
+        if (!(ok = wait(ctl->q_full[0], q_phase.take()) && scores(0) && (n == 1 || scores(1)))) break;
+        for (int j = 0; j < n; ++j) {
+          const int b = j & 1;
+          const uint32_t phase = (places >> b) & 1u;
+          places ^= 1u << b;
+          if (!(ok = wait(ctl->full[v.st], v.phase) && (j > 0 || !used || wait(ctl->o_free[0], o_phase.take())) &&
+                     wait(ctl->p_full[b][0], phase)))
+            break;
+          fence_after_sync();
+          if (elect_one()) pv(v.st, b, 0, j > 0);
+          __syncwarp();
+          if (!(ok = wait(ctl->p_full[b][1], phase))) break;
+          fence_after_sync();
+          if (elect_one()) {
+            pv(v.st, b, 1, true);
+            mma_commit(smem_u32(&ctl->empty[v.st]));
+            mma_commit(smem_u32(&ctl->o_full[1]));  // O holds the blocks so far
+            if (j + 1 == n) mma_commit(smem_u32(&ctl->o_full[0]));
+          }
+          __syncwarp();
+          v.next();
+          v.next();
+          if (j + 2 < n && !(ok = scores(j + 2))) break;
+        }
+        if (!ok) break;
+        used = true;
+        ring = k;
+        if (lane == 0) mbar_arrive(smem_u32(&ctl->tile_free[slot]));
+        __syncwarp();
+      }
+      for (int i = 0; !kOne && ok; ++i) {
         const int slot = i & 1;
         if (!(ok = wait(ctl->tile_full[slot], (uint32_t)((i / 2) & 1)))) break;
         const Tile t = ctl->tile[slot];
@@ -471,7 +532,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (n > 0) {
           fence_after_sync();
           if (elect_one()) {
-            qk(ring.st);
+            qk(ring.st, s);
             if (n == 1) mma_commit(smem_u32(&ctl->q_free[s]));
           }
         }
@@ -496,15 +557,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                      take_turn()))
             break;
           fence_after_sync();
-          if (elect_one()) pv(v.st, 0, j > 0);
+          if (elect_one()) pv(v.st, s, 0, j > 0);
           __syncwarp();
           if (!(ok = wait(ctl->p_full[s][1], phase))) break;
           fence_after_sync();
           if (elect_one()) {
-            pv(v.st, 1, true);
+            pv(v.st, s, 1, true);
             mma_commit(smem_u32(&ctl->empty[v.st]));
             if (more) {
-              qk(k.st);
+              qk(k.st, s);
               if (j + 2 == n) mma_commit(smem_u32(&ctl->q_free[s]));
             } else {
               mma_commit(smem_u32(&ctl->o_full[s]));
@@ -569,15 +630,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) give_up(ctl, a.status);
     }
-  } else {
+  } else if (!kOne || warp < 4) {
     regs_increase<kRegsSoftmax>();
     const int s = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)(warp & 3) << 21;  // TMEM lane 32 * (warp % 4) in bits 16 and up
-    const uint32_t t_s = tmem + lane_base + col_s(s), t_o = tmem + lane_base + col_o(s);
+    const uint32_t t_o = tmem + lane_base + col_o(s);
     const int r_tok = row / a.G, r_head = row % a.G;
     const int w_tok = (row & ~31) / a.G;  // the warp's first token
     const float ninf = __int_as_float(0xff800000);
     Phase s_phase, o_phase;
+    uint32_t places = 0;  // bit b: the parity of place b's next scores
+    uint32_t before = 0;  // blocks of the tiles before
     bool ok = true;
     for (int i = 0; ok; ++i) {
       const int slot = i & 1;
@@ -596,7 +659,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       // It goes by the row alone, so that no later row changes its bits.
       float m = tok < kBlock ? ninf : 0.0f, l = 0.0f;
       for (int j = 0; j < n; ++j) {
-        if (!(ok = wait(ctl->s_full[s], s_phase.take()))) break;
+        const int b = kOne ? j & 1 : s;  // the place of the block's scores and weights
+        const uint32_t t_s = tmem + lane_base + col_s(b);
+        const uint32_t s_parity = kOne ? (places >> b) & 1u : s_phase.take();
+        places ^= 1u << b;
+        if (!(ok = wait(ctl->s_full[b], s_parity))) break;
         fence_after_sync();
         uint32_t x[4][32];
 #pragma unroll
@@ -650,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_st();
           fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[s][part]));
+          if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[b][part]));
         };
         sum0 = sum1 = 0ull;
         weights(0);
@@ -661,6 +728,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float f = move ? fast_exp2((m - top) * a.scale_log2) : 1.0f;
           if (move) m = top;
           if (j > 0) {
+            // with one half the scores run ahead of O
+            if (kOne && !(ok = wait(ctl->o_full[1], (before + j - 1) & 1u))) break;
+            if (kOne) fence_after_sync();
             l *= f;
 #pragma unroll 1
             for (int c = 0; c < 8; ++c) {
@@ -682,6 +752,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         hand_over(1);
       }
       if (!ok) break;
+      before += n;
       if (!(ok = wait(ctl->tile_guarded[slot], (uint32_t)((i / 2) & 1)))) break;
       const bool dirty = ctl->tile[slot].dirty != 0;
       __syncwarp();
@@ -808,26 +879,29 @@ extern "C" int prompt_attn(const void* q, const void* k, const void* v, int64_t 
       !encode_rows(&mk, k, k_stride, num_kv_heads, total_tokens, 1, kBlock) ||
       !encode_rows(&mv, v, v_stride, num_kv_heads, total_tokens, 1, kBlock))
     return SDVA_ERR_CUDA;
-  // the shared-memory limit is a per-device attribute of the function: set it
-  // on every call, for the device current now
-  if (cudaFuncSetAttribute(prompt_attn_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
-      cudaSuccess)
-    return SDVA_ERR_CUDA;
-  // At most this many tiles: one per span of rows and a ragged one per lane.
-  // Where tiles of one half leave the GPU not much over one each, the shorter
-  // chain of one half wins over the work that two halves share (40 tokens of
-  // 24 / 4 heads 7.6 against 9.7 us, 512 11.4 / 12.8, 1,024 16.5 / 18.1, 2,048
-  // of 8 / 8 24.1 / 25.7; from 272 half tiles on 152 SMs two halves win: 1,024
-  // of 32 / 8 17.8 / 18.4, 2,048 of 24 / 4 27.0 / 37.6).
+  // One half to a tile where two would not give each SM a tile (a lane counted
+  // with half a tile for its ragged end): its chain of blocks is the shorter
+  // one, 1,200 to 1,900 cycles a block against 2,150 for two halves, whose blocks
+  // serve twice the rows.  2,048 tokens of 8 / 8 heads 19.5 against 25.5 us, 4,096
+  // 31.0 / 44.1, 16,384 of 2 / 1 100 / 153, 1,200 of 32 / 8 (154 tiles on 152 SMs)
+  // 18.3 / 19.5, 512 of 24 / 4 9.8 / 11.5; 1,300 of 32 / 8 (166) 21.8 / 20.0, 2,048 of
+  // 24 / 4 (197) 29.8 / 26.2, eight ragged prompts (447) 46.7 / 37.1.
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return SDVA_ERR_CUDA;
-  auto tiles_of = [&](int span) { return ((long long)total_tokens / span + num_lanes) * num_kv_heads; };
-  a.span = 3 * tiles_of(2 * a.T) <= 2 * sms ? a.T : 2 * a.T;
-  const long long tiles = tiles_of(a.span);
+  const long long rows = (long long)total_tokens + (long long)a.T * num_lanes;
+  a.span = 20 * rows * num_kv_heads <= 21LL * sms * 2 * a.T ? a.T : 2 * a.T;
+  // at most this many tiles: one per span of rows and a ragged one per lane
+  const long long tiles = ((long long)total_tokens / a.span + num_lanes) * num_kv_heads;
   if (tiles > 0x7fffffffLL) return SDVA_ERR_UNSUPPORTED;  // more rows of K and V than memory holds
-  prompt_attn_kernel<<<(unsigned)tiles, kThreads, kSmemBytes,
+  // the shared-memory limit is a per-device attribute of the function: set it
+  // on every call, for the device current now
+  const auto kernel = a.span == a.T ? prompt_attn_kernel<true> : prompt_attn_kernel<false>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmemBytes) !=
+      cudaSuccess)
+    return SDVA_ERR_CUDA;
+  kernel<<<(unsigned)tiles, kThreads, kSmemBytes,
                        reinterpret_cast<cudaStream_t>(stream)>>>(mq, mk, mv, a);
   return cudaGetLastError() == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
 }
