@@ -712,6 +712,10 @@ __global__ void __launch_bounds__(kLongThreads, 2)
           w[u] = v0 + at < p.vectors ? stage[at]
                                      : make_uint4(Elem<T>::kNone, Elem<T>::kNone, Elem<T>::kNone, Elem<T>::kNone);
         }
+        // The loads are done before the next copy may overwrite the stage: the
+        // arrival alone can pass loads that still wait for their turn while the
+        // team keeps shared memory busy.
+        tc::fence_proxy_async_smem();
         arrive(ctl->empty[st]);
         if (++st == kStages) {
           st = 0;

@@ -603,6 +603,17 @@ def test_token_logprobs_rows_that_are_not_scored():
     assert torch.equal(lp2[on], lp[on]) and torch.equal(en2[on], en[on]) and torch.equal(tt2[on], tt[on])
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_token_logprobs_rows_that_stream_past_long_lists(dtype):
+    """Several rows to a block, lists of 32: the end of a row takes longer than
+    the next row's copies, which must not overtake its readers."""
+    g = _gen(58)
+    x = _logits(g, 1000, 58010, dtype)
+    tokens = torch.randint(58010, (1000,), generator=g, device="cuda", dtype=torch.int32)
+    for _ in range(3):
+        _check_scores(x, tokens, 32)
+
+
 @pytest.mark.parametrize("n", [1, 40])
 def test_token_logprobs_without_the_optional_outputs_and_replayed(n):
     import speculative_decode_verify_append_gb300 as sdva
