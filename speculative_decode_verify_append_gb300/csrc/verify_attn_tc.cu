@@ -1090,7 +1090,9 @@ __global__ void __launch_bounds__(Smem<KVT>::kThreads, 1) verify_split_tc_kernel
             x[q + 2] = __float_as_uint(b.x);
             x[q + 3] = __float_as_uint(b.y);
           }
-          // the row scales are used: this warp's share of releasing the stage
+          // the row scales are read, before the copy that may now overwrite them:
+          // this warp's share of releasing the stage
+          fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl->empty[s]));
         }
