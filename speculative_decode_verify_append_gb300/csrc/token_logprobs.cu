@@ -678,14 +678,13 @@ __global__ void __launch_bounds__(kLongThreads, 2)
       }
     }
     if (ok) ok = publish(-1);
-    if (!ok) {
-      give_up();
-      // this warp's copies still in flight (bounded)
-      int none = 0;
-      for (uint32_t f = fills > kStages ? fills - kStages : 0; f < fills; ++f)
-        tc::mbar_wait<false>(smem_u32(&ctl->full[f % kStages]), (f / kStages) & 1u, &none, 400000000LL);
-      if (asks > 0) tc::mbar_wait<false>(smem_u32(&ctl->next_full), (asks - 1) & 1u, &none, 400000000LL);
-    }
+    if (!ok) give_up();
+    // No copy outlives the CTA, whichever warp gave up (bounded; where none
+    // did, the sums wait for the same copies).
+    int none = 0;
+    for (uint32_t f = fills > kStages ? fills - kStages : 0; f < fills; ++f)
+      tc::mbar_wait<false>(smem_u32(&ctl->full[f % kStages]), (f / kStages) & 1u, &none, 400000000LL);
+    if (asks > 0) tc::mbar_wait<false>(smem_u32(&ctl->next_full), (asks - 1) & 1u, &none, 400000000LL);
   } else if (warp < kStreamWarps) {
     // ---- the sums ----
     uint32_t st = 0, phase = 0;

@@ -1,0 +1,69 @@
+"""Calls whose waits run out late: a warp gives up while the one that copies
+has issued its last copy and is done.  No copy may outlive its block, whose
+shared memory the next block gets: what runs beside and after is right."""
+import pytest
+import torch
+
+from gpu_util import SM_SCALE
+from test_gpu_prompt import _cu, _gen, _logits, _run_attn, _score, _status
+
+pytestmark = pytest.mark.gpu
+
+
+def _without_patience(run, beside):
+    """run() with a limit of zero cycles, beside() on another stream meanwhile."""
+    import speculative_decode_verify_append_gb300 as sdva
+    other = torch.cuda.Stream()
+    other.wait_stream(torch.cuda.current_stream())
+    prev = sdva.sdva_debug_set_wait_limit(0)
+    try:
+        run()
+        with torch.cuda.stream(other):
+            got = beside()
+        torch.cuda.synchronize()
+    finally:
+        sdva.sdva_debug_set_wait_limit(prev)
+    return got
+
+
+def _scores_beside():
+    """Short rows: small blocks, no waits, in the shared memory that others leave."""
+    import speculative_decode_verify_append_gb300 as sdva
+    g = _gen(3)
+    x = _logits(g, 4000, 5000, torch.float32)
+    tokens = torch.randint(5000, (4000,), generator=g, device="cuda", dtype=torch.int32)
+    want = _score(x, tokens, 5)
+    got = [torch.zeros_like(t) for t in want]
+
+    def beside():
+        for _ in range(4):
+            sdva.token_logprobs(x, tokens, *got)
+        return got
+    return want, beside
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_sums_that_wait_for_a_long_list(dtype):
+    """A NaN and rising values: the list of a row is looked for element by
+    element, some hundred microseconds, in which the sums of the rows behind it
+    wait for their place and the copies are all issued."""
+    g = _gen(1)
+    n, V = 1600, 34000
+    x = (torch.arange(V, device="cuda") * 1e-3).expand(n, V).to(dtype).contiguous()
+    x[:, 100] = float("nan")
+    tokens = torch.randint(V, (n,), generator=g, device="cuda", dtype=torch.int32)
+    want, beside = _scores_beside()
+    st = _status()
+    import speculative_decode_verify_append_gb300 as sdva
+    out = [torch.empty(n, device="cuda"), torch.empty(n, device="cuda"),
+           torch.empty((n, 32), dtype=torch.int32, device="cuda"), torch.empty((n, 32), device="cuda")]
+    got = _without_patience(lambda: sdva.token_logprobs(x, tokens, *out, st), beside)
+    assert int(st.item()) in (0, sdva.STATUS_TIMEOUT)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # the same call with its usual patience
+    st.zero_()
+    lp, _, tt, _ = _score(x, tokens, 32, st)
+    assert int(st.item()) == 0 and lp.isnan().all()
+    xd = x[0].float()
+    order = torch.argsort(torch.where(xd.isnan(), float("-inf"), xd), descending=True, stable=True)[:32]
+    assert (tt == order.to(torch.int32)).all()
