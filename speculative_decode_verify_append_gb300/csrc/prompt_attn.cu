@@ -316,6 +316,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     return mbar_wait<false>(smem_u32(&bar), parity, abort_flag, limit);
   };
 
+  // the loader's: stage fills issued, those of them that the guard looks at first, bit i: whether the fill i before
+  // the last one is such; Q loads; requests for another CTA's place and their answers
+  long long fills = 0, guard0 = 0;
+  uint32_t recent = 0, q_loads[2] = {0, 0}, asks = 0, answers = 0;
   if (bad) {  // the same for the whole CTA
     if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(a.status, SDVA_STATUS_BAD_COUNT);
   } else if (warp >= kLoaderWarp) {
@@ -323,9 +327,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     if (warp == kLoaderWarp) {
       const uint32_t half_bytes = (uint32_t)(a.G * a.T) * 128u;  // one 64-dim panel of one half's Q
-      long long fills = 0;  // stage fills issued
-      uint32_t q_loads[2] = {0, 0};
-      long long guard0 = 0;  // guarded blocks issued
       // a V block that the guard looks at first lands on the guard's barrier; the guard passes it on
       auto load = [&](const CUtensorMap* map, int hk, int row, bool guarded) {
         const int s = (int)(fills % kStages);
@@ -340,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         ++fills;
         guard0 += guarded;
+        recent = recent << 1 | (uint32_t)guarded;
         return true;
       };
       uint32_t r = blockIdx.x;
@@ -353,7 +355,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         t.t0 = pos * a.span;
         return true;
       };
-      uint32_t asks = 0, answers = 0;
       auto ask = [&]() {
         if (lane == 0) take_over_next(smem_u32(ctl->next_cta), smem_u32(&ctl->next_full));
         __syncwarp();
@@ -409,18 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (!ok) break;
       }
-      if (!ok) {
-        give_up(ctl, a.status);
-        // this warp's copies still in flight (bounded)
-        int none = 0;
-        for (long long g = max(0LL, guard0 - kStages); g < guard0; ++g)
-          mbar_wait<false>(smem_u32(&ctl->guard[g % kGuardRing]), (uint32_t)((g / kGuardRing) & 1), &none, 400000000LL);
-        for (long long f = max(0LL, fills - kStages); f < fills; ++f)
-          mbar_wait<false>(smem_u32(&ctl->full[f % kStages]), (uint32_t)((f / kStages) & 1), &none, 400000000LL);
-        if (asks > answers) mbar_wait<false>(smem_u32(&ctl->next_full), answers & 1u, &none, 400000000LL);
-        for (int s = 0; s < 2; ++s)
-          if (q_loads[s]) mbar_wait<false>(smem_u32(&ctl->q_full[s]), (q_loads[s] - 1) & 1u, &none, 400000000LL);
-      }
+      if (!ok) give_up(ctl, a.status);
     } else if (kOne ? warp == kIssueWarp : warp == kIssueWarp || warp == kIssueWarp + 1) {
       const int s = warp - kIssueWarp;
       // Descriptors differ in their start address alone: the low words are
@@ -819,6 +809,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp == kGuardWarp) {
     fence_after_sync();
     tmem_dealloc(tmem, kTmemCols);
+  } else if (warp == kLoaderWarp && ctl->abort) {
+    // No copy outlives the CTA, whichever warp gave up (bounded; where none
+    // did, all were waited for).  A block that the guard has not passed on
+    // completes the guard's barrier alone.
+    int none = 0;
+#pragma unroll 1
+    for (int i = 0; i < kStages && i < fills; ++i) {
+      const long long f = fills - 1 - i, g = guard0 - 1;
+      const bool guarded = recent >> i & 1u;
+      mbar_wait<false>(smem_u32(guarded ? &ctl->guard[g % kGuardRing] : &ctl->full[f % kStages]),
+                       (uint32_t)((guarded ? g / kGuardRing : f / kStages) & 1), &none, 400000000LL);
+      guard0 -= guarded;
+    }
+    if (asks > answers) mbar_wait<false>(smem_u32(&ctl->next_full), answers & 1u, &none, 400000000LL);
+#pragma unroll 1
+    for (int s = 0; s < 2; ++s)
+      if (q_loads[s]) mbar_wait<false>(smem_u32(&ctl->q_full[s]), (q_loads[s] - 1) & 1u, &none, 400000000LL);
   }
 }
 

@@ -67,3 +67,29 @@ def test_sums_that_wait_for_a_long_list(dtype):
     xd = x[0].float()
     order = torch.argsort(torch.where(xd.isnan(), float("-inf"), xd), descending=True, stable=True)[:32]
     assert (tt == order.to(torch.int32)).all()
+
+
+@pytest.mark.parametrize("lens,hq,hkv", [([256] * 400, 1, 1), ([42] * 500, 24, 4), ([128] * 150, 1, 1)])
+def test_products_that_wait_for_rows_of_infinities(lens, hq, hkv):
+    """Infinities in every row of V: what the guard took out is added again from
+    global memory, some hundred microseconds a tile, in which the next tile's
+    products wait for their place and the few copies of it are all issued."""
+    import speculative_decode_verify_append_gb300 as sdva
+    T = sum(lens)
+    g = _gen(5)
+    q, k, v = (torch.randn((T, h, 128), generator=g, device="cuda").to(torch.bfloat16) for h in (hq, hkv, hkv))
+    cu = _cu(lens)
+    inf = torch.full_like(v, float("inf"))
+    want, beside = _scores_beside()
+    good = _run_attn(q, k, v, cu)
+    st = _status()
+    out = torch.empty_like(q)
+    got = _without_patience(lambda: sdva.prompt_attn(q, k, inf, cu, float(SM_SCALE), out, None, st), beside)
+    assert int(st.item()) in (0, sdva.STATUS_TIMEOUT)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    # the same call with its usual patience, and one with finite values
+    st.zero_()
+    out, lse = _run_attn(q, k, inf, cu, status=st)
+    assert int(st.item()) == 0 and torch.equal(lse, good[1]) and (out == float("inf")).all()
+    out, lse = _run_attn(q, k, v, cu, status=st)
+    assert int(st.item()) == 0 and torch.equal(out, good[0]) and torch.equal(lse, good[1])
