@@ -826,13 +826,12 @@ __global__ void __launch_bounds__(Smem<KVT>::kThreads, 1) verify_split_tc_kernel
         ph_b = ph_c;
       }
     }
-    if (!ok) {
-      fail(ctl, a.status);
-      // drain this CTA's own copies still in flight (bounded)
-      for (long long g = max(0LL, issued - kNS); g < issued; ++g) {
-        int dummy = 0;
-        mbar_wait<kSpinWait>(smem_u32(&ctl->full[(uint32_t)g % (uint32_t)kNS]), (uint32_t)(((uint32_t)g / (uint32_t)kNS) & 1), &dummy, 400000000LL);
-      }
+    if (!ok) fail(ctl, a.status);
+    // No copy outlives the CTA, whichever role gave up (bounded; where none
+    // did, the others wait for the same copies).
+    for (long long g = max(0LL, issued - kNS); g < issued; ++g) {
+      int dummy = 0;
+      mbar_wait<false>(smem_u32(&ctl->full[(uint32_t)g % (uint32_t)kNS]), (uint32_t)(((uint32_t)g / (uint32_t)kNS) & 1), &dummy, 400000000LL);
     }
   } else if (warp == kQkWarp || warp == kQkWarp + 1) {
     // ------------------------------------------------------------------
@@ -899,14 +898,13 @@ __global__ void __launch_bounds__(Smem<KVT>::kThreads, 1) verify_split_tc_kernel
       g += seg_len;
       it.next_unit(ctl->pref, a.B, a.Hkv);
     }
-    if (!ok) {
-      fail(ctl, a.status);
-      // let the tensor core finish what this thread issued before tensor memory is freed
-      if (last >= 0) {
-        int dummy = 0;
-        const long long n = last >> 1;
-        mbar_wait<kSpinWait>(smem_u32(&ctl->s_full[j][n & 1]), (uint32_t)((n >> 1) & 1), &dummy, 400000000LL);
-      }
+    if (!ok) fail(ctl, a.status);
+    // let the tensor core finish what this thread issued before tensor memory
+    // is freed, whichever role gave up
+    if (last >= 0) {
+      int dummy = 0;
+      const long long n = last >> 1;
+      mbar_wait<false>(smem_u32(&ctl->s_full[j][n & 1]), (uint32_t)((n >> 1) & 1), &dummy, 400000000LL);
     }
   } else if (warp == kPvWarp) {
     // ------------------------------------------------------------------
@@ -948,13 +946,11 @@ __global__ void __launch_bounds__(Smem<KVT>::kThreads, 1) verify_split_tc_kernel
       g += seg_len;
       it.next_unit(ctl->pref, a.B, a.Hkv);
     }
-    if (!ok) {
-      fail(ctl, a.status);
-      if (last >= 0) {
-        int dummy = 0;
-        mbar_wait<kSpinWait>(smem_u32(&ctl->v16_empty[(uint32_t)last % (uint32_t)kV16Stages]), (uint32_t)(((uint32_t)last / (uint32_t)kV16Stages) & 1), &dummy,
-                  400000000LL);
-      }
+    if (!ok) fail(ctl, a.status);
+    if (last >= 0) {  // as the QK issuers
+      int dummy = 0;
+      mbar_wait<false>(smem_u32(&ctl->v16_empty[(uint32_t)last % (uint32_t)kV16Stages]), (uint32_t)(((uint32_t)last / (uint32_t)kV16Stages) & 1), &dummy,
+                400000000LL);
     }
   } else if (warp >= kConvWarp) {
     if (!conv_on_idle) convert(threadIdx.x - kConvWarp * 32);

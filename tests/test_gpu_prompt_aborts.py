@@ -1,10 +1,13 @@
 """Calls whose waits run out late: a warp gives up while the one that copies
 has issued its last copy and is done.  No copy may outlive its block, whose
 shared memory the next block gets: what runs beside and after is right."""
+import numpy as np
 import pytest
 import torch
 
-from gpu_util import SM_SCALE
+import oracle
+import synth
+from gpu_util import ALL_KV, KV_NAMES, SM_SCALE, assert_close, bf16_dev, fill_both, i32_dev
 from test_gpu_prompt import _cu, _gen, _logits, _run_attn, _score, _status
 
 pytestmark = pytest.mark.gpu
@@ -93,3 +96,34 @@ def test_products_that_wait_for_rows_of_infinities(lens, hq, hkv):
     assert int(st.item()) == 0 and torch.equal(lse, good[1]) and (out == float("inf")).all()
     out, lse = _run_attn(q, k, v, cu, status=st)
     assert int(st.item()) == 0 and torch.equal(out, good[0]) and torch.equal(lse, good[1])
+
+
+@pytest.mark.parametrize("kind", ALL_KV, ids=[KV_NAMES[k] for k in ALL_KV])
+def test_a_window_over_few_pages(kind):
+    """verify_attn with no more pages to a CTA than it has stages: the producer
+    is done at once, with all its copies in flight, and the others give up."""
+    import speculative_decode_verify_append_gb300 as sdva
+    lens, W, hq, hkv = [900] * 6, 4, 12, 2
+    spec = synth.Spec("late", 72, len(lens), 0, 0, hq, hkv, W, kind, None, 0.7, True)
+    step = synth.make_step(spec, seq_lens=np.array(lens, np.int32), with_accept=False)
+    gc, oc, _ = fill_both(spec, step)
+    q, t, L = bf16_dev(step.q), i32_dev(step.page_table), i32_dev(step.seq_lens)
+    ws = torch.empty(sdva.verify_attn_workspace_size(len(lens), W, hq, hkv, max(lens)), dtype=torch.uint8,
+                     device="cuda")
+    out = torch.zeros((len(lens), W, hq, 128), dtype=torch.bfloat16, device="cuda")
+    st = _status()
+    want, beside = _scores_beside()
+
+    def run():
+        for _ in range(8):
+            sdva.verify_attn(gc, q, t, L, max(lens), float(SM_SCALE), out, ws, st)
+
+    got = _without_patience(run, beside)
+    assert int(st.item()) == sdva.STATUS_TIMEOUT
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    st.zero_()
+    sdva.verify_attn(gc, q, t, L, max(lens), float(SM_SCALE), out, ws, st)
+    torch.cuda.synchronize()
+    assert int(st.item()) == 0
+    ref, _ = oracle.verify_attn(oc, step.q, step.page_table, step.seq_lens, SM_SCALE, threads=16)
+    assert_close(out.float().cpu().numpy(), ref, "after the calls that gave up")
