@@ -238,7 +238,10 @@ int kv_append_packed(const sdva_kv_cache* cache, const void* k_new, const void* 
  * 1024, at most 128 q heads per kv head and 65535 kv heads (else
  * SDVA_ERR_UNSUPPORTED), num_q_heads a multiple of num_kv_heads, sm_scale
  * positive and finite.  Scores, running maximum, sum and output accumulate
- * in fp32; the softmax weights are rounded to bf16 for the product with V.
+ * in fp32, about a maximum that the row's own stays within 2^8 of: finite
+ * values up to 2^119 / n in magnitude, n the keys that a row sees, give finite
+ * outputs; larger ones may become infinite or NaN.  The softmax weights are
+ * rounded to bf16 for the product with V.
  * Returns SDVA_OK or a negative SDVA_ERR_*.
  */
 int prompt_attn(const void* q, const void* k, const void* v, int64_t q_stride, int64_t k_stride, int64_t v_stride,

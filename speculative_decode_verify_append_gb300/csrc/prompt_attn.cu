@@ -26,7 +26,7 @@
 //     those they do see from global memory;
 //   * warps 0-3 and 4-7 (softmax, one warpgroup per half): a thread owns a
 //     row: reads its 128 scores, masks the last blocks, keeps a running
-//     reference (0, or a maximum far from it) and sum, writes P as bf16 over
+//     reference (its maximum, or one near it) and sum, writes P as bf16 over
 //     the scores, in two parts, so that the PV of the first runs under the
 //     weights of the second.  Once the QK of a block is done, so is the PV
 //     before it (one issuer, in order), so the thread may rescale its O in
@@ -66,12 +66,11 @@ constexpr uint32_t kPanel = kStageBytes / 2;
 constexpr uint32_t kOffKv = 2 * kStageBytes;  // behind the Q of both halves
 constexpr uint32_t kOffCtl = kOffKv + kStages * kStageBytes;
 constexpr int kGuardRing = 8;  // barriers of the guard's blocks, more than there are stages
-// A row's reference moves when its scores leave 2^kLag around it: fp32 sums
-// and bf16 weights keep their relative precision over that range, and only
-// far-off scores ever rescale O (at 2^8, keys with a few channels eight times
-// the rest did so in half of their blocks: 36.7 against 28.7 us at 1,501 + 999 +
-// 2,047 + 3 tokens of 8 / 8 heads).
-constexpr float kLag = 40.0f;  // log2 units
+// A row's reference is the maximum of its first block of keys, and moves to a
+// later maximum where that lies more than 2^kLag above it: the largest weight
+// is then between 1 and 2^kLag, so that small values are not lost and the sum
+// over n keys stays finite for values below 2^(127 - kLag) / n.
+constexpr float kLag = 8.0f;  // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 // tensor memory: S (fp32, 128 columns) of half s, overlaid by its P (bf16, 64 columns); O (fp32, 128 columns)
 __device__ __forceinline__ uint32_t col_s(int s) { return 128u * s; }
@@ -641,13 +640,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = sh.n[s], first = t.t0 + s * a.T;
       const int tok = first + r_tok;
       const bool valid = r_tok < a.T && tok < t.len;
-      // A row whose keys are all in the first block moves to its maximum as
-      // reference (from -inf any is far): its largest weight is then 1, and
-      // rounding it to bf16 costs nothing, which with few keys is most of the
-      // error (against fp64, of the output's norm: one key 0 instead of 1.4e-3,
-      // four 1.4e-3 instead of 2.1e-3, 1.3e-3 of it from rounding the output).
-      // It goes by the row alone, so that no later row changes its bits.
-      float m = tok < kBlock ? ninf : 0.0f, l = 0.0f;
+      // The largest weight of a row with few keys is 1, and rounding it to bf16
+      // costs nothing, which is most of the error there (against fp64, of the
+      // output's norm: one key 0 instead of 1.4e-3, four 1.4e-3 instead of
+      // 2.1e-3, 1.3e-3 of it from rounding the output).
+      float m = ninf, l = 0.0f;
       for (int j = 0; j < n; ++j) {
         const int b = kOne ? j & 1 : s;  // the place of the block's scores and weights
         const uint32_t t_s = tmem + lane_base + col_s(b);
@@ -670,10 +667,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (hidden & (1u << k)) x[c][k] = 0xff800000u;
           }
         }
-        // The weights of the first 64 keys are taken about the reference that
-        // the row has, beside this block's maximum (64 three-way maxima are a
-        // third of the work on a block); only where that lies too far off are
-        // they taken again.
+        // Behind the first block, the weights of the first 64 keys are taken
+        // about the reference that the row has, beside this block's maximum (64
+        // three-way maxima are a third of the work on a block); only where that
+        // lies too far off are they taken again.
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -709,28 +706,25 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[b][part]));
         };
+        if (j == 0) m = top;
         sum0 = sum1 = 0ull;
         weights(0);
-        // from 0 the first block may lie far below, too; no NaN moves it
-        const float above = (top - m) * a.scale_log2;
-        const bool move = above > kLag || (j == 0 && above < -kLag);
-        if (__any_sync(0xffffffffu, move && valid)) {
+        const bool move = (top - m) * a.scale_log2 > kLag;  // of NaN, as of two -inf: no
+        if (__any_sync(0xffffffffu, move && valid)) {  // not at j = 0
           const float f = move ? fast_exp2((m - top) * a.scale_log2) : 1.0f;
           if (move) m = top;
-          if (j > 0) {
-            // with one half the scores run ahead of O
-            if (kOne && !(ok = wait(ctl->o_full[1], (before + j - 1) & 1u))) break;
-            if (kOne) fence_after_sync();
-            l *= f;
+          // with one half the scores run ahead of O
+          if (kOne && !(ok = wait(ctl->o_full[1], (before + j - 1) & 1u))) break;
+          if (kOne) fence_after_sync();
+          l *= f;
 #pragma unroll 1
-            for (int c = 0; c < 8; ++c) {
-              uint32_t o[16];
-              tmem_ld16(t_o + 16 * c, o);
-              tmem_wait_ld();
+          for (int c = 0; c < 8; ++c) {
+            uint32_t o[16];
+            tmem_ld16(t_o + 16 * c, o);
+            tmem_wait_ld();
 #pragma unroll
-              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-              tmem_st16(t_o + 16 * c, o);
-            }
+            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+            tmem_st16(t_o + 16 * c, o);
           }
           sum0 = sum1 = 0ull;
           weights(0);
