@@ -155,7 +155,7 @@ typedef struct {
  *                  any chunk length when filling a context.
  *   page_table, max_pages_per_lane, seq_lens: as above (seq_lens is read only).
  *   status       : nullable device int.
- * A lane with L_b < 0 or L_b + n_new > 64 * max_pages_per_lane gets
+ * A lane with L_b < 0 or L_b + n_new > 64 * max_pages_per_lane (or 2^31 - 1) gets
  * SDVA_STATUS_OVERFLOW; a lane whose touched pages include an invalid id gets
  * SDVA_STATUS_BAD_PAGE; in both cases nothing of that lane is written.
  * Precondition: inputs are finite; no two lanes map the same physical page

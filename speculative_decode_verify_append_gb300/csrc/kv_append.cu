@@ -52,14 +52,15 @@ __device__ __forceinline__ int lane_tokens(const AppendArgs& a, int b, bool repo
 }
 
 // Lane admission shared by both kernels: the lane's token range [L, L + n)
-// must fit its page-table row and every touched page id must be valid;
-// otherwise the lane is skipped and flagged (once, by the lane's first CTA).
+// must fit its page-table row and an int32, and every touched page id must be
+// valid; otherwise the lane is skipped and flagged (once, by the lane's first
+// CTA).
 __device__ bool lane_admitted(const AppendArgs& a, int b, int L, int n, bool report) {
   __shared__ int s_bad;
   if (threadIdx.x == 0) s_bad = 0;
   __syncthreads();
   const long long end = (long long)L + n;
-  if (L < 0 || end > (long long)a.max_pages * kPage) {
+  if (L < 0 || end > min((long long)a.max_pages * kPage, 0x7fffffffLL)) {
     if (report && threadIdx.x == 0) raise_status(a.status, SDVA_STATUS_OVERFLOW);
     return false;
   }
@@ -102,7 +103,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_fp8_kernel(AppendArgs a
   const int lp = L / kPage + slot;
   if ((long long)lp * kPage >= (long long)L + n) return;
   const int pid = a.page_table[(size_t)b * a.max_pages + lp];
-  const int t0 = max(L, lp * kPage), t1 = min(L + n, lp * kPage + kPage);
+  const int t0 = max(L, lp * kPage), t1 = min(L + n - lp * kPage, kPage) + lp * kPage;
   const int start = t0 - lp * kPage, count = t1 - t0;
   const size_t token_stride = (size_t)a.num_kv_heads * kHeadDim;
   const uint16_t* src = (is_v ? a.v_new : a.k_new) + ((size_t)b * a.n_new + (t0 - L)) * token_stride +
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_int4_kernel(AppendArgs 
   const int lp = L / kPage + slot;
   if ((long long)lp * kPage >= (long long)L + n) return;
   const int pid = a.page_table[(size_t)b * a.max_pages + lp];
-  const int t0 = max(L, lp * kPage), t1 = min(L + n, lp * kPage + kPage);
+  const int t0 = max(L, lp * kPage), t1 = min(L + n - lp * kPage, kPage) + lp * kPage;
   const int count = t1 - t0;
   const int H = a.num_kv_heads;
   const size_t token_stride = (size_t)H * kHeadDim;
@@ -238,7 +239,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_rowscaled_kernel(Append
   const int lp = L / kPage + slot;
   if ((long long)lp * kPage >= (long long)L + n) return;
   const int pid = a.page_table[(size_t)b * a.max_pages + lp];
-  const int t0 = max(L, lp * kPage), t1 = min(L + n, lp * kPage + kPage);
+  const int t0 = max(L, lp * kPage), t1 = min(L + n - lp * kPage, kPage) + lp * kPage;
   const int count = t1 - t0;
   const int H = a.num_kv_heads;
   const size_t token_stride = (size_t)H * kHeadDim;

@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 4) append_packed_kernel(PackedArgs a
   const int L = a.seq_lens[b];
   const long long end = (long long)L + n;
   const bool report = page == 0 && hk == 0 && th == 0;
-  if (L < 0 || end > (long long)a.max_pages * kPage) {
+  if (L < 0 || end > min((long long)a.max_pages * kPage, 0x7fffffffLL)) {  // positions are int32
     if (report) raise_status(a.status, SDVA_STATUS_OVERFLOW);
     return;
   }
