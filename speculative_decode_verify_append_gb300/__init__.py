@@ -443,6 +443,16 @@ def _arg(t: torch.Tensor | None, dtype: torch.dtype, shape: tuple, device: int, 
     return t.data_ptr()
 
 
+def _status_arg(status: torch.Tensor | None, device: int):
+    """The address of a call's status word, on the current device (None: not given)."""
+    if status is None:
+        return None
+    if status.get_device() != device or status.numel() == 0:
+        raise ValueError(f"status must be an int32 word on the current device, cuda:{device}; got "
+                         f"{status.numel()} on {status.device}")
+    return _dptr(status, torch.int32, "status")
+
+
 def _rows(t: torch.Tensor, shape: tuple, device: int, name: str) -> int:
     """Elements between the token rows of a bf16 [T][H][128] tensor whose rows
     are contiguous inside (a tensor of its own, or a slice of a fused projection)."""
@@ -468,14 +478,15 @@ def kv_append_packed(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, c
     shape = (T, cache.num_kv_heads, HEAD_DIM)
     ks, vs = _rows(k_new, shape, dev, "k_new"), _rows(v_new, shape, dev, "v_new")
     pages = page_table.shape[1]
-    if cache.k_codes.get_device() != dev:
-        raise ValueError(f"the cache is on {cache.k_codes.device}, the current device is cuda:{dev}")
+    for t in (cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales):
+        if t.get_device() != dev:
+            raise ValueError(f"the cache is on {t.device}, the current device is cuda:{dev}")
     s = cache.struct()
     rc = _lib.kv_append_packed(ctypes.byref(s), k_new.data_ptr(), v_new.data_ptr(), ks, vs, T,
                                _arg(cu_tokens, torch.int32, (B + 1,), dev, "cu_tokens"), B,
                                _arg(page_table, torch.int32, (B, pages), dev, "page_table"), pages,
                                _arg(seq_lens, torch.int32, (B,), dev, "seq_lens"),
-                               _dptr(status, torch.int32, "status"), _stream(stream))
+                               _status_arg(status, dev), _stream(stream))
     _check("kv_append_packed", rc)
 
 
@@ -494,7 +505,7 @@ def prompt_attn(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_tokens: to
                           _arg(cu_tokens, torch.int32, (B + 1,), dev, "cu_tokens"), B, float(sm_scale),
                           _arg(out, torch.bfloat16, (T, Hq, HEAD_DIM), dev, "out"),
                           _arg(lse, torch.float32, (T, Hq), dev, "lse"),
-                          _dptr(status, torch.int32, "status"), _stream(stream))
+                          _status_arg(status, dev), _stream(stream))
     _check("prompt_attn", rc)
 
 
@@ -534,7 +545,7 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: torch.T
                              _arg(entropy, torch.float32, lead, dev, "entropy"),
                              _arg(top_tokens, torch.int32, lead + (top,), dev, "top_tokens"),
                              _arg(top_logprobs, torch.float32, lead + (top,), dev, "top_logprobs"),
-                             _dptr(status, torch.int32, "status"), _stream(stream))
+                             _status_arg(status, dev), _stream(stream))
     _check("token_logprobs", rc)
 
 
