@@ -176,9 +176,16 @@ def _dptr(t: torch.Tensor | None, dtype: torch.dtype | None = None, name: str = 
     return t.data_ptr()
 
 
+# The current stream's handle itself, where this build of torch gives it: a
+# torch.cuda.Stream object costs a few microseconds.
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int | None:
-    if stream is None:  # the handle itself: a torch.cuda.Stream object costs a few microseconds
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        if _current_handle is None:
+            return torch.cuda.current_stream().cuda_stream
+        return _current_handle(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)

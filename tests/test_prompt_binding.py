@@ -98,3 +98,16 @@ def test_a_cache_with_a_part_on_another_device_is_refused(calls, part):
     with pytest.raises(ValueError, match="cache"):
         calls.kv_append_packed(other=part)
     assert len(calls.reached) == 1
+
+
+def test_the_current_stream_with_and_without_its_raw_handle(monkeypatch):
+    import __graft_entry__
+    __graft_entry__._load_builder().build()
+    import speculative_decode_verify_append_gb300 as sdva
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda: types.SimpleNamespace(cuda_stream=77))
+    monkeypatch.setattr(sdva, "_current_handle", lambda device: 100 + device)
+    assert sdva._stream(None) == 103
+    monkeypatch.setattr(sdva, "_current_handle", None)
+    assert sdva._stream(None) == 77
+    assert sdva._stream(5) == 5
