@@ -99,6 +99,14 @@ struct Tile {
   int dirty;      // the guard took values out that some of the tile's rows see
 };
 
+// What the loader has issued: stage fills, those of them that the guard looks
+// at first (bit i of recent: the fill i before the last one), Q loads, requests
+// for another CTA's place and their answers.
+struct Issued {
+  long long fills, guarded;
+  uint32_t recent, q_loads[2], asks, answers;
+};
+
 struct Ctl {
   uint64_t q_full[2], q_free[2], full[kStages], empty[kStages];
   uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2], turn[2], drain[2];
@@ -107,6 +115,7 @@ struct Ctl {
   alignas(16) uint32_t next_cta[4];  // the answer to a request for another CTA's place
   uint64_t next_full;
   Tile tile[2];
+  Issued issued;
   uint32_t tmem_base;
   int abort;
 };
@@ -315,10 +324,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     return mbar_wait<false>(smem_u32(&bar), parity, abort_flag, limit);
   };
 
-  // the loader's: stage fills issued, those of them that the guard looks at first, bit i: whether the fill i before
-  // the last one is such; Q loads; requests for another CTA's place and their answers
-  long long fills = 0, guard0 = 0;
-  uint32_t recent = 0, q_loads[2] = {0, 0}, asks = 0, answers = 0;
   if (bad) {  // the same for the whole CTA
     if (blockIdx.x == 0 && threadIdx.x == 0) raise_status(a.status, SDVA_STATUS_BAD_COUNT);
   } else if (warp >= kLoaderWarp) {
@@ -326,6 +331,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     if (warp == kLoaderWarp) {
       const uint32_t half_bytes = (uint32_t)(a.G * a.T) * 128u;  // one 64-dim panel of one half's Q
+      long long fills = 0;  // stage fills issued
+      uint32_t q_loads[2] = {0, 0};
+      long long guard0 = 0;  // guarded blocks issued
+      uint32_t recent = 0;   // bit i: whether the fill i before the last one was such a block
       // a V block that the guard looks at first lands on the guard's barrier; the guard passes it on
       auto load = [&](const CUtensorMap* map, int hk, int row, bool guarded) {
         const int s = (int)(fills % kStages);
@@ -354,6 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         t.t0 = pos * a.span;
         return true;
       };
+      uint32_t asks = 0, answers = 0;
       auto ask = [&]() {
         if (lane == 0) take_over_next(smem_u32(ctl->next_cta), smem_u32(&ctl->next_full));
         __syncwarp();
@@ -410,6 +420,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
       }
       if (!ok) give_up(ctl, a.status);
+      if (lane == 0) ctl->issued = {fills, guard0, recent, {q_loads[0], q_loads[1]}, asks, answers};
+      __syncwarp();
     } else if (kOne ? warp == kIssueWarp : warp == kIssueWarp || warp == kIssueWarp + 1) {
       const int s = warp - kIssueWarp;
       // Descriptors differ in their start address alone: the low words are
@@ -807,19 +819,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     // No copy outlives the CTA, whichever warp gave up (bounded; where none
     // did, all were waited for).  A block that the guard has not passed on
     // completes the guard's barrier alone.
+    const Issued n = ctl->issued;
     int none = 0;
-#pragma unroll 1
-    for (int i = 0; i < kStages && i < fills; ++i) {
-      const long long f = fills - 1 - i, g = guard0 - 1;
-      const bool guarded = recent >> i & 1u;
+    long long g = n.guarded;
+    for (long long f = n.fills - 1; f >= 0 && f >= n.fills - kStages; --f) {
+      const bool guarded = n.recent >> (n.fills - 1 - f) & 1u;
+      g -= guarded;
       mbar_wait<false>(smem_u32(guarded ? &ctl->guard[g % kGuardRing] : &ctl->full[f % kStages]),
                        (uint32_t)((guarded ? g / kGuardRing : f / kStages) & 1), &none, 400000000LL);
-      guard0 -= guarded;
     }
-    if (asks > answers) mbar_wait<false>(smem_u32(&ctl->next_full), answers & 1u, &none, 400000000LL);
-#pragma unroll 1
+    if (n.asks > n.answers) mbar_wait<false>(smem_u32(&ctl->next_full), n.answers & 1u, &none, 400000000LL);
     for (int s = 0; s < 2; ++s)
-      if (q_loads[s]) mbar_wait<false>(smem_u32(&ctl->q_full[s]), (q_loads[s] - 1) & 1u, &none, 400000000LL);
+      if (n.q_loads[s]) mbar_wait<false>(smem_u32(&ctl->q_full[s]), (n.q_loads[s] - 1) & 1u, &none, 400000000LL);
   }
 }
 
