@@ -679,10 +679,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (hidden & (1u << k)) x[c][k] = 0xff800000u;
           }
         }
-        // Behind the first block, the weights of the first 64 keys are taken
-        // about the reference that the row has, beside this block's maximum (64
-        // three-way maxima are a third of the work on a block); only where that
-        // lies too far off are they taken again.
+        // The weights of the first 64 keys are taken about the reference that
+        // the row has, beside this block's maximum (64 three-way maxima are a
+        // third of the work on a block); only where that lies too far off, as in
+        // the first block, are they taken again.
         float mx[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -718,25 +718,27 @@ __global__ void __launch_bounds__(kThreads, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl->p_full[b][part]));
         };
-        if (j == 0) m = top;
         sum0 = sum1 = 0ull;
         weights(0);
-        const bool move = (top - m) * a.scale_log2 > kLag;  // of NaN, as of two -inf: no
-        if (__any_sync(0xffffffffu, move && valid)) {  // not at j = 0
+        // from -inf, at j = 0, any maximum is far; no NaN moves the reference
+        const bool move = (top - m) * a.scale_log2 > kLag;
+        if (__any_sync(0xffffffffu, move && valid)) {
           const float f = move ? fast_exp2((m - top) * a.scale_log2) : 1.0f;
           if (move) m = top;
-          // with one half the scores run ahead of O
-          if (kOne && !(ok = wait(ctl->o_full[1], (before + j - 1) & 1u))) break;
-          if (kOne) fence_after_sync();
-          l *= f;
+          if (j > 0) {
+            // with one half the scores run ahead of O
+            if (kOne && !(ok = wait(ctl->o_full[1], (before + j - 1) & 1u))) break;
+            if (kOne) fence_after_sync();
+            l *= f;
 #pragma unroll 1
-          for (int c = 0; c < 8; ++c) {
-            uint32_t o[16];
-            tmem_ld16(t_o + 16 * c, o);
-            tmem_wait_ld();
+            for (int c = 0; c < 8; ++c) {
+              uint32_t o[16];
+              tmem_ld16(t_o + 16 * c, o);
+              tmem_wait_ld();
 #pragma unroll
-            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-            tmem_st16(t_o + 16 * c, o);
+              for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+              tmem_st16(t_o + 16 * c, o);
+            }
           }
           sum0 = sum1 = 0ull;
           weights(0);
