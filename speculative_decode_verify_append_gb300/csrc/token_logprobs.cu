@@ -711,9 +711,9 @@ __global__ void __launch_bounds__(kLongThreads, 2)
           w[u] = v0 + at < p.vectors ? stage[at]
                                      : make_uint4(Elem<T>::kNone, Elem<T>::kNone, Elem<T>::kNone, Elem<T>::kNone);
         }
-        // The loads are done before the next copy may overwrite the stage: the
-        // arrival alone can pass loads that still wait for their turn while the
-        // team keeps shared memory busy.
+        // The next copy may overwrite the stage: the arrival orders these loads
+        // before ordinary accesses that follow it, not before those of the
+        // copies, which are another proxy's; the fence does.
         tc::fence_proxy_async_smem();
         arrive(ctl->empty[st]);
         if (++st == kStages) {

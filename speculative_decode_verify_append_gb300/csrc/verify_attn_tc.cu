@@ -1086,8 +1086,8 @@ __global__ void __launch_bounds__(Smem<KVT>::kThreads, 1) verify_split_tc_kernel
             x[q + 2] = __float_as_uint(b.x);
             x[q + 3] = __float_as_uint(b.y);
           }
-          // the row scales are read, before the copy that may now overwrite them:
-          // this warp's share of releasing the stage
+          // the row scales are read: this warp's share of releasing the stage
+          // (the arrival alone orders no copy, another proxy's, behind the loads)
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(&ctl->empty[s]));
