@@ -202,6 +202,9 @@ int kv_append_quant_ragged(const sdva_kv_cache* cache, const void* k_new, const 
  * leaves, byte for byte; lanes are checked and skipped as there.  Offsets
  * that do not satisfy 0 <= cu_tokens[0] <= cu_tokens[1] <= ... <=
  * total_tokens set SDVA_STATUS_BAD_COUNT and nothing is written.
+ * Every block reads all offsets, which grows with the square of the number of
+ * lanes: 1,024 lanes of one token take 26 us, 4,096 136 and 16,384 1,300 (INT8,
+ * 4 kv heads); many lanes of one length are kv_append_quant's work.
  * Every other argument, precondition and return code is that of
  * kv_append_quant.
  */
@@ -233,7 +236,9 @@ int kv_append_packed(const sdva_kv_cache* cache, const void* k_new, const void* 
  *   Rows outside every lane's range are neither read into a result nor
  *   written.  A row depends on its own lane's rows 0 .. t only: infinities
  *   and NaN in later rows or other lanes do not reach it.  Inside a row they
- *   behave as the formula does (a NaN score or +inf makes the row NaN).
+ *   behave as the formula does (a NaN score or +inf makes the row NaN); an
+ *   infinite v whose weight fp32 does not hold (a score some 87 below the
+ *   row's largest, or -inf) makes its element that infinity or NaN.
  * total_tokens >= 0 (0 enqueues nothing and returns SDVA_OK), num_lanes <=
  * 1024, at most 128 q heads per kv head and 65535 kv heads (else
  * SDVA_ERR_UNSUPPORTED), num_q_heads a multiple of num_kv_heads, sm_scale
@@ -552,7 +557,9 @@ typedef enum {
  * A token at -inf has log probability -inf and no part in the entropy.  A
  * row without a distribution (all -inf, or holding +inf or NaN) gets NaN in
  * logprobs, entropy and top_logprobs; its top_tokens still follow the order.
- * Sums are fp32, in an order that the sizes alone fix.  num_rows >= 0 (0 enqueues nothing and returns SDVA_OK).
+ * Sums are fp32, in an order that the sizes, the GPU's number of SMs and the
+ * row's offset from a 16-byte boundary fix.  num_rows >= 0 (0 enqueues nothing
+ * and returns SDVA_OK).
  * Returns SDVA_OK, SDVA_ERR_INVALID, SDVA_ERR_UNSUPPORTED or SDVA_ERR_CUDA.
  */
 int token_logprobs(const void* logits, int logits_dtype, int64_t row_stride, int num_rows, int vocab,

@@ -87,7 +87,7 @@ class VerifyStep:
 
 
 class PromptStep:
-    """A packed batch of prompts of up to max_tokens tokens, cu_tokens int32 [B + 1] (device)."""
+    """A packed batch of whole prompts of up to max_tokens tokens, cu_tokens int32 [B + 1] (device)."""
 
     def __init__(self, max_tokens: int, num_q_heads: int, device="cuda", sm_scale: float | None = None):
         self.sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(128.0)
