@@ -60,9 +60,9 @@ DEFAULT_WORKLOAD = "multi_lane"
 # from an ncu capture of the kernels built from sources with this SHA-256
 # (verify_attn_tc.cu, tc_primitives.cuh, verify_attn.cu, in that order, comments stripped);
 # reported as null once the sources differ (the counters are then stale).
-NCU_TRAFFIC = {"sources_sha256": "44309ab667511223cc8f80338fd680afc3acd8be96ad613058a6664407bfaf02",
-               "bytes": {"multi_lane": 314707456, "long_context": 249022464, "int4_12slot": 338031360,
-                         "multi_lane_int8": 324021760, "multi_lane_fp8row": 323727872}}
+NCU_TRAFFIC = {"sources_sha256": "f305de7b9574cb3e7a900b54a0ef8fdb3eba9f11d7e81f0809973da99f8a0805",
+               "bytes": {"multi_lane": 314624512, "long_context": 249033216, "int4_12slot": 337997568,
+                         "multi_lane_int8": 324094720, "multi_lane_fp8row": 323726336}}
 TRAFFIC_SOURCES = ("verify_attn_tc.cu", "tc_primitives.cuh", "verify_attn.cu")
 
 
