@@ -3,8 +3,8 @@
 //
 // What is written is what kv_append_quant writes (sdva.h).  The call is bound
 // by memory: 512 bytes in and 128 to 264 out per token and kv head (65,536
-// tokens, 4 kv heads: FP8 35 us, 5.8 TB/s; FP8 rows 34, 6.0; INT8 39, 5.2; INT4
-// 36, 4.8).  One CTA
+// tokens, 4 kv heads: FP8 36.3 us, 5.5 TB/s; FP8 rows 35.5, 5.7; INT8 39.5, 5.1;
+// INT4 37.2, 4.6, which issues more instructions).  One CTA
 // per (touched page, kv head) takes K and V together: eight threads per token
 // row, each with dims [8 t, 8 t + 8) of both 64-dim halves, so that a row's
 // loads and stores are whole 128- and 64-byte runs; all of a thread's loads

@@ -36,9 +36,9 @@
 // issuer and one softmax warpgroup, the scores in the places of both halves in
 // turns, so that a block's products run under the softmax of the one before.
 // Bound by the tensor cores from some thousand tokens on (16,384 tokens of 24 /
-// 4 heads 890 to 980 us with the clock that power leaves, 1,680 to 1,850 TFLOP/s,
+// 4 heads 845 to 990 us with the clock that power leaves, 1,660 to 1,950 TFLOP/s,
 // where a library product reaches 1,690 sustained and 1,865 in a burst; 8,192
-// 229 us, 1,800), below by the chain of blocks of the longest tile, a few
+// 226 us, 1,825), below by the chain of blocks of the longest tile, a few
 // hundred cycles each for the products, the scores' way to the softmax and the
 // weights' way back.
 // Every wait is bounded: on timeout the CTA raises SDVA_STATUS_TIMEOUT,
@@ -69,7 +69,9 @@ constexpr int kGuardRing = 8;  // barriers of the guard's blocks, more than ther
 // A row's reference is the maximum of its first block of keys, and moves to a
 // later maximum where that lies more than 2^kLag above it: the largest weight
 // is then between 1 and 2^kLag, so that small values are not lost and the sum
-// over n keys stays finite for values below 2^(127 - kLag) / n.
+// over n keys stays finite for values below 2^(127 - kLag) / n.  Few rows move:
+// 4,550 tokens of 8 / 8 heads take 24.5 us with a few key channels eight times
+// the rest and without.
 constexpr float kLag = 8.0f;  // log2 units
 constexpr float kLog2e = 1.4426950408889634f;
 // tensor memory: S (fp32, 128 columns) of half s, overlaid by its P (bf16, 64 columns); O (fp32, 128 columns)
@@ -896,10 +898,10 @@ extern "C" int prompt_attn(const void* q, const void* k, const void* v, int64_t 
   // One half to a tile where two would not give each SM a tile (a lane counted
   // with half a tile for its ragged end): its chain of blocks is the shorter
   // one, 1,200 to 1,900 cycles a block against 2,150 for two halves, whose blocks
-  // serve twice the rows.  2,048 tokens of 8 / 8 heads 19.5 against 25.5 us, 4,096
-  // 31.0 / 44.1, 16,384 of 2 / 1 100 / 153, 1,200 of 32 / 8 (154 tiles on 152 SMs)
-  // 18.3 / 19.5, 512 of 24 / 4 9.8 / 11.5; 1,300 of 32 / 8 (166) 21.8 / 20.0, 2,048 of
-  // 24 / 4 (197) 29.8 / 26.2, eight ragged prompts (447) 46.7 / 37.1.
+  // serve twice the rows.  2,048 tokens of 8 / 8 heads 20.4 against 26.4 us, 4,096
+  // 33.2 / 45.0, 16,384 of 2 / 1 104 / 149, 1,200 of 32 / 8 (154 tiles on 152 SMs)
+  // 19.5 / 20.2, 512 of 24 / 4 10.1 / 12.0; 1,300 of 32 / 8 (166) 23.2 / 21.1, 2,048 of
+  // 24 / 4 (197) 31.5 / 27.8, eight ragged prompts (447) 49.1 / 39.0.
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess ||
       cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

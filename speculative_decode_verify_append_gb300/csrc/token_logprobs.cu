@@ -7,7 +7,7 @@
 // all in one pass with a running maximum per thread.  The call is bound by
 // reading the logits (16-bit logits also by the work per element, about four
 // instructions): 4,096 bf16 rows of 151,936 with a list of 5 200 us, 6.2 TB/s;
-// few rows by a chain of steps (one fp32 row 4.4 us, with a list of 20 8.4).
+// few rows by a chain of steps (one fp32 row 4.8 us, with a list of 20 8.2).
 //
 // Few rows: a cluster of up to 8 CTAs per row, joined through distributed
 // shared memory; no workspace, no second launch.  A thread reads 16-byte
