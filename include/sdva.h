@@ -36,6 +36,19 @@
  *   token_logprobs   -- log probability of given tokens, entropy and the most
  *                       probable tokens of each logits row
  *
+ * Two put a layer's queries and keys to their positions on the way:
+ *   kv_append_rope   -- kv_append_quant (window, ragged, or a draft tree) with
+ *                       the rotation of its queries and keys
+ *   kv_append_packed_rope -- kv_append_packed with the same
+ *
+ * Three serve the recurrent layers of hybrid models (the gated delta rule),
+ * whose context is a matrix per head instead of cached keys and values:
+ *   prompt_delta     -- packed prompts, which leaves each lane's state
+ *   verify_delta     -- a verify window (chain or draft tree), its updates
+ *                       recorded, or committed at once (a plain decode step)
+ *   commit_delta     -- the state moved by the recorded updates of the
+ *                       accepted tokens
+ *
  * Conventions for every call
  *   - Every pointer argument is a DEVICE pointer (cudaMalloc / torch CUDA
  *     memory on the current device) unless stated otherwise; the caller owns
@@ -212,6 +225,70 @@ int kv_append_packed(const sdva_kv_cache* cache, const void* k_new, const void* 
                      int64_t v_stride, int total_tokens, const int32_t* cu_tokens, int num_lanes,
                      const int32_t* page_table, int max_pages_per_lane, const int32_t* seq_lens, int32_t* status,
                      sdva_stream_t stream);
+
+/* Which dims of a head are turned together (kv_append_rope). */
+typedef enum {
+    SDVA_ROPE_HALVES = 0,    /* dims (i, i + rot_dim / 2) */
+    SDVA_ROPE_NEIGHBOURS = 1 /* dims (2 i, 2 i + 1) */
+} sdva_rope_pairing;
+
+/*
+ * kv_append_rope -- kv_append_quant of a verify window whose keys, and the
+ * queries that go with them, are still to be turned to their positions (the
+ * pages start behind the rotation; models of the kind they serve have it).
+ * With (c_i, s_i) the cosine and sine of pair i in the table's row of the
+ * token's position, i in [0, rot_dim / 2), a pair (x1, x2) of a q or k head
+ * becomes
+ *     (x1 c_i - x2 s_i, x2 c_i + x1 s_i),
+ * in fp32, every product and sum rounded, then rounded to bf16; the other dims
+ * and V stay as they are.  The cache holds afterwards what kv_append_quant (or
+ * kv_append_quant_ragged) of those bf16 keys leaves, byte for byte.
+ *   q, k_new, v_new: bf16, row (lane b, window slot i) at row b * n_new + i,
+ *                row r at q + r * q_stride elements (k_stride, v_stride),
+ *                [heads][128] contiguous inside the row.  The strides are at
+ *                least heads * 128 and multiples of 8: slices of a fused
+ *                projection do.
+ *   n_lane     : nullable int32 [num_lanes]: lane b takes its first n_lane[b]
+ *                rows, as in kv_append_quant_ragged; the others are neither
+ *                read nor written.
+ *   rope       : fp32 [num_positions][rot_dim] (device): a position's cosines
+ *                c_0 .. c_{rot_dim / 2 - 1}, then its sines.
+ *   rot_dim    : 16, 32, 64 or 128, the first dims of a head, paired as
+ *                `pairing` (sdva_rope_pairing) says.
+ *   positions  : nullable int32 [num_lanes][n_new]: the position of every row,
+ *                for a draft tree (L_b + a slot's depth).  NULL: L_b + i.  The
+ *                row goes to cache slot L_b + i either way.
+ *   q_out      : bf16 [num_lanes][n_new][num_q_heads][128] (out)
+ *   k_out      : nullable bf16 [num_lanes][n_new][num_kv_heads][128] (out): the
+ *                turned keys.
+ *   q, k_new, v_new, rope, q_out and k_out are 16-byte aligned (else
+ *   SDVA_ERR_INVALID).
+ * Lanes are checked as by kv_append_quant; a position outside
+ * [0, num_positions) is SDVA_STATUS_OVERFLOW.  Nothing of a skipped lane is
+ * written, q_out and k_out included.  Every block of a lane reads all its
+ * positions, where they are given.
+ * Precondition besides kv_append_quant's: the turned keys are finite in bf16.
+ * Returns SDVA_OK or a negative SDVA_ERR_*.
+ */
+int kv_append_rope(const sdva_kv_cache* cache, const void* q, const void* k_new, const void* v_new, int64_t q_stride,
+                   int64_t k_stride, int64_t v_stride, int num_q_heads, int num_lanes, int n_new,
+                   const int32_t* n_lane, const float* rope, int num_positions, int rot_dim, int pairing,
+                   const int32_t* positions, const int32_t* page_table, int max_pages_per_lane,
+                   const int32_t* seq_lens, void* q_out, void* k_out, int32_t* status, sdva_stream_t stream);
+
+/*
+ * kv_append_packed_rope -- kv_append_packed of a prompt batch with the same
+ * rotation: row t of lane b is at position L_b + t - cu_tokens[b].  q_out and
+ * k_out ([total_tokens][heads][128], k_out nullable) are what prompt_attn
+ * takes.  Rows outside every lane's range are neither read nor written.
+ *   Every argument is that of kv_append_packed or kv_append_rope; rows are
+ *   total_tokens, offsets and lanes are checked as by kv_append_packed.
+ */
+int kv_append_packed_rope(const sdva_kv_cache* cache, const void* q, const void* k_new, const void* v_new,
+                          int64_t q_stride, int64_t k_stride, int64_t v_stride, int num_q_heads, int total_tokens,
+                          const int32_t* cu_tokens, int num_lanes, const float* rope, int num_positions, int rot_dim,
+                          int pairing, const int32_t* page_table, int max_pages_per_lane, const int32_t* seq_lens,
+                          void* q_out, void* k_out, int32_t* status, sdva_stream_t stream);
 
 /*
  * prompt_attn -- causal attention of whole prompts, packed one behind the
@@ -565,6 +642,107 @@ typedef enum {
 int token_logprobs(const void* logits, int logits_dtype, int64_t row_stride, int num_rows, int vocab,
                    const int32_t* tokens, int num_top, float* logprobs, float* entropy, int32_t* top_tokens,
                    float* top_logprobs, int32_t* status, sdva_stream_t stream);
+
+/*
+ * The gated delta rule (the recurrent layers that NInfer's gdn_replay serves:
+ * review, sections "저장소 구조" and "아키텍처 ③"; the pages give no formula, this
+ * is the usual one).  A value head h has a state S of 128 value rows by 128 key
+ * columns.  For a token t whose parent is p (the token before it; in a draft
+ * tree its parent slot), with k, q of key head h / (num_v_heads / num_k_heads)
+ *     kn   = k_t / sqrt(|k_t|^2 + qk_eps),  qn likewise   (qk_eps < 0: as they are)
+ *     u_t  = beta_t (v_t - e^log_decay_t S_p kn)
+ *     S_t  = e^log_decay_t S_p + u_t kn'
+ *     o_t  = scale S_t qn
+ * Shared by the three calls:
+ *   state    : fp32 [num_slots][num_v_heads][128 values][128 keys] (in/out)
+ *   slots    : int32 [num_lanes]: the lane's state.  A slot outside
+ *              [0, num_slots) sets SDVA_STATUS_BAD_PAGE.  No two lanes of a call
+ *              that writes states share a slot.
+ *   q, k     : bf16, row r at q + r * q_stride elements, [num_k_heads][128]
+ *              contiguous inside the row; v the same with [num_v_heads][128].
+ *              Strides at least heads * 128 and multiples of 8.
+ *   log_decay, beta: fp32 [rows][num_v_heads].  A log decay of -inf forgets.
+ *   num_v_heads is a multiple of num_k_heads; lanes and heads up to 65535
+ *   (else SDVA_ERR_UNSUPPORTED); scale positive and finite.
+ *   state, q, k, v, out and deltas are 16-byte aligned (else SDVA_ERR_INVALID).
+ * Precondition: the values of a lane's rows and of the state that it starts
+ * from are finite (log decays: or -inf) and stay in fp32's range.  Other lanes'
+ * and other rows' do not reach it.  Accuracy: states, updates and sums are
+ * fp32; products on the tensor cores take their operands in two fp16 parts
+ * (22 bits).
+ */
+
+/*
+ * prompt_delta -- the rule over packed prompts, as prompt_attn takes them: row
+ * t of lane b, cu_tokens[b] <= t < cu_tokens[b + 1].
+ *   seq_lens : nullable int32 [num_lanes], L_b: a lane with L_b == 0 starts from
+ *              a state of zeros (its slot's is not read), another one from its
+ *              slot's; NULL: every lane from its slot's.  L_b < 0 sets
+ *              SDVA_STATUS_OVERFLOW.
+ *   out      : bf16 [total_tokens][num_v_heads][128] (out)
+ *   state    : holds S of the lane's last token afterwards; a lane without
+ *              tokens is not examined.
+ *   workspace: device scratch of prompt_delta_workspace_size(...) bytes,
+ *              256-byte aligned; its contents between calls do not matter, and
+ *              calls that share it must not overlap on the GPU.
+ * Offsets that are not in order set SDVA_STATUS_BAD_COUNT and nothing is
+ * written; of a lane that is skipped nothing is written, nor are rows outside
+ * every lane's range.  total_tokens >= 0 (0 enqueues nothing).
+ * Returns SDVA_OK or a negative SDVA_ERR_*.
+ */
+size_t prompt_delta_workspace_size(int total_tokens, int num_lanes, int num_k_heads, int num_v_heads);
+int prompt_delta(float* state, int num_slots, const void* q, const void* k, const void* v, int64_t q_stride,
+                 int64_t k_stride, int64_t v_stride, const float* log_decay, const float* beta, int num_k_heads,
+                 int num_v_heads, int total_tokens, const int32_t* cu_tokens, int num_lanes, const int32_t* slots,
+                 const int32_t* seq_lens, float scale, float qk_eps, void* out, void* workspace,
+                 size_t workspace_bytes, int32_t* status, sdva_stream_t stream);
+
+/*
+ * verify_delta -- the rule over a window of 1 .. 16 rows per lane, from the
+ * lane's state: row (lane b, slot i) is row b * window + i of q, k, v,
+ * log_decay and beta.
+ *   n_lane : nullable int32 [num_lanes]: lane b's window is its first n_lane[b]
+ *            rows; a count outside [0, window] sets SDVA_STATUS_BAD_COUNT.
+ *   parent : nullable int32 [num_lanes][window] (entry 0 is not read): a draft
+ *            tree, as in verify_attn_tree; a parent outside [0, i) of one of the
+ *            lane's rows sets SDVA_STATUS_BAD_TREE.  NULL: a chain.
+ *   out    : bf16 [num_lanes][window][num_v_heads][128] (out)
+ *   deltas : fp32 [num_lanes][window][num_v_heads][128] (out): the updates
+ *            w_i = u_i / sqrt(|k_i|^2 + qk_eps), so that S_i = e^log_decay_i S_p +
+ *            w_i k_i'.  The state is not written; commit_delta moves it once the
+ *            accepted tokens are known.
+ *            NULL: the lane's rows are committed in the same pass: its state is
+ *            S of its last one afterwards (a plain decode step; no parent then,
+ *            else SDVA_ERR_INVALID for a window above 1).
+ * Rows from a lane's count on, and all rows of a lane that is skipped, are
+ * zeros in out and deltas; their inputs are not read.
+ * Returns SDVA_OK or a negative SDVA_ERR_*.
+ */
+int verify_delta(float* state, int num_slots, const void* q, const void* k, const void* v, int64_t q_stride,
+                 int64_t k_stride, int64_t v_stride, const float* log_decay, const float* beta, int num_k_heads,
+                 int num_v_heads, int num_lanes, int window, const int32_t* n_lane, const int32_t* parent,
+                 const int32_t* slots, float scale, float qk_eps, void* out, float* deltas, int32_t* status,
+                 sdva_stream_t stream);
+
+/*
+ * commit_delta -- the replay of a verify window's accepted updates (NInfer's
+ * commit(m): review, section "아키텍처 ③"): from the state that verify_delta
+ * read, S of the last accepted token.
+ *   k, log_decay, deltas: as verify_delta took and wrote them (window rows per
+ *                lane).
+ *   accept_len : int32 [num_lanes]: a, as the acceptance calls write it; rows
+ *                0 .. a are committed.  -1 leaves the lane as it is; outside
+ *                [-1, window) sets SDVA_STATUS_BAD_COUNT.
+ *   path       : nullable int32 [num_lanes][window]: the committed slots are
+ *                path[b][0 .. a], as spec_accept_tree writes them; one outside
+ *                [0, window) sets SDVA_STATUS_BAD_TREE.  NULL: slots 0 .. a.
+ * A lane that is skipped keeps its state.
+ * Returns SDVA_OK or a negative SDVA_ERR_*.
+ */
+int commit_delta(float* state, int num_slots, const void* k, int64_t k_stride, const float* log_decay,
+                 const float* deltas, int num_k_heads, int num_v_heads, int num_lanes, int window,
+                 const int32_t* accept_len, const int32_t* path, const int32_t* slots, int32_t* status,
+                 sdva_stream_t stream);
 
 /*
  * sdva_debug_set_wait_limit -- diagnostic hook (no counterpart in the pages).

@@ -29,6 +29,16 @@ The calls mirror ``include/sdva.h``:
     prompt_attn(q, k, v, cu_tokens, sm_scale, out, lse=None, status=None, stream=None)
     token_logprobs(logits, tokens, logprobs, entropy=None, top_tokens=None, top_logprobs=None, status=None,
                    stream=None)
+    kv_append_rope(cache, q, k_new, v_new, rope, page_table, seq_lens, q_out, k_out=None, n_lane=None,
+                   positions=None, interleaved=False, status=None, stream=None)
+    kv_append_packed_rope(cache, q, k_new, v_new, cu_tokens, rope, page_table, seq_lens, q_out, k_out=None,
+                          interleaved=False, status=None, stream=None)
+    prompt_delta_workspace_size(total_tokens, num_lanes, num_k_heads, num_v_heads)
+    prompt_delta(state, q, k, v, log_decay, beta, cu_tokens, slots, scale, out, workspace, seq_lens=None,
+                 qk_eps=1e-6, status=None, stream=None)
+    verify_delta(state, q, k, v, log_decay, beta, slots, scale, out, deltas=None, n_lane=None, parent=None,
+                 qk_eps=1e-6, status=None, stream=None)
+    commit_delta(state, k, log_decay, deltas, slots, accept_len, path=None, status=None, stream=None)
     sdva_status_string(code)
 """
 from __future__ import annotations
@@ -64,6 +74,8 @@ STATUS_BAD_TREE = 32
 LOGITS_F32 = 0
 LOGITS_BF16 = 1
 LOGITS_F16 = 2
+ROPE_HALVES = 0
+ROPE_NEIGHBOURS = 1
 MAX_TOP = 32  # SDVA_MAX_TOP: most tokens token_logprobs lists per row
 LAZY_WALK_MIN_LANES = 48  # SDVA_LAZY_WALK_MIN_LANES: spec_accept_lazy walks rows from this many lanes on
 
@@ -129,6 +141,22 @@ _lib.prompt_attn.restype = _I
 _lib.prompt_attn.argtypes = [_P, _P, _P, _L, _L, _L, _I, _I, _I, _P, _I, ctypes.c_float, _P, _P, _P, _P]
 _lib.token_logprobs.restype = _I
 _lib.token_logprobs.argtypes = [_P, _I, _L, _I, _I, _P, _I, _P, _P, _P, _P, _P, _P]
+_F = ctypes.c_float
+_lib.kv_append_rope.restype = _I
+_lib.kv_append_rope.argtypes = [ctypes.POINTER(_KVCacheStruct), _P, _P, _P, _L, _L, _L, _I, _I, _I, _P, _P, _I, _I, _I,
+                                _P, _P, _I, _P, _P, _P, _P, _P]
+_lib.kv_append_packed_rope.restype = _I
+_lib.kv_append_packed_rope.argtypes = [ctypes.POINTER(_KVCacheStruct), _P, _P, _P, _L, _L, _L, _I, _I, _P, _I, _P, _I,
+                                       _I, _I, _P, _I, _P, _P, _P, _P, _P]
+_lib.prompt_delta_workspace_size.restype = ctypes.c_size_t
+_lib.prompt_delta_workspace_size.argtypes = [_I, _I, _I, _I]
+_lib.prompt_delta.restype = _I
+_lib.prompt_delta.argtypes = [_P, _I, _P, _P, _P, _L, _L, _L, _P, _P, _I, _I, _I, _P, _I, _P, _P, _F, _F, _P, _P,
+                              ctypes.c_size_t, _P, _P]
+_lib.verify_delta.restype = _I
+_lib.verify_delta.argtypes = [_P, _I, _P, _P, _P, _L, _L, _L, _P, _P, _I, _I, _I, _I, _P, _P, _P, _F, _F, _P, _P, _P, _P]
+_lib.commit_delta.restype = _I
+_lib.commit_delta.argtypes = [_P, _I, _P, _L, _P, _P, _I, _I, _I, _I, _P, _P, _P, _P, _P]
 _lib.sdva_debug_set_wait_limit.restype = ctypes.c_longlong
 _lib.sdva_debug_set_wait_limit.argtypes = [ctypes.c_longlong]
 _lib.sdva_status_string.restype = ctypes.c_char_p
@@ -137,7 +165,8 @@ _lib.sdva_status_string.argtypes = [_I]
 EXPORTED = ("kv_append_quant", "kv_append_quant_ragged", "verify_attn_workspace_size", "verify_attn",
             "verify_attn_tree", "verify_attn_ragged", "verify_step", "verify_attn_noalloc", "spec_accept", "spec_accept_lazy", "spec_accept_tree",
             "spec_accept_sampled_workspace_size", "spec_accept_sampled", "kv_append_packed", "prompt_attn",
-            "token_logprobs", "sdva_debug_set_wait_limit", "sdva_status_string")
+            "token_logprobs", "kv_append_rope", "kv_append_packed_rope", "prompt_delta_workspace_size", "prompt_delta",
+            "verify_delta", "commit_delta", "sdva_debug_set_wait_limit", "sdva_status_string")
 NOALLOC_SCRATCH_BYTES = 32 << 20
 
 
@@ -485,10 +514,7 @@ def kv_append_packed(cache: KVCache, k_new: torch.Tensor, v_new: torch.Tensor, c
     shape = (T, cache.num_kv_heads, HEAD_DIM)
     ks, vs = _rows(k_new, shape, dev, "k_new"), _rows(v_new, shape, dev, "v_new")
     pages = page_table.shape[1]
-    for t in (cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales):
-        if t.get_device() != dev:
-            raise ValueError(f"the cache is on {t.device}, the current device is cuda:{dev}")
-    s = cache.struct()
+    s = _cache_on(cache, dev)
     rc = _lib.kv_append_packed(ctypes.byref(s), k_new.data_ptr(), v_new.data_ptr(), ks, vs, T,
                                _arg(cu_tokens, torch.int32, (B + 1,), dev, "cu_tokens"), B,
                                _arg(page_table, torch.int32, (B, pages), dev, "page_table"), pages,
@@ -554,6 +580,173 @@ def token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: torch.T
                              _arg(top_logprobs, torch.float32, lead + (top,), dev, "top_logprobs"),
                              _status_arg(status, dev), _stream(stream))
     _check("token_logprobs", rc)
+
+
+def _window_rows(t: torch.Tensor, shape: tuple, device: int, name: str) -> int:
+    """_rows of a bf16 [B][W][H][128] tensor whose B * W token rows are one stride apart."""
+    st = t.stride()
+    if (t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != device or st[3] != 1 or
+            (st[2] != HEAD_DIM and shape[2] > 1)):
+        if t.shape == shape and t.dtype is torch.bfloat16 and t.get_device() == device:
+            raise ValueError(f"{name} must be contiguous inside a token row")
+        _refuse(t, torch.bfloat16, shape, device, name)
+    if shape[1] == 1:  # of an axis of one the stride means nothing
+        return st[0] if shape[0] > 1 else shape[2] * HEAD_DIM
+    if shape[0] > 1 and st[0] != shape[1] * st[1]:
+        raise ValueError(f"the token rows of {name} must be one stride apart")
+    return st[1]
+
+
+def _cache_on(cache: KVCache, device: int) -> _KVCacheStruct:
+    for t in (cache.k_codes, cache.v_codes, cache.k_scales, cache.v_scales):
+        if t.get_device() != device:
+            raise ValueError(f"the cache is on {t.device}, the current device is cuda:{device}")
+    return cache.struct()
+
+
+def kv_append_rope(cache: KVCache, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor, rope: torch.Tensor,
+                   page_table: torch.Tensor, seq_lens: torch.Tensor, q_out: torch.Tensor,
+                   k_out: torch.Tensor | None = None, n_lane: torch.Tensor | None = None,
+                   positions: torch.Tensor | None = None, interleaved: bool = False,
+                   status: torch.Tensor | None = None, stream=None) -> None:
+    """q bf16 [B][W][Hq][128], k_new, v_new bf16 [B][W][Hkv][128], token rows of any
+    stride; rope fp32 [positions][rot_dim]: cosines, then sines (step.rope_table);
+    page_table int32 [B][max_pages]; seq_lens int32 [B]; q_out, k_out contiguous,
+    like q and k_new; n_lane int32 [B]; positions int32 [B][W] (None: seq_lens[b] + i)."""
+    dev = torch.cuda.current_device()
+    if q.dim() != 4 or k_new.dim() != 4 or v_new.dim() != 4 or page_table.dim() != 2 or rope.dim() != 2:
+        raise ValueError(f"q, k_new and v_new must be [B][W][H][{HEAD_DIM}], page_table [B][max_pages], "
+                         "rope [positions][rot_dim]")
+    B, W, Hq, Hkv, pages = q.shape[0], q.shape[1], q.shape[2], cache.num_kv_heads, page_table.shape[1]
+    kv = (B, W, Hkv, HEAD_DIM)
+    qs = _window_rows(q, (B, W, Hq, HEAD_DIM), dev, "q")
+    ks, vs = _window_rows(k_new, kv, dev, "k_new"), _window_rows(v_new, kv, dev, "v_new")
+    s = _cache_on(cache, dev)
+    rc = _lib.kv_append_rope(ctypes.byref(s), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs, Hq, B, W,
+                             _arg(n_lane, torch.int32, (B,), dev, "n_lane"),
+                             _arg(rope, torch.float32, rope.shape, dev, "rope"), rope.shape[0], rope.shape[1],
+                             ROPE_NEIGHBOURS if interleaved else ROPE_HALVES,
+                             _arg(positions, torch.int32, (B, W), dev, "positions"),
+                             _arg(page_table, torch.int32, (B, pages), dev, "page_table"), pages,
+                             _arg(seq_lens, torch.int32, (B,), dev, "seq_lens"),
+                             _arg(q_out, torch.bfloat16, (B, W, Hq, HEAD_DIM), dev, "q_out"),
+                             _arg(k_out, torch.bfloat16, kv, dev, "k_out"), _status_arg(status, dev), _stream(stream))
+    _check("kv_append_rope", rc)
+
+
+def kv_append_packed_rope(cache: KVCache, q: torch.Tensor, k_new: torch.Tensor, v_new: torch.Tensor,
+                          cu_tokens: torch.Tensor, rope: torch.Tensor, page_table: torch.Tensor,
+                          seq_lens: torch.Tensor, q_out: torch.Tensor, k_out: torch.Tensor | None = None,
+                          interleaved: bool = False, status: torch.Tensor | None = None, stream=None) -> None:
+    """kv_append_packed with the rotation of kv_append_rope: q bf16 [T][Hq][128],
+    k_new, v_new bf16 [T][Hkv][128], token rows of any stride; q_out, k_out
+    contiguous, like q and k_new."""
+    dev = torch.cuda.current_device()
+    if q.dim() != 3 or k_new.dim() != 3 or v_new.dim() != 3 or page_table.dim() != 2 or rope.dim() != 2:
+        raise ValueError(f"q, k_new and v_new must be [T][H][{HEAD_DIM}], page_table [B][max_pages], "
+                         "rope [positions][rot_dim]")
+    T, Hq, Hkv, B, pages = q.shape[0], q.shape[1], cache.num_kv_heads, seq_lens.numel(), page_table.shape[1]
+    kv = (T, Hkv, HEAD_DIM)
+    qs = _rows(q, (T, Hq, HEAD_DIM), dev, "q")
+    ks, vs = _rows(k_new, kv, dev, "k_new"), _rows(v_new, kv, dev, "v_new")
+    s = _cache_on(cache, dev)
+    rc = _lib.kv_append_packed_rope(ctypes.byref(s), q.data_ptr(), k_new.data_ptr(), v_new.data_ptr(), qs, ks, vs, Hq, T,
+                                    _arg(cu_tokens, torch.int32, (B + 1,), dev, "cu_tokens"), B,
+                                    _arg(rope, torch.float32, rope.shape, dev, "rope"), rope.shape[0], rope.shape[1],
+                                    ROPE_NEIGHBOURS if interleaved else ROPE_HALVES,
+                                    _arg(page_table, torch.int32, (B, pages), dev, "page_table"), pages,
+                                    _arg(seq_lens, torch.int32, (B,), dev, "seq_lens"),
+                                    _arg(q_out, torch.bfloat16, (T, Hq, HEAD_DIM), dev, "q_out"),
+                                    _arg(k_out, torch.bfloat16, kv, dev, "k_out"), _status_arg(status, dev),
+                                    _stream(stream))
+    _check("kv_append_packed_rope", rc)
+
+
+def _state(state: torch.Tensor, device: int) -> tuple:
+    """The address, slots and heads of a contiguous fp32 [slots][Hv][128][128] pool of states."""
+    if state.dim() != 4:
+        raise ValueError(f"state must be [slots][Hv][{HEAD_DIM}][{HEAD_DIM}]")
+    n, Hv = state.shape[0], state.shape[1]
+    return _arg(state, torch.float32, (n, Hv, HEAD_DIM, HEAD_DIM), device, "state"), n, Hv
+
+
+def prompt_delta_workspace_size(total_tokens: int, num_lanes: int, num_k_heads: int, num_v_heads: int) -> int:
+    return int(_lib.prompt_delta_workspace_size(total_tokens, num_lanes, num_k_heads, num_v_heads))
+
+
+def prompt_delta(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                 beta: torch.Tensor, cu_tokens: torch.Tensor, slots: torch.Tensor, scale: float, out: torch.Tensor,
+                 workspace: torch.Tensor, seq_lens: torch.Tensor | None = None, qk_eps: float = 1e-6,
+                 status: torch.Tensor | None = None, stream=None) -> None:
+    """state fp32 [slots][Hv][128][128] (values by keys, in/out); q, k bf16
+    [T][Hk][128], v bf16 [T][Hv][128], token rows of any stride; log_decay, beta
+    fp32 [T][Hv]; cu_tokens int32 [B + 1]; slots int32 [B]; out bf16 [T][Hv][128];
+    workspace: uint8 device tensor of at least prompt_delta_workspace_size(T, B, Hk,
+    Hv) bytes; seq_lens int32 [B] (0: the lane starts from zeros)."""
+    dev = torch.cuda.current_device()
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError(f"q, k and v must be [T][H][{HEAD_DIM}]")
+    p, n, Hv = _state(state, dev)
+    T, Hk, B = q.shape[0], q.shape[1], slots.numel()
+    qk, vs_ = (T, Hk, HEAD_DIM), (T, Hv, HEAD_DIM)
+    qs, ks, vs = _rows(q, qk, dev, "q"), _rows(k, qk, dev, "k"), _rows(v, vs_, dev, "v")
+    if workspace.get_device() != dev:
+        raise ValueError(f"workspace must be on the current device, cuda:{dev}")
+    rc = _lib.prompt_delta(p, n, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+                           _arg(log_decay, torch.float32, (T, Hv), dev, "log_decay"),
+                           _arg(beta, torch.float32, (T, Hv), dev, "beta"), Hk, Hv, T,
+                           _arg(cu_tokens, torch.int32, (B + 1,), dev, "cu_tokens"), B,
+                           _arg(slots, torch.int32, (B,), dev, "slots"),
+                           _arg(seq_lens, torch.int32, (B,), dev, "seq_lens"), float(scale), float(qk_eps),
+                           _arg(out, torch.bfloat16, vs_, dev, "out"), _dptr(workspace, None, "workspace"),
+                           workspace.numel() * workspace.element_size(), _status_arg(status, dev), _stream(stream))
+    _check("prompt_delta", rc)
+
+
+def verify_delta(state: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, log_decay: torch.Tensor,
+                 beta: torch.Tensor, slots: torch.Tensor, scale: float, out: torch.Tensor,
+                 deltas: torch.Tensor | None = None, n_lane: torch.Tensor | None = None,
+                 parent: torch.Tensor | None = None, qk_eps: float = 1e-6, status: torch.Tensor | None = None,
+                 stream=None) -> None:
+    """state fp32 [slots][Hv][128][128] (values by keys); q, k bf16 [B][W][Hk][128],
+    v bf16 [B][W][Hv][128], token rows of any stride; log_decay, beta fp32
+    [B][W][Hv]; slots int32 [B]; out bf16, deltas fp32 [B][W][Hv][128] (None: the
+    window is committed to the state); n_lane int32 [B]; parent int32 [B][W]."""
+    dev = torch.cuda.current_device()
+    if q.dim() != 4 or k.dim() != 4 or v.dim() != 4:
+        raise ValueError(f"q, k and v must be [B][W][H][{HEAD_DIM}]")
+    p, n, Hv = _state(state, dev)
+    B, W, Hk = q.shape[:3]
+    qk, vs_, g = (B, W, Hk, HEAD_DIM), (B, W, Hv, HEAD_DIM), (B, W, Hv)
+    qs, ks, vs = _window_rows(q, qk, dev, "q"), _window_rows(k, qk, dev, "k"), _window_rows(v, vs_, dev, "v")
+    rc = _lib.verify_delta(p, n, q.data_ptr(), k.data_ptr(), v.data_ptr(), qs, ks, vs,
+                           _arg(log_decay, torch.float32, g, dev, "log_decay"),
+                           _arg(beta, torch.float32, g, dev, "beta"), Hk, Hv, B, W,
+                           _arg(n_lane, torch.int32, (B,), dev, "n_lane"),
+                           _arg(parent, torch.int32, (B, W), dev, "parent"),
+                           _arg(slots, torch.int32, (B,), dev, "slots"), float(scale), float(qk_eps),
+                           _arg(out, torch.bfloat16, vs_, dev, "out"), _arg(deltas, torch.float32, vs_, dev, "deltas"),
+                           _status_arg(status, dev), _stream(stream))
+    _check("verify_delta", rc)
+
+
+def commit_delta(state: torch.Tensor, k: torch.Tensor, log_decay: torch.Tensor, deltas: torch.Tensor,
+                 slots: torch.Tensor, accept_len: torch.Tensor, path: torch.Tensor | None = None,
+                 status: torch.Tensor | None = None, stream=None) -> None:
+    """state fp32 [slots][Hv][128][128] (in/out); k, log_decay, deltas as verify_delta
+    took and wrote them; accept_len int32 [B]; path int32 [B][W] (None: a chain)."""
+    dev = torch.cuda.current_device()
+    if k.dim() != 4:
+        raise ValueError(f"k must be [B][W][Hk][{HEAD_DIM}]")
+    p, n, Hv = _state(state, dev)
+    B, W, Hk = k.shape[:3]
+    ks = _window_rows(k, (B, W, Hk, HEAD_DIM), dev, "k")
+    rc = _lib.commit_delta(p, n, k.data_ptr(), ks, _arg(log_decay, torch.float32, (B, W, Hv), dev, "log_decay"),
+                           _arg(deltas, torch.float32, (B, W, Hv, HEAD_DIM), dev, "deltas"), Hk, Hv, B, W,
+                           _arg(accept_len, torch.int32, (B,), dev, "accept_len"),
+                           _arg(path, torch.int32, (B, W), dev, "path"), _arg(slots, torch.int32, (B,), dev, "slots"),
+                           _status_arg(status, dev), _stream(stream))
+    _check("commit_delta", rc)
 
 
 def raw_library() -> ctypes.CDLL:
