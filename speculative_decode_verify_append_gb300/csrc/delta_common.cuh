@@ -1,13 +1,17 @@
 // delta_common.cuh -- what the kernels of the gated delta rule share.
 //
 // A value head has a state S of 128 value rows by 128 key columns, fp32.  With
-// k and q a token's key and query of the head's key head, as they are, and
-// r_k = 1 / sqrt(|k|^2 + eps), r_q likewise (1 for a negative eps):
-//     u_t = b_t (v_t - r_k e^g_t S_p k_t)
-//     S_t = e^g_t S_p + r_k u_t k_t'
-//     o_t = scale r_q S_t q_t
-// Products with k and q themselves are exact to start with; the factors go to
-// the results.
+// k' = 2^-e k and q' = 2^-e q a token's key and query brought to a largest
+// element in [1, 2) (exact), and r = 2^e / sqrt(|k|^2 + eps) their factor
+// (2^e for a negative eps), so that kn = r k':
+//     u_t = b_t (v_t - r e^g_t S_p k'_t)
+//     S_t = e^g_t S_p + r u_t k'_t'
+//     o_t = scale r_q S_t q'_t
+// k' and q' are exact in fp16: the 8 bits of a bf16 number, and elements below
+// 2^-14 of the row's largest to 2^-25 of it.  The other operand of a product on
+// the tensor cores goes in two fp16 parts, x = hi + lo + at most 2^-25 or 2^-23
+// |x|, so that the state keeps what fp32 gives it; what goes to the output
+// alone is taken in one part (2^-12 of a value, bf16's rounding is 2^-9).
 #pragma once
 
 #include "sdva_common.cuh"
@@ -27,6 +31,35 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 __device__ __forceinline__ float norm_factor(float sum_sq, float eps) {
   return eps < 0.0f ? 1.0f : rsqrtf(sum_sq + eps);
+}
+
+// The power of two that brings a magnitude to [1, 2) (to [2, 4) at fp32's upper
+// end, below 1 for subnormals), and its inverse.
+struct Scale {
+  float down, up;
+};
+__device__ __forceinline__ Scale scale_of_row(float amax) {
+  const uint32_t e = min(max(__float_as_uint(amax) >> 23, 1u), 253u);
+  return {__uint_as_float((254u - e) << 23), __uint_as_float(e << 23)};
+}
+// r = 2^e / sqrt(|k|^2 + eps) from sum_sq = |k'|^2.  eps 2^-2e overflows for rows
+// below 2^-64 or so, whose kn is below 2^-54 then and taken as 0.
+__device__ __forceinline__ float row_factor(float sum_sq, float eps, Scale s) {
+  return eps < 0.0f ? s.up : rsqrtf(sum_sq + eps * s.down * s.down);
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit elements held as two to a thread.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+// Two values in two fp16 parts.
+__device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
+  const __half2 h = __floats2half2_rn(x0, x1);
+  const float2 f = __half22float2(h);
+  hi = *reinterpret_cast<const uint32_t*>(&h);
+  lo = pack_f16x2(x0 - f.x, x1 - f.y);
 }
 
 }  // namespace delta
