@@ -62,5 +62,13 @@ __device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint
   lo = pack_f16x2(x0 - f.x, x1 - f.y);
 }
 
+__device__ __forceinline__ void split_f16(float2 x, uint32_t& hi, uint32_t& lo) { split_f16(x.x, x.y, hi, lo); }
+
+__device__ __forceinline__ float max3(float x, float y, float z) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(x), "f"(y), "f"(z));
+  return r;
+}
+
 }  // namespace delta
 }  // namespace sdva

@@ -12,17 +12,32 @@
 // what a chain does.  Both calls are bound by the state: 64 KB a head, read by
 // verify_delta and also written by commit_delta and by a committed window.
 //
-// verify_delta: a warp has 16 value rows of a head's state in registers, as the
-// tensor cores' B operand (and, committed, as their accumulators); its loads are
-// the first thing a CTA issues, under which the window's rows are normalised,
-// multiplied with each other and T is solved for, 16 columns in 16 lanes.
-// commit_delta: fp32 multiply-adds of one row of the state per warp.
+// verify_delta has two kernels.  rows_kernel takes a chain of up to kSeqRows
+// tokens one after the other in fp32: a warp has 16 value rows of a head's state
+// in registers, eight lanes to a row, and needs no other warp.
+// window_kernel takes up to 16 in the form above: a CTA has a head, a warp 16
+// value rows of its state as the tensor cores' B operand (and, committed, as
+// their accumulators).  The state's loads are the first thing that it issues;
+// under them the window's rows are normalised, and under the products with S
+// two more warps multiply the rows with each other and solve for T and P, a
+// column to a lane.
+// commit_delta: fp32 multiply-adds, eight value rows of a state to a warp.
 #include "delta_common.cuh"
+#include "tc_primitives.cuh"
 
 namespace sdva {
 namespace {
 
 using namespace delta;
+using tc::f2_pack;
+using tc::f2_unpack;
+using tc::ffma2;
+using tc::fmul2;
+
+__device__ __forceinline__ float f2_sum(unsigned long long x) {
+  const float2 f = f2_unpack(x);
+  return f.x + f.y;
+}
 
 struct VerifyArgs {
   float* state;
@@ -42,7 +57,6 @@ struct VerifyArgs {
   float scale, eps;
 };
 
-constexpr int kRows = kMaxWindow;  // of the tensor cores' tile; rows behind the lane's count are zeros
 
 __device__ __forceinline__ int key_at(int row, int piece) { return row * 256 + ((piece ^ (row & 7)) << 4); }
 // 16 x 16 fp16, 32-byte rows: their two pieces change places every four rows
@@ -50,99 +64,333 @@ __device__ __forceinline__ int tri_at(int row, int col) {
   return row * 32 + (((col >> 3) ^ ((row >> 2) & 1)) << 4) + (col & 7) * 2;
 }
 
+// The lane's rows, and what is wrong with it (then none).
+struct LaneRows {
+  int n, slot, wrong;
+};
+__device__ __forceinline__ LaneRows lane_rows(const VerifyArgs& a, int b) {
+  LaneRows r = {a.n_lane != nullptr ? a.n_lane[b] : a.window, a.slots[b], 0};
+  if (r.n < 0 || r.n > a.window) {
+    r.wrong = SDVA_STATUS_BAD_COUNT;
+  } else if (r.n > 0 && (r.slot < 0 || r.slot >= a.num_slots)) {
+    r.wrong = SDVA_STATUS_BAD_PAGE;
+  }
+  if (r.wrong) r.n = r.slot = 0;
+  return r;
+}
+
+constexpr int kSeqRows = 4;
+constexpr int kSeqThreads = 128;
+
+// Value rows 4 i + lane / 8 of a warp's 16; key dims 4 (lane & 7) + 32 p.
+template <bool kCommit>
+__global__ void __launch_bounds__(kSeqThreads) rows_kernel(VerifyArgs a) {
+  const int h = blockIdx.y, b = blockIdx.z, th = threadIdx.x, lane = th & 31, W = a.window;
+  const int kh = h / (a.hv / a.hk), j = lane & 7, gr = lane >> 3;
+  const int row16 = (blockIdx.x * (kSeqThreads / 32) + (th >> 5)) * 16;
+  const LaneRows lr = lane_rows(a, b);
+  if (lr.wrong && blockIdx.x == 0 && h == 0 && th == 0) raise_status(a.status, lr.wrong);
+  const int n = lr.n;
+  float* const st = a.state + ((size_t)lr.slot * a.hv + h) * kStateElems + (size_t)(row16 + gr) * kHeadDim + 4 * j;
+  unsigned long long S[4][4][2];
+  if (n > 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float4 x = *reinterpret_cast<const float4*>(st + (size_t)4 * i * kHeadDim + 32 * p);
+        S[i][p][0] = f2_pack(x.x, x.y);
+        S[i][p][1] = f2_pack(x.z, x.w);
+      }
+  }
+  const int row = row16 + 4 * (j & 3) + gr;  // the value row whose results this thread writes (j < 4)
+  for (int t = 0; t < W; ++t) {
+    const size_t r = (size_t)b * W + t, at = (r * a.hv + h) * kHeadDim + row;
+    if (t >= n) {
+      if (j < 4) {
+        a.out[at] = 0;
+        if (!kCommit) a.deltas[at] = 0.0f;
+      }
+      continue;
+    }
+    const uint16_t* const kr = a.k + r * (size_t)a.k_stride + (size_t)kh * kHeadDim + 4 * j;
+    const uint16_t* const qr = a.q + r * (size_t)a.q_stride + (size_t)kh * kHeadDim + 4 * j;
+    const uint16_t* const vr = a.v + r * (size_t)a.v_stride + (size_t)h * kHeadDim + row16 + gr;
+    uint2 kw[4], qw[4];
+    float v[4];
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      kw[p] = __ldg(reinterpret_cast<const uint2*>(kr + 32 * p));
+      qw[p] = __ldg(reinterpret_cast<const uint2*>(qr + 32 * p));
+      v[p] = __uint_as_float((uint32_t)__ldg(vr + 4 * p) << 16);
+    }
+    const float eg = expf(a.log_decay[r * a.hv + h]), beta = a.beta[r * a.hv + h];
+    unsigned long long k2[4][2], q2[4][2], kk2 = 0, qq2 = 0, kq2 = 0;
+#pragma unroll
+    for (int p = 0; p < 4; ++p) {
+      k2[p][0] = f2_pack(bf16_lo(kw[p].x), bf16_hi(kw[p].x));
+      k2[p][1] = f2_pack(bf16_lo(kw[p].y), bf16_hi(kw[p].y));
+      q2[p][0] = f2_pack(bf16_lo(qw[p].x), bf16_hi(qw[p].x));
+      q2[p][1] = f2_pack(bf16_lo(qw[p].y), bf16_hi(qw[p].y));
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        kk2 = ffma2(k2[p][e], k2[p][e], kk2);
+        qq2 = ffma2(q2[p][e], q2[p][e], qq2);
+        kq2 = ffma2(k2[p][e], q2[p][e], kq2);
+      }
+    }
+    float sum[11];  // k.k, q.q, k.q, then S k and S q of the four rows
+    sum[0] = f2_sum(kk2), sum[1] = f2_sum(qq2), sum[2] = f2_sum(kq2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      unsigned long long x = 0, y = 0;
+#pragma unroll
+      for (int p = 0; p < 4; ++p)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          x = ffma2(S[i][p][e], k2[p][e], x);
+          y = ffma2(S[i][p][e], q2[p][e], y);
+        }
+      sum[3 + i] = f2_sum(x);
+      sum[7 + i] = f2_sum(y);
+    }
+#pragma unroll
+    for (int o = 1; o < 8; o <<= 1)
+#pragma unroll
+      for (int x = 0; x < 11; ++x) sum[x] += __shfl_xor_sync(0xffffffffu, sum[x], o);
+    const float rk = norm_factor(sum[0], a.eps), rq = norm_factor(sum[1], a.eps);
+    float w[4], o = 0.0f, mine = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = rk * (beta * (v[i] - rk * eg * sum[3 + i]));
+      if ((j & 3) == i) {
+        mine = w[i];
+        o = a.scale * rq * fmaf(eg, sum[7 + i], w[i] * sum[2]);
+      }
+    }
+    if (j < 4) {
+      a.out[at] = (uint16_t)(pack_bf16x2(o, 0.0f) & 0xFFFFu);
+      if (!kCommit) a.deltas[at] = mine;
+    }
+    if (kCommit || t + 1 < n) {
+      const unsigned long long eg2 = f2_pack(eg, eg);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const unsigned long long w2 = f2_pack(w[i], w[i]);
+#pragma unroll
+        for (int p = 0; p < 4; ++p)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) S[i][p][e] = ffma2(w2, k2[p][e], fmul2(eg2, S[i][p][e]));
+      }
+    }
+  }
+  if (kCommit && n > 0) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const float2 x = f2_unpack(S[i][p][0]), y = f2_unpack(S[i][p][1]);
+        *reinterpret_cast<float4*>(st + (size_t)4 * i * kHeadDim + 32 * p) = make_float4(x.x, x.y, y.x, y.y);
+      }
+  }
+}
+
+constexpr int kRows = kMaxWindow;  // of the tensor cores' tile; rows behind the lane's count are zeros
+constexpr int kWarps = 8;          // with a part of the state
+constexpr int kThreads = (kWarps + 2) * 32;
+
 struct VerifySmem {
-  alignas(16) uint8_t key[2][kRows * kHeadDim * 2];  // k', q' in fp16
-  alignas(16) uint8_t tri[3][kRows * kRows * 2];     // T in two parts, P
-  float gram[2][kRows][kRows + 1];                   // k' . k', q' . k'
+  // k', q' in fp16.  Of 16 key dims a B operand's thread c has 4 c .. 4 c + 3 of the
+  // state, so that the rows hold dims 0 1 4 5 8 9 12 13, then 2 3 6 7 10 11 14 15.
+  alignas(16) uint8_t key[2][kRows * kHeadDim * 2];
+  alignas(16) uint8_t tri[3][kRows * kRows * 2];  // T in two parts, P
+  float gram[2][kRows][kRows + 1];                // k' . k', q' . k'
   alignas(16) float a[kRows][kRows];
-  float d[kRows][33];  // D, and a in column 16
-  float r[2][kRows];   // factors of k', q'
-  float k_own[kRows];  // 1 / sqrt(|k|^2 + eps)
+  float d[2][kRows][kRows + 1];  // D, and a in column 16; a copy for T and one for P
+  float r[2][kRows];             // factors of k', q'
+  float k_own[kRows];            // 1 / sqrt(|k|^2 + eps)
   float fa[kRows], beta[kRows], eg[kRows], fc[kRows], o1[kRows], o2[kRows];
   float t_up, c_up, f;
   int par[kRows];
 };
 
-// kWarps warps of 16 value rows each; kCommit: the window's updates go to the state.
-template <int kWarps, bool kCommit>
-__global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) verify_delta_kernel(VerifyArgs a) {
-  constexpr int kThreads = kWarps * 32;
+// Over the 16 lanes of a half warp.
+__device__ __forceinline__ float half_max(float x) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  return x;
+}
+
+// What the two further warps do: the products of rows (m = 0: k' with k', then T;
+// m = 1: q' with k', then P).
+template <bool kCommit>
+__device__ __forceinline__ void solve(VerifySmem& s, const VerifyArgs& a, int m, int n, int lane) {
+  const int g = lane >> 2, c = lane & 3, j = lane & 15;
+  const uint32_t kbase = smem_u32(s.key[0]), base = smem_u32(s.key[m]);
+  // D by columns; lane 16 stands for the state in front of the window, the root's parent
+  if (lane <= kRows) {
+    float d = lane == kRows ? 1.0f : 0.0f;
+    for (int i = 0; i < n; ++i) {
+      if (a.parent != nullptr && i > 0) d = s.d[m][s.par[i]][lane];
+      d = i == lane ? 1.0f : i < lane && lane < kRows ? 0.0f : d * s.eg[i];
+      s.d[m][i][lane] = d;
+    }
+  }
+  float acc[2][4] = {};
+#pragma unroll
+  for (int ks = 0; ks < 8; ++ks) {
+    uint32_t f[4], b0[2], b1[2];
+    ldmatrix_x4(base + key_at(lane & 15, 2 * ks + (lane >> 4)), f[0], f[1], f[2], f[3]);
+    ldmatrix_x4(kbase + key_at((lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)), b0[0], b1[0], b0[1], b1[1]);
+    mma_f16_16816(acc[0], f, b0[0], b1[0]);
+    mma_f16_16816(acc[1], f, b0[1], b1[1]);
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) s.gram[m][g + (i >> 1) * 8][8 * t + 2 * c + (i & 1)] = acc[t][i];
+  __syncwarp();
+  // a column to a lane (lanes 16 .. 31 do the same again)
+  const float rk = s.r[0][j];
+  float d[kRows];
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) d[i] = i < n ? s.d[m][i][j] : 0.0f;
+  if (m == 1) {
+    float p[kRows], top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      p[i] = d[i] != 0.0f ? d[i] * rk * s.gram[1][i][j] : 0.0f;
+      top = fmaxf(top, fabsf(p[i]));
+    }
+    const Scale ps = scale_of_row(half_max(top));
+    if (lane < kRows) {
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) *reinterpret_cast<__half*>(s.tri[2] + tri_at(i, j)) = __float2half_rn(p[i] * ps.down);
+      const float rq = a.scale * s.r[1][j], fall = j < n ? s.d[1][j][kRows] : 0.0f;
+      s.o1[j] = rq * fall;
+      s.o2[j] = rq * ps.up;
+    }
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i)
+    if (lane < kRows) s.a[i][j] = i > j && d[i] != 0.0f ? s.beta[i] * s.r[0][i] * (d[i] * rk) * s.gram[0][i][j] : 0.0f;
+  __syncwarp();
+  float t[kRows], top = 0.0f;
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) {
+    if (i >= n) {  // no update needs these rows
+      t[i] = 0.0f;
+      continue;
+    }
+    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int l = 0; l < i; l += 4) {
+      const float4 r = *reinterpret_cast<const float4*>(&s.a[i][l]);
+      x[0] = fmaf(r.x, t[l], x[0]);
+      if (l + 1 < i) x[1] = fmaf(r.y, t[l + 1], x[1]);
+      if (l + 2 < i) x[2] = fmaf(r.z, t[l + 2], x[2]);
+      if (l + 3 < i) x[3] = fmaf(r.w, t[l + 3], x[3]);
+    }
+    t[i] = i == j ? 1.0f : -((x[0] + x[1]) + (x[2] + x[3]));
+    top = fmaxf(top, fabsf(t[i]));
+  }
+  const Scale ts = scale_of_row(half_max(top));
+  if (lane < kRows) {
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const float x = t[i] * ts.down;
+      const __half hi = __float2half_rn(x);
+      *reinterpret_cast<__half*>(s.tri[0] + tri_at(i, j)) = hi;
+      *reinterpret_cast<__half*>(s.tri[1] + tri_at(i, j)) = __float2half_rn(x - __half2float(hi));
+    }
+    s.fa[j] = j < n ? s.d[0][j][kRows] * rk : 0.0f;
+  }
+  if (lane == 0) s.t_up = ts.up;
+  if (kCommit) {  // factors of the updates in the state behind the window, the largest brought to [1, 2)
+    const float fc = j < n ? s.d[0][n - 1][j] * rk : 0.0f;
+    const Scale cs = scale_of_row(fmaxf(half_max(fabsf(fc)), 0x1p-60f));  // S times the scales stays in fp32's range
+    if (lane < kRows) s.fc[j] = fc * cs.down;
+    if (lane == 0) {
+      s.c_up = cs.up;
+      s.f = s.d[0][n - 1][kRows];
+    }
+  }
+}
+
+// kCommit: the window's updates go to the state.
+template <bool kCommit>
+__global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(VerifyArgs a) {
   __shared__ VerifySmem s;
-  const int h = blockIdx.y, b = blockIdx.z, th = threadIdx.x, lane = th & 31, warp = th >> 5, W = a.window;
+  const int h = blockIdx.x, b = blockIdx.y, th = threadIdx.x, lane = th & 31, warp = th >> 5, W = a.window;
   const int g = lane >> 2, c = lane & 3, kh = h / (a.hv / a.hk);
-  const int row16 = (blockIdx.x * kWarps + warp) * 16;  // the warp's first value row
-  const bool report = blockIdx.x == 0 && h == 0 && th == 0;
+  const int row16 = warp * 16;  // the warp's first value row
+  const bool report = h == 0 && th == 0;
   const size_t row0 = (size_t)b * W;
-  int n = a.n_lane != nullptr ? a.n_lane[b] : W;
-  const int slot = a.slots[b];
-  int wrong = 0;
-  if (n < 0 || n > W) {
-    wrong = SDVA_STATUS_BAD_COUNT;
-  } else if (n > 0 && (slot < 0 || slot >= a.num_slots)) {
-    wrong = SDVA_STATUS_BAD_PAGE;
-  }
-  if (wrong) {
-    if (report) raise_status(a.status, wrong);
-    n = 0;
-  }
-  // S[t][m]: value rows 8 t + g, key dims 16 m + 2 c, + 1 and 16 m + 8 + 2 c, + 1
-  float2 S[2][8][2];
-  float* const st = a.state + ((size_t)(n > 0 ? slot : 0) * a.hv + h) * kStateElems + (size_t)(row16 + g) * kHeadDim + 2 * c;
-  if (n > 0) {
+  const LaneRows lr = lane_rows(a, b);
+  int n = lr.n;
+  if (lr.wrong && report) raise_status(a.status, lr.wrong);
+  // S[t][m]: value rows 8 t + g, key dims 16 m + 4 c ..
+  float4 S[2][8];
+  float* const st = a.state + ((size_t)lr.slot * a.hv + h) * kStateElems + (size_t)(row16 + g) * kHeadDim + 4 * c;
+  uint32_t v[2][2] = {};  // rows g, g + 8 of the window, value rows 8 t + 2 c, + 1
+  if (warp < kWarps && n > 0) {
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int m = 0; m < 8; ++m)
+      for (int m = 0; m < 8; ++m) S[t][m] = *reinterpret_cast<const float4*>(st + (size_t)8 * t * kHeadDim + 16 * m);
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          S[t][m][i] = *reinterpret_cast<const float2*>(st + (size_t)8 * t * kHeadDim + 16 * m + 8 * i);
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (g + 8 * i < n)
+          v[i][t] = *reinterpret_cast<const uint32_t*>(a.v + (row0 + g + 8 * i) * (size_t)a.v_stride +
+                                                       (size_t)h * kHeadDim + row16 + 8 * t + 2 * c);
   }
-  uint32_t v[2][2];  // rows g, g + 8 of the window, value rows 8 t + 2 c, + 1
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      v[i][t] = g + 8 * i < n ? *reinterpret_cast<const uint32_t*>(a.v + (row0 + g + 8 * i) * (size_t)a.v_stride +
-                                                                  (size_t)h * kHeadDim + row16 + 8 * t + 2 * c)
-                              : 0u;
   int bad = 0;
-  if (th < kRows) {
-    const bool on = th < n;
-    s.eg[th] = on ? expf(a.log_decay[(row0 + th) * a.hv + h]) : 1.0f;
-    s.beta[th] = on ? a.beta[(row0 + th) * a.hv + h] : 0.0f;
-    const int p = on && a.parent != nullptr && th > 0 ? a.parent[row0 + th] : th - 1;
-    bad = on && th > 0 && (p < 0 || p >= th);
-    s.par[th] = p;
+  if (th >= kThreads - kRows) {
+    const int i = th - (kThreads - kRows);
+    const bool on = i < n;
+    s.eg[i] = on ? expf(a.log_decay[(row0 + i) * a.hv + h]) : 1.0f;
+    s.beta[i] = on ? a.beta[(row0 + i) * a.hv + h] : 0.0f;
+    const int p = on && a.parent != nullptr && i > 0 ? a.parent[row0 + i] : i - 1;
+    bad = on && i > 0 && (p < 0 || p >= i);
+    s.par[i] = p;
   }
   // k' and q': 16 threads to a row
+  if (th < kWarps * 32) {
 #pragma unroll
-  for (int x = th; x < 2 * kRows * 16; x += kThreads) {
-    const int m = x >> 8, r = (x >> 4) & 15, p = x & 15;
-    uint4 w = make_uint4(0u, 0u, 0u, 0u);
-    if (r < n)
-      w = __ldg(reinterpret_cast<const uint4*>((m ? a.q : a.k) + (row0 + r) * (size_t)(m ? a.q_stride : a.k_stride) +
-                                               (size_t)kh * kHeadDim) + p);
-    uint32_t y[4] = {w.x, w.y, w.z, w.w}, top = 0;
+    for (int x = th; x < 2 * kRows * 16; x += kWarps * 32) {
+      const int m = x >> 8, r = (x >> 4) & 15, p = x & 15;
+      uint4 w = make_uint4(0u, 0u, 0u, 0u);
+      if (r < n)
+        w = __ldg(reinterpret_cast<const uint4*>((m ? a.q : a.k) + (row0 + r) * (size_t)(m ? a.q_stride : a.k_stride) +
+                                                 (size_t)kh * kHeadDim) + p);
+      uint32_t y[4] = {w.x, w.y, w.z, w.w}, top = 0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) top = max(top, max(y[i] << 16 & 0x7FFF0000u, y[i] & 0x7FFF0000u));
+      for (int i = 0; i < 4; ++i) top = max(top, max(y[i] << 16 & 0x7FFF0000u, y[i] & 0x7FFF0000u));
 #pragma unroll
-    for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const Scale sc = scale_of_row(__uint_as_float(top));
-    float sq = 0.0f;
+      for (int o = 1; o < 16; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+      const Scale sc = scale_of_row(__uint_as_float(top));
+      float sq = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float f0 = bf16_lo(y[i]) * sc.down, f1 = bf16_hi(y[i]) * sc.down;
-      sq = fmaf(f0, f0, fmaf(f1, f1, sq));
-      y[i] = pack_f16x2(f0, f1);
+      for (int i = 0; i < 4; ++i) {
+        const float f0 = bf16_lo(y[i]) * sc.down, f1 = bf16_hi(y[i]) * sc.down;
+        sq = fmaf(f0, f0, fmaf(f1, f1, sq));
+        y[i] = pack_f16x2(f0, f1);
+      }
+#pragma unroll
+      for (int o = 1; o < 16; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
+      if (p == 0) {
+        const float f = r < n ? row_factor(sq, a.eps, sc) : 0.0f;
+        s.r[m][r] = f;
+        // small rows by their own sum, where 2^-e would overflow
+        if (m == 0) s.k_own[r] = a.eps < 0.0f ? 1.0f : sc.up < 1.0f ? rsqrtf(fmaf(sq * sc.up, sc.up, a.eps)) : f * sc.down;
+      }
+      uint8_t* const to = s.key[m] + 8 * (p & 1);
+      *reinterpret_cast<uint2*>(to + key_at(r, p & ~1)) = make_uint2(y[0], y[2]);
+      *reinterpret_cast<uint2*>(to + key_at(r, p | 1)) = make_uint2(y[1], y[3]);
     }
-#pragma unroll
-    for (int o = 1; o < 16; o <<= 1) sq += __shfl_xor_sync(0xffffffffu, sq, o);
-    if (p == 0) {
-      s.r[m][r] = r < n ? row_factor(sq, a.eps, sc) : 0.0f;
-      // small rows by their own sum, where 2^-e would overflow
-      if (m == 0) s.k_own[r] = a.eps < 0.0f ? 1.0f : sc.up < 1.0f ? rsqrtf(fmaf(sq * sc.up, sc.up, a.eps)) : s.r[0][r] * sc.down;
-    }
-    *reinterpret_cast<uint4*>(s.key[m] + key_at(r, p)) = make_uint4(y[0], y[1], y[2], y[3]);
   }
   if (__syncthreads_or(bad)) {
     if (report) raise_status(a.status, SDVA_STATUS_BAD_TREE);
@@ -151,50 +399,32 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) verify_delta_kernel(
   const size_t at0 = (row0 * a.hv + h) * kHeadDim + row16 + 2 * c;  // this thread's first output
   const size_t row_out = (size_t)a.hv * kHeadDim;
   if (n == 0) {
-    for (int r = g; r < W; r += 8)
+    if (warp < kWarps)
+      for (int r = g; r < W; r += 8)
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        *reinterpret_cast<uint32_t*>(a.out + at0 + r * row_out + 8 * t) = 0u;
-        if (!kCommit) *reinterpret_cast<float2*>(a.deltas + at0 + r * row_out + 8 * t) = make_float2(0.0f, 0.0f);
-      }
+        for (int t = 0; t < 2; ++t) {
+          *reinterpret_cast<uint32_t*>(a.out + at0 + r * row_out + 8 * t) = 0u;
+          if (!kCommit) *reinterpret_cast<float2*>(a.deltas + at0 + r * row_out + 8 * t) = make_float2(0.0f, 0.0f);
+        }
+    return;
+  }
+  if (warp >= kWarps) {
+    solve<kCommit>(s, a, warp - kWarps, n, lane);
+    __syncthreads();
     return;
   }
   const uint32_t kbase = smem_u32(s.key[0]), qbase = smem_u32(s.key[1]);
   const int a_row = lane & 15, a_piece = lane >> 4;
-  // the products of rows, one warp for k' and one for q'; D meanwhile by a third where there is one
-  if (warp < 2) {
-    float acc[2][4] = {};
-#pragma unroll
-    for (int ks = 0; ks < 8; ++ks) {
-      uint32_t f[4], b0[2], b1[2];
-      ldmatrix_x4((warp ? qbase : kbase) + key_at(a_row, 2 * ks + a_piece), f[0], f[1], f[2], f[3]);
-      ldmatrix_x4(kbase + key_at((lane & 7) + ((lane >> 4) << 3), 2 * ks + ((lane >> 3) & 1)), b0[0], b1[0], b0[1], b1[1]);
-      mma_f16_16816(acc[0], f, b0[0], b1[0]);
-      mma_f16_16816(acc[1], f, b0[1], b1[1]);
-    }
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) s.gram[warp][g + (i >> 1) * 8][8 * t + 2 * c + (i & 1)] = acc[t][i];
-  }
-  if (warp == 2 && lane <= kRows) {
-    // lane 16 stands for the state in front of the window, the root's parent
-    float d = lane == kRows ? 1.0f : 0.0f;
-    for (int i = 0; i < n; ++i) {
-      if (a.parent != nullptr && i > 0) d = s.d[s.par[i]][lane];
-      d = i == lane ? 1.0f : i < lane && lane < kRows ? 0.0f : d * s.eg[i];
-      s.d[i][lane] = d;
-    }
-  }
-  // S q' and S k' need no T
+  // S k' in two parts, S q' in one
   float sig[2], isig[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     float x = 0.0f;
 #pragma unroll
-    for (int m = 0; m < 8; ++m)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) x = fmaxf(x, fmaxf(fabsf(S[t][m][i].x), fabsf(S[t][m][i].y)));
+    for (int m = 0; m < 8; ++m) {
+      x = max3(x, fabsf(S[t][m].x), fabsf(S[t][m].y));
+      x = max3(x, fabsf(S[t][m].z), fabsf(S[t][m].w));
+    }
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
     const Scale sc = scale_of_row(x);
@@ -209,84 +439,11 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) verify_delta_kernel(
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       uint32_t hi[2], lo[2];
-#pragma unroll
-      for (int i = 0; i < 2; ++i) split_f16(S[t][m][i].x * sig[t], S[t][m][i].y * sig[t], hi[i], lo[i]);
+      split_f16(f2_unpack(fmul2(f2_pack(S[t][m].x, S[t][m].y), f2_pack(sig[t], sig[t]))), hi[0], lo[0]);
+      split_f16(f2_unpack(fmul2(f2_pack(S[t][m].z, S[t][m].w), f2_pack(sig[t], sig[t]))), hi[1], lo[1]);
       mma_f16_16816(sk[0][t], fk, hi[0], hi[1]);
       mma_f16_16816(sk[1][t], fk, lo[0], lo[1]);
       mma_f16_16816(sq[t], fq, hi[0], hi[1]);
-    }
-  }
-  __syncthreads();
-  if (warp == 0) {
-    // T and P: a column to a lane (lanes 16 .. 31 do the same again)
-    const int j = lane & 15;
-    const float rk = s.r[0][j];
-    float p[kRows], top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const float d = i < n ? s.d[i][j] : 0.0f, w = d * rk;
-      const float x = s.beta[i] * s.r[0][i] * w * s.gram[0][i][j];
-      p[i] = w * s.gram[1][i][j];
-      if (d == 0.0f) p[i] = 0.0f;
-      top = fmaxf(top, fabsf(p[i]));
-      if (lane < kRows) s.a[i][j] = i > j && d != 0.0f ? x : 0.0f;
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const Scale ps = scale_of_row(top);
-    if (lane < kRows) {
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) *reinterpret_cast<__half*>(s.tri[2] + tri_at(i, j)) = __float2half_rn(p[i] * ps.down);
-      const float rq = s.r[1][j], fall = j < n ? s.d[j][kRows] : 0.0f;
-      s.fa[j] = fall * rk;
-      s.o1[j] = a.scale * rq * fall;
-      s.o2[j] = a.scale * rq * ps.up;
-    }
-    __syncwarp();
-    float t[kRows];
-    top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      if (i >= n) {  // rows of the unit matrix, which no update needs
-        t[i] = 0.0f;
-        continue;
-      }
-      float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int l = 0; l < i; l += 4) {
-        const float4 r = *reinterpret_cast<const float4*>(&s.a[i][l]);
-        x[0] = fmaf(r.x, t[l], x[0]);
-        if (l + 1 < i) x[1] = fmaf(r.y, t[l + 1], x[1]);
-        if (l + 2 < i) x[2] = fmaf(r.z, t[l + 2], x[2]);
-        if (l + 3 < i) x[3] = fmaf(r.w, t[l + 3], x[3]);
-      }
-      t[i] = i == j ? 1.0f : -((x[0] + x[1]) + (x[2] + x[3]));
-      top = fmaxf(top, fabsf(t[i]));
-    }
-#pragma unroll
-    for (int o = 8; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    const Scale ts = scale_of_row(top);
-    if (lane < kRows) {
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) {
-        const float x = t[i] * ts.down;
-        const __half hi = __float2half_rn(x);
-        *reinterpret_cast<__half*>(s.tri[0] + tri_at(i, j)) = hi;
-        *reinterpret_cast<__half*>(s.tri[1] + tri_at(i, j)) = __float2half_rn(x - __half2float(hi));
-      }
-    }
-    if (lane == 0) s.t_up = ts.up;
-    if (kCommit) {  // factors of the updates in the state behind the window, the largest brought to [1, 2)
-      const float fc = j < n ? s.d[n - 1][j] * rk : 0.0f;
-      float x = fabsf(fc);
-#pragma unroll
-      for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-      const Scale cs = scale_of_row(fmaxf(x, 0x1p-60f));  // S times the scales stays in fp32's range
-      if (lane < kRows) s.fc[j] = fc * cs.down;
-      if (lane == 0) {
-        s.c_up = cs.up;
-        s.f = s.d[n - 1][kRows];
-      }
     }
   }
   __syncthreads();
@@ -365,7 +522,7 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) verify_delta_kernel(
     }
   }
   if (kCommit) {
-    // S as accumulators: value rows g (t = 0) and g + 8 (t = 1), key dims 8 x + 2 c, + 1
+    // S as accumulators: value rows g (t = 0) and g + 8 (t = 1), columns as the rows of k' have their dims
     float in[2], back[2];
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
@@ -377,19 +534,24 @@ __global__ void __launch_bounds__(kWarps * 32, 16 / kWarps) verify_delta_kernel(
     const float f = s.f, c_up = s.c_up;
     const float c_down = 1.0f / c_up;  // a power of two
 #pragma unroll
+    for (int t = 0; t < 2; ++t) in[t] *= f;
+#pragma unroll
     for (int m = 0; m < 8; ++m) {
       uint32_t k0[2], k1[2];
       ldmatrix_x4_trans(kbase + key_at((lane & 7) + ((lane >> 3) & 1) * 8, 2 * m + (lane >> 4)), k0[0], k1[0], k0[1], k1[1]);
+      float lo[4] = {S[0][m].x * in[0] * c_down, S[0][m].y * in[0] * c_down, S[1][m].x * in[1] * c_down,
+                     S[1][m].y * in[1] * c_down};
+      float hi[4] = {S[0][m].z * in[0] * c_down, S[0][m].w * in[0] * c_down, S[1][m].z * in[1] * c_down,
+                     S[1][m].w * in[1] * c_down};
+      mma_f16_16816(lo, ch, k0[0], k1[0]);
+      mma_f16_16816(hi, ch, k0[1], k1[1]);
+      mma_f16_16816(lo, cl, k0[0], k1[0]);
+      mma_f16_16816(hi, cl, k0[1], k1[1]);
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        float acc[4] = {S[0][m][i].x * f * in[0] * c_down, S[0][m][i].y * f * in[0] * c_down,
-                        S[1][m][i].x * f * in[1] * c_down, S[1][m][i].y * f * in[1] * c_down};
-        mma_f16_16816(acc, ch, k0[i], k1[i]);
-        mma_f16_16816(acc, cl, k0[i], k1[i]);
-        *reinterpret_cast<float2*>(st + 16 * m + 8 * i) = make_float2(acc[0] * c_up * back[0], acc[1] * c_up * back[0]);
-        *reinterpret_cast<float2*>(st + (size_t)8 * kHeadDim + 16 * m + 8 * i) =
-            make_float2(acc[2] * c_up * back[1], acc[3] * c_up * back[1]);
-      }
+      for (int t = 0; t < 2; ++t)
+        *reinterpret_cast<float4*>(st + (size_t)8 * t * kHeadDim + 16 * m) =
+            make_float4(lo[2 * t] * c_up * back[t], lo[2 * t + 1] * c_up * back[t], hi[2 * t] * c_up * back[t],
+                        hi[2 * t + 1] * c_up * back[t]);
     }
   }
 }
@@ -407,18 +569,18 @@ struct CommitArgs {
   int num_slots, hk, hv, window;
 };
 
-constexpr int kCommitThreads = 256;
-constexpr int kCommitRows = 32;  // value rows of a CTA, four to a warp
+constexpr int kCommitThreads = 128;
+constexpr int kCommitRows = 32;  // value rows of a CTA, eight to a warp
 
 __global__ void __launch_bounds__(kCommitThreads) commit_delta_kernel(CommitArgs a) {
   constexpr int kPer = kCommitRows / (kCommitThreads / 32);
   const int h = blockIdx.y, b = blockIdx.z, th = threadIdx.x, lane = th & 31, W = a.window;
   const int kh = h / (a.hv / a.hk), r0 = blockIdx.x * kCommitRows;
-  __shared__ int at[kMaxWindow];
-  __shared__ float eg[kMaxWindow];
-  __shared__ float w[kCommitRows][kMaxWindow];
+  __shared__ alignas(16) float w[kMaxWindow][kCommitRows];
+  __shared__ alignas(16) uint16_t key[kMaxWindow][kHeadDim];
   const bool report = blockIdx.x == 0 && h == 0 && th == 0;
   const int m = a.accept_len[b] + 1, slot = a.slots[b];
+  const size_t row0 = (size_t)b * W;
   if (m < 0 || m > W) {
     if (report) raise_status(a.status, SDVA_STATUS_BAD_COUNT);
     return;
@@ -430,44 +592,74 @@ __global__ void __launch_bounds__(kCommitThreads) commit_delta_kernel(CommitArgs
   }
   // a warp's rows, four key dims of each to a thread
   float* const st = a.state + ((size_t)slot * a.hv + h) * kStateElems + (size_t)(r0 + (th >> 5) * kPer) * kHeadDim + 4 * lane;
-  float4 S[kPer];
+  unsigned long long S[kPer][2];
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) S[i] = *reinterpret_cast<const float4*>(st + i * kHeadDim);
-  const size_t row0 = (size_t)b * W;
-  int wrong = 0;
-  if (th < m) {
-    const int p = a.path != nullptr ? a.path[row0 + th] : th;
+  for (int i = 0; i < kPer; ++i) {
+    const float4 x = *reinterpret_cast<const float4*>(st + i * kHeadDim);
+    S[i][0] = f2_pack(x.x, x.y);
+    S[i][1] = f2_pack(x.z, x.w);
+  }
+  // committed slot j's update (eight threads) and key (sixteen), and in every warp's lane j its e^g
+  const auto slot_of = [&](int j) { return a.path != nullptr ? a.path[row0 + j] : j; };
+  bool wrong = false;
+  float eg = 1.0f;
+  if (lane < m) {
+    const int p = slot_of(lane);
     wrong = p < 0 || p >= W;
-    at[th] = p;
-    if (!wrong) eg[th] = expf(a.log_decay[(row0 + p) * a.hv + h]);
+    if (!wrong) eg = expf(a.log_decay[(row0 + p) * a.hv + h]);
+  }
+  {
+    const int j = th >> 3, p = j < m ? slot_of(j) : -1;
+    if (p >= 0 && p < W)
+      *reinterpret_cast<float4*>(&w[j][4 * (th & 7)]) =
+          __ldg(reinterpret_cast<const float4*>(a.deltas + ((row0 + p) * a.hv + h) * kHeadDim + r0) + (th & 7));
+  }
+#pragma unroll
+  for (int x = th; x < kMaxWindow * 16; x += kCommitThreads) {
+    const int j = x >> 4, p = j < m ? slot_of(j) : -1;
+    if (p >= 0 && p < W)
+      *reinterpret_cast<uint4*>(&key[j][8 * (x & 15)]) =
+          __ldg(reinterpret_cast<const uint4*>(a.k + (row0 + p) * (size_t)a.k_stride + (size_t)kh * kHeadDim) + (x & 15));
   }
   if (__syncthreads_or(wrong)) {
     if (report) raise_status(a.status, SDVA_STATUS_BAD_TREE);
     return;
   }
   // products of e^g behind each update, and all of them
-  float f = 1.0f;
-  for (int x = th; x < m * kCommitRows; x += kCommitThreads) {
-    const int j = x / kCommitRows, r = x % kCommitRows;
-    float rest = 1.0f;
-    for (int i = j + 1; i < m; ++i) rest *= eg[i];
-    w[r][j] = rest * a.deltas[((row0 + at[j]) * a.hv + h) * kHeadDim + r0 + r];
+  float rest = __shfl_down_sync(0xffffffffu, eg, 1);
+  if (lane == 31) rest = 1.0f;
+#pragma unroll
+  for (int o = 1; o < kMaxWindow; o <<= 1) {
+    const float x = __shfl_down_sync(0xffffffffu, rest, o);
+    if (lane + o < 32) rest *= x;
   }
-  for (int i = 0; i < m; ++i) f *= eg[i];
-  __syncthreads();
+  const float f = __shfl_sync(0xffffffffu, rest * eg, 0);
+  const unsigned long long f2 = f2_pack(f, f);
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) S[i].x *= f, S[i].y *= f, S[i].z *= f, S[i].w *= f;
+  for (int i = 0; i < kPer; ++i) S[i][0] = fmul2(S[i][0], f2), S[i][1] = fmul2(S[i][1], f2);
   for (int j = 0; j < m; ++j) {
-    const uint2 kk = __ldg(reinterpret_cast<const uint2*>(a.k + (row0 + at[j]) * (size_t)a.k_stride + (size_t)kh * kHeadDim) + lane);
-    const float k0 = bf16_lo(kk.x), k1 = bf16_hi(kk.x), k2 = bf16_lo(kk.y), k3 = bf16_hi(kk.y);
+    const float cj = __shfl_sync(0xffffffffu, rest, j);
+    const uint2 kk = *reinterpret_cast<const uint2*>(&key[j][4 * lane]);
+    const unsigned long long k0 = f2_pack(cj * bf16_lo(kk.x), cj * bf16_hi(kk.x));
+    const unsigned long long k1 = f2_pack(cj * bf16_lo(kk.y), cj * bf16_hi(kk.y));
+    const float4* const wj = reinterpret_cast<const float4*>(&w[j][(th >> 5) * kPer]);
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const float x = w[(th >> 5) * kPer + i][j];
-      S[i].x = fmaf(x, k0, S[i].x), S[i].y = fmaf(x, k1, S[i].y), S[i].z = fmaf(x, k2, S[i].z), S[i].w = fmaf(x, k3, S[i].w);
+    for (int i = 0; i < kPer / 4; ++i) {
+      const float4 x = wj[i];
+      const float y[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const unsigned long long w2 = f2_pack(y[e], y[e]);
+        S[4 * i + e][0] = ffma2(w2, k0, S[4 * i + e][0]);
+        S[4 * i + e][1] = ffma2(w2, k1, S[4 * i + e][1]);
+      }
     }
   }
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) *reinterpret_cast<float4*>(st + i * kHeadDim) = S[i];
+  for (int i = 0; i < kPer; ++i) {
+    const float2 x = f2_unpack(S[i][0]), y = f2_unpack(S[i][1]);
+    *reinterpret_cast<float4*>(st + i * kHeadDim) = make_float4(x.x, x.y, y.x, y.y);
+  }
 }
 
 }  // namespace
@@ -511,10 +703,14 @@ extern "C" int verify_delta(float* state, int num_slots, const void* q, const vo
                         window,
                         scale,
                         qk_eps};
-  constexpr int kWarps = 4;
-  const dim3 grid(kHeadDim / (16 * kWarps), num_v_heads, num_lanes);
-  (deltas == nullptr ? verify_delta_kernel<kWarps, true>
-                     : verify_delta_kernel<kWarps, false>)<<<grid, kWarps * 32, 0, reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
+  if (window <= kSeqRows && parent == nullptr) {
+    const dim3 grid(kHeadDim / (16 * (kSeqThreads / 32)), num_v_heads, num_lanes);
+    (deltas == nullptr ? rows_kernel<true> : rows_kernel<false>)<<<grid, kSeqThreads, 0, cs>>>(a);
+  } else {
+    const dim3 grid(num_v_heads, num_lanes);
+    (deltas == nullptr ? window_kernel<true> : window_kernel<false>)<<<grid, kThreads, 0, cs>>>(a);
+  }
   return cudaGetLastError() == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
 }
 
