@@ -60,9 +60,7 @@ struct VerifyArgs {
 
 __device__ __forceinline__ int key_at(int row, int piece) { return row * 256 + ((piece ^ (row & 7)) << 4); }
 // 16 x 16 fp16, 32-byte rows: their two pieces change places every four rows
-__device__ __forceinline__ int tri_at(int row, int col) {
-  return row * 32 + (((col >> 3) ^ ((row >> 2) & 1)) << 4) + (col & 7) * 2;
-}
+__device__ __forceinline__ int tri_at(int row, int piece) { return row * 32 + ((piece ^ ((row >> 2) & 1)) << 4); }
 
 // The lane's rows, and what is wrong with it (then none).
 struct LaneRows {
@@ -203,39 +201,55 @@ struct VerifySmem {
   // k', q' in fp16.  Of 16 key dims a B operand's thread c has 4 c .. 4 c + 3 of the
   // state, so that the rows hold dims 0 1 4 5 8 9 12 13, then 2 3 6 7 10 11 14 15.
   alignas(16) uint8_t key[2][kRows * kHeadDim * 2];
-  alignas(16) uint8_t tri[3][kRows * kRows * 2];  // T in two parts, P
+  alignas(16) uint8_t tri[3][kRows * kRows * 2];  // the columns of T in two parts and of P
   float gram[2][kRows][kRows + 1];                // k' . k', q' . k'
-  alignas(16) float a[kRows][kRows];
-  float d[2][kRows][kRows + 1];  // D, and a in column 16; a copy for T and one for P
-  float r[2][kRows];             // factors of k', q'
-  float k_own[kRows];            // 1 / sqrt(|k|^2 + eps)
-  float fa[kRows], beta[kRows], eg[kRows], fc[kRows], o1[kRows], o2[kRows];
+  alignas(16) float a[kRows][kRows + 4];          // columns of A
+  float d[2][kRows][kRows + 1];                   // D, and a in column 16 (trees); a copy for T and one for P
+  alignas(16) float r[2][kRows];                  // factors of k', q'
+  alignas(16) float eg[kRows];
+  alignas(16) float beta[kRows];
+  alignas(16) int par[kRows];
+  float k_own[kRows];  // 1 / sqrt(|k|^2 + eps)
+  float fa[kRows], fc[kRows], o1[kRows], o2[kRows];
   float t_up, c_up, f;
-  int par[kRows];
 };
 
-// Over the 16 lanes of a half warp.
-__device__ __forceinline__ float half_max(float x) {
+__device__ __forceinline__ float warp_max(float x) {
 #pragma unroll
-  for (int o = 8; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
   return x;
 }
 
+// Sixteen floats of shared memory, the same for every thread.
+__device__ __forceinline__ void load16(const float* p, float (&x)[kRows]) {
+#pragma unroll
+  for (int i = 0; i < kRows; i += 4) {
+    const float4 y = *reinterpret_cast<const float4*>(p + i);
+    x[i] = y.x, x[i + 1] = y.y, x[i + 2] = y.z, x[i + 3] = y.w;
+  }
+}
+// A column of T or P as a row of shared memory; what fp16 leaves over into the next matrix.
+template <bool kParts>
+__device__ __forceinline__ void store_column(uint8_t* to, int j, const float (&x)[kRows], float scale) {
+  uint32_t hi[kRows / 2], lo[kRows / 2];
+#pragma unroll
+  for (int i = 0; i < kRows / 2; ++i) split_f16(x[2 * i] * scale, x[2 * i + 1] * scale, hi[i], lo[i]);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    *reinterpret_cast<uint4*>(to + tri_at(j, p)) = make_uint4(hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
+    if (kParts)
+      *reinterpret_cast<uint4*>(to + kRows * kRows * 2 + tri_at(j, p)) =
+          make_uint4(lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
+  }
+}
+
 // What the two further warps do: the products of rows (m = 0: k' with k', then T;
-// m = 1: q' with k', then P).
+// m = 1: q' with k', then P).  Lane j < 16 has column j; lane 16 stands for the
+// state in front of the window, the root's parent, so that its column of D is a.
 template <bool kCommit>
 __device__ __forceinline__ void solve(VerifySmem& s, const VerifyArgs& a, int m, int n, int lane) {
-  const int g = lane >> 2, c = lane & 3, j = lane & 15;
+  const int g = lane >> 2, c = lane & 3, j = min(lane, kRows);
   const uint32_t kbase = smem_u32(s.key[0]), base = smem_u32(s.key[m]);
-  // D by columns; lane 16 stands for the state in front of the window, the root's parent
-  if (lane <= kRows) {
-    float d = lane == kRows ? 1.0f : 0.0f;
-    for (int i = 0; i < n; ++i) {
-      if (a.parent != nullptr && i > 0) d = s.d[m][s.par[i]][lane];
-      d = i == lane ? 1.0f : i < lane && lane < kRows ? 0.0f : d * s.eg[i];
-      s.d[m][i][lane] = d;
-    }
-  }
   float acc[2][4] = {};
 #pragma unroll
   for (int ks = 0; ks < 8; ++ks) {
@@ -245,76 +259,97 @@ __device__ __forceinline__ void solve(VerifySmem& s, const VerifyArgs& a, int m,
     mma_f16_16816(acc[0], f, b0[0], b1[0]);
     mma_f16_16816(acc[1], f, b0[1], b1[1]);
   }
+  float d[kRows], x[kRows];
+  load16(s.eg, x);
+  if (a.parent == nullptr) {
+    float y = j == kRows ? 1.0f : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) d[i] = y = i == j ? 1.0f : y * x[i];
+  } else {
+    int par[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; i += 4) {
+      const int4 y = *reinterpret_cast<const int4*>(s.par + i);
+      par[i] = y.x, par[i + 1] = y.y, par[i + 2] = y.z, par[i + 3] = y.w;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const float y = i == 0 ? (j == kRows ? 1.0f : 0.0f) : s.d[m][par[i]][j];
+      d[i] = i == j ? 1.0f : i < j && j < kRows ? 0.0f : y * x[i];
+      if (lane <= kRows) s.d[m][i][j] = d[i];
+    }
+  }
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
     for (int i = 0; i < 4; ++i) s.gram[m][g + (i >> 1) * 8][8 * t + 2 * c + (i & 1)] = acc[t][i];
-  __syncwarp();
-  // a column to a lane (lanes 16 .. 31 do the same again)
-  const float rk = s.r[0][j];
-  float d[kRows];
+  // the factors that go with a: lane 16 has a, lane i gets a_i
+  if (lane == kRows) {
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) d[i] = i < n ? s.d[m][i][j] : 0.0f;
+    for (int i = 0; i < kRows; ++i) (m ? s.o1 : s.fa)[i] = d[i];
+  }
+  __syncwarp();
+  const bool on = lane < kRows;
+  const float rk = on ? s.r[0][j] : 0.0f;
+  float top = 0.0f;
   if (m == 1) {
-    float p[kRows], top = 0.0f;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-      p[i] = d[i] != 0.0f ? d[i] * rk * s.gram[1][i][j] : 0.0f;
-      top = fmaxf(top, fabsf(p[i]));
+      x[i] = on && d[i] != 0.0f ? d[i] * rk * s.gram[1][i][j & 15] : 0.0f;
+      top = fmaxf(top, fabsf(x[i]));
     }
-    const Scale ps = scale_of_row(half_max(top));
-    if (lane < kRows) {
-#pragma unroll
-      for (int i = 0; i < kRows; ++i) *reinterpret_cast<__half*>(s.tri[2] + tri_at(i, j)) = __float2half_rn(p[i] * ps.down);
-      const float rq = a.scale * s.r[1][j], fall = j < n ? s.d[1][j][kRows] : 0.0f;
-      s.o1[j] = rq * fall;
+    const Scale ps = scale_of_row(warp_max(top));
+    if (on) {
+      store_column<false>(s.tri[2], j, x, ps.down);
+      const float rq = a.scale * s.r[1][j];
+      s.o1[j] = j < n ? rq * s.o1[j] : 0.0f;
       s.o2[j] = rq * ps.up;
     }
     return;
   }
+  float br[kRows];
+  load16(s.beta, x);
+  load16(s.r[0], br);
 #pragma unroll
-  for (int i = 0; i < kRows; ++i)
-    if (lane < kRows) s.a[i][j] = i > j && d[i] != 0.0f ? s.beta[i] * s.r[0][i] * (d[i] * rk) * s.gram[0][i][j] : 0.0f;
-  __syncwarp();
-  float t[kRows], top = 0.0f;
+  for (int i = 0; i < kRows; ++i) br[i] = on && i > j && d[i] != 0.0f ? br[i] * x[i] * (d[i] * rk) * s.gram[0][i][j & 15] : 0.0f;
+  if (on) {
 #pragma unroll
-  for (int i = 0; i < kRows; ++i) {
-    if (i >= n) {  // no update needs these rows
-      t[i] = 0.0f;
-      continue;
-    }
-    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-    for (int l = 0; l < i; l += 4) {
-      const float4 r = *reinterpret_cast<const float4*>(&s.a[i][l]);
-      x[0] = fmaf(r.x, t[l], x[0]);
-      if (l + 1 < i) x[1] = fmaf(r.y, t[l + 1], x[1]);
-      if (l + 2 < i) x[2] = fmaf(r.z, t[l + 2], x[2]);
-      if (l + 3 < i) x[3] = fmaf(r.w, t[l + 3], x[3]);
-    }
-    t[i] = i == j ? 1.0f : -((x[0] + x[1]) + (x[2] + x[3]));
-    top = fmaxf(top, fabsf(t[i]));
+    for (int i = 0; i < kRows; i += 4)
+      *reinterpret_cast<float4*>(&s.a[j][i]) = make_float4(br[i], br[i + 1], br[i + 2], br[i + 3]);
   }
-  const Scale ts = scale_of_row(half_max(top));
-  if (lane < kRows) {
+  __syncwarp();
+  // the columns of the inverse of 1 + A: as soon as a row is known it leaves the rows below
 #pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const float x = t[i] * ts.down;
-      const __half hi = __float2half_rn(x);
-      *reinterpret_cast<__half*>(s.tri[0] + tri_at(i, j)) = hi;
-      *reinterpret_cast<__half*>(s.tri[1] + tri_at(i, j)) = __float2half_rn(x - __half2float(hi));
+  for (int i = 0; i < kRows; ++i) x[i] = i == j ? 1.0f : 0.0f;
+#pragma unroll
+  for (int l = 0; l < kRows - 1; ++l) {
+#pragma unroll
+    for (int i = (l + 1) & ~3; i < kRows; i += 4) {
+      const float4 y = *reinterpret_cast<const float4*>(&s.a[l][i]);
+      if (i > l) x[i] = fmaf(-y.x, x[l], x[i]);
+      if (i + 1 > l) x[i + 1] = fmaf(-y.y, x[l], x[i + 1]);
+      if (i + 2 > l) x[i + 2] = fmaf(-y.z, x[l], x[i + 2]);
+      x[i + 3] = fmaf(-y.w, x[l], x[i + 3]);
     }
-    s.fa[j] = j < n ? s.d[0][j][kRows] * rk : 0.0f;
+  }
+#pragma unroll
+  for (int i = 0; i < kRows; ++i) top = fmaxf(top, fabsf(x[i]));
+  const Scale ts = scale_of_row(warp_max(top));
+  if (on) {
+    store_column<true>(s.tri[0], j, x, ts.down);
+    s.fa[j] = j < n ? s.fa[j] * rk : 0.0f;
   }
   if (lane == 0) s.t_up = ts.up;
   if (kCommit) {  // factors of the updates in the state behind the window, the largest brought to [1, 2)
-    const float fc = j < n ? s.d[0][n - 1][j] * rk : 0.0f;
-    const Scale cs = scale_of_row(fmaxf(half_max(fabsf(fc)), 0x1p-60f));  // S times the scales stays in fp32's range
-    if (lane < kRows) s.fc[j] = fc * cs.down;
-    if (lane == 0) {
-      s.c_up = cs.up;
-      s.f = s.d[0][n - 1][kRows];
-    }
+    float fc = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i)
+      if (i == n - 1) fc = d[i];
+    if (lane == kRows) s.f = fc;
+    fc = j < n ? fc * rk : 0.0f;
+    const Scale cs = scale_of_row(fmaxf(warp_max(fabsf(fc)), 0x1p-60f));  // S times the scales stays in fp32's range
+    if (on) s.fc[j] = fc * cs.down;
+    if (lane == 0) s.c_up = cs.up;
   }
 }
 
@@ -330,6 +365,19 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
   const LaneRows lr = lane_rows(a, b);
   int n = lr.n;
   if (lr.wrong && report) raise_status(a.status, lr.wrong);
+  // the window's rows first: what waits for them takes longer than what waits for the state
+  uint4 rows[2 * kRows * 16 / (kWarps * 32)];
+  constexpr int kPieces = sizeof(rows) / sizeof(rows[0]);  // of a thread: k', then q', 16 threads to a row
+  static_assert(kPieces == 2, "a thread has one piece of k' and one of q'");
+  if (warp < kWarps) {
+    const int r = th >> 4, p = th & 15;
+#pragma unroll
+    for (int m = 0; m < kPieces; ++m)
+      rows[m] = r < n ? __ldg(reinterpret_cast<const uint4*>((m ? a.q : a.k) +
+                                                             (row0 + r) * (size_t)(m ? a.q_stride : a.k_stride) +
+                                                             (size_t)kh * kHeadDim) + p)
+                      : make_uint4(0u, 0u, 0u, 0u);
+  }
   // S[t][m]: value rows 8 t + g, key dims 16 m + 4 c ..
   float4 S[2][8];
   float* const st = a.state + ((size_t)lr.slot * a.hv + h) * kStateElems + (size_t)(row16 + g) * kHeadDim + 4 * c;
@@ -357,15 +405,11 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
     bad = on && i > 0 && (p < 0 || p >= i);
     s.par[i] = p;
   }
-  // k' and q': 16 threads to a row
-  if (th < kWarps * 32) {
+  if (warp < kWarps) {
+    const int r = th >> 4, p = th & 15;
 #pragma unroll
-    for (int x = th; x < 2 * kRows * 16; x += kWarps * 32) {
-      const int m = x >> 8, r = (x >> 4) & 15, p = x & 15;
-      uint4 w = make_uint4(0u, 0u, 0u, 0u);
-      if (r < n)
-        w = __ldg(reinterpret_cast<const uint4*>((m ? a.q : a.k) + (row0 + r) * (size_t)(m ? a.q_stride : a.k_stride) +
-                                                 (size_t)kh * kHeadDim) + p);
+    for (int m = 0; m < kPieces; ++m) {
+      const uint4 w = rows[m];
       uint32_t y[4] = {w.x, w.y, w.z, w.w}, top = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = max(top, max(y[i] << 16 & 0x7FFF0000u, y[i] & 0x7FFF0000u));
@@ -477,10 +521,10 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
   }
   uint32_t fh[4], fl[4], fp[4];
   {
-    const uint32_t tri = smem_u32(s.tri[0]) + tri_at(a_row, 8 * a_piece);
-    ldmatrix_x4(tri, fh[0], fh[1], fh[2], fh[3]);
-    ldmatrix_x4(tri + kRows * kRows * 2, fl[0], fl[1], fl[2], fl[3]);
-    ldmatrix_x4(tri + 2 * kRows * kRows * 2, fp[0], fp[1], fp[2], fp[3]);
+    const uint32_t tri = smem_u32(s.tri[0]) + tri_at((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
+    ldmatrix_x4_trans(tri, fh[0], fh[1], fh[2], fh[3]);
+    ldmatrix_x4_trans(tri + kRows * kRows * 2, fl[0], fl[1], fl[2], fl[3]);
+    ldmatrix_x4_trans(tri + 2 * kRows * kRows * 2, fp[0], fp[1], fp[2], fp[3]);
   }
   uint32_t ch[4], cl[4];  // the updates with their factors, value rows by tokens
 #pragma unroll
