@@ -17,10 +17,9 @@
 // in registers, eight lanes to a row, and needs no other warp.
 // window_kernel takes up to 16 in the form above: a CTA has a head, a warp 16
 // value rows of its state as the tensor cores' B operand (and, committed, as
-// their accumulators).  The state's loads are the first thing that it issues;
-// under them the window's rows are normalised, and under the products with S
-// two more warps multiply the rows with each other and solve for T and P, a
-// column to a lane.
+// their accumulators), copied to shared memory while the window's rows are
+// normalised.  Two more warps multiply the rows with each other and solve for T
+// and P, a column to a lane, under the products with S.
 // commit_delta: fp32 multiply-adds, eight value rows of a state to a warp.
 #include "delta_common.cuh"
 #include "tc_primitives.cuh"
@@ -61,6 +60,8 @@ struct VerifyArgs {
 __device__ __forceinline__ int key_at(int row, int piece) { return row * 256 + ((piece ^ (row & 7)) << 4); }
 // 16 x 16 fp16, 32-byte rows: their two pieces change places every four rows
 __device__ __forceinline__ int tri_at(int row, int piece) { return row * 32 + ((piece ^ ((row >> 2) & 1)) << 4); }
+// 128 fp32: four threads read 64 bytes of a row, eight in one pass those of two rows
+__device__ __forceinline__ int state_at(int row, int piece) { return row * 512 + ((piece ^ ((row & 1) << 2)) << 4); }
 
 // The lane's rows, and what is wrong with it (then none).
 struct LaneRows {
@@ -206,9 +207,9 @@ struct VerifySmem {
   alignas(16) float a[kRows][kRows + 4];          // columns of A
   float d[2][kRows][kRows + 1];                   // D, and a in column 16 (trees); a copy for T and one for P
   alignas(16) float r[2][kRows];                  // factors of k', q'
-  alignas(16) float eg[kRows];
+  alignas(16) float eg[2][kRows];
   alignas(16) float beta[kRows];
-  alignas(16) int par[kRows];
+  alignas(16) int par[2][kRows];
   float k_own[kRows];  // 1 / sqrt(|k|^2 + eps)
   float fa[kRows], fc[kRows], o1[kRows], o2[kRows];
   float t_up, c_up, f;
@@ -243,11 +244,53 @@ __device__ __forceinline__ void store_column(uint8_t* to, int j, const float (&x
   }
 }
 
-// What the two further warps do: the products of rows (m = 0: k' with k', then T;
-// m = 1: q' with k', then P).  Lane j < 16 has column j; lane 16 stands for the
-// state in front of the window, the root's parent, so that its column of D is a.
+// D by columns, for each of the two further warps (m): lane j < 16 has column j;
+// lane 16 stands for the state in front of the window, the root's parent, so
+// that its column is a.  Returns whether a parent is wrong.
+__device__ __forceinline__ bool ways(VerifySmem& s, const VerifyArgs& a, int m, int n, size_t row0, int h, int lane,
+                                     float (&d)[kRows]) {
+  const int j = min(lane, kRows);
+  bool bad = false;
+  if (lane < kRows) {
+    const bool on = lane < n;
+    s.eg[m][lane] = on ? expf(a.log_decay[(row0 + lane) * a.hv + h]) : 1.0f;
+    if (m == 0) s.beta[lane] = on ? a.beta[(row0 + lane) * a.hv + h] : 0.0f;
+    int p = lane - 1;
+    if (on && a.parent != nullptr && lane > 0) {
+      p = a.parent[row0 + lane];
+      bad = p < 0 || p >= lane;
+      if (bad) p = 0;
+    }
+    s.par[m][lane] = p;
+  }
+  __syncwarp();
+  float x[kRows];
+  load16(s.eg[m], x);
+  if (a.parent == nullptr) {
+    float y = j == kRows ? 1.0f : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) d[i] = y = i == j ? 1.0f : y * x[i];
+  } else {
+    int par[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; i += 4) {
+      const int4 y = *reinterpret_cast<const int4*>(s.par[m] + i);
+      par[i] = y.x, par[i + 1] = y.y, par[i + 2] = y.z, par[i + 3] = y.w;
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+      const float y = i == 0 ? (j == kRows ? 1.0f : 0.0f) : s.d[m][par[i]][j];
+      d[i] = i == j ? 1.0f : i < j && j < kRows ? 0.0f : y * x[i];
+      if (lane <= kRows) s.d[m][i][j] = d[i];
+    }
+  }
+  return bad;
+}
+
+// What they do behind the barrier: the products of rows (m = 0: k' with k', then
+// T; m = 1: q' with k', then P).
 template <bool kCommit>
-__device__ __forceinline__ void solve(VerifySmem& s, const VerifyArgs& a, int m, int n, int lane) {
+__device__ __forceinline__ void solve(VerifySmem& s, const VerifyArgs& a, int m, int n, int lane, const float (&d)[kRows]) {
   const int g = lane >> 2, c = lane & 3, j = min(lane, kRows);
   const uint32_t kbase = smem_u32(s.key[0]), base = smem_u32(s.key[m]);
   float acc[2][4] = {};
@@ -259,26 +302,7 @@ __device__ __forceinline__ void solve(VerifySmem& s, const VerifyArgs& a, int m,
     mma_f16_16816(acc[0], f, b0[0], b1[0]);
     mma_f16_16816(acc[1], f, b0[1], b1[1]);
   }
-  float d[kRows], x[kRows];
-  load16(s.eg, x);
-  if (a.parent == nullptr) {
-    float y = j == kRows ? 1.0f : 0.0f;
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) d[i] = y = i == j ? 1.0f : y * x[i];
-  } else {
-    int par[kRows];
-#pragma unroll
-    for (int i = 0; i < kRows; i += 4) {
-      const int4 y = *reinterpret_cast<const int4*>(s.par + i);
-      par[i] = y.x, par[i + 1] = y.y, par[i + 2] = y.z, par[i + 3] = y.w;
-    }
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      const float y = i == 0 ? (j == kRows ? 1.0f : 0.0f) : s.d[m][par[i]][j];
-      d[i] = i == j ? 1.0f : i < j && j < kRows ? 0.0f : y * x[i];
-      if (lane <= kRows) s.d[m][i][j] = d[i];
-    }
-  }
+  float x[kRows];
 #pragma unroll
   for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -355,7 +379,7 @@ __device__ __forceinline__ void solve(VerifySmem& s, const VerifyArgs& a, int m,
 
 // kCommit: the window's updates go to the state.
 template <bool kCommit>
-__global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a) {
   __shared__ VerifySmem s;
   const int h = blockIdx.x, b = blockIdx.y, th = threadIdx.x, lane = th & 31, warp = th >> 5, W = a.window;
   const int g = lane >> 2, c = lane & 3, kh = h / (a.hv / a.hk);
@@ -378,15 +402,19 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
                                                              (size_t)kh * kHeadDim) + p)
                       : make_uint4(0u, 0u, 0u, 0u);
   }
-  // S[t][m]: value rows 8 t + g, key dims 16 m + 4 c ..
-  float4 S[2][8];
-  float* const st = a.state + ((size_t)lr.slot * a.hv + h) * kStateElems + (size_t)(row16 + g) * kHeadDim + 4 * c;
+  // the warp's 16 value rows of the state to its part of shared memory
+  extern __shared__ __align__(128) uint8_t state_smem[];
+  uint8_t* const mine = state_smem + warp * 16 * kHeadDim * 4;
+  float* const st = a.state + ((size_t)lr.slot * a.hv + h) * kStateElems + (size_t)row16 * kHeadDim;
   uint32_t v[2][2] = {};  // rows g, g + 8 of the window, value rows 8 t + 2 c, + 1
-  if (warp < kWarps && n > 0) {
+  float d[kRows];         // of the two further warps
+  bool bad = false;
+  if (warp < kWarps) {
+    if (n > 0) {
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int m = 0; m < 8; ++m) S[t][m] = *reinterpret_cast<const float4*>(st + (size_t)8 * t * kHeadDim + 16 * m);
+      for (int r = 0; r < 16; ++r) cp_async_16(smem_u32(mine) + state_at(r, lane), st + (size_t)r * kHeadDim + 4 * lane);
+    }
+    cp_async_commit();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -394,16 +422,8 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
         if (g + 8 * i < n)
           v[i][t] = *reinterpret_cast<const uint32_t*>(a.v + (row0 + g + 8 * i) * (size_t)a.v_stride +
                                                        (size_t)h * kHeadDim + row16 + 8 * t + 2 * c);
-  }
-  int bad = 0;
-  if (th >= kThreads - kRows) {
-    const int i = th - (kThreads - kRows);
-    const bool on = i < n;
-    s.eg[i] = on ? expf(a.log_decay[(row0 + i) * a.hv + h]) : 1.0f;
-    s.beta[i] = on ? a.beta[(row0 + i) * a.hv + h] : 0.0f;
-    const int p = on && a.parent != nullptr && i > 0 ? a.parent[row0 + i] : i - 1;
-    bad = on && i > 0 && (p < 0 || p >= i);
-    s.par[i] = p;
+  } else if (n > 0) {
+    bad = ways(s, a, warp - kWarps, n, row0, h, lane, d);
   }
   if (warp < kWarps) {
     const int r = th >> 4, p = th & 15;
@@ -443,6 +463,7 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
   const size_t at0 = (row0 * a.hv + h) * kHeadDim + row16 + 2 * c;  // this thread's first output
   const size_t row_out = (size_t)a.hv * kHeadDim;
   if (n == 0) {
+    cp_async_wait<0>();
     if (warp < kWarps)
       for (int r = g; r < W; r += 8)
 #pragma unroll
@@ -453,21 +474,27 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
     return;
   }
   if (warp >= kWarps) {
-    solve<kCommit>(s, a, warp - kWarps, n, lane);
+    solve<kCommit>(s, a, warp - kWarps, n, lane, d);
     __syncthreads();
     return;
   }
   const uint32_t kbase = smem_u32(s.key[0]), qbase = smem_u32(s.key[1]);
   const int a_row = lane & 15, a_piece = lane >> 4;
-  // S k' in two parts, S q' in one
+  cp_async_wait<0>();
+  __syncwarp();
+  // S k' in two parts, S q' in one; of the state value rows 8 t + g, key dims 16 m + 4 c ..
+  const auto state_of = [&](int t, int m) {
+    return *reinterpret_cast<const float4*>(mine + state_at(8 * t + g, 4 * m + c));
+  };
   float sig[2], isig[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     float x = 0.0f;
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
-      x = max3(x, fabsf(S[t][m].x), fabsf(S[t][m].y));
-      x = max3(x, fabsf(S[t][m].z), fabsf(S[t][m].w));
+      const float4 y = state_of(t, m);
+      x = max3(x, fabsf(y.x), fabsf(y.y));
+      x = max3(x, fabsf(y.z), fabsf(y.w));
     }
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -483,8 +510,9 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       uint32_t hi[2], lo[2];
-      split_f16(f2_unpack(fmul2(f2_pack(S[t][m].x, S[t][m].y), f2_pack(sig[t], sig[t]))), hi[0], lo[0]);
-      split_f16(f2_unpack(fmul2(f2_pack(S[t][m].z, S[t][m].w), f2_pack(sig[t], sig[t]))), hi[1], lo[1]);
+      const float4 y = state_of(t, m);
+      split_f16(f2_unpack(fmul2(f2_pack(y.x, y.y), f2_pack(sig[t], sig[t]))), hi[0], lo[0]);
+      split_f16(f2_unpack(fmul2(f2_pack(y.z, y.w), f2_pack(sig[t], sig[t]))), hi[1], lo[1]);
       mma_f16_16816(sk[0][t], fk, hi[0], hi[1]);
       mma_f16_16816(sk[1][t], fk, lo[0], lo[1]);
       mma_f16_16816(sq[t], fq, hi[0], hi[1]);
@@ -583,17 +611,16 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
     for (int m = 0; m < 8; ++m) {
       uint32_t k0[2], k1[2];
       ldmatrix_x4_trans(kbase + key_at((lane & 7) + ((lane >> 3) & 1) * 8, 2 * m + (lane >> 4)), k0[0], k1[0], k0[1], k1[1]);
-      float lo[4] = {S[0][m].x * in[0] * c_down, S[0][m].y * in[0] * c_down, S[1][m].x * in[1] * c_down,
-                     S[1][m].y * in[1] * c_down};
-      float hi[4] = {S[0][m].z * in[0] * c_down, S[0][m].w * in[0] * c_down, S[1][m].z * in[1] * c_down,
-                     S[1][m].w * in[1] * c_down};
+      const float4 s0 = state_of(0, m), s1 = state_of(1, m);
+      float lo[4] = {s0.x * in[0] * c_down, s0.y * in[0] * c_down, s1.x * in[1] * c_down, s1.y * in[1] * c_down};
+      float hi[4] = {s0.z * in[0] * c_down, s0.w * in[0] * c_down, s1.z * in[1] * c_down, s1.w * in[1] * c_down};
       mma_f16_16816(lo, ch, k0[0], k1[0]);
       mma_f16_16816(hi, ch, k0[1], k1[1]);
       mma_f16_16816(lo, cl, k0[0], k1[0]);
       mma_f16_16816(hi, cl, k0[1], k1[1]);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        *reinterpret_cast<float4*>(st + (size_t)8 * t * kHeadDim + 16 * m) =
+        *reinterpret_cast<float4*>(st + (size_t)(8 * t + g) * kHeadDim + 16 * m + 4 * c) =
             make_float4(lo[2 * t] * c_up * back[t], lo[2 * t + 1] * c_up * back[t], hi[2 * t] * c_up * back[t],
                         hi[2 * t + 1] * c_up * back[t]);
     }
@@ -753,7 +780,11 @@ extern "C" int verify_delta(float* state, int num_slots, const void* q, const vo
     (deltas == nullptr ? rows_kernel<true> : rows_kernel<false>)<<<grid, kSeqThreads, 0, cs>>>(a);
   } else {
     const dim3 grid(num_v_heads, num_lanes);
-    (deltas == nullptr ? window_kernel<true> : window_kernel<false>)<<<grid, kThreads, 0, cs>>>(a);
+    const auto kernel = deltas == nullptr ? window_kernel<true> : window_kernel<false>;
+    constexpr int bytes = (int)(kStateElems * sizeof(float));
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+      return SDVA_ERR_CUDA;
+    kernel<<<grid, kThreads, bytes, cs>>>(a);
   }
   return cudaGetLastError() == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
 }
