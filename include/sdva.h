@@ -715,7 +715,7 @@ int prompt_delta(float* state, int num_slots, const void* q, const void* k, cons
  *            S of its last one afterwards (a plain decode step; no parent then,
  *            else SDVA_ERR_INVALID for a window above 1).
  * Rows from a lane's count on, and all rows of a lane that is skipped, are
- * zeros in out and deltas; their inputs are not read.
+ * zeros in out and deltas; their inputs reach nothing.
  * Returns SDVA_OK or a negative SDVA_ERR_*.
  */
 int verify_delta(float* state, int num_slots, const void* q, const void* k, const void* v, int64_t q_stride,

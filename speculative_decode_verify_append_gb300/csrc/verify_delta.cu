@@ -17,7 +17,7 @@
 // in registers, eight lanes to a row, and needs no other warp.
 // window_kernel takes up to 16 in the form above: a CTA has a head, a warp 16
 // value rows of its state as the tensor cores' B operand (and, committed, as
-// their accumulators), copied to shared memory while the window's rows are
+// their accumulators), loaded into registers while the window's rows are
 // normalised.  Two more warps multiply the rows with each other and solve for T
 // and P, a column to a lane, under the products with S.
 // commit_delta: fp32 multiply-adds, eight value rows of a state to a warp.
@@ -60,10 +60,9 @@ struct VerifyArgs {
 __device__ __forceinline__ int key_at(int row, int piece) { return row * 256 + ((piece ^ (row & 7)) << 4); }
 // 16 x 16 fp16, 32-byte rows: their two pieces change places every four rows
 __device__ __forceinline__ int tri_at(int row, int piece) { return row * 32 + ((piece ^ ((row >> 2) & 1)) << 4); }
-// 128 fp32: four threads read 64 bytes of a row, eight in one pass those of two rows
-__device__ __forceinline__ int state_at(int row, int piece) { return row * 512 + ((piece ^ ((row & 1) << 2)) << 4); }
 
-// The lane's rows, and what is wrong with it (then none).
+// The lane's rows, and what is wrong with it (then none).  The window's own
+// arrays are read without waiting for it; what lies behind the count is dropped.
 struct LaneRows {
   int n, slot, wrong;
 };
@@ -199,6 +198,7 @@ constexpr int kWarps = 8;          // with a part of the state
 constexpr int kThreads = (kWarps + 2) * 32;
 
 struct VerifySmem {
+  uint4 raw[2][kWarps * 32];  // the window's k and q, 16 bytes to a thread
   // k', q' in fp16.  Of 16 key dims a B operand's thread c has 4 c .. 4 c + 3 of the
   // state, so that the rows hold dims 0 1 4 5 8 9 12 13, then 2 3 6 7 10 11 14 15.
   alignas(16) uint8_t key[2][kRows * kHeadDim * 2];
@@ -252,15 +252,14 @@ __device__ __forceinline__ bool ways(VerifySmem& s, const VerifyArgs& a, int m, 
   const int j = min(lane, kRows);
   bool bad = false;
   if (lane < kRows) {
-    const bool on = lane < n;
-    s.eg[m][lane] = on ? expf(a.log_decay[(row0 + lane) * a.hv + h]) : 1.0f;
-    if (m == 0) s.beta[lane] = on ? a.beta[(row0 + lane) * a.hv + h] : 0.0f;
-    int p = lane - 1;
-    if (on && a.parent != nullptr && lane > 0) {
-      p = a.parent[row0 + lane];
-      bad = p < 0 || p >= lane;
-      if (bad) p = 0;
-    }
+    const bool in = lane < a.window, on = lane < n;
+    const float ld = in ? a.log_decay[(row0 + lane) * a.hv + h] : 0.0f;
+    const float beta = in ? a.beta[(row0 + lane) * a.hv + h] : 0.0f;
+    int p = in && a.parent != nullptr ? a.parent[row0 + lane] : lane - 1;
+    bad = on && lane > 0 && (p < 0 || p >= lane);
+    if (bad || !on) p = max(lane - 1, 0);
+    s.eg[m][lane] = on ? expf(ld) : 1.0f;
+    if (m == 0) s.beta[lane] = on ? beta : 0.0f;
     s.par[m][lane] = p;
   }
   __syncwarp();
@@ -379,7 +378,7 @@ __device__ __forceinline__ void solve(VerifySmem& s, const VerifyArgs& a, int m,
 
 // kCommit: the window's updates go to the state.
 template <bool kCommit>
-__global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(VerifyArgs a) {
   __shared__ VerifySmem s;
   const int h = blockIdx.x, b = blockIdx.y, th = threadIdx.x, lane = th & 31, warp = th >> 5, W = a.window;
   const int g = lane >> 2, c = lane & 3, kh = h / (a.hv / a.hk);
@@ -389,32 +388,31 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a) {
   const LaneRows lr = lane_rows(a, b);
   int n = lr.n;
   if (lr.wrong && report) raise_status(a.status, lr.wrong);
-  // the window's rows first: what waits for them takes longer than what waits for the state
-  uint4 rows[2 * kRows * 16 / (kWarps * 32)];
-  constexpr int kPieces = sizeof(rows) / sizeof(rows[0]);  // of a thread: k', then q', 16 threads to a row
-  static_assert(kPieces == 2, "a thread has one piece of k' and one of q'");
+  // The window's rows by way of shared memory, to a place of the thread's own: a
+  // wait for loads into registers would wait for the state's too.
+  const int r_row = th >> 4, r_piece = th & 15;  // 16 threads to a row
   if (warp < kWarps) {
-    const int r = th >> 4, p = th & 15;
+    if (r_row < W) {
 #pragma unroll
-    for (int m = 0; m < kPieces; ++m)
-      rows[m] = r < n ? __ldg(reinterpret_cast<const uint4*>((m ? a.q : a.k) +
-                                                             (row0 + r) * (size_t)(m ? a.q_stride : a.k_stride) +
-                                                             (size_t)kh * kHeadDim) + p)
-                      : make_uint4(0u, 0u, 0u, 0u);
+      for (int m = 0; m < 2; ++m)
+        cp_async_16(smem_u32(&s.raw[m][th]), (m ? a.q : a.k) + (row0 + r_row) * (size_t)(m ? a.q_stride : a.k_stride) +
+                                                 (size_t)kh * kHeadDim + 8 * r_piece);
+    }
+    cp_async_commit();
   }
-  // the warp's 16 value rows of the state to its part of shared memory
-  extern __shared__ __align__(128) uint8_t state_smem[];
-  uint8_t* const mine = state_smem + warp * 16 * kHeadDim * 4;
-  float* const st = a.state + ((size_t)lr.slot * a.hv + h) * kStateElems + (size_t)row16 * kHeadDim;
+  // S[t][m]: value rows 8 t + g, key dims 16 m + 4 c ..
+  float4 S[2][8];
+  float* const st = a.state + ((size_t)lr.slot * a.hv + h) * kStateElems + (size_t)(row16 + g) * kHeadDim + 4 * c;
   uint32_t v[2][2] = {};  // rows g, g + 8 of the window, value rows 8 t + 2 c, + 1
   float d[kRows];         // of the two further warps
   bool bad = false;
   if (warp < kWarps) {
     if (n > 0) {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) cp_async_16(smem_u32(mine) + state_at(r, lane), st + (size_t)r * kHeadDim + 4 * lane);
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int m = 0; m < 8; ++m) S[t][m] = *reinterpret_cast<const float4*>(st + (size_t)8 * t * kHeadDim + 16 * m);
     }
-    cp_async_commit();
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -422,14 +420,15 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a) {
         if (g + 8 * i < n)
           v[i][t] = *reinterpret_cast<const uint32_t*>(a.v + (row0 + g + 8 * i) * (size_t)a.v_stride +
                                                        (size_t)h * kHeadDim + row16 + 8 * t + 2 * c);
-  } else if (n > 0) {
+  } else {
     bad = ways(s, a, warp - kWarps, n, row0, h, lane, d);
   }
   if (warp < kWarps) {
-    const int r = th >> 4, p = th & 15;
+    const int r = r_row, p = r_piece;
+    cp_async_wait<0>();
 #pragma unroll
-    for (int m = 0; m < kPieces; ++m) {
-      const uint4 w = rows[m];
+    for (int m = 0; m < 2; ++m) {
+      const uint4 w = r < n ? s.raw[m][th] : make_uint4(0u, 0u, 0u, 0u);
       uint32_t y[4] = {w.x, w.y, w.z, w.w}, top = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = max(top, max(y[i] << 16 & 0x7FFF0000u, y[i] & 0x7FFF0000u));
@@ -463,7 +462,6 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a) {
   const size_t at0 = (row0 * a.hv + h) * kHeadDim + row16 + 2 * c;  // this thread's first output
   const size_t row_out = (size_t)a.hv * kHeadDim;
   if (n == 0) {
-    cp_async_wait<0>();
     if (warp < kWarps)
       for (int r = g; r < W; r += 8)
 #pragma unroll
@@ -480,19 +478,14 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a) {
   }
   const uint32_t kbase = smem_u32(s.key[0]), qbase = smem_u32(s.key[1]);
   const int a_row = lane & 15, a_piece = lane >> 4;
-  cp_async_wait<0>();
-  __syncwarp();
-  // S k' in two parts, S q' in one; of the state value rows 8 t + g, key dims 16 m + 4 c ..
-  const auto state_of = [&](int t, int m) {
-    return *reinterpret_cast<const float4*>(mine + state_at(8 * t + g, 4 * m + c));
-  };
+  // S k' in two parts, S q' in one
   float sig[2], isig[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     float x = 0.0f;
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
-      const float4 y = state_of(t, m);
+      const float4 y = S[t][m];
       x = max3(x, fabsf(y.x), fabsf(y.y));
       x = max3(x, fabsf(y.z), fabsf(y.w));
     }
@@ -510,7 +503,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
       uint32_t hi[2], lo[2];
-      const float4 y = state_of(t, m);
+      const float4 y = S[t][m];
       split_f16(f2_unpack(fmul2(f2_pack(y.x, y.y), f2_pack(sig[t], sig[t]))), hi[0], lo[0]);
       split_f16(f2_unpack(fmul2(f2_pack(y.z, y.w), f2_pack(sig[t], sig[t]))), hi[1], lo[1]);
       mma_f16_16816(sk[0][t], fk, hi[0], hi[1]);
@@ -611,7 +604,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a) {
     for (int m = 0; m < 8; ++m) {
       uint32_t k0[2], k1[2];
       ldmatrix_x4_trans(kbase + key_at((lane & 7) + ((lane >> 3) & 1) * 8, 2 * m + (lane >> 4)), k0[0], k1[0], k0[1], k1[1]);
-      const float4 s0 = state_of(0, m), s1 = state_of(1, m);
+      const float4 s0 = S[0][m], s1 = S[1][m];
       float lo[4] = {s0.x * in[0] * c_down, s0.y * in[0] * c_down, s1.x * in[1] * c_down, s1.y * in[1] * c_down};
       float hi[4] = {s0.z * in[0] * c_down, s0.w * in[0] * c_down, s1.z * in[1] * c_down, s1.w * in[1] * c_down};
       mma_f16_16816(lo, ch, k0[0], k1[0]);
@@ -620,7 +613,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a) {
       mma_f16_16816(hi, cl, k0[1], k1[1]);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        *reinterpret_cast<float4*>(st + (size_t)(8 * t + g) * kHeadDim + 16 * m + 4 * c) =
+        *reinterpret_cast<float4*>(st + (size_t)8 * t * kHeadDim + 16 * m) =
             make_float4(lo[2 * t] * c_up * back[t], lo[2 * t + 1] * c_up * back[t], hi[2 * t] * c_up * back[t],
                         hi[2 * t + 1] * c_up * back[t]);
     }
@@ -781,10 +774,7 @@ extern "C" int verify_delta(float* state, int num_slots, const void* q, const vo
   } else {
     const dim3 grid(num_v_heads, num_lanes);
     const auto kernel = deltas == nullptr ? window_kernel<true> : window_kernel<false>;
-    constexpr int bytes = (int)(kStateElems * sizeof(float));
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-      return SDVA_ERR_CUDA;
-    kernel<<<grid, kThreads, bytes, cs>>>(a);
+    kernel<<<grid, kThreads, 0, cs>>>(a);
   }
   return cudaGetLastError() == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
 }
