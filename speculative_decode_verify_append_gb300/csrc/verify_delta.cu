@@ -17,7 +17,7 @@
 // in registers, eight lanes to a row, and needs no other warp.
 // window_kernel takes up to 16 in the form above: a CTA has a head, a warp 16
 // value rows of its state as the tensor cores' B operand (and, committed, as
-// their accumulators), loaded into registers while the window's rows are
+// their accumulators), copied to shared memory while the window's rows are
 // normalised.  Two more warps multiply the rows with each other and solve for T
 // and P, a column to a lane, under the products with S.
 // commit_delta: fp32 multiply-adds, eight value rows of a state to a warp.
@@ -196,12 +196,14 @@ __global__ void __launch_bounds__(kSeqThreads) rows_kernel(VerifyArgs a) {
 constexpr int kRows = kMaxWindow;  // of the tensor cores' tile; rows behind the lane's count are zeros
 constexpr int kWarps = 8;          // with a part of the state
 constexpr int kThreads = (kWarps + 2) * 32;
+constexpr int kStateBytes = (int)(kStateElems * sizeof(float));
 
 struct VerifySmem {
-  uint4 raw[2][kWarps * 32];  // the window's k and q, 16 bytes to a thread
+  uint64_t bar[kWarps];  // the copies of each warp's part of the state
   // k', q' in fp16.  Of 16 key dims a B operand's thread c has 4 c .. 4 c + 3 of the
   // state, so that the rows hold dims 0 1 4 5 8 9 12 13, then 2 3 6 7 10 11 14 15.
   alignas(16) uint8_t key[2][kRows * kHeadDim * 2];
+  alignas(16) uint8_t v[kRows * kHeadDim * 2];
   alignas(16) uint8_t tri[3][kRows * kRows * 2];  // the columns of T in two parts and of P
   float gram[2][kRows][kRows + 1];                // k' . k', q' . k'
   alignas(16) float a[kRows][kRows + 4];          // columns of A
@@ -213,6 +215,7 @@ struct VerifySmem {
   float k_own[kRows];  // 1 / sqrt(|k|^2 + eps)
   float fa[kRows], fc[kRows], o1[kRows], o2[kRows];
   float t_up, c_up, f;
+  int never;  // 0: no role's wait ends another's
 };
 
 __device__ __forceinline__ float warp_max(float x) {
@@ -261,6 +264,7 @@ __device__ __forceinline__ bool ways(VerifySmem& s, const VerifyArgs& a, int m, 
     s.eg[m][lane] = on ? expf(ld) : 1.0f;
     if (m == 0) s.beta[lane] = on ? beta : 0.0f;
     s.par[m][lane] = p;
+    if (m == 0 && lane == 0) s.never = 0;
   }
   __syncwarp();
   float x[kRows];
@@ -378,7 +382,7 @@ __device__ __forceinline__ void solve(VerifySmem& s, const VerifyArgs& a, int m,
 
 // kCommit: the window's updates go to the state.
 template <bool kCommit>
-__global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a, long long limit) {
   __shared__ VerifySmem s;
   const int h = blockIdx.x, b = blockIdx.y, th = threadIdx.x, lane = th & 31, warp = th >> 5, W = a.window;
   const int g = lane >> 2, c = lane & 3, kh = h / (a.hv / a.hk);
@@ -388,47 +392,43 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
   const LaneRows lr = lane_rows(a, b);
   int n = lr.n;
   if (lr.wrong && report) raise_status(a.status, lr.wrong);
-  // The window's rows by way of shared memory, to a place of the thread's own: a
-  // wait for loads into registers would wait for the state's too.
-  const int r_row = th >> 4, r_piece = th & 15;  // 16 threads to a row
-  if (warp < kWarps) {
-    if (r_row < W) {
+  // The window's rows (16 threads to a row), the state by bulk copies: loads
+  // through L1 come back in order, and the little ones of both CTAs of an SM would
+  // wait for 64 KB each time.
+  const int r_row = th >> 4, r_piece = th & 15;
+  uint4 rows[2] = {};
+  if (r_row < W) {  // 16 rows of the first eight warps
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
-        cp_async_16(smem_u32(&s.raw[m][th]), (m ? a.q : a.k) + (row0 + r_row) * (size_t)(m ? a.q_stride : a.k_stride) +
-                                                 (size_t)kh * kHeadDim + 8 * r_piece);
-    }
-    cp_async_commit();
+    for (int m = 0; m < 2; ++m)
+      rows[m] = __ldg(reinterpret_cast<const uint4*>((m ? a.q : a.k) + (row0 + r_row) * (size_t)(m ? a.q_stride : a.k_stride) +
+                                                     (size_t)kh * kHeadDim) + r_piece);
+    cp_async_16(smem_u32(s.v) + key_at(r_row, r_piece),
+                a.v + (row0 + r_row) * (size_t)a.v_stride + (size_t)h * kHeadDim + 8 * r_piece);
   }
-  // S[t][m]: value rows 8 t + g, key dims 16 m + 4 c ..
-  float4 S[2][8];
-  float* const st = a.state + ((size_t)lr.slot * a.hv + h) * kStateElems + (size_t)(row16 + g) * kHeadDim + 4 * c;
-  uint32_t v[2][2] = {};  // rows g, g + 8 of the window, value rows 8 t + 2 c, + 1
+  cp_async_commit();
+  extern __shared__ __align__(128) uint8_t state_smem[];
+  const uint8_t* const mine = state_smem + warp * (kStateBytes / kWarps);
+  float* const st = a.state + ((size_t)lr.slot * a.hv + h) * kStateElems + (size_t)row16 * kHeadDim;
+  const uint32_t bar = smem_u32(&s.bar[warp & (kWarps - 1)]);
   float d[kRows];         // of the two further warps
   bool bad = false;
   if (warp < kWarps) {
     if (n > 0) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int m = 0; m < 8; ++m) S[t][m] = *reinterpret_cast<const float4*>(st + (size_t)8 * t * kHeadDim + 16 * m);
+      if (lane == 0) {  // 8 KB: a value row's 512 bytes leave the reads below two to a bank
+        tc::mbar_init(bar, 1);
+        tc::mbar_fence_init();
+        tc::mbar_arrive_expect_tx(bar, kStateBytes / kWarps);
+        tc::bulk_load(smem_u32(mine), st, kStateBytes / kWarps, bar);
+      }
     }
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-        if (g + 8 * i < n)
-          v[i][t] = *reinterpret_cast<const uint32_t*>(a.v + (row0 + g + 8 * i) * (size_t)a.v_stride +
-                                                       (size_t)h * kHeadDim + row16 + 8 * t + 2 * c);
   } else {
     bad = ways(s, a, warp - kWarps, n, row0, h, lane, d);
   }
   if (warp < kWarps) {
     const int r = r_row, p = r_piece;
-    cp_async_wait<0>();
 #pragma unroll
     for (int m = 0; m < 2; ++m) {
-      const uint4 w = r < n ? s.raw[m][th] : make_uint4(0u, 0u, 0u, 0u);
+      const uint4 w = r < n ? rows[m] : make_uint4(0u, 0u, 0u, 0u);
       uint32_t y[4] = {w.x, w.y, w.z, w.w}, top = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) top = max(top, max(y[i] << 16 & 0x7FFF0000u, y[i] & 0x7FFF0000u));
@@ -461,7 +461,14 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
   }
   const size_t at0 = (row0 * a.hv + h) * kHeadDim + row16 + 2 * c;  // this thread's first output
   const size_t row_out = (size_t)a.hv * kHeadDim;
+  const auto state_here = [&] {
+    if (!tc::mbar_wait<false>(bar, 0, &s.never, limit)) {
+      if (lane == 0) raise_status(a.status, SDVA_STATUS_TIMEOUT);
+      tc::mbar_wait<false>(bar, 0, &s.never);  // the copies end before the CTA does
+    }
+  };
   if (n == 0) {
+    if (warp < kWarps && lr.n > 0) state_here();
     if (warp < kWarps)
       for (int r = g; r < W; r += 8)
 #pragma unroll
@@ -478,7 +485,16 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
   }
   const uint32_t kbase = smem_u32(s.key[0]), qbase = smem_u32(s.key[1]);
   const int a_row = lane & 15, a_piece = lane >> 4;
-  // S k' in two parts, S q' in one
+  state_here();
+  // S k' in two parts, S q' in one; of the state value rows 8 t + g, key dims 16 m + 4 c ..
+  const auto state_of = [&](int t, int m) {
+    return *reinterpret_cast<const float4*>(mine + (8 * t + g) * kHeadDim * 4 + 64 * m + 16 * c);
+  };
+  float4 S[2][8];
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+#pragma unroll
+    for (int m = 0; m < 8; ++m) S[t][m] = state_of(t, m);
   float sig[2], isig[2];
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
@@ -511,6 +527,7 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
       mma_f16_16816(sq[t], fq, hi[0], hi[1]);
     }
   }
+  cp_async_wait<0>();  // v
   __syncthreads();
   // x; its columns' scales leave u, at most 32 x, inside fp16's range, and are no finer than the state needs
   float xs[2][2], xi[2][2];
@@ -518,6 +535,10 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     float x[2][2];
+    uint32_t v[2];  // rows g, g + 8 of the window, value rows 8 t + 2 c, + 1
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+      v[r] = 8 * r + g < n ? *reinterpret_cast<const uint32_t*>(s.v + key_at(8 * r + g, 2 * warp + t) + 4 * c) : 0u;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float up = __shfl_sync(0xffffffffu, isig[t], 4 * (2 * c + i));
@@ -525,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float y = (sk[0][t][2 * r + i] + sk[1][t][2 * r + i]) * up;
-        x[r][i] = s.beta[8 * r + g] * ((i ? bf16_hi(v[r][t]) : bf16_lo(v[r][t])) - s.fa[8 * r + g] * y);
+        x[r][i] = s.beta[8 * r + g] * ((i ? bf16_hi(v[r]) : bf16_lo(v[r])) - s.fa[8 * r + g] * y);
         top = fmaxf(top, fabsf(x[r][i]));
       }
 #pragma unroll
@@ -604,7 +625,7 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
     for (int m = 0; m < 8; ++m) {
       uint32_t k0[2], k1[2];
       ldmatrix_x4_trans(kbase + key_at((lane & 7) + ((lane >> 3) & 1) * 8, 2 * m + (lane >> 4)), k0[0], k1[0], k0[1], k1[1]);
-      const float4 s0 = S[0][m], s1 = S[1][m];
+      const float4 s0 = state_of(0, m), s1 = state_of(1, m);
       float lo[4] = {s0.x * in[0] * c_down, s0.y * in[0] * c_down, s1.x * in[1] * c_down, s1.y * in[1] * c_down};
       float hi[4] = {s0.z * in[0] * c_down, s0.w * in[0] * c_down, s1.z * in[1] * c_down, s1.w * in[1] * c_down};
       mma_f16_16816(lo, ch, k0[0], k1[0]);
@@ -613,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, kCommit ? 1 : 2) window_kernel(Verif
       mma_f16_16816(hi, cl, k0[1], k1[1]);
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        *reinterpret_cast<float4*>(st + (size_t)8 * t * kHeadDim + 16 * m) =
+        *reinterpret_cast<float4*>(st + (size_t)(8 * t + g) * kHeadDim + 16 * m + 4 * c) =
             make_float4(lo[2 * t] * c_up * back[t], lo[2 * t + 1] * c_up * back[t], hi[2 * t] * c_up * back[t],
                         hi[2 * t + 1] * c_up * back[t]);
     }
@@ -774,7 +795,9 @@ extern "C" int verify_delta(float* state, int num_slots, const void* q, const vo
   } else {
     const dim3 grid(num_v_heads, num_lanes);
     const auto kernel = deltas == nullptr ? window_kernel<true> : window_kernel<false>;
-    kernel<<<grid, kThreads, 0, cs>>>(a);
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStateBytes) != cudaSuccess)
+      return SDVA_ERR_CUDA;
+    kernel<<<grid, kThreads, kStateBytes, cs>>>(a, wait_limit());
   }
   return cudaGetLastError() == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
 }
