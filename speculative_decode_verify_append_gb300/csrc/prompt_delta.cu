@@ -15,14 +15,16 @@
 // not depend on the state: k' and q' in fp16, T in two parts, P, and each
 // token's factors, laid out as the other kernel's shared memory holds them.
 // state_kernel goes through a lane's chunks with a head's state in registers.
-// A warp has eight value columns of it and works alone: S as 16 x 8 accumulators
-// (key dims by values) becomes the B operand of S k' by transposing 8 x 8 tiles
-// between registers, and so do x and u.  This chain, state to state, is what a
-// long prompt's time is made of (a prompt alone has 16 such warps per head), so
-// that nothing else is on it: each of its warps has another one, a chunk behind,
-// that takes S and u out of shared memory, makes the outputs, and copies the
-// chunks that come.  One barrier of the CTA per chunk.
+// A warp has 16 value rows of it, as accumulators of values by key dims, which
+// are the B operand of S k' as they stand; x and u (tokens by values) become
+// operands by transposing 8 x 8 tiles between registers.  No warp needs another
+// one's values.  This chain, state to state, is what a long prompt's time is made
+// of (a prompt alone has eight such warps per head), so that nothing else is on
+// it: each of its warps has another one, a chunk behind, that takes S and u out
+// of shared memory, makes the outputs, and copies the chunks that come.  One
+// barrier of the CTA per chunk.
 #include "delta_common.cuh"
+#include "tc_primitives.cuh"
 
 namespace sdva {
 namespace {
@@ -98,14 +100,18 @@ __device__ __forceinline__ void store_column(uint8_t* to, int j, const float (&x
 constexpr int kChunkThreads = 128;
 
 struct ChunkSmem {
-  alignas(16) uint8_t key[2][kKeyBytes];      // k', q'
-  float gram[2][kChunk][kChunk + 4];          // k' . k', q' . k' (row, column)
-  alignas(16) float a[4][kChunk][kChunk + 4];  // A of each warp's value head
+  union {
+    alignas(16) uint8_t key[2][kKeyBytes];       // k', q', until their products are there
+    alignas(16) float a[4][kChunk][kChunk + 4];  // A of each warp's value head
+  };
+  float gram[2][kChunk][kChunk + 4];  // k' . k', q' . k' (row, column)
+  alignas(16) float eg[4][kChunk];    // of each warp's value head
+  alignas(16) float br[4][kChunk];
   float sum_sq[2][kChunk], up[2][kChunk], down[2][kChunk], l1[kChunk], top[kChunk];
   uint32_t found[kChunkThreads / 32];
 };
 
-__global__ void __launch_bounds__(kChunkThreads) chunk_kernel(PromptArgs a) {
+__global__ void __launch_bounds__(kChunkThreads, 6) chunk_kernel(PromptArgs a) {
   __shared__ ChunkSmem s;
   const int slot = blockIdx.x, kh = blockIdx.y, th = threadIdx.x, lane = th & 31, warp = th >> 5;
   constexpr uint32_t kBad = 1u << 20;  // above every count: the host refuses more lanes than 65,535
@@ -128,6 +134,12 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(PromptArgs a) {
   const int valid = min(a.cu[b + 1] - t0, kChunk);
   if (valid <= 0) return;
 
+  // decays and strengths of the warp's first value head, ahead of their use
+  const int group = a.hv / a.hk;
+  const bool on = lane < valid;
+  const auto decay_at = [&](int task) { return ((size_t)t0 + lane) * a.hv + kh * group + (task >> 1); };
+  float log_decay = on && warp < 2 * group ? a.log_decay[decay_at(warp)] : 0.0f;
+  float beta_ = on && warp < 2 * group ? a.beta[decay_at(warp)] : 0.0f;
   // k' and q': four threads to a row, 16-byte pieces p, p + 4, p + 8, p + 12
   {
     const int r = th >> 2, p = th & 3;
@@ -210,8 +222,6 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(PromptArgs a) {
   }
   __syncthreads();
   // T, and P with the factors, of the key head's value heads: a task per warp, a column to a lane, and token `lane`
-  const int group = a.hv / a.hk;
-  const bool on = lane < valid;
   const Scale sk = {s.down[0][lane], s.up[0][lane]}, sq = {s.down[1][lane], s.up[1][lane]};
   const float rk = on ? row_factor(s.sum_sq[0][lane], a.eps, sk) : 0.0f;
   const float rq = on ? row_factor(s.sum_sq[1][lane], a.eps, sq) : 0.0f;
@@ -219,9 +229,16 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(PromptArgs a) {
     const int h = kh * group + (task >> 1);
     uint8_t* const rec = a.heads + ((size_t)slot * a.hv + h) * kHeadRecord;
     float* const fac = reinterpret_cast<float*>(rec + 3 * kTriBytes);
-    const size_t at = ((size_t)t0 + lane) * a.hv + h;
-    const float eg = on ? expf(a.log_decay[at]) : 1.0f, beta = on ? a.beta[at] : 0.0f;
+    if (task != warp) {
+      log_decay = on ? a.log_decay[decay_at(task)] : 0.0f;
+      beta_ = on ? a.beta[decay_at(task)] : 0.0f;
+    }
+    const float eg = on ? expf(log_decay) : 1.0f, beta = beta_;
     float x[kChunk], d = 0.0f, top = 0.0f;
+    __syncwarp();
+    s.eg[warp][lane] = eg;
+    s.br[warp][lane] = beta * rk;
+    __syncwarp();
     if (task & 1) {
       // products of e^g up to this token, and from the next one on
       float fall = eg, rest = __shfl_down_sync(0xffffffffu, eg, 1);
@@ -234,11 +251,15 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(PromptArgs a) {
       }
       const float all = __shfl_sync(0xffffffffu, fall, 31);
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) {
-        const float egi = __shfl_sync(0xffffffffu, eg, i);
-        d = i == lane ? 1.0f : d * egi;
-        x[i] = i >= lane ? d * rk * s.gram[1][i][lane] : 0.0f;
-        top = fmaxf(top, fabsf(x[i]));
+      for (int i = 0; i < kChunk; i += 4) {
+        const float4 e = *reinterpret_cast<const float4*>(&s.eg[warp][i]);
+        const float egs[4] = {e.x, e.y, e.z, e.w};
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          d = i + y == lane ? 1.0f : d * egs[y];
+          x[i + y] = i + y >= lane ? d * rk * s.gram[1][i + y][lane] : 0.0f;
+          top = fmaxf(top, fabsf(x[i + y]));
+        }
       }
       const Scale ps = scale_of_row(warp_max(top));
       store_column<false>(rec + 2 * kTriBytes, lane, x, ps.down);
@@ -262,13 +283,15 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(PromptArgs a) {
     }
     // A by columns, then those of the inverse of 1 + A: as soon as a row is known it leaves the rows below
     float (*const A)[kChunk + 4] = s.a[warp];
-    const float br = beta * rk;
-    __syncwarp();
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      const float egi = __shfl_sync(0xffffffffu, eg, i), bri = __shfl_sync(0xffffffffu, br, i);
-      d = i == lane ? 1.0f : d * egi;
-      x[i] = i > lane ? bri * (d * rk) * s.gram[0][i][lane] : 0.0f;
+    for (int i = 0; i < kChunk; i += 4) {
+      const float4 e = *reinterpret_cast<const float4*>(&s.eg[warp][i]), f = *reinterpret_cast<const float4*>(&s.br[warp][i]);
+      const float egs[4] = {e.x, e.y, e.z, e.w}, brs[4] = {f.x, f.y, f.z, f.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        d = i + y == lane ? 1.0f : d * egs[y];
+        x[i + y] = i + y > lane ? brs[y] * (d * rk) * s.gram[0][i + y][lane] : 0.0f;
+      }
     }
 #pragma unroll
     for (int i = 0; i < kChunk; i += 4) *reinterpret_cast<float4*>(&A[lane][i]) = make_float4(x[i], x[i + 1], x[i + 2], x[i + 3]);
@@ -299,39 +322,72 @@ __global__ void __launch_bounds__(kChunkThreads) chunk_kernel(PromptArgs a) {
   }
 }
 
-constexpr int kWarps = 4;     // of the chain, eight value columns each
-constexpr int kStages = 3;    // the outputs' chunk, the chain's, and the one that comes
+constexpr int kWarps = 2;  // of the chain, 16 value rows each, and as many for the outputs
 constexpr int kThreads = 2 * kWarps * 32;
-constexpr int kValueBytes = kChunk * kWarps * 16;  // the chunk's values of the CTA's columns
-constexpr int kStageBytes = kKeyRecord + kHeadRecord + kValueBytes;
-// What a warp of the chain hands over: S (16 words a thread), u (4), the scales of both (4)
-constexpr int kHandBytes = 6 * 32 * 16;
-constexpr int kStateSmem = kStages * kStageBytes + 2 * kWarps * kHandBytes;
+constexpr int kValueBytes = kWarps * kChunk * 32;
+// Of a chunk the chain takes k', T, the factors and its values, the outputs q',
+// P and the factors; each in two places, the one in use and the one that comes.
+constexpr int kChainBytes = kKeyBytes + 2 * kTriBytes + kFactorBytes;
+constexpr int kOutBytes = kKeyBytes + kTriBytes + kFactorBytes;
+// What a warp of the chain hands over: S (32 words a thread), u (8), the scales of both
+constexpr int kHandBytes = 11 * 32 * 16;
+constexpr int kStateSmem = 2 * (kChainBytes + kValueBytes + kOutBytes + kWarps * kHandBytes);
 
 // A column of T or P in A's place: rows are stored by columns, so the matrices come transposed.
 __device__ __forceinline__ uint32_t tri_a(uint32_t tri, int m, int jt, int lane) {
   return tri + tri_at(16 * jt + (lane & 7) + ((lane >> 4) << 3), 2 * m + ((lane >> 3) & 1));
 }
+// The values of a chunk: 2 kWarps 16-byte pieces to a row, eight rows of a piece in different banks.
 __device__ __forceinline__ int value_at(int row, int piece) {
-  return (row * kWarps + (piece ^ ((row >> 1) & (kWarps - 1)))) << 4;
+  return (row * 2 * kWarps + (piece ^ ((row >> 1) & (2 * kWarps - 1)))) << 4;
 }
 
-__global__ void __launch_bounds__(kThreads, 2) state_kernel(PromptArgs a) {
+// One of a chunk's scalars.
+template <int kWhich>
+__device__ __forceinline__ float at(float4 lo, float4 hi) {
+  static_assert(kWhich < kScalars, "two vectors");
+  return kWhich == 0 ? lo.x : kWhich == 1 ? lo.y : kWhich == 2 ? lo.z : kWhich == 3 ? lo.w
+         : kWhich == 4 ? hi.x : kWhich == 5 ? hi.y : kWhich == 6 ? hi.z : hi.w;
+}
+
+// kWide: as many registers as two CTAs leave an SM's warps, for grids that give each SM no more.  One prompt of 8,192
+// tokens, 32 heads: 338 us with them, 361 without; eight of 2,048: 542 and 474, with three CTAs to an SM.  Which of the
+// two stores S for the outputs at once and which behind the products is by the same measurements.
+template <bool kWide>
+__global__ void __launch_bounds__(kThreads, kWide ? 2 : 3) state_kernel(PromptArgs a, long long limit) {
   extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int never;  // 0: no role's wait ends another's
   const int th = threadIdx.x, lane = th & 31, g = lane >> 2, c = lane & 3;
+  if (th == 0) never = 0;
   const bool chain = th < kWarps * 32;
   const int warp = (th >> 5) & (kWarps - 1);
   const int h = blockIdx.y, kh = h / (a.hv / a.hk);
+  // Longer lanes first where a thread can have one each: the last to start decides when the call ends.
+  int b = blockIdx.z;
   bool bad = false;
-  for (int i = th; i < a.num_lanes; i += kThreads) {
-    const int lo = a.cu[i], hi = a.cu[i + 1];
-    bad |= lo < 0 || hi < lo || hi > a.total;
+  {
+    __shared__ int length[kThreads];
+    __shared__ int mine;
+    const bool sorted = a.num_lanes <= kThreads;
+    for (int i = th; i < a.num_lanes; i += kThreads) {
+      const int lo = a.cu[i], hi = a.cu[i + 1];
+      bad |= lo < 0 || hi < lo || hi > a.total;
+      if (sorted) length[i] = hi - lo;
+    }
+    if (__syncthreads_or(bad)) {
+      if (blockIdx.x == 0 && h == 0 && b == 0 && th == 0) raise_status(a.status, SDVA_STATUS_BAD_COUNT);
+      return;
+    }
+    if (sorted && a.num_lanes > 1) {
+      if (th < a.num_lanes) {
+        int rank = 0;
+        for (int i = 0; i < a.num_lanes; ++i) rank += length[i] > length[th] || (length[i] == length[th] && i < th);
+        if (rank == b) mine = th;
+      }
+      __syncthreads();
+      b = mine;
+    }
   }
-  if (__syncthreads_or(bad)) {
-    if (blockIdx.x == 0 && h == 0 && blockIdx.z == 0 && th == 0) raise_status(a.status, SDVA_STATUS_BAD_COUNT);
-    return;
-  }
-  const int b = blockIdx.z;
   const bool report = blockIdx.x == 0 && h == 0 && th == 0;
   const int row0 = a.cu[b], n = a.cu[b + 1] - row0;
   if (n == 0) return;
@@ -341,244 +397,302 @@ __global__ void __launch_bounds__(kThreads, 2) state_kernel(PromptArgs a) {
     return;
   }
   const int chunks = (n + kChunk - 1) / kChunk, base = chunk_base(row0, b);
-  const uint32_t sbase = smem_u32(smem);
-  uint8_t* const hand = smem + kStages * kStageBytes + warp * 2 * kHandBytes + lane * 16;
-  const int col0 = (blockIdx.x * kWarps + warp) * 8;  // the warp's first value column
+  uint8_t* const chain_smem = smem;                                       // k', T in two parts, factors; values
+  uint8_t* const out_smem = smem + 2 * (kChainBytes + kValueBytes);       // q', P, factors
+  uint8_t* const hand = out_smem + 2 * kOutBytes + warp * 2 * kHandBytes + lane * 16;
+  const int row16 = (blockIdx.x * kWarps + warp) * 16;  // the warp's first value row
 
   if (!chain) {
     const int ot = th - kWarps * 32;
-    const uint16_t* const vcol = a.v + (size_t)row0 * (size_t)a.v_stride + (size_t)h * kHeadDim + blockIdx.x * kWarps * 8;
-    const auto fetch = [&](int i) {  // chunk i into its stage
-      if (i >= chunks) return;
-      const uint8_t* const keys = a.keys + ((size_t)(base + i) * a.hk + kh) * kKeyRecord + ot * 16;
-      const uint8_t* const heads = a.heads + ((size_t)(base + i) * a.hv + h) * kHeadRecord + ot * 16;
-      const uint32_t to = sbase + (i % kStages) * kStageBytes + ot * 16;
-      constexpr int kStep = kWarps * 32 * 16;
+    bool dead = false;  // of thread 0: a wait ran out; nothing more is copied, and what follows is undefined
+    __shared__ uint64_t bars[2];
+    if (ot == 0) {
+      tc::mbar_init(smem_u32(&bars[0]), 1);
+      tc::mbar_init(smem_u32(&bars[1]), 1);
+      tc::mbar_fence_init();
+    }
+    const uint16_t* const vcol = a.v + (size_t)row0 * (size_t)a.v_stride + (size_t)h * kHeadDim + blockIdx.x * kWarps * 16;
+    // What the next interval needs: chunk i + 1 for the chain, chunk i for the outputs.  Records by bulk copies of one
+    // thread; the values' 16-byte pieces by all (those behind the lane's rows are dropped where they are read).
+    const auto fetch = [&](int i, uint32_t bar) {
+      if (ot == 0 && !dead) {
+        const int bytes = (i + 1 < chunks ? kChainBytes : 0) + (i >= 0 && i < chunks ? kOutBytes : 0);
+        if (bytes != 0) tc::mbar_arrive_expect_tx(bar, bytes);
+        if (i + 1 < chunks) {
+          const uint8_t* const keys = a.keys + ((size_t)(base + i + 1) * a.hk + kh) * kKeyRecord;
+          const uint8_t* const heads = a.heads + ((size_t)(base + i + 1) * a.hv + h) * kHeadRecord;
+          const uint32_t to = smem_u32(chain_smem) + ((i + 1) & 1) * (kChainBytes + kValueBytes);
+          tc::bulk_load(to, keys, kKeyBytes, bar);
+          tc::bulk_load(to + kKeyBytes, heads, 2 * kTriBytes, bar);
+          tc::bulk_load(to + kKeyBytes + 2 * kTriBytes, heads + 3 * kTriBytes, kFactorBytes, bar);
+        }
+        if (i >= 0 && i < chunks) {
+          const uint32_t to = smem_u32(out_smem) + (i & 1) * kOutBytes;
+          tc::bulk_load(to, a.keys + ((size_t)(base + i) * a.hk + kh) * kKeyRecord + kKeyBytes, kKeyBytes, bar);
+          tc::bulk_load(to + kKeyBytes, a.heads + ((size_t)(base + i) * a.hv + h) * kHeadRecord + 2 * kTriBytes,
+                        kTriBytes + kFactorBytes, bar);
+        }
+      }
+      if (i + 1 < chunks) {
+        const uint32_t to = smem_u32(chain_smem) + ((i + 1) & 1) * (kChainBytes + kValueBytes) + kChainBytes;
 #pragma unroll
-      for (int x = 0; x < kKeyRecord; x += kStep) cp_async_16(to + x, keys + x);
-#pragma unroll
-      for (int x = 0; x < kHeadRecord; x += kStep)
-        if (x + kStep <= kHeadRecord || x + ot * 16 < kHeadRecord) cp_async_16(to + kKeyRecord + x, heads + x);
-      // values: kWarps 16-byte pieces of a row; those behind the lane's rows are dropped where they are read
-      const int r = ot / kWarps, p = ot % kWarps;
-      static_assert(kChunk * kWarps == kWarps * 32, "one piece to a thread");
-      if (i * kChunk + r < n)
-        cp_async_16(sbase + (i % kStages) * kStageBytes + kKeyRecord + kHeadRecord + value_at(r, p),
-                    vcol + ((size_t)i * kChunk + r) * (size_t)a.v_stride + 8 * p);
+        for (int x = ot; x < kChunk * 2 * kWarps; x += kWarps * 32) {
+          const int r = x / (2 * kWarps), p = x % (2 * kWarps);
+          const int t = (i + 1) * kChunk + r;
+          if (t < n) cp_async_16(to + value_at(r, p), vcol + (size_t)t * (size_t)a.v_stride + 8 * p);
+        }
+      }
     };
-    uint16_t* const orow = a.out + ((size_t)row0 * a.hv + h) * kHeadDim + col0 + 2 * c;
-    fetch(0);
-    cp_async_commit();
+    uint16_t* const orow = a.out + ((size_t)row0 * a.hv + h) * kHeadDim + row16 + 2 * c;
+    fetch(-1, smem_u32(&bars[0]));
     for (int i = 0; i <= chunks; ++i) {
-      cp_async_wait<0>();
-      __syncthreads();  // chunk i is there; chunk i - 1 has been handed over, chunk i - 2 is done with
-      fetch(i + 1);
-      cp_async_commit();
+      const uint32_t bar = smem_u32(&bars[i & 1]), parity = (i >> 1) & 1;
+      if (ot == 0 && !dead && !tc::mbar_wait<false>(bar, parity, &never, limit)) {
+        raise_status(a.status, SDVA_STATUS_TIMEOUT);
+        dead = true;
+        tc::mbar_wait<false>(bar, parity, &never);  // the copies end before the CTA does
+      }
+      cp_async_wait_all();
+      __syncthreads();  // chunk i is there for the chain and chunk i - 1 for the outputs, which has been handed over
+      fetch(i, smem_u32(&bars[(i + 1) & 1]));
       if (i == 0) continue;
       const int ch = i - 1;
-      const uint32_t key = sbase + (ch % kStages) * kStageBytes, tri = key + kKeyRecord;
-      const float* const fac = reinterpret_cast<const float*>(smem + (ch % kStages) * kStageBytes + kKeyRecord + 3 * kTriBytes);
+      const uint8_t* const stage = out_smem + (ch & 1) * kOutBytes;
+      const uint32_t key = smem_u32(stage), tri = key + kKeyBytes;
+      const float* const fac = reinterpret_cast<const float*>(stage + kKeyBytes + kTriBytes);
       const uint8_t* const from = hand + (ch & 1) * kHandBytes;
-      uint32_t S[16], u[4];
+      float qs[2][2][4] = {}, p[2][2][4] = {};
 #pragma unroll
-      for (int x = 0; x < 4; ++x) {
-        const uint4 y = *reinterpret_cast<const uint4*>(from + x * 512);
-        S[4 * x] = y.x, S[4 * x + 1] = y.y, S[4 * x + 2] = y.z, S[4 * x + 3] = y.w;
-      }
-      {
-        const uint4 y = *reinterpret_cast<const uint4*>(from + 4 * 512);
-        u[0] = y.x, u[1] = y.y, u[2] = y.z, u[3] = y.w;
-      }
-      const float4 up = *reinterpret_cast<const float4*>(from + 5 * 512);
-      float qs[2][4] = {}, p[2][4] = {};
-#pragma unroll
-      for (int m = 0; m < 8; ++m)
+      for (int m = 0; m < 8; ++m) {
+        const uint4 S = *reinterpret_cast<const uint4*>(from + m * 512);
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           uint32_t f[4];
-          ldmatrix_x4(key + kKeyBytes + key_at(16 * r + (lane & 15), 2 * m + (lane >> 4)), f[0], f[1], f[2], f[3]);
-          mma_f16_16816(qs[r], f, S[2 * m], S[2 * m + 1]);
+          ldmatrix_x4(key + key_at(16 * r + (lane & 15), 2 * m + (lane >> 4)), f[0], f[1], f[2], f[3]);
+          mma_f16_16816(qs[r][0], f, S.x, S.y);
+          mma_f16_16816(qs[r][1], f, S.z, S.w);
         }
+      }
+      const uint4 u[2] = {*reinterpret_cast<const uint4*>(from + 8 * 512), *reinterpret_cast<const uint4*>(from + 9 * 512)};
+      const float2 up = *reinterpret_cast<const float2*>(from + 10 * 512);
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int jt = 0; jt <= m; ++jt) {
           uint32_t f[4];
-          ldmatrix_x4_trans(tri_a(tri + 2 * kTriBytes, m, jt, lane), f[0], f[1], f[2], f[3]);
-          mma_f16_16816(p[m], f, u[2 * jt], u[2 * jt + 1]);
+          ldmatrix_x4_trans(tri_a(tri, m, jt, lane), f[0], f[1], f[2], f[3]);
+          mma_f16_16816(p[m][0], f, u[jt].x, u[jt].y);
+          mma_f16_16816(p[m][1], f, u[jt].z, u[jt].w);
         }
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int t = 16 * m + 8 * r + g;
-          const float o1 = fac[3 * kChunk + t], o2 = fac[4 * kChunk + t];
+          const float o1 = fac[3 * kChunk + t] * up.x, o2 = fac[4 * kChunk + t] * up.y;
           if (ch * kChunk + t < n)
-            *reinterpret_cast<uint32_t*>(orow + ((size_t)ch * kChunk + t) * a.hv * kHeadDim) =
-                pack_bf16x2(fmaf(o1, qs[m][2 * r] * up.x, o2 * (p[m][2 * r] * up.z)),
-                            fmaf(o1, qs[m][2 * r + 1] * up.y, o2 * (p[m][2 * r + 1] * up.w)));
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+              *reinterpret_cast<uint32_t*>(orow + ((size_t)ch * kChunk + t) * a.hv * kHeadDim + 8 * x) =
+                  pack_bf16x2(fmaf(o1, qs[m][x][2 * r], o2 * p[m][x][2 * r]),
+                              fmaf(o1, qs[m][x][2 * r + 1], o2 * p[m][x][2 * r + 1]));
         }
     }
     return;
   }
 
-  // S[m]: key dims 16 m + g and + 8, value columns 2 c and + 1, times sig
-  float S[8][4];
-  float* const st = a.state + ((size_t)slot * a.hv + h) * kStateElems + (size_t)(col0 + 2 * c) * kHeadDim + g;
+  // S[x]: value rows g (0, 1) and g + 8 (2, 3), key dims 8 x + 2 c and + 1, times sig
+  float S[16][4];
+  float* const st = a.state + ((size_t)slot * a.hv + h) * kStateElems + (size_t)(row16 + g) * kHeadDim + 2 * c;
 #pragma unroll
-  for (int m = 0; m < 8; ++m)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) S[m][i] = L > 0 ? st[(size_t)(i & 1) * kHeadDim + 16 * m + (i >> 1) * 8] : 0.0f;
-  // powers of two that keep the operands in fp16's range, per value column
-  float sig[2], isig[2], top[2];
-  const auto tops = [&] {  // the largest of S per column
+  for (int x = 0; x < 16; ++x)
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      top[i] = 0.0f;
-#pragma unroll
-      for (int m = 0; m < 8; ++m) top[i] = max3(top[i], fabsf(S[m][i]), fabsf(S[m][i + 2]));
+      const float2 y = L > 0 ? *reinterpret_cast<const float2*>(st + i * 8 * kHeadDim + 8 * x) : make_float2(0.0f, 0.0f);
+      S[x][2 * i] = y.x, S[x][2 * i + 1] = y.y;
     }
+  // A power of two that keeps the operands in fp16's range, from the largest of the warp's part of S
+  float sig, isig;
+  {
+    float top = 0.0f;
 #pragma unroll
-    for (int o = 4; o <= 16; o <<= 1)
+    for (int x = 0; x < 16; ++x) top = max3(max3(top, fabsf(S[x][0]), fabsf(S[x][1])), fabsf(S[x][2]), fabsf(S[x][3]));
+    const Scale sc = scale_of_row(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
+    sig = sc.down, isig = sc.up;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) top[i] = fmaxf(top[i], __shfl_xor_sync(0xffffffffu, top[i], o));
-  };
-  tops();
+    for (int x = 0; x < 16; ++x)
 #pragma unroll
-  for (int i = 0; i < 2; ++i) {
-    const Scale sc = scale_of_row(top[i]);
-    sig[i] = sc.down, isig[i] = sc.up;
-    top[i] *= sc.down;
-#pragma unroll
-    for (int m = 0; m < 8; ++m) S[m][i] *= sc.down, S[m][i + 2] *= sc.down;
+      for (int i = 0; i < 4; ++i) S[x][i] *= sig;
   }
 
   for (int ch = 0; ch < chunks; ++ch) {
     __syncthreads();
-    const uint8_t* const stage = smem + (ch % kStages) * kStageBytes;
-    const uint32_t key = sbase + (ch % kStages) * kStageBytes, tri = key + kKeyRecord;
-    const float* const fac = reinterpret_cast<const float*>(stage + kKeyRecord + 3 * kTriBytes);
+    const uint8_t* const stage = chain_smem + (ch & 1) * (kChainBytes + kValueBytes);
+    const uint32_t key = smem_u32(stage), tri = key + kKeyBytes;
+    const float* const fac = reinterpret_cast<const float*>(stage + kKeyBytes + 2 * kTriBytes);
     const float* const sca = fac + kFactors * kChunk;
     uint8_t* const to = hand + (ch & 1) * kHandBytes;
 
-    // values, rows 16 m + 8 r + g, and the scale for x, u and the state behind the chunk, by bounds of all of them
-    float v[2][2][2], vtop[2] = {0.0f, 0.0f};
+    // values of the rows 16 m + 8 r + g
+    uint32_t v[2][2][2], vmax = 0;
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int t = 16 * m + 8 * r + g;
-        uint32_t w = *reinterpret_cast<const uint32_t*>(stage + kKeyRecord + kHeadRecord + value_at(t, warp) + 4 * c);
-        if (ch * kChunk + t >= n) w = 0u;
-        v[m][r][0] = bf16_lo(w), v[m][r][1] = bf16_hi(w);
+        const int row = 16 * m + 8 * r + g;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) vtop[i] = fmaxf(vtop[i], fabsf(v[m][r][i]));
+        for (int t = 0; t < 2; ++t) {
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(stage + kChainBytes + value_at(row, 2 * warp + t) + 4 * c);
+          v[m][r][t] = ch * kChunk + row < n ? w : 0u;
+        }
       }
+    const float4 s0 = *reinterpret_cast<const float4*>(sca), s1 = *reinterpret_cast<const float4*>(sca + 4);
+    // S k' in two parts: rows are tokens 16 r + g (+ 8), columns value rows 8 t + 2 c (+ 1).  A step's rows of k'
+    // are loaded before the one in front of it is stored for the outputs: a load would wait for that store.
+    float sh[2][2][4] = {}, sl[2][2][4] = {}, top = 0.0f;
+    uint32_t f[2][4], held[8][4];
 #pragma unroll
-    for (int o = 4; o <= 16; o <<= 1)
-#pragma unroll
-      for (int i = 0; i < 2; ++i) vtop[i] = fmaxf(vtop[i], __shfl_xor_sync(0xffffffffu, vtop[i], o));
-    float nsig[2], nisig[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float x = top[i] * isig[i];
-      const float bx = sca[kMaxB] * (vtop[i] + x * sca[kSumA]), bu = sca[kSumT] * bx;
-      const float all = fmaxf(max3(bx, bu, sca[kMaxC] * bu), fmaf(sca[kSumC], bu, x * fabsf(sca[kF])));
-      // all * nsig in [2^13, 2^14): sums of products are rounded up past it by less than a factor of two
-      const uint32_t e = min(max(__float_as_uint(all) >> 23, 14u), 253u);
-      nsig[i] = all == 0.0f ? sig[i] : __uint_as_float((254u + 13u - e) << 23);
-      nisig[i] = all == 0.0f ? isig[i] : __uint_as_float((e - 13u) << 23);
-    }
-    // S k' in two parts: rows are tokens
-    float sh[2][4] = {}, sl[2][4] = {};
-    uint32_t out[16];
+    for (int r = 0; r < 2; ++r) ldmatrix_x4(key + key_at(16 * r + (lane & 15), lane >> 4), f[r][0], f[r][1], f[r][2], f[r][3]);
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
-      uint32_t lo[2];
+      uint32_t hi[4], lo[4], e[2][4];  // of both tiles of value rows; the next rows of k'
+      if (m < 7) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        split_f16(S[m][2 * i], S[m][2 * i + 1], out[2 * m + i], lo[i]);
-        out[2 * m + i] = transpose8(out[2 * m + i]);
-        lo[i] = transpose8(lo[i]);
+        for (int r = 0; r < 2; ++r)
+          ldmatrix_x4(key + key_at(16 * r + (lane & 15), 2 * m + 2 + (lane >> 4)), e[r][0], e[r][1], e[r][2], e[r][3]);
       }
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        uint32_t f[4];
-        ldmatrix_x4(key + key_at(16 * r + (lane & 15), 2 * m + (lane >> 4)), f[0], f[1], f[2], f[3]);
-        mma_f16_16816(sh[r], f, out[2 * m], out[2 * m + 1]);
-        mma_f16_16816(sl[r], f, lo[0], lo[1]);
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < 2; ++i) split_f16(S[2 * m + i][2 * t], S[2 * m + i][2 * t + 1], hi[2 * t + i], lo[2 * t + i]);
+#pragma unroll
+      for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          mma_f16_16816(sh[r][t], f[r], hi[2 * t], hi[2 * t + 1]);
+          mma_f16_16816(sl[r][t], f[r], lo[2 * t], lo[2 * t + 1]);
+        }
+      if (m == 7) {
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          const uint32_t w = v[x >> 2][(x >> 1) & 1][x & 1];
+          vmax = max(vmax, max(w << 16 & 0x7FFF0000u, w & 0x7FFF0000u));
+        }
+        vmax = __reduce_max_sync(0xffffffffu, vmax);
       }
+      if (kWide) *reinterpret_cast<uint4*>(to + m * 512) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) f[0][i] = e[0][i], f[1][i] = e[1][i], held[m][i] = hi[i];
+    }
+    if (!kWide) {
+#pragma unroll
+      for (int m = 0; m < 8; ++m)
+        *reinterpret_cast<uint4*>(to + m * 512) = make_uint4(held[m][0], held[m][1], held[m][2], held[m][3]);
     }
 #pragma unroll
-    for (int x = 0; x < 4; ++x)
-      *reinterpret_cast<uint4*>(to + x * 512) = make_uint4(out[4 * x], out[4 * x + 1], out[4 * x + 2], out[4 * x + 3]);
-    *reinterpret_cast<float4*>(to + 5 * 512) = make_float4(isig[0], isig[1], nisig[0], nisig[1]);
+    for (int x = 0; x < 16; ++x) top = max3(max3(top, fabsf(S[x][0]), fabsf(S[x][1])), fabsf(S[x][2]), fabsf(S[x][3]));
+    // the scale for x, u and the state behind the chunk, by bounds of all of them
+    float nsig, nisig;
+    {
+      const float x = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))) * isig;
+      const float bx = at<kMaxB>(s0, s1) * (__uint_as_float(vmax) + x * at<kSumA>(s0, s1)), bu = at<kSumT>(s0, s1) * bx;
+      const float all = fmaxf(max3(bx, bu, at<kMaxC>(s0, s1) * bu), fmaf(at<kSumC>(s0, s1), bu, x * fabsf(at<kF>(s0, s1))));
+      // all * nsig in [2^13, 2^14): sums of products are rounded up past it by less than a factor of two
+      const uint32_t y = min(max(__float_as_uint(all) >> 23, 14u), 253u);
+      nsig = all == 0.0f ? sig : __uint_as_float((254u + 13u - y) << 23);
+      nisig = all == 0.0f ? isig : __uint_as_float((y - 13u) << 23);
+    }
+    *reinterpret_cast<float2*>(to + 10 * 512) = make_float2(isig, nisig);
     // x, in two parts as B operands
-    uint32_t xh[2][2], xl[2][2];
+    uint32_t xh[2][2][2], xl[2][2][2];
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int t = 16 * m + 8 * r + g;
-        const float fa = fac[t], beta = fac[kChunk + t];
-        float x[2];
+        const int row = 16 * m + 8 * r + g;
+        const float fai = fac[row] * isig, bn = fac[kChunk + row] * nsig;
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-          x[i] = (beta * nsig[i]) * (v[m][r][i] - (fa * isig[i]) * (sh[m][2 * r + i] + sl[m][2 * r + i]));
-        split_f16(x[0], x[1], xh[m][r], xl[m][r]);
-        xh[m][r] = transpose8(xh[m][r]);
-        xl[m][r] = transpose8(xl[m][r]);
+        for (int t = 0; t < 2; ++t) {
+          const float x0 = bn * (bf16_lo(v[m][r][t]) - fai * (sh[m][t][2 * r] + sl[m][t][2 * r]));
+          const float x1 = bn * (bf16_hi(v[m][r][t]) - fai * (sh[m][t][2 * r + 1] + sl[m][t][2 * r + 1]));
+          split_f16(x0, x1, xh[m][t][r], xl[m][t][r]);
+          xh[m][t][r] = transpose8(xh[m][t][r]);
+          xl[m][t][r] = transpose8(xl[m][t][r]);
+        }
       }
     // u = T x
-    float u[2][4] = {}, ul_[2][4] = {};
+    uint32_t th_[3][4], tl[3][4];  // T: rows and columns 0, 0; 16, 0; 16, 16
+#pragma unroll
+    for (int x = 0; x < 3; ++x) {
+      ldmatrix_x4_trans(tri_a(tri, (x + 1) / 2, x / 2, lane), th_[x][0], th_[x][1], th_[x][2], th_[x][3]);
+      ldmatrix_x4_trans(tri_a(tri + kTriBytes, (x + 1) / 2, x / 2, lane), tl[x][0], tl[x][1], tl[x][2], tl[x][3]);
+    }
+    float u[2][2][4] = {}, ul[2][2][4] = {};
 #pragma unroll
     for (int m = 0; m < 2; ++m)
 #pragma unroll
-      for (int jt = 0; jt <= m; ++jt) {
-        uint32_t f[4], e[4];
-        ldmatrix_x4_trans(tri_a(tri, m, jt, lane), f[0], f[1], f[2], f[3]);
-        ldmatrix_x4_trans(tri_a(tri + kTriBytes, m, jt, lane), e[0], e[1], e[2], e[3]);
-        mma_f16_16816(u[m], f, xh[jt][0], xh[jt][1]);
-        mma_f16_16816(ul_[m], f, xl[jt][0], xl[jt][1]);
-        mma_f16_16816(ul_[m], e, xh[jt][0], xh[jt][1]);
-      }
-    // u for the outputs (one part), and with its factors for the state (two)
-    uint32_t uo[2][2], uh[2][2], ul[2][2];
+      for (int jt = 0; jt <= m; ++jt)
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+        for (int t = 0; t < 2; ++t) {
+          mma_f16_16816(u[m][t], th_[m + jt], xh[jt][t][0], xh[jt][t][1]);
+          mma_f16_16816(ul[m][t], th_[m + jt], xl[jt][t][0], xl[jt][t][1]);
+          mma_f16_16816(ul[m][t], tl[m + jt], xh[jt][t][0], xh[jt][t][1]);
+        }
+    // a factor past fp32's range belongs to a state of zeros
+    const float grow = fminf(at<kF>(s0, s1) * isig * nsig, 3.0e38f), t_up = at<kTUp>(s0, s1);
+#pragma unroll
+    for (int x = 0; x < 16; ++x)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[x][i] *= grow;
+    // u for the outputs (one part), and with its factors, value rows by tokens, for the state (two)
+    uint32_t ch_[2][4], cl[2][4];
+#pragma unroll
+    for (int m = 0; m < 2; ++m) {
+      uint32_t uo[2][2];
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
         const float fc = fac[2 * kChunk + 16 * m + 8 * r + g];
-        const float u0 = (u[m][2 * r] + ul_[m][2 * r]) * sca[kTUp], u1 = (u[m][2 * r + 1] + ul_[m][2 * r + 1]) * sca[kTUp];
-        split_f16(u0 * fc, u1 * fc, uh[m][r], ul[m][r]);
-        uh[m][r] = transpose8(uh[m][r]);
-        ul[m][r] = transpose8(ul[m][r]);
-        uo[m][r] = transpose8(pack_f16x2(u0, u1));
-      }
-    *reinterpret_cast<uint4*>(to + 4 * 512) = make_uint4(uo[0][0], uo[0][1], uo[1][0], uo[1][1]);
-    // the state behind the chunk; a factor past fp32's range belongs to a state of zeros
-    const float f0 = fminf(sca[kF] * isig[0] * nsig[0], 3.0e38f), f1 = fminf(sca[kF] * isig[1] * nsig[1], 3.0e38f);
 #pragma unroll
-    for (int m = 0; m < 8; ++m) {
-      S[m][0] *= f0, S[m][1] *= f1, S[m][2] *= f0, S[m][3] *= f1;
+        for (int t = 0; t < 2; ++t) {
+          const float u0 = (u[m][t][2 * r] + ul[m][t][2 * r]) * t_up;
+          const float u1 = (u[m][t][2 * r + 1] + ul[m][t][2 * r + 1]) * t_up;
+          split_f16(u0 * fc, u1 * fc, ch_[m][2 * r + t], cl[m][2 * r + t]);
+          ch_[m][2 * r + t] = transpose8(ch_[m][2 * r + t]);
+          cl[m][2 * r + t] = transpose8(cl[m][2 * r + t]);
+          uo[t][r] = transpose8(pack_f16x2(u0, u1));
+        }
+      }
+      *reinterpret_cast<uint4*>(to + (8 + m) * 512) = make_uint4(uo[0][0], uo[0][1], uo[1][0], uo[1][1]);
+    }
+    // the state behind the chunk
+#pragma unroll
+    for (int m = 0; m < 8; ++m)
 #pragma unroll
       for (int jt = 0; jt < 2; ++jt) {
-        uint32_t f[4];
-        ldmatrix_x4_trans(key + key_at(16 * jt + (lane & 7) + ((lane >> 4) << 3), 2 * m + ((lane >> 3) & 1)), f[0], f[1],
-                          f[2], f[3]);
-        mma_f16_16816(S[m], f, uh[jt][0], uh[jt][1]);
-        mma_f16_16816(S[m], f, ul[jt][0], ul[jt][1]);
-      }
-    }
-    tops();
+        uint32_t b0[2], b1[2];
+        ldmatrix_x4_trans(key + key_at(16 * jt + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * m + (lane >> 4)), b0[0], b1[0],
+                          b0[1], b1[1]);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) sig[i] = nsig[i], isig[i] = nisig[i];
+        for (int i = 0; i < 2; ++i) {
+          mma_f16_16816(S[2 * m + i], ch_[jt], b0[i], b1[i]);
+          mma_f16_16816(S[2 * m + i], cl[jt], b0[i], b1[i]);
+        }
+      }
+    sig = nsig, isig = nisig;
   }
   __syncthreads();  // the last chunk is handed over
 #pragma unroll
-  for (int m = 0; m < 8; ++m)
+  for (int x = 0; x < 16; ++x)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) st[(size_t)(i & 1) * kHeadDim + 16 * m + (i >> 1) * 8] = S[m][i] * isig[i & 1];
+    for (int i = 0; i < 2; ++i)
+      *reinterpret_cast<float2*>(st + i * 8 * kHeadDim + 8 * x) = make_float2(S[x][2 * i] * isig, S[x][2 * i + 1] * isig);
+}
+
+int num_sms() {
+  int dev = 0, n = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+    return 0;
+  return n;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -643,8 +757,10 @@ extern "C" int prompt_delta(float* state, int num_slots, const void* q, const vo
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   chunk_kernel<<<dim3((unsigned)chunk_slots, num_k_heads), kChunkThreads, 0, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return SDVA_ERR_CUDA;
-  if (cudaFuncSetAttribute(state_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStateSmem) != cudaSuccess)
+  const dim3 grid(kHeadDim / (16 * kWarps), num_v_heads, num_lanes);
+  const auto kernel = (int64_t)grid.x * grid.y * grid.z <= 2 * num_sms() ? state_kernel<true> : state_kernel<false>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStateSmem) != cudaSuccess)
     return SDVA_ERR_CUDA;
-  state_kernel<<<dim3(kHeadDim / (8 * kWarps), num_v_heads, num_lanes), kThreads, kStateSmem, s>>>(a);
+  kernel<<<grid, kThreads, kStateSmem, s>>>(a, wait_limit());
   return cudaGetLastError() == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
 }
