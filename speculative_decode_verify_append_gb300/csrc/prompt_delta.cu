@@ -73,15 +73,9 @@ struct PromptArgs {
 // has at most n / 32 + 1 chunks, and the next lane's base is at least as far.
 __host__ __device__ __forceinline__ int chunk_base(int at, int lane) { return at / kChunk + lane; }
 
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
-__device__ __forceinline__ float warp_sum(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-  return x;
+// The largest of a warp's x >= 0.
+__device__ __forceinline__ float positive_max(float x) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
 }
 
 // A column of T or P; what fp16 leaves over into the next matrix.
@@ -97,6 +91,16 @@ __device__ __forceinline__ void store_column(uint8_t* to, int j, const float (&x
   }
 }
 
+// A warp's bytes from shared memory to a record, 512 at a time: a column of its own is 16 bytes of 32 lines a store,
+// which kept L1 busy for 80% of the kernel's time.
+template <int kBytes>
+__device__ __forceinline__ void copy_out(uint8_t* to, const uint8_t* from, int lane) {
+  __syncwarp();
+#pragma unroll
+  for (int x = 16 * lane; x < kBytes; x += 512)
+    *reinterpret_cast<uint4*>(to + x) = *reinterpret_cast<const uint4*>(from + x);
+}
+
 constexpr int kChunkThreads = 128;
 
 struct ChunkSmem {
@@ -107,7 +111,7 @@ struct ChunkSmem {
   float gram[2][kChunk][kChunk + 4];  // k' . k', q' . k' (row, column)
   alignas(16) float eg[4][kChunk];    // of each warp's value head
   alignas(16) float br[4][kChunk];
-  float sum_sq[2][kChunk], up[2][kChunk], down[2][kChunk], l1[kChunk], top[kChunk];
+  float sum_sq[2][kChunk], up[2][kChunk], down[2][kChunk];
   uint32_t found[kChunkThreads / 32];
 };
 
@@ -166,27 +170,22 @@ __global__ void __launch_bounds__(kChunkThreads, 6) chunk_kernel(PromptArgs a) {
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const Scale sc = scale_of_row(__uint_as_float(top));
-      float sq = 0.0f, l1 = 0.0f;
+      unsigned long long sq2 = 0;
+      const unsigned long long down = tc::f2_pack(sc.down, sc.down);
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float f0 = bf16_lo(x[i]) * sc.down, f1 = bf16_hi(x[i]) * sc.down;
-        sq = fmaf(f0, f0, fmaf(f1, f1, sq));
-        l1 += fabsf(f0) + fabsf(f1);
-        x[i] = pack_f16x2(f0, f1);
+        const unsigned long long f = tc::fmul2(tc::f2_pack(bf16_lo(x[i]), bf16_hi(x[i])), down);
+        sq2 = tc::ffma2(f, f, sq2);
+        const float2 y = tc::f2_unpack(f);
+        x[i] = pack_f16x2(y.x, y.y);
       }
-#pragma unroll
-      for (int o = 1; o <= 2; o <<= 1) {
-        sq += __shfl_xor_sync(0xffffffffu, sq, o);
-        l1 += __shfl_xor_sync(0xffffffffu, l1, o);
-      }
+      float sq = tc::f2_unpack(sq2).x + tc::f2_unpack(sq2).y;
+      sq += __shfl_xor_sync(0xffffffffu, sq, 1);
+      sq += __shfl_xor_sync(0xffffffffu, sq, 2);
       if (p == 0) {
         s.sum_sq[m][r] = sq;
         s.up[m][r] = sc.up;
         s.down[m][r] = sc.down;
-        if (m == 0) {
-          s.l1[r] = l1;
-          s.top[r] = __uint_as_float(top) * sc.down;
-        }
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -235,7 +234,7 @@ __global__ void __launch_bounds__(kChunkThreads, 6) chunk_kernel(PromptArgs a) {
     }
     const float eg = on ? expf(log_decay) : 1.0f, beta = beta_;
     float x[kChunk], d = 0.0f, top = 0.0f;
-    __syncwarp();
+    __syncwarp();  // the task before is done with the warp's places
     s.eg[warp][lane] = eg;
     s.br[warp][lane] = beta * rk;
     __syncwarp();
@@ -261,16 +260,19 @@ __global__ void __launch_bounds__(kChunkThreads, 6) chunk_kernel(PromptArgs a) {
           top = fmaxf(top, fabsf(x[i + y]));
         }
       }
-      const Scale ps = scale_of_row(warp_max(top));
-      store_column<false>(rec + 2 * kTriBytes, lane, x, ps.down);
+      const Scale ps = scale_of_row(positive_max(top));
+      uint8_t* const mine = reinterpret_cast<uint8_t*>(s.a[warp]);
+      store_column<false>(mine, lane, x, ps.down);
+      copy_out<kTriBytes>(rec + 2 * kTriBytes, mine, lane);
       const float fa = fall * rk, fc = rest * rk;
       fac[lane] = fa;
       fac[kChunk + lane] = beta;
       fac[2 * kChunk + lane] = fc;
       fac[3 * kChunk + lane] = a.scale * rq * fall;
       fac[4 * kChunk + lane] = a.scale * rq * ps.up;
-      const float sum_a = warp_max(fabsf(fa) * s.l1[lane]), max_b = warp_max(fabsf(beta)), max_c = warp_max(fabsf(fc));
-      const float sum_c = warp_sum(fabsf(fc) * s.top[lane]);
+      // |S k'| is at most sqrt(128) |k'| times the largest of S, an element of k' below 4
+      const float sum_a = positive_max(fabsf(fa) * 11.4f * sqrtf(s.sum_sq[0][lane])), max_b = positive_max(fabsf(beta));
+      const float max_c = positive_max(fabsf(fc)), sum_c = 4.0f * kChunk * max_c;
       if (lane == 0) {
         float* const g = fac + kFactors * kChunk;
         g[kF] = all;
@@ -311,9 +313,12 @@ __global__ void __launch_bounds__(kChunkThreads, 6) chunk_kernel(PromptArgs a) {
     }
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) top = fmaxf(top, fabsf(x[i]));
-    top = warp_max(top);
+    top = positive_max(top);
     const Scale ts = scale_of_row(top);
-    store_column<true>(rec, lane, x, ts.down);
+    uint8_t* const mine = reinterpret_cast<uint8_t*>(A);
+    __syncwarp();
+    store_column<true>(mine, lane, x, ts.down);
+    copy_out<2 * kTriBytes>(rec, mine, lane);
     if (lane == 0) {
       float* const g = fac + kFactors * kChunk;
       g[kSumT] = top * kChunk;
@@ -546,7 +551,6 @@ __global__ void __launch_bounds__(kThreads, kWide ? 2 : 3) state_kernel(PromptAr
           v[m][r][t] = ch * kChunk + row < n ? w : 0u;
         }
       }
-    const float4 s0 = *reinterpret_cast<const float4*>(sca), s1 = *reinterpret_cast<const float4*>(sca + 4);
     // S k' in two parts: rows are tokens 16 r + g (+ 8), columns value rows 8 t + 2 c (+ 1).  A step's rows of k'
     // are loaded before the one in front of it is stored for the outputs: a load would wait for that store.
     float sh[2][2][4] = {}, sl[2][2][4] = {}, top = 0.0f;
@@ -591,6 +595,7 @@ __global__ void __launch_bounds__(kThreads, kWide ? 2 : 3) state_kernel(PromptAr
     }
 #pragma unroll
     for (int x = 0; x < 16; ++x) top = max3(max3(top, fabsf(S[x][0]), fabsf(S[x][1])), fabsf(S[x][2]), fabsf(S[x][3]));
+    const float4 s0 = *reinterpret_cast<const float4*>(sca), s1 = *reinterpret_cast<const float4*>(sca + 4);
     // the scale for x, u and the state behind the chunk, by bounds of all of them
     float nsig, nisig;
     {
