@@ -197,6 +197,9 @@ constexpr int kRows = kMaxWindow;  // of the tensor cores' tile; rows behind the
 constexpr int kWarps = 8;          // with a part of the state
 constexpr int kThreads = (kWarps + 2) * 32;
 constexpr int kStateBytes = (int)(kStateElems * sizeof(float));
+// From a value row of the state to the next in shared memory: four threads read 64 bytes of a row, eight in one pass
+// those of two rows, out of different banks.
+constexpr int kStatePitch = kHeadDim * 4 + 64;
 
 struct VerifySmem {
   uint64_t bar[kWarps];  // the copies of each warp's part of the state
@@ -407,19 +410,20 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a, long 
   }
   cp_async_commit();
   extern __shared__ __align__(128) uint8_t state_smem[];
-  const uint8_t* const mine = state_smem + warp * (kStateBytes / kWarps);
+  const uint8_t* const mine = state_smem + warp * 16 * kStatePitch;
   float* const st = a.state + ((size_t)lr.slot * a.hv + h) * kStateElems + (size_t)row16 * kHeadDim;
   const uint32_t bar = smem_u32(&s.bar[warp & (kWarps - 1)]);
   float d[kRows];         // of the two further warps
   bool bad = false;
   if (warp < kWarps) {
     if (n > 0) {
-      if (lane == 0) {  // 8 KB: a value row's 512 bytes leave the reads below two to a bank
+      if (lane == 0) {
         tc::mbar_init(bar, 1);
         tc::mbar_fence_init();
         tc::mbar_arrive_expect_tx(bar, kStateBytes / kWarps);
-        tc::bulk_load(smem_u32(mine), st, kStateBytes / kWarps, bar);
       }
+      __syncwarp();
+      if (lane < 16) tc::bulk_load(smem_u32(mine) + lane * kStatePitch, st + (size_t)lane * kHeadDim, kHeadDim * 4, bar);
     }
   } else {
     bad = ways(s, a, warp - kWarps, n, row0, h, lane, d);
@@ -488,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a, long 
   state_here();
   // S k' in two parts, S q' in one; of the state value rows 8 t + g, key dims 16 m + 4 c ..
   const auto state_of = [&](int t, int m) {
-    return *reinterpret_cast<const float4*>(mine + (8 * t + g) * kHeadDim * 4 + 64 * m + 16 * c);
+    return *reinterpret_cast<const float4*>(mine + (8 * t + g) * kStatePitch + 64 * m + 16 * c);
   };
   float4 S[2][8];
 #pragma unroll
@@ -795,9 +799,9 @@ extern "C" int verify_delta(float* state, int num_slots, const void* q, const vo
   } else {
     const dim3 grid(num_v_heads, num_lanes);
     const auto kernel = deltas == nullptr ? window_kernel<true> : window_kernel<false>;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStateBytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kWarps * 16 * kStatePitch) != cudaSuccess)
       return SDVA_ERR_CUDA;
-    kernel<<<grid, kThreads, kStateBytes, cs>>>(a, wait_limit());
+    kernel<<<grid, kThreads, kWarps * 16 * kStatePitch, cs>>>(a, wait_limit());
   }
   return cudaGetLastError() == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
 }
