@@ -458,6 +458,7 @@ __global__ void __launch_bounds__(kThreads, kWide ? 2 : 3) state_kernel(PromptAr
         tc::mbar_wait<false>(bar, parity, &never);  // the copies end before the CTA does
       }
       cp_async_wait_all();
+      tc::fence_proxy_async_smem();
       __syncthreads();  // chunk i is there for the chain and chunk i - 1 for the outputs, which has been handed over
       fetch(i, smem_u32(&bars[(i + 1) & 1]));
       if (i == 0) continue;
@@ -531,6 +532,7 @@ __global__ void __launch_bounds__(kThreads, kWide ? 2 : 3) state_kernel(PromptAr
   }
 
   for (int ch = 0; ch < chunks; ++ch) {
+    tc::fence_proxy_async_smem();  // what was read of a place is read before the next bulk copy into it
     __syncthreads();
     const uint8_t* const stage = chain_smem + (ch & 1) * (kChainBytes + kValueBytes);
     const uint32_t key = smem_u32(stage), tri = key + kKeyBytes;
@@ -551,6 +553,8 @@ __global__ void __launch_bounds__(kThreads, kWide ? 2 : 3) state_kernel(PromptAr
           v[m][r][t] = ch * kChunk + row < n ? w : 0u;
         }
       }
+    float4 s0, s1;  // the chunk's scalars: early where there are registers for them
+    if (kWide) s0 = *reinterpret_cast<const float4*>(sca), s1 = *reinterpret_cast<const float4*>(sca + 4);
     // S k' in two parts: rows are tokens 16 r + g (+ 8), columns value rows 8 t + 2 c (+ 1).  A step's rows of k'
     // are loaded before the one in front of it is stored for the outputs: a load would wait for that store.
     float sh[2][2][4] = {}, sl[2][2][4] = {}, top = 0.0f;
@@ -595,7 +599,7 @@ __global__ void __launch_bounds__(kThreads, kWide ? 2 : 3) state_kernel(PromptAr
     }
 #pragma unroll
     for (int x = 0; x < 16; ++x) top = max3(max3(top, fabsf(S[x][0]), fabsf(S[x][1])), fabsf(S[x][2]), fabsf(S[x][3]));
-    const float4 s0 = *reinterpret_cast<const float4*>(sca), s1 = *reinterpret_cast<const float4*>(sca + 4);
+    if (!kWide) s0 = *reinterpret_cast<const float4*>(sca), s1 = *reinterpret_cast<const float4*>(sca + 4);
     // the scale for x, u and the state behind the chunk, by bounds of all of them
     float nsig, nisig;
     {

@@ -12,8 +12,8 @@
 // what a chain does.  Both calls are bound by the state: 64 KB a head, read by
 // verify_delta and also written by commit_delta and by a committed window.
 //
-// verify_delta has two kernels.  rows_kernel takes a chain of up to kSeqRows
-// tokens one after the other in fp32: a warp has 16 value rows of a head's state
+// verify_delta has two kernels.  rows_kernel takes a chain of two or three
+// tokens at most, one after the other in fp32: a warp has 16 value rows of a head's state
 // in registers, eight lanes to a row, and needs no other warp.
 // window_kernel takes up to 16 in the form above: a CTA has a head, a warp 16
 // value rows of its state as the tensor cores' B operand (and, committed, as
@@ -77,7 +77,10 @@ __device__ __forceinline__ LaneRows lane_rows(const VerifyArgs& a, int b) {
   return r;
 }
 
-constexpr int kSeqRows = 4;
+// Tokens that rows_kernel takes.  64 lanes, 16 / 32 heads, us of rows_kernel and of window_kernel: recorded, 1 token 27.9
+// and 38.9, 2 35.1 and 38.8, 3 42.9 and 39.1; committed, 1 43.6 and 61.1, 3 57.4 and 61.4, 4 63.9 and 61.6.  Of one
+// lane: recorded, 2 3.2 and 4.8, 4 4.8 and 5.2; committed, 3 4.5 and 7.1.
+constexpr int kSeqRecorded = 2, kSeqCommitted = 3;
 constexpr int kSeqThreads = 128;
 
 // Value rows 4 i + lane / 8 of a warp's 16; key dims 4 (lane & 7) + 32 p.
@@ -793,7 +796,7 @@ extern "C" int verify_delta(float* state, int num_slots, const void* q, const vo
                         scale,
                         qk_eps};
   const cudaStream_t cs = reinterpret_cast<cudaStream_t>(stream);
-  if (window <= kSeqRows && parent == nullptr) {
+  if (window <= (deltas != nullptr ? kSeqRecorded : kSeqCommitted) && parent == nullptr) {
     const dim3 grid(kHeadDim / (16 * (kSeqThreads / 32)), num_v_heads, num_lanes);
     (deltas == nullptr ? rows_kernel<true> : rows_kernel<false>)<<<grid, kSeqThreads, 0, cs>>>(a);
   } else {
