@@ -327,24 +327,23 @@ __global__ void __launch_bounds__(kChunkThreads, 6) chunk_kernel(PromptArgs a) {
   }
 }
 
-constexpr int kWarps = 2;  // of the chain, 16 value rows each, and as many for the outputs
-constexpr int kThreads = 2 * kWarps * 32;
-constexpr int kValueBytes = kWarps * kChunk * 32;
 // Of a chunk the chain takes k', T, the factors and its values, the outputs q',
 // P and the factors; each in two places, the one in use and the one that comes.
 constexpr int kChainBytes = kKeyBytes + 2 * kTriBytes + kFactorBytes;
 constexpr int kOutBytes = kKeyBytes + kTriBytes + kFactorBytes;
 // What a warp of the chain hands over: S (32 words a thread), u (8), the scales of both
 constexpr int kHandBytes = 11 * 32 * 16;
-constexpr int kStateSmem = 2 * (kChainBytes + kValueBytes + kOutBytes + kWarps * kHandBytes);
+template <int kWarps>
+constexpr int kStateSmem = 2 * (kChainBytes + kWarps * kChunk * 32 + kOutBytes + kWarps * kHandBytes);
 
 // A column of T or P in A's place: rows are stored by columns, so the matrices come transposed.
 __device__ __forceinline__ uint32_t tri_a(uint32_t tri, int m, int jt, int lane) {
   return tri + tri_at(16 * jt + (lane & 7) + ((lane >> 4) << 3), 2 * m + ((lane >> 3) & 1));
 }
 // The values of a chunk: 2 kWarps 16-byte pieces to a row, eight rows of a piece in different banks.
+template <int kWarps>
 __device__ __forceinline__ int value_at(int row, int piece) {
-  return (row * 2 * kWarps + (piece ^ ((row >> 1) & (2 * kWarps - 1)))) << 4;
+  return (row * 2 * kWarps + (piece ^ (kWarps == 4 ? row & 7 : (row >> 1) & 3))) << 4;
 }
 
 // One of a chunk's scalars.
@@ -355,11 +354,14 @@ __device__ __forceinline__ float at(float4 lo, float4 hi) {
          : kWhich == 4 ? hi.x : kWhich == 5 ? hi.y : kWhich == 6 ? hi.z : hi.w;
 }
 
-// kWide: as many registers as two CTAs leave an SM's warps, for grids that give each SM no more.  One prompt of 8,192
-// tokens, 32 heads: 338 us with them, 361 without; eight of 2,048: 542 and 474, with three CTAs to an SM.  Which of the
-// two stores S for the outputs at once and which behind the products is by the same measurements.
-template <bool kWide>
-__global__ void __launch_bounds__(kThreads, kWide ? 2 : 3) state_kernel(PromptArgs a, long long limit) {
+// kWarps warps of the chain, 16 value rows each, and as many for the outputs; kCtas CTAs to an SM.  Three, which leaves
+// fewer registers, is for grids of many rounds (see launch_state).
+template <int kWarps, int kCtas>
+__global__ void __launch_bounds__(kWarps * 64, kCtas) state_kernel(PromptArgs a, long long limit) {
+  static_assert(kWarps == 2 || kWarps == 4, "the values' places in shared memory");
+  constexpr int kThreads = 2 * kWarps * 32;
+  constexpr int kValueBytes = kWarps * kChunk * 32;
+  constexpr bool kWide = kWarps * kCtas <= 4;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int never;  // 0: no role's wait ends another's
   const int th = threadIdx.x, lane = th & 31, g = lane >> 2, c = lane & 3;
@@ -444,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, kWide ? 2 : 3) state_kernel(PromptAr
         for (int x = ot; x < kChunk * 2 * kWarps; x += kWarps * 32) {
           const int r = x / (2 * kWarps), p = x % (2 * kWarps);
           const int t = (i + 1) * kChunk + r;
-          if (t < n) cp_async_16(to + value_at(r, p), vcol + (size_t)t * (size_t)a.v_stride + 8 * p);
+          if (t < n) cp_async_16(to + value_at<kWarps>(r, p), vcol + (size_t)t * (size_t)a.v_stride + 8 * p);
         }
       }
     };
@@ -549,7 +551,7 @@ __global__ void __launch_bounds__(kThreads, kWide ? 2 : 3) state_kernel(PromptAr
         const int row = 16 * m + 8 * r + g;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(stage + kChainBytes + value_at(row, 2 * warp + t) + 4 * c);
+          const uint32_t w = *reinterpret_cast<const uint32_t*>(stage + kChainBytes + value_at<kWarps>(row, 2 * warp + t) + 4 * c);
           v[m][r][t] = ch * kChunk + row < n ? w : 0u;
         }
       }
@@ -588,6 +590,8 @@ __global__ void __launch_bounds__(kThreads, kWide ? 2 : 3) state_kernel(PromptAr
         }
         vmax = __reduce_max_sync(0xffffffffu, vmax);
       }
+      // stored at once, or behind the products: 361 us against 405 for 8,192 tokens with the fewer registers, 350
+      // against 340 with the more
       if (kWide) *reinterpret_cast<uint4*>(to + m * 512) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
 #pragma unroll
       for (int i = 0; i < 4; ++i) f[0][i] = e[0][i], f[1][i] = e[1][i], held[m][i] = hi[i];
@@ -697,11 +701,30 @@ __global__ void __launch_bounds__(kThreads, kWide ? 2 : 3) state_kernel(PromptAr
       *reinterpret_cast<float2*>(st + i * 8 * kHeadDim + 8 * x) = make_float2(S[x][2 * i] * isig, S[x][2 * i + 1] * isig);
 }
 
+template <int kWarps, int kCtas>
+int launch_as(const PromptArgs& a, cudaStream_t s) {
+  const auto kernel = state_kernel<kWarps, kCtas>;
+  constexpr int bytes = kStateSmem<kWarps>;
+  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    return SDVA_ERR_CUDA;
+  kernel<<<dim3(kHeadDim / (16 * kWarps), a.hv, a.num_lanes), kWarps * 64, bytes, s>>>(a, wait_limit());
+  return cudaGetLastError() == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
+}
+
 int num_sms() {
   int dev = 0, n = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return 0;
   return n;
+}
+
+// A chain is fastest alone with its SM: 1.06 us a chunk with two to an SM, 1.5 with four, 2.0 and more where they are of
+// two CTAs.  So CTAs of two while each has an SM of its own, then of four, and where those would not all run at once
+// either, three CTAs of two.  Of 2,048 tokens a prompt, us with two / four / three CTAs of two: 16 heads, two prompts 90 /
+// 119 / 91, three 150 / 125 / 150, four 157 / 131 / 157; 32 heads, eight prompts 531 / 498 / 457.
+int launch_state(const PromptArgs& a, cudaStream_t s) {
+  const int64_t ctas = (int64_t)a.hv * a.num_lanes * (kHeadDim / 32), sms = num_sms();
+  return ctas <= sms ? launch_as<2, 2>(a, s) : ctas <= 2 * sms ? launch_as<4, 1>(a, s) : launch_as<2, 3>(a, s);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
@@ -766,10 +789,5 @@ extern "C" int prompt_delta(float* state, int num_slots, const void* q, const vo
   const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   chunk_kernel<<<dim3((unsigned)chunk_slots, num_k_heads), kChunkThreads, 0, s>>>(a);
   if (cudaGetLastError() != cudaSuccess) return SDVA_ERR_CUDA;
-  const dim3 grid(kHeadDim / (16 * kWarps), num_v_heads, num_lanes);
-  const auto kernel = (int64_t)grid.x * grid.y * grid.z <= 2 * num_sms() ? state_kernel<true> : state_kernel<false>;
-  if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStateSmem) != cudaSuccess)
-    return SDVA_ERR_CUDA;
-  kernel<<<grid, kThreads, kStateSmem, s>>>(a, wait_limit());
-  return cudaGetLastError() == cudaSuccess ? SDVA_OK : SDVA_ERR_CUDA;
+  return launch_state(a, s);
 }
