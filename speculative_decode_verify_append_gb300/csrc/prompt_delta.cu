@@ -559,7 +559,7 @@ __global__ void __launch_bounds__(kWarps * 64, kCtas) state_kernel(PromptArgs a,
     if (kWide) s0 = *reinterpret_cast<const float4*>(sca), s1 = *reinterpret_cast<const float4*>(sca + 4);
     // S k' in two parts: rows are tokens 16 r + g (+ 8), columns value rows 8 t + 2 c (+ 1).  A step's rows of k'
     // are loaded before the one in front of it is stored for the outputs: a load would wait for that store.
-    float sh[2][2][4] = {}, sl[2][2][4] = {}, top = 0.0f;
+    float sk[2][2][4] = {}, top = 0.0f;
     uint32_t f[2][4], held[8][4];
 #pragma unroll
     for (int r = 0; r < 2; ++r) ldmatrix_x4(key + key_at(16 * r + (lane & 15), lane >> 4), f[r][0], f[r][1], f[r][2], f[r][3]);
@@ -576,12 +576,9 @@ __global__ void __launch_bounds__(kWarps * 64, kCtas) state_kernel(PromptArgs a,
 #pragma unroll
         for (int i = 0; i < 2; ++i) split_f16(S[2 * m + i][2 * t], S[2 * m + i][2 * t + 1], hi[2 * t + i], lo[2 * t + i]);
 #pragma unroll
-      for (int r = 0; r < 2; ++r)
+      for (int x = 0; x < 4; ++x) mma_f16_16816(sk[x & 1][x >> 1], f[x & 1], hi[x & 2], hi[(x & 2) + 1]);
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          mma_f16_16816(sh[r][t], f[r], hi[2 * t], hi[2 * t + 1]);
-          mma_f16_16816(sl[r][t], f[r], lo[2 * t], lo[2 * t + 1]);
-        }
+      for (int x = 0; x < 4; ++x) mma_f16_16816(sk[x & 1][x >> 1], f[x & 1], lo[x & 2], lo[(x & 2) + 1]);
       if (m == 7) {
 #pragma unroll
         for (int x = 0; x < 8; ++x) {
@@ -626,8 +623,8 @@ __global__ void __launch_bounds__(kWarps * 64, kCtas) state_kernel(PromptArgs a,
         const float fai = fac[row] * isig, bn = fac[kChunk + row] * nsig;
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const float x0 = bn * (bf16_lo(v[m][r][t]) - fai * (sh[m][t][2 * r] + sl[m][t][2 * r]));
-          const float x1 = bn * (bf16_hi(v[m][r][t]) - fai * (sh[m][t][2 * r + 1] + sl[m][t][2 * r + 1]));
+          const float x0 = bn * (bf16_lo(v[m][r][t]) - fai * sk[m][t][2 * r]);
+          const float x1 = bn * (bf16_hi(v[m][r][t]) - fai * sk[m][t][2 * r + 1]);
           split_f16(x0, x1, xh[m][t][r], xl[m][t][r]);
           xh[m][t][r] = transpose8(xh[m][t][r]);
           xl[m][t][r] = transpose8(xl[m][t][r]);
@@ -640,16 +637,16 @@ __global__ void __launch_bounds__(kWarps * 64, kCtas) state_kernel(PromptArgs a,
       ldmatrix_x4_trans(tri_a(tri, (x + 1) / 2, x / 2, lane), th_[x][0], th_[x][1], th_[x][2], th_[x][3]);
       ldmatrix_x4_trans(tri_a(tri + kTriBytes, (x + 1) / 2, x / 2, lane), tl[x][0], tl[x][1], tl[x][2], tl[x][3]);
     }
-    float u[2][2][4] = {}, ul[2][2][4] = {};
+    float u[2][2][4] = {};
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int p = 0; p < 3; ++p)  // the parts' products: one each of all tiles, then the next
 #pragma unroll
-      for (int jt = 0; jt <= m; ++jt)
+      for (int x = 0; x < 3; ++x)
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          mma_f16_16816(u[m][t], th_[m + jt], xh[jt][t][0], xh[jt][t][1]);
-          mma_f16_16816(ul[m][t], th_[m + jt], xl[jt][t][0], xl[jt][t][1]);
-          mma_f16_16816(ul[m][t], tl[m + jt], xh[jt][t][0], xh[jt][t][1]);
+          const int m = (x + 1) / 2, jt = x / 2;
+          const uint32_t(&b)[2] = p == 1 ? xl[jt][t] : xh[jt][t];
+          mma_f16_16816(u[m][t], p == 2 ? tl[x] : th_[x], b[0], b[1]);
         }
     // a factor past fp32's range belongs to a state of zeros
     const float grow = fminf(at<kF>(s0, s1) * isig * nsig, 3.0e38f), t_up = at<kTUp>(s0, s1);
@@ -667,8 +664,8 @@ __global__ void __launch_bounds__(kWarps * 64, kCtas) state_kernel(PromptArgs a,
         const float fc = fac[2 * kChunk + 16 * m + 8 * r + g];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
-          const float u0 = (u[m][t][2 * r] + ul[m][t][2 * r]) * t_up;
-          const float u1 = (u[m][t][2 * r + 1] + ul[m][t][2 * r + 1]) * t_up;
+          const float u0 = u[m][t][2 * r] * t_up;
+          const float u1 = u[m][t][2 * r + 1] * t_up;
           split_f16(u0 * fc, u1 * fc, ch_[m][2 * r + t], cl[m][2 * r + t]);
           ch_[m][2 * r + t] = transpose8(ch_[m][2 * r + t]);
           cl[m][2 * r + t] = transpose8(cl[m][2 * r + t]);
