@@ -354,14 +354,12 @@ __device__ __forceinline__ float at(float4 lo, float4 hi) {
          : kWhich == 4 ? hi.x : kWhich == 5 ? hi.y : kWhich == 6 ? hi.z : hi.w;
 }
 
-// kWarps warps of the chain, 16 value rows each, and as many for the outputs; kCtas CTAs to an SM.  Three, which leaves
-// fewer registers, is for grids of many rounds (see launch_state).
-template <int kWarps, int kCtas>
-__global__ void __launch_bounds__(kWarps * 64, kCtas) state_kernel(PromptArgs a, long long limit) {
+// kWarps warps of the chain, 16 value rows each, and as many for the outputs; with two of them three CTAs fit an SM.
+template <int kWarps>
+__global__ void __launch_bounds__(kWarps * 64, kWarps == 2 ? 3 : 1) state_kernel(PromptArgs a, long long limit) {
   static_assert(kWarps == 2 || kWarps == 4, "the values' places in shared memory");
   constexpr int kThreads = 2 * kWarps * 32;
   constexpr int kValueBytes = kWarps * kChunk * 32;
-  constexpr bool kWide = kWarps * kCtas <= 4;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int never;  // 0: no role's wait ends another's
   const int th = threadIdx.x, lane = th & 31, g = lane >> 2, c = lane & 3;
@@ -555,12 +553,10 @@ __global__ void __launch_bounds__(kWarps * 64, kCtas) state_kernel(PromptArgs a,
           v[m][r][t] = ch * kChunk + row < n ? w : 0u;
         }
       }
-    float4 s0, s1;  // the chunk's scalars: early where there are registers for them
-    if (kWide) s0 = *reinterpret_cast<const float4*>(sca), s1 = *reinterpret_cast<const float4*>(sca + 4);
     // S k' in two parts: rows are tokens 16 r + g (+ 8), columns value rows 8 t + 2 c (+ 1).  A step's rows of k'
     // are loaded before the one in front of it is stored for the outputs: a load would wait for that store.
     float sk[2][2][4] = {}, top = 0.0f;
-    uint32_t f[2][4], held[8][4];
+    uint32_t f[2][4];
 #pragma unroll
     for (int r = 0; r < 2; ++r) ldmatrix_x4(key + key_at(16 * r + (lane & 15), lane >> 4), f[r][0], f[r][1], f[r][2], f[r][3]);
 #pragma unroll
@@ -587,20 +583,13 @@ __global__ void __launch_bounds__(kWarps * 64, kCtas) state_kernel(PromptArgs a,
         }
         vmax = __reduce_max_sync(0xffffffffu, vmax);
       }
-      // stored at once, or behind the products: 361 us against 405 for 8,192 tokens with the fewer registers, 350
-      // against 340 with the more
-      if (kWide) *reinterpret_cast<uint4*>(to + m * 512) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(to + m * 512) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) f[0][i] = e[0][i], f[1][i] = e[1][i], held[m][i] = hi[i];
-    }
-    if (!kWide) {
-#pragma unroll
-      for (int m = 0; m < 8; ++m)
-        *reinterpret_cast<uint4*>(to + m * 512) = make_uint4(held[m][0], held[m][1], held[m][2], held[m][3]);
+      for (int i = 0; i < 4; ++i) f[0][i] = e[0][i], f[1][i] = e[1][i];
     }
 #pragma unroll
     for (int x = 0; x < 16; ++x) top = max3(max3(top, fabsf(S[x][0]), fabsf(S[x][1])), fabsf(S[x][2]), fabsf(S[x][3]));
-    if (!kWide) s0 = *reinterpret_cast<const float4*>(sca), s1 = *reinterpret_cast<const float4*>(sca + 4);
+    const float4 s0 = *reinterpret_cast<const float4*>(sca), s1 = *reinterpret_cast<const float4*>(sca + 4);
     // the scale for x, u and the state behind the chunk, by bounds of all of them
     float nsig, nisig;
     {
@@ -698,9 +687,9 @@ __global__ void __launch_bounds__(kWarps * 64, kCtas) state_kernel(PromptArgs a,
       *reinterpret_cast<float2*>(st + i * 8 * kHeadDim + 8 * x) = make_float2(S[x][2 * i] * isig, S[x][2 * i + 1] * isig);
 }
 
-template <int kWarps, int kCtas>
+template <int kWarps>
 int launch_as(const PromptArgs& a, cudaStream_t s) {
-  const auto kernel = state_kernel<kWarps, kCtas>;
+  const auto kernel = state_kernel<kWarps>;
   constexpr int bytes = kStateSmem<kWarps>;
   if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
     return SDVA_ERR_CUDA;
@@ -715,13 +704,18 @@ int num_sms() {
   return n;
 }
 
-// A chain is fastest alone with its SM: 1.06 us a chunk with two to an SM, 1.5 with four, 2.0 and more where they are of
-// two CTAs.  So CTAs of two while each has an SM of its own, then of four, and where those would not all run at once
-// either, three CTAs of two.  Of 2,048 tokens a prompt, us with two / four / three CTAs of two: 16 heads, two prompts 90 /
-// 119 / 91, three 150 / 125 / 150, four 157 / 131 / 157; 32 heads, eight prompts 531 / 498 / 457.
+// Two warps of the chain to a CTA, up to three CTAs on an SM, or four warps and one CTA.  A chunk takes the chain 1.05 us
+// with one CTA of two on the SM, 2.0 with two, 2.35 with three, and 1.45 in a CTA of four: whichever ends first by how
+// many rounds its grid makes, lanes being of one length.  Of 2,048 tokens a lane, us with two and with four: 16 heads, two
+// lanes 92 and 110, three 148 and 116, four 155 and 123, six 188 and 224; 32 heads, four lanes 261 and 238, eight 445
+// and 468.  Short lanes make many short rounds, of which those of three CTAs an SM overlap: 60 lanes of 100 tokens, 16
+// heads, 133 and 145.
 int launch_state(const PromptArgs& a, cudaStream_t s) {
-  const int64_t ctas = (int64_t)a.hv * a.num_lanes * (kHeadDim / 32), sms = num_sms();
-  return ctas <= sms ? launch_as<2, 2>(a, s) : ctas <= 2 * sms ? launch_as<4, 1>(a, s) : launch_as<2, 3>(a, s);
+  const int64_t sms = num_sms() > 0 ? num_sms() : 1, twos = (int64_t)a.hv * a.num_lanes * (kHeadDim / 32);
+  const int64_t rest = twos % (3 * sms);
+  const int64_t with_two = twos / (3 * sms) * 47 + (rest == 0 ? 0 : rest <= sms ? 21 : rest <= 2 * sms ? 40 : 47);
+  const int64_t with_four = (twos / 2 + sms - 1) / sms * 29;
+  return with_two <= with_four || a.total < (int64_t)a.num_lanes * 256 ? launch_as<2>(a, s) : launch_as<4>(a, s);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
