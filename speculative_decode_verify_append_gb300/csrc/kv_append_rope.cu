@@ -12,6 +12,8 @@
 // (kv heads, then groups of four q heads).  A kv head's CTA holds its page's K
 // and V (kv_page.cuh); a q CTA gives one warp a token's four heads, eight
 // threads each, so that the heads share the loads of the table's row.
+// 41,175 tokens of 8 lanes, 24 / 4 heads: FP8, 128 dims turned, 121 us (5.7 TB/s);
+// INT4, 64 dims, 117.  64 lanes of up to 16 rows, INT8: 7.1 us; one token: 3.1.
 #include "kv_page.cuh"
 
 namespace sdva {
@@ -22,6 +24,7 @@ using kvpage::kThreads;
 using kvpage::slot_base;
 
 constexpr int kQHeads = 4;  // q heads of a CTA
+constexpr int kAhead = 2;   // tokens of a thread whose loads are under way together
 
 struct RopeArgs {
   const uint16_t* q;
@@ -127,8 +130,10 @@ __device__ __forceinline__ void turn(Piece& p, const float* t, int rot, int sub)
   }
 }
 
+// Four CTAs to an SM and two tokens ahead: of the batch above 121 us; three CTAs and one token 132, three and four 122,
+// four and one 123, five and two 124.
 template <int KVT, bool kNeighbours>
-__global__ void __launch_bounds__(kThreads, 3) append_rope_kernel(RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) append_rope_kernel(RopeArgs a) {
   const int slot = blockIdx.x, th = threadIdx.x;
   bool bad = false;
   int b, page, n;
@@ -243,10 +248,19 @@ __global__ void __launch_bounds__(kThreads, 3) append_rope_kernel(RopeArgs a) {
   const int head = ((int)blockIdx.y - a.num_kv_heads) * kQHeads + ((th >> 3) & (kQHeads - 1));
   if (head >= a.num_q_heads) return;
   const uint16_t* const src = a.q + (size_t)head * kHeadDim;
-  for (int t = th >> 5; t < count; t += kThreads / 32) {
-    Piece p = load_piece(src + (row0 + t) * (size_t)a.q_stride, sub);
-    turn<kNeighbours>(p, turns(t), a.rot, sub);
-    store_piece(a.q_out + ((row0 + t) * a.num_q_heads + head) * kHeadDim, sub, p);
+  // a thread's tokens t, t + 8, ..: kAhead loads in flight
+  constexpr int kStep = kThreads / 32;
+  for (int t = th >> 5; t < count; t += kAhead * kStep) {
+    Piece p[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (t + i * kStep < count) p[i] = load_piece(src + (row0 + t + i * kStep) * (size_t)a.q_stride, sub);
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i)
+      if (t + i * kStep < count) {
+        turn<kNeighbours>(p[i], turns(t + i * kStep), a.rot, sub);
+        store_piece(a.q_out + ((row0 + t + i * kStep) * a.num_q_heads + head) * kHeadDim, sub, p[i]);
+      }
   }
 }
 
