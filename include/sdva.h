@@ -666,10 +666,15 @@ int token_logprobs(const void* logits, int logits_dtype, int64_t row_stride, int
  *   (else SDVA_ERR_UNSUPPORTED); scale positive and finite.
  *   state, q, k, v, out and deltas are 16-byte aligned (else SDVA_ERR_INVALID).
  * Precondition: the values of a lane's rows and of the state that it starts
- * from are finite (log decays: or -inf) and stay in fp32's range.  Other lanes'
- * and other rows' do not reach it.  Accuracy: states, updates and sums are
- * fp32; products on the tensor cores take their operands in two fp16 parts
- * (22 bits).
+ * from are finite (log decays: or -inf), and they, their products and, with a
+ * qk_eps of 0, the squares of q and k stay in fp32's range (a row of zeros has
+ * no direction then).  Other lanes' and other rows' values do not reach a lane.
+ * Accuracy: states, updates and sums are fp32.  Products on the tensor cores
+ * take the state and the updates in two fp16 parts, which leaves some 2^-22 of
+ * the largest value among 16 value rows (prompt_delta) or of a value row
+ * (verify_delta), and what goes to out alone in one (2^-12).  verify_delta of up
+ * to two rows that are recorded, or three that are committed, and commit_delta
+ * compute in fp32 throughout.
  */
 
 /*
@@ -687,7 +692,8 @@ int token_logprobs(const void* logits, int logits_dtype, int64_t row_stride, int
  *              calls that share it must not overlap on the GPU.
  * Offsets that are not in order set SDVA_STATUS_BAD_COUNT and nothing is
  * written; of a lane that is skipped nothing is written, nor are rows outside
- * every lane's range.  total_tokens >= 0 (0 enqueues nothing).
+ * every lane's range.  total_tokens >= 0 (0 enqueues nothing).  Every block
+ * reads all offsets, as kv_append_packed's do.
  * Returns SDVA_OK or a negative SDVA_ERR_*.
  */
 size_t prompt_delta_workspace_size(int total_tokens, int num_lanes, int num_k_heads, int num_v_heads);
@@ -746,8 +752,9 @@ int commit_delta(float* state, int num_slots, const void* k, int64_t k_stride, c
 
 /*
  * sdva_debug_set_wait_limit -- diagnostic hook (no counterpart in the pages).
- * Every device-side wait of the tensor-core kernels of verify_attn and
- * prompt_attn and of token_logprobs' kernel for long rows gives up after
+ * Every device-side wait of the tensor-core kernels of verify_attn,
+ * prompt_attn, prompt_delta and verify_delta and of token_logprobs' kernel for
+ * long rows gives up after
  * `cycles` clock cycles (default about 4e9, two seconds); the CTA then
  * raises SDVA_STATUS_TIMEOUT, waits (with its own bound) for the copies and
  * tensor-core work it issued, frees its tensor memory and returns, leaving

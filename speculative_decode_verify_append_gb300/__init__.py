@@ -177,9 +177,9 @@ class SdvaError(RuntimeError):
 
 
 def sdva_debug_set_wait_limit(cycles: int) -> int:
-    """Bound every device wait of the tensor-core kernels of verify_attn and
-    prompt_attn and of token_logprobs' kernel for long rows at `cycles`
-    clock cycles (negative: the default, about two seconds); returns the
+    """Bound every device wait of the tensor-core kernels of verify_attn,
+    prompt_attn, prompt_delta and verify_delta and of token_logprobs' kernel for
+    long rows at `cycles` clock cycles (negative: the default, about two seconds); returns the
     previous bound.  A wait that runs out raises STATUS_TIMEOUT."""
     return int(_lib.sdva_debug_set_wait_limit(int(cycles)))
 

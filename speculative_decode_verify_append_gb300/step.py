@@ -6,7 +6,8 @@ a CUDA graph capture, issues exactly the three library calls per step with
 no allocation.  With ``num_top`` it also owns the buffers of ``score``, which
 reports the log probabilities of the step's tokens.  ``PromptStep`` takes a
 packed batch of prompts to where the first verify step can follow: attention
-over their own keys and values, and the same K/V into the cache.
+over their own keys and values, and the same K/V into the cache.  ``DeltaStep``
+owns the states of a recurrent layer and the buffers of its calls.
 ``fill_context`` writes one lane's prompt K/V into the cache in page-aligned
 chunks (the prefill side of the append call).
 """
@@ -35,7 +36,7 @@ class VerifyStep:
         self.accept_len = torch.zeros(num_lanes, dtype=torch.int32, device=dev)
         self.out_tokens = torch.zeros((num_lanes, window), dtype=torch.int32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.q = None  # append_rope's queries
+        self.q = torch.empty_like(self.out)  # append_rope's queries
         self.num_top = num_top
         if num_top is not None:
             self.logprobs = torch.zeros((num_lanes, window), device=dev)
@@ -55,8 +56,6 @@ class VerifyStep:
         """append of a window whose queries and keys are still to be turned to
         their positions (rope: rope_table); returns the turned queries, which
         attend takes and the next call writes again."""
-        if self.q is None:
-            self.q = torch.empty_like(self.out)
         kv_append_rope(cache, q, k_win, v_win, rope, page_table, seq_lens, self.q, None, n_lane, positions, interleaved,
                        self.status, stream)
         return self.q
@@ -100,15 +99,20 @@ class VerifyStep:
 
 
 class PromptStep:
-    """A packed batch of whole prompts of up to max_tokens tokens, cu_tokens int32 [B + 1] (device)."""
+    """A packed batch of whole prompts of up to max_tokens tokens, cu_tokens int32 [B + 1] (device).
+    With num_kv_heads, run can turn queries and keys to their positions."""
 
-    def __init__(self, max_tokens: int, num_q_heads: int, device="cuda", sm_scale: float | None = None):
+    def __init__(self, max_tokens: int, num_q_heads: int, device="cuda", sm_scale: float | None = None,
+                 num_kv_heads: int | None = None):
         self.sm_scale = sm_scale if sm_scale is not None else 1.0 / math.sqrt(128.0)
         dev = torch.device(device)
         self.out = torch.empty((max_tokens, num_q_heads, 128), dtype=torch.bfloat16, device=dev)
         self.lse = torch.empty((max_tokens, num_q_heads), device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.turned = None  # queries and keys of run with a rope
+        self.turned = None  # run's queries and keys with a rope
+        if num_kv_heads is not None:
+            self.turned = [torch.empty((max_tokens, n, 128), dtype=torch.bfloat16, device=dev)
+                           for n in (num_q_heads, num_kv_heads)]
 
     def run(self, cache: KVCache, q, k, v, cu_tokens, page_table, seq_lens, stream=None, rope=None, interleaved=False):
         """The prompts' attention (q [T][Hq][128], k, v [T][Hkv][128], bf16), and
@@ -121,8 +125,7 @@ class PromptStep:
         out, lse = self.out[:T], self.lse[:T]
         if rope is not None:
             if self.turned is None:
-                most, dev = self.out.shape[0], self.out.device
-                self.turned = [torch.empty((most, x.shape[1], 128), dtype=torch.bfloat16, device=dev) for x in (q, k)]
+                raise ValueError("run() with a rope needs num_kv_heads")
             turned = [x[:T] for x in self.turned]
             kv_append_packed_rope(cache, q, k, v, cu_tokens, rope, page_table, seq_lens, *turned, interleaved,
                                   self.status, stream)

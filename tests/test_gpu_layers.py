@@ -1,12 +1,10 @@
 """The rotated appends and the gated delta rule as a hybrid model's layers use
 them together, and at offsets past 32 bits."""
-import math
-
 import numpy as np
 import pytest
 import torch
 
-from test_gpu_delta import D, EPS, SCALE, _check_lane, _check_out, _gen, _i32, _inputs, _norm_near, _status, _tol, _walk, _workspace
+from test_gpu_delta import D, SCALE, _check_lane, _check_out, _gen, _i32, _inputs, _norm_near, _status, _tol, _walk, _workspace
 from test_gpu_rope import _same, _turn
 
 pytestmark = pytest.mark.gpu
@@ -32,13 +30,15 @@ def test_an_attention_layer_and_a_recurrent_one_through_prompts_and_verify_steps
     table = _i32(np.arange(12).reshape(3, 4))
     rope = rope_table(300, 64)
     caches = [sdva.KVCache(fmt, 12, HKV) for _ in range(2)]
-    prompts = [PromptStep(T, HQ) for _ in range(2)]
+    prompts = [PromptStep(T, HQ, num_kv_heads=HKV), PromptStep(T, HQ)]
     q, k, v = _qkv(g, (T,))
     pos = torch.cat([torch.arange(n) for n in lens]).cuda()
     out, lse = prompts[0].run(caches[0], q, k, v, cu, table, seq, rope=rope)
     out1, lse1 = prompts[1].run(caches[1], _turn(q, rope, pos, False), _turn(k, rope, pos, False), v, cu, table, seq)
     torch.cuda.synchronize()
     assert torch.equal(out, out1) and torch.equal(lse, lse1)
+    with pytest.raises(ValueError, match="num_kv_heads"):
+        prompts[1].run(caches[1], q, k, v, cu, table, seq, rope=rope)
     _same(*caches)
 
     delta = DeltaStep(B, HK, HV, window=W, max_tokens=T)
