@@ -25,17 +25,18 @@
 // barrier of the CTA per chunk.
 //
 // 16 / 32 heads: one prompt of 16,384 tokens 670 us, of which 105 are
-// chunk_kernel's (bound by its shared-memory accesses: L1 is busy for 80% of it)
-// and the rest 512 chunks at 1.06 us; eight of 2,048 445 us.  8 / 24 heads, eight
-// prompts of 1 to 2,011 tokens 118 us; 4 / 8 heads, 40 tokens 10.3.  A chunk is
+// chunk_kernel's (shared memory comes first: L1 is at 65% of its peak, DRAM at 17%)
+// and the rest 512 chunks at 1.10 us; eight of 2,048 445 us.  8 / 24 heads, eight
+// prompts of 1 to 2,011 tokens 118 us; 4 / 8 heads, 40 tokens 10.9.  A chunk is
 // 146 products of 16 x 8 x 16 a warp, 8 cycles each, in some 2,100 cycles; the
 // others are the turns of accumulators into operands in front of and behind T,
 // which depend on each other, and the barrier.  The legacy tensor path
 // (mma.sync) is taken with intent: its operands are the chain's own registers,
 // 16 value rows are its tile, and a head's chain is spread over eight quarters of
-// SMs.  A tcgen05 product has 128 rows: one SM would hold a head's whole chain,
-// its products alone take 1,400 of the cycles that two chunks take here, and each
-// of its three dependent steps adds a way through tensor memory.
+// SMs.  A tcgen05 product has 128 rows: one SM would hold a head's whole chain.
+// By arithmetic (not built) the chain's products would take some 600 cycles a
+// chunk there (8 warps' 146 of 2,048 multiply-adds at 3,900 a cycle), and each of
+// its three dependent steps would add a way through tensor memory.
 #include "delta_common.cuh"
 #include "tc_primitives.cuh"
 

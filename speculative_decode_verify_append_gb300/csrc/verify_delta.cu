@@ -23,11 +23,11 @@
 // commit_delta: fp32 multiply-adds, eight value rows of a state to a warp.
 //
 // 64 lanes, 16 / 32 heads (134 MB of states), and what a copy's rate would take:
-// a plain step 43.6 us (40.4), 16 rows recorded 41.9 (26.4), committed 63.7
+// a plain step 43.8 us (40.4), 16 rows recorded 42.0 (26.4), committed 63.8
 // (44.0), the commit of up to 16 updates 52.3 (43.3).  8 lanes of 16 rows 7.1 us,
-// one lane's commit 3.4.  A window's CTA lives some 10,000 cycles, of which the
-// loads take 4,000, S k' and S q' 3,000 (T is there by then) and the rest 3,000;
-// with two on an SM, 128 KB are under way.
+// one lane's commit 3.5.  A window's CTA lives some 11,000 cycles (clock readings
+// in the kernel): the loads take 5,000, S k' and S q' 3,000 (T is there by then)
+// and the rest 3,000; with two on an SM, 128 KB are under way.
 #include "delta_common.cuh"
 #include "tc_primitives.cuh"
 
