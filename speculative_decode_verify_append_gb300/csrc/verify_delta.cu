@@ -483,6 +483,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a, long 
   };
   if (n == 0) {
     if (warp < kWarps && lr.n > 0) state_here();
+    cp_async_wait<0>();  // v: no copy outlives the CTA
     if (warp < kWarps)
       for (int r = g; r < W; r += 8)
 #pragma unroll
