@@ -36,7 +36,7 @@ class VerifyStep:
         self.accept_len = torch.zeros(num_lanes, dtype=torch.int32, device=dev)
         self.out_tokens = torch.zeros((num_lanes, window), dtype=torch.int32, device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.q = torch.empty_like(self.out)  # append_rope's queries
+        self.q = torch.zeros_like(self.out)  # append_rope's queries
         self.num_top = num_top
         if num_top is not None:
             self.logprobs = torch.zeros((num_lanes, window), device=dev)
@@ -55,7 +55,9 @@ class VerifyStep:
                     interleaved=False, stream=None):
         """append of a window whose queries and keys are still to be turned to
         their positions (rope: rope_table); returns the turned queries, which
-        attend takes and the next call writes again."""
+        attend takes and the next call writes again.  Rows of a lane that the
+        append skips (status says so) and rows behind a lane's count are not
+        written: they hold zeros or an earlier call's."""
         kv_append_rope(cache, q, k_win, v_win, rope, page_table, seq_lens, self.q, None, n_lane, positions, interleaved,
                        self.status, stream)
         return self.q
@@ -111,7 +113,7 @@ class PromptStep:
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
         self.turned = None  # run's queries and keys with a rope
         if num_kv_heads is not None:
-            self.turned = [torch.empty((max_tokens, n, 128), dtype=torch.bfloat16, device=dev)
+            self.turned = [torch.zeros((max_tokens, n, 128), dtype=torch.bfloat16, device=dev)
                            for n in (num_q_heads, num_kv_heads)]
 
     def run(self, cache: KVCache, q, k, v, cu_tokens, page_table, seq_lens, stream=None, rope=None, interleaved=False):
@@ -120,7 +122,9 @@ class PromptStep:
         holds.  Returns out [T][Hq][128] and lse [T][Hq], which the next run
         writes again.  A lane that goes on from cached tokens attends its new
         ones alone here: whole prompts start at seq_lens 0.  With rope (a
-        rope_table) the queries and keys are turned to their positions first."""
+        rope_table) the queries and keys are turned to their positions first;
+        of a lane that the append skips (status says so) they are not, and its
+        out and lse mean nothing."""
         T = q.shape[0]
         out, lse = self.out[:T], self.lse[:T]
         if rope is not None:

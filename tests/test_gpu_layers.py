@@ -265,3 +265,27 @@ def test_prompt_shapes_of_grids(lanes):
             h = slice(4, 8)  # of key heads 2 and 3
             _check_lane(n, torch.zeros((4, D, D), device="cuda"), out[a:a + n, h], None, state[i, h],
                         *(y[a:a + n, 2:4] for y in x[:2]), *(y[a:a + n, h] for y in x[2:]))
+
+
+def test_a_prompt_lane_that_is_skipped_leaves_the_others_right():
+    """Of a batch with a bad page in one lane, the status says so and the other lanes' attention is theirs alone."""
+    import speculative_decode_verify_append_gb300 as sdva
+    from speculative_decode_verify_append_gb300.step import PromptStep, rope_table
+    g = torch.Generator(device="cuda").manual_seed(31)
+    hq, hkv, lens = 4, 2, [70, 40, 33]
+    T = sum(lens)
+    q, k, v = (torch.randn((T, h, 128), generator=g, device="cuda").bfloat16() for h in (hq, hkv, hkv))
+    cu = torch.tensor([0, 70, 110, 143], dtype=torch.int32, device="cuda")
+    zeros = torch.zeros(3, dtype=torch.int32, device="cuda")
+    rope = rope_table(128, 128)
+    res = []
+    for page in (2, 9):  # 9: no page of the cache
+        cache = sdva.KVCache(sdva.KV_INT8_G64, 4, hkv)
+        table = torch.tensor([[0, 1], [page, -1], [3, -1]], dtype=torch.int32, device="cuda")
+        ps = PromptStep(T, hq, num_kv_heads=hkv)
+        assert not any(x.any() for x in ps.turned)  # nothing of what the memory held before
+        out, lse = ps.run(cache, q, k, v, cu, table, zeros, rope=rope)
+        res.append((out.clone(), lse.clone(), int(ps.status)))
+    assert res[0][2] == 0 and res[1][2] & sdva.STATUS_BAD_PAGE
+    for rows in (slice(0, 70), slice(110, 143)):
+        assert torch.equal(res[0][0][rows], res[1][0][rows]) and torch.equal(res[0][1][rows], res[1][1][rows])
