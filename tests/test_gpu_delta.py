@@ -712,3 +712,21 @@ def test_the_binding_refuses():
     for change in (dict(k=k[:, :3]), dict(deltas=deltas.half()), dict(accept_len=acc[:1]), dict(path=acc), dict(state=state[:, :3])):
         with pytest.raises((ValueError, sdva.SdvaError)):
             sdva.commit_delta(**{**dict(state=state, k=k, log_decay=gd, deltas=deltas, slots=slots, accept_len=acc), **change})
+
+
+@pytest.mark.parametrize("W,keep", [(1, True), (2, True), (1, False), (3, False)])
+def test_short_chains_give_outputs_of_fp32(W, keep):
+    """Chains that fp32 takes owe out nothing but its own rounding: the tolerance of an operand in one fp16 part, which
+    the tensor cores' outputs have, is left out here."""
+    import speculative_decode_verify_append_gb300 as sdva
+    B, hk, hv = 3, 2, 4
+    g = _gen(90 + W)
+    q, k, v, gd, b = _inputs(g, (B, W), hk, hv)
+    state = torch.randn((B, hv, D, D), generator=g, device="cuda") * 0.3
+    before, slots = state.clone(), _i32(range(B))
+    out = torch.empty((B, W, hv, D), dtype=torch.bfloat16, device="cuda")
+    deltas = torch.empty((B, W, hv, D), device="cuda") if keep else None
+    sdva.verify_delta(state, q, k, v, gd, b, slots, SCALE, out, deltas)
+    for i in range(B):
+        want, _, _, (M, _) = _walk(before[i], q[i], k[i], v[i], gd[i], b[i])
+        _near(out[i], want, 2.0 ** -8 * want.abs() + SCALE * _tol(W, M)[None, :, None], "out")
