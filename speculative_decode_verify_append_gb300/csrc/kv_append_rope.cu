@@ -12,8 +12,9 @@
 // (kv heads, then groups of four q heads).  A kv head's CTA holds its page's K
 // and V (kv_page.cuh); a q CTA gives one warp a token's four heads, eight
 // threads each, so that the heads share the loads of the table's row.
-// 41,175 tokens of 8 lanes, 24 / 4 heads: FP8, 128 dims turned, 121 us (5.7 TB/s);
-// INT4, 64 dims, 117.  64 lanes of up to 16 rows, INT8: 7.1 us; one token: 3.1.
+// 41,175 tokens of 8 lanes, 24 / 4 heads: FP8, 128 dims turned, 122 us (5.7 TB/s);
+// INT4, 64 dims, 123 by halves and 116 by neighbours.  64 lanes of up to 16 rows,
+// INT8: 6.7 us; one token: 3.3.
 #include "kv_page.cuh"
 
 namespace sdva {

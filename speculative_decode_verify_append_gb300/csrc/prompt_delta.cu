@@ -24,7 +24,7 @@
 // of shared memory, makes the outputs, and copies the chunks that come.  One
 // barrier of the CTA per chunk.
 //
-// 16 / 32 heads: one prompt of 16,384 tokens 670 us, of which 105 are
+// 16 / 32 heads: one prompt of 16,384 tokens 668 us, of which 105 are
 // chunk_kernel's (shared memory comes first: L1 is at 65% of its peak, DRAM at 17%)
 // and the rest 512 chunks at 1.10 us; eight of 2,048 445 us.  8 / 24 heads, eight
 // prompts of 1 to 2,011 tokens 118 us; 4 / 8 heads, 40 tokens 10.9.  A chunk is
@@ -718,7 +718,7 @@ int num_sms() {
   return n;
 }
 
-// Two warps of the chain to a CTA, up to three CTAs on an SM, or four warps and one CTA.  A chunk takes the chain 1.05 us
+// Two warps of the chain to a CTA, up to three CTAs on an SM, or four warps and one CTA.  A chunk takes the chain 1.1 us
 // with one CTA of two on the SM, 2.0 with two, 2.35 with three, and 1.45 in a CTA of four: whichever ends first by how
 // many rounds its grid makes, lanes being of one length.  Of 2,048 tokens a lane, us with two and with four: 16 heads, two
 // lanes 92 and 110, three 148 and 116, four 155 and 123, six 188 and 224; 32 heads, four lanes 261 and 238, eight 445
