@@ -635,14 +635,13 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a, long 
     const float f = s.f, c_up = s.c_up;
     const float c_down = 1.0f / c_up;  // a power of two
 #pragma unroll
-    for (int t = 0; t < 2; ++t) in[t] *= f;
-#pragma unroll
     for (int m = 0; m < 8; ++m) {
       uint32_t k0[2], k1[2];
       ldmatrix_x4_trans(kbase + key_at((lane & 7) + ((lane >> 3) & 1) * 8, 2 * m + (lane >> 4)), k0[0], k1[0], k0[1], k1[1]);
       const float4 s0 = state_of(0, m), s1 = state_of(1, m);
-      float lo[4] = {s0.x * in[0] * c_down, s0.y * in[0] * c_down, s1.x * in[1] * c_down, s1.y * in[1] * c_down};
-      float hi[4] = {s0.z * in[0] * c_down, s0.w * in[0] * c_down, s1.z * in[1] * c_down, s1.w * in[1] * c_down};
+      // f first: of a row of zeros in front and behind, in is 2^126, and its product with f may be infinite
+      float lo[4] = {s0.x * f * in[0] * c_down, s0.y * f * in[0] * c_down, s1.x * f * in[1] * c_down, s1.y * f * in[1] * c_down};
+      float hi[4] = {s0.z * f * in[0] * c_down, s0.w * f * in[0] * c_down, s1.z * f * in[1] * c_down, s1.w * f * in[1] * c_down};
       mma_f16_16816(lo, ch, k0[0], k1[0]);
       mma_f16_16816(hi, ch, k0[1], k1[1]);
       mma_f16_16816(lo, cl, k0[0], k1[0]);
