@@ -668,8 +668,7 @@ int token_logprobs(const void* logits, int logits_dtype, int64_t row_stride, int
  * Precondition: the values of a lane's rows and of the state that it starts
  * from are finite (log decays: or -inf), and they, their products and, with a
  * qk_eps of 0, the squares of q and k stay in fp32's range (a row of zeros has
- * no direction then; with a negative one a key of verify_delta is zeros or
- * 2^-60 and more in size).  Other lanes' and other rows' values do not reach a lane.
+ * no direction then).  Other lanes' and other rows' values do not reach a lane.
  * Accuracy: states, updates and sums are fp32.  Products on the tensor cores
  * take the state and the updates in two fp16 parts, which leaves some 2^-22 of
  * the largest value among 16 value rows (prompt_delta) or of a value row

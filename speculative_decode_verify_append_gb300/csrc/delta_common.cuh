@@ -42,6 +42,12 @@ __device__ __forceinline__ Scale scale_of_row(float amax) {
   const uint32_t e = min(max(__float_as_uint(amax) >> 23, 1u), 253u);
   return {__uint_as_float((254u - e) << 23), __uint_as_float(e << 23)};
 }
+// As scale_of_row, to the top of fp16's range, [2^13, 2^14): what is 2^-16 of the largest
+// still has two whole parts.  All of a row of zeros, or of less than 2^-113, stays below.
+__device__ __forceinline__ Scale scale_to_top(float amax) {
+  const uint32_t e = min(max(__float_as_uint(amax) >> 23, 14u), 253u);
+  return {__uint_as_float((254u + 13u - e) << 23), __uint_as_float((e - 13u) << 23)};
+}
 // r = 2^e / sqrt(|k|^2 + eps) from sum_sq = |k'|^2.  eps 2^-2e overflows for rows
 // below 2^-64 or so, whose kn is below 2^-54 then and taken as 0.
 __device__ __forceinline__ float row_factor(float sum_sq, float eps, Scale s) {
@@ -54,6 +60,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
+// The same of 32-bit elements, two to a thread.
+__device__ __forceinline__ void transpose8(float& x0, float& x1) {
+  const uint32_t a = __float_as_uint(x0), b = __float_as_uint(x1);
+  const uint32_t lo = transpose8(__byte_perm(a, b, 0x5410)), hi = transpose8(__byte_perm(a, b, 0x7632));
+  x0 = __uint_as_float(__byte_perm(lo, hi, 0x5410));
+  x1 = __uint_as_float(__byte_perm(lo, hi, 0x7632));
+}
 // Two values in two fp16 parts.
 __device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint32_t& lo) {
   const __half2 h = __floats2half2_rn(x0, x1);
@@ -63,6 +76,12 @@ __device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint
 }
 
 __device__ __forceinline__ void split_f16(float2 x, uint32_t& hi, uint32_t& lo) { split_f16(x.x, x.y, hi, lo); }
+
+// x in two parts of 11 bits, off by 2^-23 |x| at most in all of fp32's range.
+__device__ __forceinline__ void split_tf32(float x, float& hi, float& lo) {
+  hi = to_tf32(x);
+  lo = to_tf32(x - hi);
+}
 
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;

@@ -20,11 +20,17 @@
 // their accumulators), copied to shared memory while the window's rows are
 // normalised.  Two more warps multiply the rows with each other and solve for T
 // and P, a column to a lane, under the products with S.
+// T goes to x, and P to u, in tf32 (T and x in two parts, P and u in one, 11 bits
+// each): where a token's map expands (beta |k|^2 above 2, which keys that are taken
+// as they are may have; decays above 1), T's entries and u range over more than
+// fp16 has, and a token owes nothing to the sizes of later ones.  With fp16 parts
+// about one power of two for T and one for x, which overflowed there, the same
+// calls were 1.5 to 2.5 us shorter.
 // commit_delta: fp32 multiply-adds, eight value rows of a state to a warp.
 //
 // 64 lanes, 16 / 32 heads (134 MB of states), and what a copy's rate would take:
-// a plain step 43.8 us (40.4), 16 rows recorded 42.0 (26.4), committed 63.8
-// (44.0), the commit of up to 16 updates 52.3 (43.3).  8 lanes of 16 rows 7.1 us,
+// a plain step 43.6 us (40.4), 16 rows recorded 44.7 (26.4), committed 66.3
+// (44.0), the commit of up to 16 updates 52.3 (43.3).  8 lanes of 16 rows 7.3 us,
 // one lane's commit 3.5.  A window's CTA lives some 11,000 cycles (clock readings
 // in the kernel): the loads take 5,000, S k' and S q' 3,000 (T is there by then)
 // and the rest 3,000; with two on an SM, 128 KB are under way.
@@ -65,8 +71,9 @@ struct VerifyArgs {
 
 
 __device__ __forceinline__ int key_at(int row, int piece) { return row * 256 + ((piece ^ (row & 7)) << 4); }
-// 16 x 16 fp16, 32-byte rows: their two pieces change places every four rows
-__device__ __forceinline__ int tri_at(int row, int piece) { return row * 32 + ((piece ^ ((row >> 2) & 1)) << 4); }
+// 16 x 16 fp32: a row's halves change places every two rows, so that four rows' eight bytes of four threads each are in
+// different banks
+__device__ __forceinline__ int tri_at(int row, int col) { return row * kMaxWindow + (col ^ ((row << 2) & 8)); }
 
 // The lane's rows, and what is wrong with it (then none).  The window's own
 // arrays are read without waiting for it; what lies behind the count is dropped.
@@ -84,9 +91,9 @@ __device__ __forceinline__ LaneRows lane_rows(const VerifyArgs& a, int b) {
   return r;
 }
 
-// Tokens that rows_kernel takes.  64 lanes, 16 / 32 heads, us of rows_kernel and of window_kernel: recorded, 1 token 27.9
-// and 38.9, 2 35.1 and 38.8, 3 42.9 and 39.1; committed, 1 43.6 and 61.1, 3 57.4 and 61.4, 4 63.9 and 61.6.  Of one
-// lane: recorded, 2 3.2 and 4.8, 4 4.8 and 5.2; committed, 3 4.5 and 7.1.
+// Tokens that rows_kernel takes.  64 lanes, 16 / 32 heads, us of rows_kernel and of window_kernel: recorded, 1 token 27.3
+// and 41.3, 2 35.0 and 41.4, 3 42.4 and 41.5; committed, 1 43.6 and 63.8, 3 57.6 and 64.1, 4 64.0 and 64.3.  Of one
+// lane: recorded, 2 3.5 and 5.4, 4 4.8 and 5.4; committed, 3 4.3 and 7.4.
 constexpr int kSeqRecorded = 2, kSeqCommitted = 3;
 constexpr int kSeqThreads = 128;
 
@@ -217,7 +224,7 @@ struct VerifySmem {
   // state, so that the rows hold dims 0 1 4 5 8 9 12 13, then 2 3 6 7 10 11 14 15.
   alignas(16) uint8_t key[2][kRows * kHeadDim * 2];
   alignas(16) uint8_t v[kRows * kHeadDim * 2];
-  alignas(16) uint8_t tri[3][kRows * kRows * 2];  // the columns of T in two parts and of P
+  alignas(16) float tri[3][kRows * kRows];        // T in two parts of 11 bits, P in one
   float gram[2][kRows][kRows + 1];                // k' . k', q' . k'
   alignas(16) float a[kRows][kRows + 4];          // columns of A
   float d[2][kRows][kRows + 1];                   // D, and a in column 16 (trees); a copy for T and one for P
@@ -227,15 +234,9 @@ struct VerifySmem {
   alignas(16) int par[2][kRows];
   float k_own[kRows];  // 1 / sqrt(|k|^2 + eps)
   float fa[kRows], fc[kRows], o1[kRows], o2[kRows];
-  float t_up, c_up, f;
+  float f;
   int never;  // 0: no role's wait ends another's
 };
-
-__device__ __forceinline__ float warp_max(float x) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-  return x;
-}
 
 // Sixteen floats of shared memory, the same for every thread.
 __device__ __forceinline__ void load16(const float* p, float (&x)[kRows]) {
@@ -245,21 +246,6 @@ __device__ __forceinline__ void load16(const float* p, float (&x)[kRows]) {
     x[i] = y.x, x[i + 1] = y.y, x[i + 2] = y.z, x[i + 3] = y.w;
   }
 }
-// A column of T or P as a row of shared memory; what fp16 leaves over into the next matrix.
-template <bool kParts>
-__device__ __forceinline__ void store_column(uint8_t* to, int j, const float (&x)[kRows], float scale) {
-  uint32_t hi[kRows / 2], lo[kRows / 2];
-#pragma unroll
-  for (int i = 0; i < kRows / 2; ++i) split_f16(x[2 * i] * scale, x[2 * i + 1] * scale, hi[i], lo[i]);
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    *reinterpret_cast<uint4*>(to + tri_at(j, p)) = make_uint4(hi[4 * p], hi[4 * p + 1], hi[4 * p + 2], hi[4 * p + 3]);
-    if (kParts)
-      *reinterpret_cast<uint4*>(to + kRows * kRows * 2 + tri_at(j, p)) =
-          make_uint4(lo[4 * p], lo[4 * p + 1], lo[4 * p + 2], lo[4 * p + 3]);
-  }
-}
-
 // D by columns, for each of the two further warps (m): lane j < 16 has column j;
 // lane 16 stands for the state in front of the window, the root's parent, so
 // that its column is a.  Returns whether a parent is wrong.
@@ -331,19 +317,13 @@ __device__ __forceinline__ void solve(VerifySmem& s, const VerifyArgs& a, int m,
   __syncwarp();
   const bool on = lane < kRows;
   const float rk = on ? s.r[0][j] : 0.0f;
-  float top = 0.0f;
   if (m == 1) {
-#pragma unroll
-    for (int i = 0; i < kRows; ++i) {
-      x[i] = on && d[i] != 0.0f ? d[i] * rk * s.gram[1][i][j & 15] : 0.0f;
-      top = fmaxf(top, fabsf(x[i]));
-    }
-    const Scale ps = scale_of_row(warp_max(top));
     if (on) {
-      store_column<false>(s.tri[2], j, x, ps.down);
+#pragma unroll
+      for (int i = 0; i < kRows; ++i) s.tri[2][tri_at(i, j)] = d[i] != 0.0f ? to_tf32(d[i] * rk * s.gram[1][i][j]) : 0.0f;
       const float rq = a.scale * s.r[1][j];
       s.o1[j] = j < n ? rq * s.o1[j] : 0.0f;
-      s.o2[j] = rq * ps.up;
+      s.o2[j] = rq;
     }
     return;
   }
@@ -372,24 +352,18 @@ __device__ __forceinline__ void solve(VerifySmem& s, const VerifyArgs& a, int m,
       x[i + 3] = fmaf(-y.w, x[l], x[i + 3]);
     }
   }
-#pragma unroll
-  for (int i = 0; i < kRows; ++i) top = fmaxf(top, fabsf(x[i]));
-  const Scale ts = scale_of_row(warp_max(top));
   if (on) {
-    store_column<true>(s.tri[0], j, x, ts.down);
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) split_tf32(x[i], s.tri[0][tri_at(i, j)], s.tri[1][tri_at(i, j)]);
     s.fa[j] = j < n ? s.fa[j] * rk : 0.0f;
   }
-  if (lane == 0) s.t_up = ts.up;
-  if (kCommit) {  // factors of the updates in the state behind the window, the largest brought to [1, 2)
+  if (kCommit) {  // factors of the updates in the state behind the window
     float fc = 0.0f;
 #pragma unroll
     for (int i = 0; i < kRows; ++i)
       if (i == n - 1) fc = d[i];
     if (lane == kRows) s.f = fc;
-    fc = j < n ? fc * rk : 0.0f;
-    const Scale cs = scale_of_row(fmaxf(warp_max(fabsf(fc)), 0x1p-60f));  // S times the scales stays in fp32's range
-    if (on) s.fc[j] = fc * cs.down;
-    if (lane == 0) s.c_up = cs.up;
+    if (on) s.fc[j] = j < n ? fc * rk : 0.0f;
   }
 }
 
@@ -522,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a, long 
     }
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
     x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-    const Scale sc = scale_of_row(x);
+    const Scale sc = scale_to_top(x);
     sig[t] = sc.down, isig[t] = sc.up;
   }
   float sk[2][2][4] = {}, sq[2][4] = {};
@@ -544,104 +518,103 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a, long 
   }
   cp_async_wait<0>();  // v
   __syncthreads();
-  // x; its columns' scales leave u, at most 32 x, inside fp16's range, and are no finer than the state needs
-  float xs[2][2], xi[2][2];
-  uint32_t xh[2][2], xl[2][2];
+  // T and P, of columns 8 kt + 2 c and + 1 of rows g and g + 8: the k indices c and c + 4 of a product are the tokens
+  // 2 c and 2 c + 1 in both operands
+  float th_[2][4], tl[2][4], p[2][4];
+#pragma unroll
+  for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const int at = tri_at(8 * r + g, 8 * kt + 2 * c);
+      const float2 x = *reinterpret_cast<const float2*>(&s.tri[0][at]), y = *reinterpret_cast<const float2*>(&s.tri[1][at]);
+      const float2 z = *reinterpret_cast<const float2*>(&s.tri[2][at]);
+      th_[kt][r] = x.x, th_[kt][2 + r] = x.y;
+      tl[kt][r] = y.x, tl[kt][2 + r] = y.y;
+      p[kt][r] = z.x, p[kt][2 + r] = z.y;
+    }
+  // x and u as they are: T's entries and the tokens' values have sizes of their own, which fp16 would need a scale for
+  uint32_t ch[4], cl[4];  // the updates with their factors, value rows by tokens
+  float in[2], back[2];   // their scale
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     float x[2][2];
     uint32_t v[2];  // rows g, g + 8 of the window, value rows 8 t + 2 c, + 1
+    float up[2];
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
-      v[r] = 8 * r + g < n ? *reinterpret_cast<const uint32_t*>(s.v + key_at(8 * r + g, 2 * warp + t) + 4 * c) : 0u;
+    for (int i = 0; i < 2; ++i) up[i] = __shfl_sync(0xffffffffu, isig[t], 4 * (2 * c + i));
+    float u[4] = {}, u1[4] = {}, u2[4] = {}, o[4] = {};
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const float up = __shfl_sync(0xffffffffu, isig[t], 4 * (2 * c + i));
-      float top = up * 0x1p-40f;
+    for (int r = 0; r < 2; ++r) {
+      const int row = 8 * r + g;
+      v[r] = row < n ? *reinterpret_cast<const uint32_t*>(s.v + key_at(row, 2 * warp + t) + 4 * c) : 0u;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const float y = (sk[0][t][2 * r + i] + sk[1][t][2 * r + i]) * up[i];
+        x[r][i] = s.beta[row] * ((i ? bf16_hi(v[r]) : bf16_lo(v[r])) - s.fa[row] * y);
+      }
+      transpose8(x[r][0], x[r][1]);
+      float hi[2], lo[2];
+      split_tf32(x[r][0], hi[0], lo[0]);
+      split_tf32(x[r][1], hi[1], lo[1]);
+      mma_tf32_1688(u, th_[r], hi[0], hi[1]);
+      mma_tf32_1688(u1, tl[r], hi[0], hi[1]);
+      mma_tf32_1688(u2, th_[r], lo[0], lo[1]);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) u[i] += u1[i] + u2[i];
+    if (!kCommit) {
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float y = (sk[0][t][2 * r + i] + sk[1][t][2 * r + i]) * up;
-        x[r][i] = s.beta[8 * r + g] * ((i ? bf16_hi(v[r]) : bf16_lo(v[r])) - s.fa[8 * r + g] * y);
-        top = fmaxf(top, fabsf(x[r][i]));
+        const int i = 8 * r + g;
+        const float rk = s.k_own[i];
+        if (i < W)
+          *reinterpret_cast<float2*>(a.deltas + at0 + i * row_out + 8 * t) =
+              i < n ? make_float2(rk * u[2 * r], rk * u[2 * r + 1]) : make_float2(0.0f, 0.0f);
       }
-#pragma unroll
-      for (int o = 4; o <= 16; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const Scale sc = scale_of_row(top);
-      xs[t][i] = sc.down, xi[t][i] = sc.up;
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      split_f16(x[r][0] * xs[t][0], x[r][1] * xs[t][1], xh[t][r], xl[t][r]);
-      xh[t][r] = transpose8(xh[t][r]);
-      xl[t][r] = transpose8(xl[t][r]);
+      transpose8(u[2 * r], u[2 * r + 1]);  // value row 8 t + g, tokens 8 r + 2 c, + 1
+      mma_tf32_1688(o, p[r], to_tf32(u[2 * r]), to_tf32(u[2 * r + 1]));
     }
-  }
-  uint32_t fh[4], fl[4], fp[4];
-  {
-    const uint32_t tri = smem_u32(s.tri[0]) + tri_at((lane & 7) + ((lane >> 4) << 3), (lane >> 3) & 1);
-    ldmatrix_x4_trans(tri, fh[0], fh[1], fh[2], fh[3]);
-    ldmatrix_x4_trans(tri + kRows * kRows * 2, fl[0], fl[1], fl[2], fl[3]);
-    ldmatrix_x4_trans(tri + 2 * kRows * kRows * 2, fp[0], fp[1], fp[2], fp[3]);
-  }
-  uint32_t ch[4], cl[4];  // the updates with their factors, value rows by tokens
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    float u[4] = {}, o[4] = {};
-    mma_f16_16816(u, fl, xh[t][0], xh[t][1]);
-    mma_f16_16816(u, fh, xl[t][0], xl[t][1]);
-    mma_f16_16816(u, fh, xh[t][0], xh[t][1]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] *= s.t_up;
-    mma_f16_16816(o, fp, transpose8(pack_f16x2(u[0], u[1])), transpose8(pack_f16x2(u[2], u[3])));
-    const float up0 = __shfl_sync(0xffffffffu, isig[t], 8 * c), up1 = __shfl_sync(0xffffffffu, isig[t], 8 * c + 4);
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       const int i = 8 * r + g;
       if (i < W) {
         const float o1 = s.o1[i], o2 = s.o2[i];
-        const size_t at = at0 + i * row_out + 8 * t;
-        *reinterpret_cast<uint32_t*>(a.out + at) =
-            i < n ? pack_bf16x2(fmaf(o1, sq[t][2 * r] * up0, o2 * (o[2 * r] * xi[t][0])),
-                                fmaf(o1, sq[t][2 * r + 1] * up1, o2 * (o[2 * r + 1] * xi[t][1])))
+        *reinterpret_cast<uint32_t*>(a.out + at0 + i * row_out + 8 * t) =
+            i < n ? pack_bf16x2(fmaf(o1, sq[t][2 * r] * up[0], o2 * o[2 * r]),
+                                fmaf(o1, sq[t][2 * r + 1] * up[1], o2 * o[2 * r + 1]))
                   : 0u;
-        if (!kCommit) {
-          const float rk = s.k_own[i];
-          *reinterpret_cast<float2*>(a.deltas + at) =
-              i < n ? make_float2(rk * (u[2 * r] * xi[t][0]), rk * (u[2 * r + 1] * xi[t][1]))
-                    : make_float2(0.0f, 0.0f);
-        }
       }
     }
     if (kCommit) {
+      // fp16's range from the largest of a value row; S in that scale stays in fp32's
+      float top = 0.0f;
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const float fc = s.fc[8 * r + g];
-        split_f16(u[2 * r] * fc, u[2 * r + 1] * fc, ch[2 * r + t], cl[2 * r + t]);
-        ch[2 * r + t] = transpose8(ch[2 * r + t]);
-        cl[2 * r + t] = transpose8(cl[2 * r + t]);
+      for (int i = 0; i < 4; ++i) {
+        u[i] *= s.fc[8 * (i >> 1) + 2 * c + (i & 1)];
+        top = fmaxf(top, fabsf(u[i]));
       }
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      const Scale sc = scale_to_top(fmaxf(top, s.f * isig[t] * 0x1p-40f));
+      in[t] = sc.down, back[t] = sc.up;
+#pragma unroll
+      for (int r = 0; r < 2; ++r) split_f16(u[2 * r] * in[t], u[2 * r + 1] * in[t], ch[2 * r + t], cl[2 * r + t]);
     }
   }
   if (kCommit) {
     // S as accumulators: value rows g (t = 0) and g + 8 (t = 1), columns as the rows of k' have their dims
-    float in[2], back[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const float s0 = __shfl_sync(0xffffffffu, xs[t][0], g >> 1), s1 = __shfl_sync(0xffffffffu, xs[t][1], g >> 1);
-      const float i0 = __shfl_sync(0xffffffffu, xi[t][0], g >> 1), i1 = __shfl_sync(0xffffffffu, xi[t][1], g >> 1);
-      in[t] = g & 1 ? s1 : s0;
-      back[t] = g & 1 ? i1 : i0;
-    }
-    const float f = s.f, c_up = s.c_up;
-    const float c_down = 1.0f / c_up;  // a power of two
+    const float f = s.f;
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
       uint32_t k0[2], k1[2];
       ldmatrix_x4_trans(kbase + key_at((lane & 7) + ((lane >> 3) & 1) * 8, 2 * m + (lane >> 4)), k0[0], k1[0], k0[1], k1[1]);
       const float4 s0 = state_of(0, m), s1 = state_of(1, m);
-      // f first: of a row of zeros in front and behind, in is 2^126, and its product with f may be infinite
-      float lo[4] = {s0.x * f * in[0] * c_down, s0.y * f * in[0] * c_down, s1.x * f * in[1] * c_down, s1.y * f * in[1] * c_down};
-      float hi[4] = {s0.z * f * in[0] * c_down, s0.w * f * in[0] * c_down, s1.z * f * in[1] * c_down, s1.w * f * in[1] * c_down};
+      // f first: of a row of zeros in front and behind, in is at its end, and its product with f may be infinite
+      float lo[4] = {s0.x * f * in[0], s0.y * f * in[0], s1.x * f * in[1], s1.y * f * in[1]};
+      float hi[4] = {s0.z * f * in[0], s0.w * f * in[0], s1.z * f * in[1], s1.w * f * in[1]};
       mma_f16_16816(lo, ch, k0[0], k1[0]);
       mma_f16_16816(hi, ch, k0[1], k1[1]);
       mma_f16_16816(lo, cl, k0[0], k1[0]);
@@ -649,8 +622,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a, long 
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         *reinterpret_cast<float4*>(st + (size_t)(8 * t + g) * kHeadDim + 16 * m + 4 * c) =
-            make_float4(lo[2 * t] * c_up * back[t], lo[2 * t + 1] * c_up * back[t], hi[2 * t] * c_up * back[t],
-                        hi[2 * t + 1] * c_up * back[t]);
+            make_float4(lo[2 * t] * back[t], lo[2 * t + 1] * back[t], hi[2 * t] * back[t], hi[2 * t + 1] * back[t]);
     }
   }
 }
