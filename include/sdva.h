@@ -666,13 +666,15 @@ int token_logprobs(const void* logits, int logits_dtype, int64_t row_stride, int
  *   (else SDVA_ERR_UNSUPPORTED); scale positive and finite.
  *   state, q, k, v, out and deltas are 16-byte aligned (else SDVA_ERR_INVALID).
  * Precondition: the values of a lane's rows and of the state that it starts
- * from are finite (log decays: or -inf), and they, their products and, with a
- * qk_eps of 0, the squares of q and k stay in fp32's range (a row of zeros has
- * no direction then).  Other lanes' and other rows' values do not reach a lane.
+ * from are finite (log decays: or -inf), and they, the states and updates that
+ * follow, their products and, with a qk_eps of 0, the squares of q and k stay in
+ * fp32's range, 2^16 below its upper end (a row of zeros has no direction then).
+ * That a token's map expands (beta |kn|^2 above 2, log decays above 0) is allowed.
+ * Other lanes' and other rows' values do not reach a lane.
  * Accuracy: states, updates and sums are fp32.  Products on the tensor cores
- * take the state and the updates in two fp16 parts, which leaves some 2^-22 of
- * the largest value among 16 value rows (prompt_delta) or of a value row
- * (verify_delta), and what goes to out alone in one (2^-12).  verify_delta of up
+ * take the state and the updates in two parts, which leaves some 2^-22 of the
+ * largest value of a value row, and what goes to out alone in one (2^-11).  No
+ * token's outputs depend on later tokens or on other value rows.  verify_delta of up
  * to two rows that are recorded, or three that are committed, and commit_delta
  * compute in fp32 throughout.
  */

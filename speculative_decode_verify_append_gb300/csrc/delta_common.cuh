@@ -9,9 +9,12 @@
 //     o_t = scale r_q S_t q'_t
 // k' and q' are exact in fp16: the 8 bits of a bf16 number, and elements below
 // 2^-14 of the row's largest to 2^-25 of it.  The other operand of a product on
-// the tensor cores goes in two fp16 parts, x = hi + lo + at most 2^-25 or 2^-23
-// |x|, so that the state keeps what fp32 gives it; what goes to the output
-// alone is taken in one part (2^-12 of a value, bf16's rounding is 2^-9).
+// the tensor cores goes in two parts of 11 bits, x = hi + lo + at most 2^-22 |x|,
+// so that the state keeps what fp32 gives it; what goes to the output alone is
+// taken in one part (2^-11 of a value, bf16's rounding is 2^-8).  What a row of the
+// state is multiplied with or grows by goes in fp16 parts, about a power of two that
+// brings the row's largest to the top of fp16's range (off by 2^-39 of it then, if that
+// is more); what has no such bound in tf32 parts, with fp32's exponents.
 #pragma once
 
 #include "sdva_common.cuh"
@@ -77,11 +80,16 @@ __device__ __forceinline__ void split_f16(float x0, float x1, uint32_t& hi, uint
 
 __device__ __forceinline__ void split_f16(float2 x, uint32_t& hi, uint32_t& lo) { split_f16(x.x, x.y, hi, lo); }
 
-// x in two parts of 11 bits, off by 2^-23 |x| at most in all of fp32's range.
+__device__ __forceinline__ float2 f16x2_to_f32(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
+
+// x in two parts of 11 bits, off by 2^-22 |x| at most in all of fp32's range (of lo what is behind them does not count).
 __device__ __forceinline__ void split_tf32(float x, float& hi, float& lo) {
   hi = to_tf32(x);
-  lo = to_tf32(x - hi);
+  lo = x - hi;
 }
+// x rounded to 22 bits, of which a product in tf32 takes the upper 11, and the others.
+__device__ __forceinline__ float round_22(float x) { return __uint_as_float((__float_as_uint(x) + 2u) & ~3u); }
+__device__ __forceinline__ float below_tf32(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xFFFFE000u); }
 
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;

@@ -12,30 +12,39 @@
 // of 0 (a log decay of -inf) is as good as any.
 //
 // Two kernels.  chunk_kernel, a CTA per chunk and key head, writes what does
-// not depend on the state: k' and q' in fp16, T in two parts, P, and each
-// token's factors, laid out as the other kernel's shared memory holds them.
+// not depend on the state: k' and q' in fp16, T, P, and each token's factors,
+// laid out as the other kernel's shared memory holds them.
 // state_kernel goes through a lane's chunks with a head's state in registers.
 // A warp has 16 value rows of it, as accumulators of values by key dims, which
-// are the B operand of S k' as they stand; x and u (tokens by values) become
-// operands by transposing 8 x 8 tiles between registers.  No warp needs another
-// one's values.  This chain, state to state, is what a long prompt's time is made
-// of (a prompt alone has eight such warps per head), so that nothing else is on
-// it: each of its warps has another one, a chunk behind, that takes S and u out
-// of shared memory, makes the outputs, and copies the chunks that come.  One
-// barrier of the CTA per chunk.
+// are the A operand of S k' as they stand; x and u come out values by tokens and
+// are A of the product behind them in turn.  No warp needs another one's values.
+// This chain, state to state, is what a long prompt's time is made of (a prompt
+// alone has eight such warps per head), so that nothing else is on it: each of its
+// warps has another one, a chunk behind, that takes S and u out of shared memory,
+// makes the outputs, and copies the chunks that come.  One barrier of the CTA per
+// chunk.
 //
-// 16 / 32 heads: one prompt of 16,384 tokens 668 us, of which 105 are
-// chunk_kernel's (shared memory comes first: L1 is at 65% of its peak, DRAM at 17%)
-// and the rest 512 chunks at 1.10 us; eight of 2,048 445 us.  8 / 24 heads, eight
-// prompts of 1 to 2,011 tokens 118 us; 4 / 8 heads, 40 tokens 10.9.  A chunk is
-// 146 products of 16 x 8 x 16 a warp, 8 cycles each, in some 2,100 cycles; the
-// others are the turns of accumulators into operands in front of and behind T,
-// which depend on each other, and the barrier.  The legacy tensor path
+// Ranges.  The state and the updates that are added to it go in two fp16 parts
+// about a power of two of each value row, chosen behind u from the largest of both;
+// T x and P u are tf32 products (T and x in two parts of 11 bits, u in one), P is
+// in fp16 about a power of two of each of its rows.  So a token's output depends
+// on the sizes of no later token and of no other value row, and T's entries and u
+// may grow as far as fp32 goes where a token's map expands (beta |k|^2 above 2, decays
+// above 1).  With one power of two for a chunk's T, x, u and 16 rows of S, which
+// failed there, the calls below took 668, 445, 119 and 11.5 us.
+//
+// 16 / 32 heads: one prompt of 16,384 tokens 722 us, of which 104 are
+// chunk_kernel's (shared memory comes first: L1 was at 65% of its peak, DRAM at 17%)
+// and the rest 512 chunks at 1.21 us; eight of 2,048 486 us.  8 / 24 heads, eight
+// prompts of 1 to 2,011 tokens 126 us; 4 / 8 heads, 40 tokens 10.5.  A chunk is
+// 158 products of 16 x 8 x 16 (or 8, tf32) a warp, 8 cycles each, in some 2,300
+// cycles; the others are the ways from one product's accumulators to the next one's
+// operands, which depend on each other, and the barrier.  The legacy tensor path
 // (mma.sync) is taken with intent: its operands are the chain's own registers,
 // 16 value rows are its tile, and a head's chain is spread over eight quarters of
 // SMs.  A tcgen05 product has 128 rows: one SM would hold a head's whole chain.
 // By arithmetic (not built) the chain's products would take some 600 cycles a
-// chunk there (8 warps' 146 of 2,048 multiply-adds at 3,900 a cycle), and each of
+// chunk there (8 warps' 158 of 2,048 multiply-adds at 3,900 a cycle), and each of
 // its three dependent steps would add a way through tensor memory.
 #include "delta_common.cuh"
 #include "tc_primitives.cuh"
@@ -47,22 +56,29 @@ using namespace delta;
 
 constexpr int kChunk = 32;
 // A chunk's records in the workspace and in shared memory (bytes).  16-byte
-// pieces of a row are stored at piece ^ (row & 7) (k', q': 256-byte rows) and
-// piece ^ (row / 2 & 3) (T, P by columns: 64 bytes each), so that eight rows of a matrix load
-// fall into different banks.
+// pieces of a row of k' and q' (256 bytes) are stored at piece ^ (row & 7), so that
+// eight rows of a matrix load fall into different banks.
 constexpr int kKeyBytes = kChunk * kHeadDim * 2;
-constexpr int kTriBytes = kChunk * kChunk * 2;
 constexpr int kKeyRecord = 2 * kKeyBytes;  // k', q' of a key head
-constexpr int kFactors = 5;                // per token: a r, b, (f / a) r, scale r_q a, scale r_q / (P's scale)
-constexpr int kScalars = 8;
+constexpr int kTBytes = kChunk * kChunk * 3;            // three 16 x 16 tiles, fp32
+constexpr int kPBytes = kChunk * kChunk * 3 / 2;        // the same, fp16
+constexpr int kFactors = 5;  // per token: a r, b, (f / a) r, scale r_q a, scale r_q / (P's scale of the row)
+constexpr int kScalars = 4;  // f
 constexpr int kFactorBytes = (kFactors * kChunk + kScalars) * 4;
-constexpr int kHeadRecord = 3 * kTriBytes + kFactorBytes;  // T hi, T lo, P, factors of a value head
-static_assert(kHeadRecord % 16 == 0, "records are copied 16 bytes at a time");
-// A chunk's scalars: f, and bounds of what the chunk can grow to
-enum { kF = 0, kSumA = 1, kMaxB = 2, kSumT = 3, kMaxC = 4, kSumC = 5, kTUp = 6 };
+constexpr int kHeadRecord = kTBytes + kPBytes + kFactorBytes;  // of a value head
+static_assert(kHeadRecord % 16 == 0 && kTBytes % 16 == 0, "records are copied 16 bytes at a time");
 
 __device__ __forceinline__ int key_at(int row, int piece) { return row * 256 + ((piece ^ (row & 7)) << 4); }
-__device__ __forceinline__ int tri_at(int row, int piece) { return row * 64 + ((piece ^ ((row >> 1) & 3)) << 4); }
+// T's element: 16 columns in rows 0 .. 15, 32 in the others; groups of eight change places so that four rows' eight bytes
+// of four threads each are in different banks.
+__device__ __forceinline__ int t_at(int row, int col) {
+  return row < 16 ? row * 16 + (col ^ ((row << 2) & 8)) : 256 + (row - 16) * 32 + (col ^ ((row & 3) << 3));
+}
+// P's 16-byte pieces, eight rows of a column: 32 bytes a column and 16 rows, columns 16 and on behind those of rows 16
+// and on.  Columns four apart change their pieces' places.
+__device__ __forceinline__ int p_at(int col, int piece) {
+  return (col + (piece & 2 ? 16 : 0)) * 32 + (((piece & 1) ^ ((col >> 2) & 1)) << 4);
+}
 
 struct PromptArgs {
   float* state;
@@ -90,19 +106,6 @@ __host__ __device__ __forceinline__ int chunk_base(int at, int lane) { return at
 // The largest of a warp's x >= 0.
 __device__ __forceinline__ float positive_max(float x) {
   return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x)));
-}
-
-// A column of T or P; what fp16 leaves over into the next matrix.
-template <bool kParts>
-__device__ __forceinline__ void store_column(uint8_t* to, int j, const float (&x)[kChunk], float scale) {
-#pragma unroll
-  for (int p = 0; p < kChunk / 8; ++p) {
-    uint32_t hi[4], lo[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) split_f16(x[8 * p + 2 * i] * scale, x[8 * p + 2 * i + 1] * scale, hi[i], lo[i]);
-    *reinterpret_cast<uint4*>(to + tri_at(j, p)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-    if (kParts) *reinterpret_cast<uint4*>(to + kTriBytes + tri_at(j, p)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-  }
 }
 
 // A warp's bytes from shared memory to a record, 512 at a time: a column of its own is 16 bytes of 32 lines a store,
@@ -241,13 +244,13 @@ __global__ void __launch_bounds__(kChunkThreads, 6) chunk_kernel(PromptArgs a) {
   for (int task = warp; task < 2 * group; task += kChunkThreads / 32) {
     const int h = kh * group + (task >> 1);
     uint8_t* const rec = a.heads + ((size_t)slot * a.hv + h) * kHeadRecord;
-    float* const fac = reinterpret_cast<float*>(rec + 3 * kTriBytes);
+    float* const fac = reinterpret_cast<float*>(rec + kTBytes + kPBytes);
     if (task != warp) {
       log_decay = on ? a.log_decay[decay_at(task)] : 0.0f;
       beta_ = on ? a.beta[decay_at(task)] : 0.0f;
     }
     const float eg = on ? expf(log_decay) : 1.0f, beta = beta_;
-    float x[kChunk], d = 0.0f, top = 0.0f;
+    float x[kChunk], d = 0.0f;
     __syncwarp();  // the task before is done with the warp's places
     s.eg[warp][lane] = eg;
     s.br[warp][lane] = beta * rk;
@@ -271,30 +274,31 @@ __global__ void __launch_bounds__(kChunkThreads, 6) chunk_kernel(PromptArgs a) {
         for (int y = 0; y < 4; ++y) {
           d = i + y == lane ? 1.0f : d * egs[y];
           x[i + y] = i + y >= lane ? d * rk * s.gram[1][i + y][lane] : 0.0f;
-          top = fmaxf(top, fabsf(x[i + y]));
         }
       }
-      const Scale ps = scale_of_row(positive_max(top));
+      // a row's scale: what a token has of the ones before it does not depend on later rows
+      float up = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i) {
+        const Scale ps = scale_to_top(positive_max(fabsf(x[i])));
+        x[i] *= ps.down;
+        up = i == lane ? ps.up : up;
+      }
       uint8_t* const mine = reinterpret_cast<uint8_t*>(s.a[warp]);
-      store_column<false>(mine, lane, x, ps.down);
-      copy_out<kTriBytes>(rec + 2 * kTriBytes, mine, lane);
+#pragma unroll
+      for (int p = 0; p < kChunk / 8; ++p)
+        if (p >= 2 || lane < 16)
+          *reinterpret_cast<uint4*>(mine + p_at(lane, p)) =
+              make_uint4(pack_f16x2(x[8 * p], x[8 * p + 1]), pack_f16x2(x[8 * p + 2], x[8 * p + 3]),
+                         pack_f16x2(x[8 * p + 4], x[8 * p + 5]), pack_f16x2(x[8 * p + 6], x[8 * p + 7]));
+      copy_out<kPBytes>(rec + kTBytes, mine, lane);
       const float fa = fall * rk, fc = rest * rk;
       fac[lane] = fa;
       fac[kChunk + lane] = beta;
       fac[2 * kChunk + lane] = fc;
       fac[3 * kChunk + lane] = a.scale * rq * fall;
-      fac[4 * kChunk + lane] = a.scale * rq * ps.up;
-      // |S k'| is at most sqrt(128) |k'| times the largest of S, an element of k' below 4
-      const float sum_a = positive_max(fabsf(fa) * 11.4f * sqrtf(s.sum_sq[0][lane])), max_b = positive_max(fabsf(beta));
-      const float max_c = positive_max(fabsf(fc)), sum_c = 4.0f * kChunk * max_c;
-      if (lane == 0) {
-        float* const g = fac + kFactors * kChunk;
-        g[kF] = all;
-        g[kSumA] = sum_a;
-        g[kMaxB] = max_b;
-        g[kMaxC] = max_c;
-        g[kSumC] = sum_c;
-      }
+      fac[4 * kChunk + lane] = a.scale * rq * up;
+      if (lane == 0) fac[kFactors * kChunk] = all;
       continue;
     }
     // A by columns, then those of the inverse of 1 + A: as soon as a row is known it leaves the rows below
@@ -325,47 +329,32 @@ __global__ void __launch_bounds__(kChunkThreads, 6) chunk_kernel(PromptArgs a) {
         x[i + 3] = fmaf(-y.w, x[l], x[i + 3]);
       }
     }
-#pragma unroll
-    for (int i = 0; i < kChunk; ++i) top = fmaxf(top, fabsf(x[i]));
-    top = positive_max(top);
-    const Scale ts = scale_of_row(top);
-    uint8_t* const mine = reinterpret_cast<uint8_t*>(A);
+    float* const mine = &A[0][0];
     __syncwarp();
-    store_column<true>(mine, lane, x, ts.down);
-    copy_out<2 * kTriBytes>(rec, mine, lane);
-    if (lane == 0) {
-      float* const g = fac + kFactors * kChunk;
-      g[kSumT] = top * kChunk;
-      g[kTUp] = ts.up;
-    }
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i)
+      if (i >= 16 || lane < 16) mine[t_at(i, lane)] = round_22(x[i]);
+    copy_out<kTBytes>(rec, reinterpret_cast<const uint8_t*>(mine), lane);
   }
 }
 
 // Of a chunk the chain takes k', T, the factors and its values, the outputs q',
 // P and the factors; each in two places, the one in use and the one that comes.
-constexpr int kChainBytes = kKeyBytes + 2 * kTriBytes + kFactorBytes;
-constexpr int kOutBytes = kKeyBytes + kTriBytes + kFactorBytes;
-// What a warp of the chain hands over: S (32 words a thread), u (8), the scales of both
-constexpr int kHandBytes = 11 * 32 * 16;
+constexpr int kChainBytes = kKeyBytes + kTBytes + kFactorBytes;
+constexpr int kOutBytes = kKeyBytes + kPBytes + kFactorBytes;
+// What a warp of the chain hands over: S (32 words a thread), u (16), the scales of S's rows
+constexpr int kHandBytes = 12 * 32 * 16 + 64;
 template <int kWarps>
 constexpr int kStateSmem = 2 * (kChainBytes + kWarps * kChunk * 32 + kOutBytes + kWarps * kHandBytes);
 
-// A column of T or P in A's place: rows are stored by columns, so the matrices come transposed.
-__device__ __forceinline__ uint32_t tri_a(uint32_t tri, int m, int jt, int lane) {
-  return tri + tri_at(16 * jt + (lane & 7) + ((lane >> 4) << 3), 2 * m + ((lane >> 3) & 1));
+// P's rows 16 m .., columns 16 jt .. as A: stored by columns, so that the matrices come transposed.
+__device__ __forceinline__ uint32_t p_a(uint32_t tri, int m, int jt, int lane) {
+  return tri + p_at(16 * jt + (lane & 7) + ((lane >> 4) << 3), 2 * m + ((lane >> 3) & 1));
 }
 // The values of a chunk: 2 kWarps 16-byte pieces to a row, eight rows of a piece in different banks.
 template <int kWarps>
 __device__ __forceinline__ int value_at(int row, int piece) {
   return (row * 2 * kWarps + (piece ^ (kWarps == 4 ? row & 7 : (row >> 1) & 3))) << 4;
-}
-
-// One of a chunk's scalars.
-template <int kWhich>
-__device__ __forceinline__ float at(float4 lo, float4 hi) {
-  static_assert(kWhich < kScalars, "two vectors");
-  return kWhich == 0 ? lo.x : kWhich == 1 ? lo.y : kWhich == 2 ? lo.z : kWhich == 3 ? lo.w
-         : kWhich == 4 ? hi.x : kWhich == 5 ? hi.y : kWhich == 6 ? hi.z : hi.w;
 }
 
 // kWarps warps of the chain, 16 value rows each, and as many for the outputs; with two of them three CTAs fit an SM.
@@ -432,7 +421,7 @@ __global__ void __launch_bounds__(kWarps * 64, kWarps == 2 ? 3 : 1) state_kernel
     }
     const uint16_t* const vcol = a.v + (size_t)row0 * (size_t)a.v_stride + (size_t)h * kHeadDim + blockIdx.x * kWarps * 16;
     // What the next interval needs: chunk i + 1 for the chain, chunk i for the outputs.  Records by bulk copies of one
-    // thread; the values' 16-byte pieces by all (those behind the lane's rows are dropped where they are read).
+    // thread; the values' 16-byte pieces by all (those behind the lane's rows are zeros).
     const auto fetch = [&](int i, uint32_t bar) {
       if (ot == 0 && !dead) {
         const int bytes = (i + 1 < chunks ? kChainBytes : 0) + (i >= 0 && i < chunks ? kOutBytes : 0);
@@ -442,14 +431,14 @@ __global__ void __launch_bounds__(kWarps * 64, kWarps == 2 ? 3 : 1) state_kernel
           const uint8_t* const heads = a.heads + ((size_t)(base + i + 1) * a.hv + h) * kHeadRecord;
           const uint32_t to = smem_u32(chain_smem) + ((i + 1) & 1) * (kChainBytes + kValueBytes);
           tc::bulk_load(to, keys, kKeyBytes, bar);
-          tc::bulk_load(to + kKeyBytes, heads, 2 * kTriBytes, bar);
-          tc::bulk_load(to + kKeyBytes + 2 * kTriBytes, heads + 3 * kTriBytes, kFactorBytes, bar);
+          tc::bulk_load(to + kKeyBytes, heads, kTBytes, bar);
+          tc::bulk_load(to + kKeyBytes + kTBytes, heads + kTBytes + kPBytes, kFactorBytes, bar);
         }
         if (i >= 0 && i < chunks) {
           const uint32_t to = smem_u32(out_smem) + (i & 1) * kOutBytes;
           tc::bulk_load(to, a.keys + ((size_t)(base + i) * a.hk + kh) * kKeyRecord + kKeyBytes, kKeyBytes, bar);
-          tc::bulk_load(to + kKeyBytes, a.heads + ((size_t)(base + i) * a.hv + h) * kHeadRecord + 2 * kTriBytes,
-                        kTriBytes + kFactorBytes, bar);
+          tc::bulk_load(to + kKeyBytes, a.heads + ((size_t)(base + i) * a.hv + h) * kHeadRecord + kTBytes,
+                        kPBytes + kFactorBytes, bar);
         }
       }
       if (i + 1 < chunks) {
@@ -458,7 +447,7 @@ __global__ void __launch_bounds__(kWarps * 64, kWarps == 2 ? 3 : 1) state_kernel
         for (int x = ot; x < kChunk * 2 * kWarps; x += kWarps * 32) {
           const int r = x / (2 * kWarps), p = x % (2 * kWarps);
           const int t = (i + 1) * kChunk + r;
-          if (t < n) cp_async_16(to + value_at<kWarps>(r, p), vcol + (size_t)t * (size_t)a.v_stride + 8 * p);
+          cp_async_16_or_zeros(to + value_at<kWarps>(r, p), vcol + (size_t)min(t, n - 1) * (size_t)a.v_stride + 8 * p, t < n);
         }
       }
     };
@@ -479,7 +468,7 @@ __global__ void __launch_bounds__(kWarps * 64, kWarps == 2 ? 3 : 1) state_kernel
       const int ch = i - 1;
       const uint8_t* const stage = out_smem + (ch & 1) * kOutBytes;
       const uint32_t key = smem_u32(stage), tri = key + kKeyBytes;
-      const float* const fac = reinterpret_cast<const float*>(stage + kKeyBytes + kTriBytes);
+      const float* const fac = reinterpret_cast<const float*>(stage + kKeyBytes + kPBytes);
       const uint8_t* const from = hand + (ch & 1) * kHandBytes;
       float qs[2][2][4] = {}, p[2][2][4] = {};
 #pragma unroll
@@ -493,36 +482,50 @@ __global__ void __launch_bounds__(kWarps * 64, kWarps == 2 ? 3 : 1) state_kernel
           mma_f16_16816(qs[r][1], f, S.z, S.w);
         }
       }
-      const uint4 u[2] = {*reinterpret_cast<const uint4*>(from + 8 * 512), *reinterpret_cast<const uint4*>(from + 9 * 512)};
-      const float2 up = *reinterpret_cast<const float2*>(from + 10 * 512);
+      // P u in one tf32 part: the k indices c and c + 4 are the tokens 2 c and 2 c + 1 in both operands
 #pragma unroll
-      for (int m = 0; m < 2; ++m)
+      for (int jt = 0; jt < 2; ++jt) {
+        float u[2][4];  // tokens 16 jt + 2 c, + 1, + 8, + 9 of value row 8 t + g
 #pragma unroll
-        for (int jt = 0; jt <= m; ++jt) {
-          uint32_t f[4];
-          ldmatrix_x4_trans(tri_a(tri, m, jt, lane), f[0], f[1], f[2], f[3]);
-          mma_f16_16816(p[m][0], f, u[jt].x, u[jt].y);
-          mma_f16_16816(p[m][1], f, u[jt].z, u[jt].w);
+        for (int r = 0; r < 2; ++r) {
+          const float4 y = *reinterpret_cast<const float4*>(from + (8 + 2 * jt + r) * 512);
+          u[0][2 * r] = to_tf32(y.x), u[0][2 * r + 1] = to_tf32(y.y), u[1][2 * r] = to_tf32(y.z), u[1][2 * r + 1] = to_tf32(y.w);
         }
+#pragma unroll
+        for (int m = jt; m < 2; ++m) {
+          uint32_t f[4];
+          ldmatrix_x4_trans(p_a(tri, m, jt, lane), f[0], f[1], f[2], f[3]);
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            const float2 y = f16x2_to_f32(f[2 * r]), z = f16x2_to_f32(f[2 * r + 1]);
+            const float pa[4] = {y.x, z.x, y.y, z.y};
+            mma_tf32_1688(p[m][0], pa, u[0][2 * r], u[0][2 * r + 1]);
+            mma_tf32_1688(p[m][1], pa, u[1][2 * r], u[1][2 * r + 1]);
+          }
+        }
+      }
+      float2 up[2];  // of the value rows 8 x + 2 c, + 1
+#pragma unroll
+      for (int x = 0; x < 2; ++x) up[x] = *reinterpret_cast<const float2*>(from - lane * 16 + 12 * 512 + (8 * x + 2 * c) * 4);
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
           const int t = 16 * m + 8 * r + g;
-          const float o1 = fac[3 * kChunk + t] * up.x, o2 = fac[4 * kChunk + t] * up.y;
+          const float o1 = fac[3 * kChunk + t], o2 = fac[4 * kChunk + t];
           if (ch * kChunk + t < n)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
               *reinterpret_cast<uint32_t*>(orow + ((size_t)ch * kChunk + t) * a.hv * kHeadDim + 8 * x) =
-                  pack_bf16x2(fmaf(o1, qs[m][x][2 * r], o2 * p[m][x][2 * r]),
-                              fmaf(o1, qs[m][x][2 * r + 1], o2 * p[m][x][2 * r + 1]));
+                  pack_bf16x2(fmaf(o1 * up[x].x, qs[m][x][2 * r], o2 * p[m][x][2 * r]),
+                              fmaf(o1 * up[x].y, qs[m][x][2 * r + 1], o2 * p[m][x][2 * r + 1]));
         }
     }
     return;
   }
 
-  // S[x]: value rows g (0, 1) and g + 8 (2, 3), key dims 8 x + 2 c and + 1, times sig
-  float S[16][4];
+  // S[x]: value rows g (0, 1) and g + 8 (2, 3), key dims 8 x + 2 c and + 1; the state is S times the row's isig
+  float S[16][4], sig[2], isig[2];
   float* const st = a.state + ((size_t)slot * a.hv + h) * kStateElems + (size_t)(row16 + g) * kHeadDim + 2 * c;
 #pragma unroll
   for (int x = 0; x < 16; ++x)
@@ -531,174 +534,154 @@ __global__ void __launch_bounds__(kWarps * 64, kWarps == 2 ? 3 : 1) state_kernel
       const float2 y = L > 0 ? *reinterpret_cast<const float2*>(st + i * 8 * kHeadDim + 8 * x) : make_float2(0.0f, 0.0f);
       S[x][2 * i] = y.x, S[x][2 * i + 1] = y.y;
     }
-  // A power of two that keeps the operands in fp16's range, from the largest of the warp's part of S
-  float sig, isig;
-  {
+  const auto row_max = [&](float x) {
+    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+    return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+  };
+  // A row's largest, `all`, brought into fp16's range; the row is times `was` now.
+  const auto choose = [&](int t, float all, float was) {
+    const Scale sc = all == 0.0f ? Scale{1.0f, 1.0f} : scale_to_top(all);
+    const float by = fminf(was * sc.down, 3.0e38f);  // past fp32's range only for a row of zeros
+#pragma unroll
+    for (int x = 0; x < 16; ++x) S[x][2 * t] *= by, S[x][2 * t + 1] *= by;
+    sig[t] = sc.down, isig[t] = sc.up;
+  };
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
     float top = 0.0f;
 #pragma unroll
-    for (int x = 0; x < 16; ++x) top = max3(max3(top, fabsf(S[x][0]), fabsf(S[x][1])), fabsf(S[x][2]), fabsf(S[x][3]));
-    const Scale sc = scale_of_row(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))));
-    sig = sc.down, isig = sc.up;
-#pragma unroll
-    for (int x = 0; x < 16; ++x)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) S[x][i] *= sig;
+    for (int x = 0; x < 16; ++x) top = max3(top, fabsf(S[x][2 * t]), fabsf(S[x][2 * t + 1]));
+    choose(t, row_max(top), 1.0f);
   }
 
   for (int ch = 0; ch < chunks; ++ch) {
     tc::fence_proxy_async_smem();  // what was read of a place is read before the next bulk copy into it
     __syncthreads();
     const uint8_t* const stage = chain_smem + (ch & 1) * (kChainBytes + kValueBytes);
-    const uint32_t key = smem_u32(stage), tri = key + kKeyBytes;
-    const float* const fac = reinterpret_cast<const float*>(stage + kKeyBytes + 2 * kTriBytes);
-    const float* const sca = fac + kFactors * kChunk;
+    const uint32_t key = smem_u32(stage);
+    const float* const T = reinterpret_cast<const float*>(stage + kKeyBytes);
+    const float* const fac = T + kTBytes / 4;
     uint8_t* const to = hand + (ch & 1) * kHandBytes;
+    if (c == 0) {
+      float* const up = reinterpret_cast<float*>(to - lane * 16 + 12 * 512);
+      up[g] = isig[0], up[8 + g] = isig[1];
+    }
 
-    // values of the rows 16 m + 8 r + g
-    uint32_t v[2][2][2], vmax = 0;
+    // S k' in two parts: rows are value rows g, g + 8, columns tokens 8 t + 2 c (+ 1).  A step's rows of k' are loaded
+    // before the one in front of it is stored for the outputs: a load would wait for that store.
+    float x[4][4] = {}, top[2] = {};
+    const auto keys = [&](int m, uint32_t (&b)[4][2]) {
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
-#pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        const int row = 16 * m + 8 * r + g;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const uint32_t w = *reinterpret_cast<const uint32_t*>(stage + kChainBytes + value_at<kWarps>(row, 2 * warp + t) + 4 * c);
-          v[m][r][t] = ch * kChunk + row < n ? w : 0u;
-        }
-      }
-    // S k' in two parts: rows are tokens 16 r + g (+ 8), columns value rows 8 t + 2 c (+ 1).  A step's rows of k'
-    // are loaded before the one in front of it is stored for the outputs: a load would wait for that store.
-    float sk[2][2][4] = {}, top = 0.0f;
-    uint32_t f[2][4];
-#pragma unroll
-    for (int r = 0; r < 2; ++r) ldmatrix_x4(key + key_at(16 * r + (lane & 15), lane >> 4), f[r][0], f[r][1], f[r][2], f[r][3]);
+      for (int i = 0; i < 2; ++i)
+        ldmatrix_x4(key + key_at(16 * i + (lane & 7) + ((lane >> 4) << 3), 2 * m + ((lane >> 3) & 1)), b[2 * i][0], b[2 * i][1],
+                    b[2 * i + 1][0], b[2 * i + 1][1]);
+    };
+    uint32_t b[2][4][2];
+    keys(0, b[0]);
 #pragma unroll
     for (int m = 0; m < 8; ++m) {
-      uint32_t hi[4], lo[4], e[2][4];  // of both tiles of value rows; the next rows of k'
-      if (m < 7) {
+      uint32_t hi[4], lo[4];
+      if (m < 7) keys(m + 1, b[(m + 1) & 1]);
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
-          ldmatrix_x4(key + key_at(16 * r + (lane & 15), 2 * m + 2 + (lane >> 4)), e[r][0], e[r][1], e[r][2], e[r][3]);
-      }
+      for (int i = 0; i < 4; ++i) split_f16(S[2 * m + (i >> 1)][2 * (i & 1)], S[2 * m + (i >> 1)][2 * (i & 1) + 1], hi[i], lo[i]);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int t = 0; t < 4; ++t) mma_f16_16816(x[t], hi, b[m & 1][t][0], b[m & 1][t][1]);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) split_f16(S[2 * m + i][2 * t], S[2 * m + i][2 * t + 1], hi[2 * t + i], lo[2 * t + i]);
+      for (int t = 0; t < 4; ++t) mma_f16_16816(x[t], lo, b[m & 1][t][0], b[m & 1][t][1]);
+      *reinterpret_cast<uint4*>(to + m * 512) = make_uint4(hi[0], hi[2], hi[1], hi[3]);
 #pragma unroll
-      for (int x = 0; x < 4; ++x) mma_f16_16816(sk[x & 1][x >> 1], f[x & 1], hi[x & 2], hi[(x & 2) + 1]);
-#pragma unroll
-      for (int x = 0; x < 4; ++x) mma_f16_16816(sk[x & 1][x >> 1], f[x & 1], lo[x & 2], lo[(x & 2) + 1]);
-      if (m == 7) {
-#pragma unroll
-        for (int x = 0; x < 8; ++x) {
-          const uint32_t w = v[x >> 2][(x >> 1) & 1][x & 1];
-          vmax = max(vmax, max(w << 16 & 0x7FFF0000u, w & 0x7FFF0000u));
-        }
-        vmax = __reduce_max_sync(0xffffffffu, vmax);
-      }
-      *reinterpret_cast<uint4*>(to + m * 512) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) f[0][i] = e[0][i], f[1][i] = e[1][i];
+      for (int i = 0; i < 4; ++i) top[i & 1] = max3(top[i & 1], fabsf(S[2 * m + (i >> 1)][2 * (i & 1)]), fabsf(S[2 * m + (i >> 1)][2 * (i & 1) + 1]));
     }
+    // values of the tokens 8 t + 2 c, + 1
+    uint32_t v[2][4];
 #pragma unroll
-    for (int x = 0; x < 16; ++x) top = max3(max3(top, fabsf(S[x][0]), fabsf(S[x][1])), fabsf(S[x][2]), fabsf(S[x][3]));
-    const float4 s0 = *reinterpret_cast<const float4*>(sca), s1 = *reinterpret_cast<const float4*>(sca + 4);
-    // the scale for x, u and the state behind the chunk, by bounds of all of them
-    float nsig, nisig;
-    {
-      const float x = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top))) * isig;
-      const float bx = at<kMaxB>(s0, s1) * (__uint_as_float(vmax) + x * at<kSumA>(s0, s1)), bu = at<kSumT>(s0, s1) * bx;
-      const float all = fmaxf(max3(bx, bu, at<kMaxC>(s0, s1) * bu), fmaf(at<kSumC>(s0, s1), bu, x * fabsf(at<kF>(s0, s1))));
-      // all * nsig in [2^13, 2^14): sums of products are rounded up past it by less than a factor of two
-      const uint32_t y = min(max(__float_as_uint(all) >> 23, 14u), 253u);
-      nsig = all == 0.0f ? sig : __uint_as_float((254u + 13u - y) << 23);
-      nisig = all == 0.0f ? isig : __uint_as_float((y - 13u) << 23);
-    }
-    *reinterpret_cast<float2*>(to + 10 * 512) = make_float2(isig, nisig);
-    // x, in two parts as B operands
-    uint32_t xh[2][2][2], xl[2][2][2];
+    for (int r = 0; r < 2; ++r)
+      ldmatrix_x4_trans(key + kChainBytes + value_at<kWarps>(lane, 2 * warp + r), v[r][0], v[r][1], v[r][2], v[r][3]);
+    // x as it is, in tf32: the tokens' values, and T's entries, have sizes of their own, which fp16 would need a scale for
+    float xl[4][4];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int t = 0; t < 4; ++t) {
+      const float2 fa = *reinterpret_cast<const float2*>(fac + 8 * t + 2 * c);
+      const float2 be = *reinterpret_cast<const float2*>(fac + kChunk + 8 * t + 2 * c);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const int row = 16 * m + 8 * r + g;
-        const float fai = fac[row] * isig, bn = fac[kChunk + row] * nsig;
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float x0 = bn * (bf16_lo(v[m][r][t]) - fai * sk[m][t][2 * r]);
-          const float x1 = bn * (bf16_hi(v[m][r][t]) - fai * sk[m][t][2 * r + 1]);
-          split_f16(x0, x1, xh[m][t][r], xl[m][t][r]);
-          xh[m][t][r] = transpose8(xh[m][t][r]);
-          xl[m][t][r] = transpose8(xl[m][t][r]);
-        }
+        x[t][2 * r] = be.x * (bf16_lo(v[r][t]) - fa.x * (isig[r] * x[t][2 * r]));
+        x[t][2 * r + 1] = be.y * (bf16_hi(v[r][t]) - fa.y * (isig[r] * x[t][2 * r + 1]));
+        split_tf32(x[t][2 * r], x[t][2 * r], xl[t][2 * r]);
+        split_tf32(x[t][2 * r + 1], x[t][2 * r + 1], xl[t][2 * r + 1]);
       }
-    // u = T x
-    uint32_t th_[3][4], tl[3][4];  // T: rows and columns 0, 0; 16, 0; 16, 16
-#pragma unroll
-    for (int x = 0; x < 3; ++x) {
-      ldmatrix_x4_trans(tri_a(tri, (x + 1) / 2, x / 2, lane), th_[x][0], th_[x][1], th_[x][2], th_[x][3]);
-      ldmatrix_x4_trans(tri_a(tri + kTriBytes, (x + 1) / 2, x / 2, lane), tl[x][0], tl[x][1], tl[x][2], tl[x][3]);
     }
-    float u[2][2][4] = {};
+    // u' = x' T': 8 x 8 pieces of T up to its diagonal.  The k indices c and c + 4 of a product are the tokens 2 c and
+    // 2 c + 1 in both operands, so that x is A as it came.
+    float2 Th[10], Tl[10];
 #pragma unroll
-    for (int p = 0; p < 3; ++p)  // the parts' products: one each of all tiles, then the next
+    for (int i = 0, y = 0; i < 4; ++i)
 #pragma unroll
-      for (int x = 0; x < 3; ++x)
+      for (int j = 0; j <= i; ++j, ++y) {
+        Th[y] = *reinterpret_cast<const float2*>(T + t_at(8 * i + g, 8 * j + 2 * c));  // whose low 13 bits do not count
+        Tl[y] = make_float2(below_tf32(Th[y].x), below_tf32(Th[y].y));
+      }
+    float u[4][4] = {};
 #pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int m = (x + 1) / 2, jt = x / 2;
-          const uint32_t(&b)[2] = p == 1 ? xl[jt][t] : xh[jt][t];
-          mma_f16_16816(u[m][t], p == 2 ? tl[x] : th_[x], b[0], b[1]);
-        }
-    // a factor past fp32's range belongs to a state of zeros
-    const float grow = fminf(at<kF>(s0, s1) * isig * nsig, 3.0e38f), t_up = at<kTUp>(s0, s1);
+    for (int p = 0; p < 3; ++p)
 #pragma unroll
-    for (int x = 0; x < 16; ++x)
+      for (int o = 0; o < 10; ++o) {
+        // rows of T in an order that leaves an accumulator two other products' time
+        constexpr int kRow[10] = {3, 2, 0, 3, 1, 3, 2, 3, 1, 2}, kCol[10] = {0, 0, 0, 1, 0, 2, 1, 3, 1, 2};
+        const int i = kRow[o], j = kCol[o];
+        const float(&y)[4] = p == 1 ? xl[j] : x[j];
+        const float xa[4] = {y[0], y[2], y[1], y[3]};
+        const float2 z = (p == 0 ? Tl : Th)[i * (i + 1) / 2 + j];
+        mma_tf32_1688(u[i], xa, z.x, z.y);
+      }
+    const float fall = fac[kFactors * kChunk];
+    // u for the outputs; with its factors, in two parts, for the state
+    float most[2] = {};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) S[x][i] *= grow;
-    // u for the outputs (one part), and with its factors, value rows by tokens, for the state (two)
-    uint32_t ch_[2][4], cl[2][4];
-#pragma unroll
-    for (int m = 0; m < 2; ++m) {
-      uint32_t uo[2][2];
+    for (int t = 0; t < 4; ++t) {
+      *reinterpret_cast<float4*>(to + (8 + t) * 512) = make_float4(u[t][0], u[t][1], u[t][2], u[t][3]);
+      const float2 fc = *reinterpret_cast<const float2*>(fac + 2 * kChunk + 8 * t + 2 * c);
 #pragma unroll
       for (int r = 0; r < 2; ++r) {
-        const float fc = fac[2 * kChunk + 16 * m + 8 * r + g];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const float u0 = u[m][t][2 * r] * t_up;
-          const float u1 = u[m][t][2 * r + 1] * t_up;
-          split_f16(u0 * fc, u1 * fc, ch_[m][2 * r + t], cl[m][2 * r + t]);
-          ch_[m][2 * r + t] = transpose8(ch_[m][2 * r + t]);
-          cl[m][2 * r + t] = transpose8(cl[m][2 * r + t]);
-          uo[t][r] = transpose8(pack_f16x2(u0, u1));
-        }
+        u[t][2 * r] *= fc.x, u[t][2 * r + 1] *= fc.y;
+        most[r] = max3(most[r], fabsf(u[t][2 * r]), fabsf(u[t][2 * r + 1]));
       }
-      *reinterpret_cast<uint4*>(to + (8 + m) * 512) = make_uint4(uo[0][0], uo[0][1], uo[1][0], uo[1][1]);
     }
+    // the rows' scales behind the chunk: 32 updates, elements of k' below 4
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      const float was = fall * isig[r];
+      choose(r, fmaf(row_max(top[r]), was, 4.0f * kChunk * row_max(most[r])), was);
+    }
+    uint32_t uh[2][4], ul[2][4];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float (&y)[4] = u[2 * j + (i >> 1)];
+        split_f16(y[2 * (i & 1)] * sig[i & 1], y[2 * (i & 1) + 1] * sig[i & 1], uh[j][i], ul[j][i]);
+      }
     // the state behind the chunk
 #pragma unroll
     for (int m = 0; m < 8; ++m)
 #pragma unroll
-      for (int jt = 0; jt < 2; ++jt) {
+      for (int j = 0; j < 2; ++j) {
         uint32_t b0[2], b1[2];
-        ldmatrix_x4_trans(key + key_at(16 * jt + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * m + (lane >> 4)), b0[0], b1[0],
+        ldmatrix_x4_trans(key + key_at(16 * j + (lane & 7) + ((lane >> 3) & 1) * 8, 2 * m + (lane >> 4)), b0[0], b1[0],
                           b0[1], b1[1]);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-          mma_f16_16816(S[2 * m + i], ch_[jt], b0[i], b1[i]);
-          mma_f16_16816(S[2 * m + i], cl[jt], b0[i], b1[i]);
+          mma_f16_16816(S[2 * m + i], uh[j], b0[i], b1[i]);
+          mma_f16_16816(S[2 * m + i], ul[j], b0[i], b1[i]);
         }
       }
-    sig = nsig, isig = nisig;
   }
   __syncthreads();  // the last chunk is handed over
 #pragma unroll
   for (int x = 0; x < 16; ++x)
 #pragma unroll
     for (int i = 0; i < 2; ++i)
-      *reinterpret_cast<float2*>(st + i * 8 * kHeadDim + 8 * x) = make_float2(S[x][2 * i] * isig, S[x][2 * i + 1] * isig);
+      *reinterpret_cast<float2*>(st + i * 8 * kHeadDim + 8 * x) = make_float2(S[x][2 * i] * isig[i], S[x][2 * i + 1] * isig[i]);
 }
 
 template <int kWarps>
@@ -718,12 +701,12 @@ int num_sms() {
   return n;
 }
 
-// Two warps of the chain to a CTA, up to three CTAs on an SM, or four warps and one CTA.  A chunk takes the chain 1.1 us
-// with one CTA of two on the SM, 2.0 with two, 2.35 with three, and 1.45 in a CTA of four: whichever ends first by how
+// Two warps of the chain to a CTA, up to three CTAs on an SM, or four warps and one CTA.  A chunk takes the chain 21
+// parts with one CTA of two on the SM, 40 with two, 47 with three, and 29 in a CTA of four: whichever ends first by how
 // many rounds its grid makes, lanes being of one length.  Of 2,048 tokens a lane, us with two and with four: 16 heads, two
-// lanes 92 and 110, three 148 and 116, four 155 and 123, six 188 and 224; 32 heads, four lanes 261 and 238, eight 445
-// and 468.  Short lanes make many short rounds, of which those of three CTAs an SM overlap: 60 lanes of 100 tokens, 16
-// heads, 133 and 145.
+// lanes 98 and 119, three 160 and 124, four 167 and 131, six 206 and 244; 32 heads, four lanes 285 and 257, eight 486
+// and 507.  Short lanes make many short rounds, of which those of three CTAs an SM overlap: 60 lanes of 100 tokens, 16
+// heads, 142 and 151.
 int launch_state(const PromptArgs& a, cudaStream_t s) {
   const int64_t sms = num_sms() > 0 ? num_sms() : 1, twos = (int64_t)a.hv * a.num_lanes * (kHeadDim / 32);
   const int64_t rest = twos % (3 * sms);

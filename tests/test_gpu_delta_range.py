@@ -25,7 +25,7 @@ import numpy as np
 import pytest
 import torch
 
-from test_gpu_delta import D, EPS, SCALE, _gen, _i32, _norm, _status, _tree, _workspace
+from test_gpu_delta import D, EPS, INF, SCALE, _gen, _i32, _norm, _status, _tree, _workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -161,6 +161,24 @@ def test_windows_that_expand(kind, W, how):
                *(y[i] for y in x), parent=parents[i] if parents else None, eps=eps)
 
 
+@pytest.mark.parametrize("kind,lens", [("one_key", [32, 5, 17]), ("long_keys", [12, 7]), ("norms_to_4", [32, 3]),
+                                       ("growing", [64, 33, 20]), ("small_strengths", [64, 40]), ("small_keys", [64, 40]),
+                                       ("tiny_keys", [40, 40])])
+def test_prompts_that_expand(kind, lens):
+    import speculative_decode_verify_append_gb300 as sdva
+    hk, hv, B, T = 1, 2, len(lens), sum(lens)
+    *x, eps = _rows(200, (T,), hk, hv, kind)
+    state = torch.randn((B, hv, D, D), generator=_gen(9), device="cuda") * (kind != "tiny_keys")
+    before, st = state.clone(), _status()
+    out = torch.empty((T, hv, D), dtype=torch.bfloat16, device="cuda")
+    cu = [0, *np.cumsum(lens)]
+    sdva.prompt_delta(state, *x, _i32(cu), _i32(range(B)), SCALE, out, _workspace(T, B, hk, hv), qk_eps=eps, status=st)
+    assert int(st.item()) == 0
+    for i in range(B):
+        r = slice(cu[i], cu[i + 1])
+        _check(before[i], out[r], None, state[i], *(y[r] for y in x), eps=eps)
+
+
 @pytest.mark.parametrize("W", [2, 4, 8, 16])
 def test_nothing_to_remember_and_growing_decays(W):
     """A state of zeros and updates of zeros stay zeros, whatever the decays are."""
@@ -189,6 +207,22 @@ def _sized(lead, seed=7):
 
 
 @pytest.mark.parametrize("power", [12, 18, 30])
+def test_prompt_tokens_of_different_sizes(power):
+    """The last tokens of a chunk are 2^power times the first ones, which do not know of them."""
+    import speculative_decode_verify_append_gb300 as sdva
+    n = 64
+    x = _sized((n,))
+    for c in (16, 60):
+        x[2][c:c + 4] *= 2.0 ** power
+    x[3][32] = -INF  # the second chunk starts small again
+    state = torch.randn((1, 2, D, D), generator=_gen(1), device="cuda")
+    before = state.clone()
+    out = torch.empty((n, 2, D), dtype=torch.bfloat16, device="cuda")
+    sdva.prompt_delta(state, *x, _i32([0, n]), _i32([0]), SCALE, out, _workspace(n, 1, 1, 2))
+    _check(before[0], out, None, state[0], *x)
+
+
+@pytest.mark.parametrize("power", [12, 18, 30])
 @pytest.mark.parametrize("keep", [True, False])
 def test_window_tokens_of_different_sizes(power, keep):
     import speculative_decode_verify_append_gb300 as sdva
@@ -204,17 +238,22 @@ def test_window_tokens_of_different_sizes(power, keep):
 
 
 @pytest.mark.parametrize("power", [12, 18, 30])
-@pytest.mark.parametrize("what", ["recorded", "committed"])
+@pytest.mark.parametrize("what", ["prompt", "recorded", "committed"])
 def test_value_rows_of_different_sizes(power, what):
     """One value row of sixteen is 2^power times the others, in the state and in the values."""
     import speculative_decode_verify_append_gb300 as sdva
-    n = 16
-    x = _sized((1, n))
+    n = 64 if what == "prompt" else 16
+    x = _sized((n,) if what == "prompt" else (1, n))
     state = torch.randn((1, 2, D, D), generator=_gen(3), device="cuda")
     state[:, :, 5::16] *= 2.0 ** power
     x[2][..., 5::16] *= 2.0 ** power
     before = state.clone()
-    out = torch.empty((1, n, 2, D), dtype=torch.bfloat16, device="cuda")
-    deltas = torch.empty((1, n, 2, D), device="cuda") if what == "recorded" else None
-    sdva.verify_delta(state, *x, _i32([0]), SCALE, out, deltas)
-    _check(before[0], out[0], None if deltas is None else deltas[0], None if what == "recorded" else state[0], *(y[0] for y in x))
+    if what == "prompt":
+        out, deltas = torch.empty((n, 2, D), dtype=torch.bfloat16, device="cuda"), None
+        sdva.prompt_delta(state, *x, _i32([0, n]), _i32([0]), SCALE, out, _workspace(n, 1, 1, 2))
+    else:
+        out = torch.empty((1, n, 2, D), dtype=torch.bfloat16, device="cuda")
+        deltas = torch.empty((1, n, 2, D), device="cuda") if what == "recorded" else None
+        sdva.verify_delta(state, *x, _i32([0]), SCALE, out, deltas)
+        out, deltas, x = out[0], None if deltas is None else deltas[0], [y[0] for y in x]
+    _check(before[0], out, deltas, None if what == "recorded" else state[0], *x)
