@@ -19,6 +19,7 @@
 
 #include "sdva_common.cuh"
 #include "sdva_internal.cuh"
+#include "tc_primitives.cuh"
 
 namespace sdva {
 namespace delta {
@@ -55,6 +56,14 @@ __device__ __forceinline__ Scale scale_to_top(float amax) {
 // below 2^-64 or so, whose kn is below 2^-54 then and taken as 0.
 __device__ __forceinline__ float row_factor(float sum_sq, float eps, Scale s) {
   return eps < 0.0f ? s.up : rsqrtf(sum_sq + eps * s.down * s.down);
+}
+
+// Waits for the bulk copies that `bar` counts.  Where that takes more than `limit` cycles (0: where they are not there
+// yet) it returns false, but not before they are, or the default limit has run out too: no copy outlives the CTA.
+__device__ __forceinline__ bool copies_here(uint32_t bar, uint32_t parity, int* never, long long limit) {
+  if (tc::mbar_test_wait(bar, parity) || (limit > 0 && tc::mbar_wait<false>(bar, parity, never, limit))) return true;
+  tc::mbar_wait<false>(bar, parity, never);
+  return false;
 }
 
 // The transpose of an 8 x 8 matrix of 16-bit elements held as two to a thread.

@@ -35,7 +35,6 @@
 // in the kernel): the loads take 5,000, S k' and S q' 3,000 (T is there by then)
 // and the rest 3,000; with two on an SM, 128 KB are under way.
 #include "delta_common.cuh"
-#include "tc_primitives.cuh"
 
 namespace sdva {
 namespace {
@@ -235,7 +234,8 @@ struct VerifySmem {
   float k_own[kRows];  // 1 / sqrt(|k|^2 + eps)
   float fa[kRows], fc[kRows], o1[kRows], o2[kRows];
   float f;
-  int never;  // 0: no role's wait ends another's
+  int never;    // 0: no role's wait ends another's
+  int gave_up;  // whether one ran out
 };
 
 // Sixteen floats of shared memory, the same for every thread.
@@ -263,7 +263,7 @@ __device__ __forceinline__ bool ways(VerifySmem& s, const VerifyArgs& a, int m, 
     s.eg[m][lane] = on ? expf(ld) : 1.0f;
     if (m == 0) s.beta[lane] = on ? beta : 0.0f;
     s.par[m][lane] = p;
-    if (m == 0 && lane == 0) s.never = 0;
+    if (m == 0 && lane == 0) s.never = s.gave_up = 0;
   }
   __syncwarp();
   float x[kRows];
@@ -449,14 +449,8 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a, long 
   }
   const size_t at0 = (row0 * a.hv + h) * kHeadDim + row16 + 2 * c;  // this thread's first output
   const size_t row_out = (size_t)a.hv * kHeadDim;
-  const auto state_here = [&] {
-    if (!tc::mbar_wait<false>(bar, 0, &s.never, limit)) {
-      if (lane == 0) raise_status(a.status, SDVA_STATUS_TIMEOUT);
-      tc::mbar_wait<false>(bar, 0, &s.never);  // the copies end before the CTA does
-    }
-  };
   if (n == 0) {
-    if (warp < kWarps && lr.n > 0) state_here();
+    if (warp < kWarps && lr.n > 0) copies_here(bar, 0, &s.never, limit);
     cp_async_wait<0>();  // v: no copy outlives the CTA
     if (warp < kWarps)
       for (int r = g; r < W; r += 8)
@@ -474,7 +468,10 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a, long 
   }
   const uint32_t kbase = smem_u32(s.key[0]), qbase = smem_u32(s.key[1]);
   const int a_row = lane & 15, a_piece = lane >> 4;
-  state_here();
+  if (!copies_here(bar, 0, &s.never, limit)) {
+    raise_status(a.status, SDVA_STATUS_TIMEOUT);
+    s.gave_up = 1;
+  }
   // S k' in two parts, S q' in one; of the state value rows 8 t + g, key dims 16 m + 4 c ..
   const auto state_of = [&](int t, int m) {
     return *reinterpret_cast<const float4*>(mine + (8 * t + g) * kStatePitch + 64 * m + 16 * c);
@@ -604,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 2) window_kernel(VerifyArgs a, long 
       for (int r = 0; r < 2; ++r) split_f16(u[2 * r] * in[t], u[2 * r + 1] * in[t], ch[2 * r + t], cl[2 * r + t]);
     }
   }
-  if (kCommit) {
+  if (kCommit && s.gave_up == 0) {  // else the head keeps its state
     // S as accumulators: value rows g (t = 0) and g + 8 (t = 1), columns as the rows of k' have their dims
     const float f = s.f;
 #pragma unroll
