@@ -760,8 +760,9 @@ int commit_delta(float* state, int num_slots, const void* k, int64_t k_stride, c
  * `cycles` clock cycles (default about 4e9, two seconds); the CTA then
  * raises SDVA_STATUS_TIMEOUT, waits (with its own bound) for the copies and
  * tensor-core work it issued, frees its tensor memory and returns, leaving
- * the context usable (the output of such a call is undefined; a head whose CTA of
- * verify_delta gave up keeps its state).  A negative
+ * the context usable (the output of such a call is undefined; of the states of
+ * prompt_delta and verify_delta the value rows of such a CTA, 32 or more of a
+ * head, stay as they were).  A negative
  * value restores the default.  Returns the previous limit.  Applies to
  * calls enqueued after it returns; not synchronised with concurrent calls.
  * Meant for tests that make a wait run out.

@@ -47,7 +47,6 @@
 // chunk there (8 warps' 158 of 2,048 multiply-adds at 3,900 a cycle), and each of
 // its three dependent steps would add a way through tensor memory.
 #include "delta_common.cuh"
-#include "tc_primitives.cuh"
 
 namespace sdva {
 namespace {
@@ -366,7 +365,8 @@ __global__ void __launch_bounds__(kWarps * 64, kWarps == 2 ? 3 : 1) state_kernel
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int never;  // 0: no role's wait ends another's
   const int th = threadIdx.x, lane = th & 31, g = lane >> 2, c = lane & 3;
-  if (th == 0) never = 0;
+  __shared__ int gave_up;  // whether a wait ran out
+  if (th == 0) never = gave_up = 0;
   const bool chain = th < kWarps * 32;
   const int warp = (th >> 5) & (kWarps - 1);
   const int h = blockIdx.y, kh = h / (a.hv / a.hk);
@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(kWarps * 64, kWarps == 2 ? 3 : 1) state_kernel
 
   if (!chain) {
     const int ot = th - kWarps * 32;
-    bool dead = false;  // of thread 0: a wait ran out; nothing more is copied, and what follows is undefined
+    bool dead = false;  // of thread 0: a wait ran out; no more records are copied, and what follows is undefined
     __shared__ uint64_t bars[2];
     if (ot == 0) {
       tc::mbar_init(smem_u32(&bars[0]), 1);
@@ -455,10 +455,9 @@ __global__ void __launch_bounds__(kWarps * 64, kWarps == 2 ? 3 : 1) state_kernel
     fetch(-1, smem_u32(&bars[0]));
     for (int i = 0; i <= chunks; ++i) {
       const uint32_t bar = smem_u32(&bars[i & 1]), parity = (i >> 1) & 1;
-      if (ot == 0 && !dead && !tc::mbar_wait<false>(bar, parity, &never, limit)) {
+      if (ot == 0 && !dead && !copies_here(bar, parity, &never, limit)) {
         raise_status(a.status, SDVA_STATUS_TIMEOUT);
-        dead = true;
-        tc::mbar_wait<false>(bar, parity, &never);  // the copies end before the CTA does
+        dead = gave_up = 1;
       }
       cp_async_wait_all();
       tc::fence_proxy_async_smem();
@@ -677,6 +676,7 @@ __global__ void __launch_bounds__(kWarps * 64, kWarps == 2 ? 3 : 1) state_kernel
       }
   }
   __syncthreads();  // the last chunk is handed over
+  if (gave_up) return;  // the state stays as it was
 #pragma unroll
   for (int x = 0; x < 16; ++x)
 #pragma unroll

@@ -1,11 +1,11 @@
-"""The waits of verify_delta that run out, without a fault: with
+"""The waits of prompt_delta and verify_delta that run out, without a fault: with
 a limit of zero cycles a wait for copies that are not there yet gives up.  The
 call says so and returns, each CTA's part of a state is what it was or what the
 call makes of it, and the next call is right."""
 import pytest
 import torch
 
-from test_gpu_delta import D, SCALE, _gen, _i32, _inputs, _status
+from test_gpu_delta import D, SCALE, _gen, _i32, _inputs, _status, _workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -26,6 +26,33 @@ def _parts_kept(state, before, after, rows):
     kept, moved = (x == b).all(1), (x == a).all(1)
     assert (kept | moved).all()
     return int((kept & ~moved).sum())
+
+
+@pytest.mark.parametrize("lens,hk,hv", [([40], 1, 2), ([700, 1, 0, 64, 333], 2, 4), ([600] * 12, 4, 16)])
+def test_a_prompt_that_gives_up_keeps_its_state(lens, hk, hv):
+    import speculative_decode_verify_append_gb300 as sdva
+    B, T = len(lens), sum(lens)
+    g = _gen(1)
+    x = _inputs(g, (T,), hk, hv)
+    cu = [0]
+    for n in lens:
+        cu.append(cu[-1] + n)
+    before = torch.randn((B, hv, D, D), generator=g, device="cuda")
+
+    def run(state, out, st):
+        sdva.prompt_delta(state, *x, _i32(cu), _i32(range(B)), SCALE, out, _workspace(T, B, hk, hv), status=st)
+
+    good, out, st = before.clone(), torch.empty((T, hv, D), dtype=torch.bfloat16, device="cuda"), _status()
+    run(good, out, st)
+    assert int(st.item()) == 0
+    state, other = before.clone(), torch.empty_like(out)
+    _impatient(lambda: run(state, other, st))
+    assert int(st.item()) == sdva.STATUS_TIMEOUT
+    assert _parts_kept(state, before, good, 32) > 0
+    st.zero_()
+    state.copy_(before)
+    run(state, other, st)
+    assert int(st.item()) == 0 and torch.equal(state, good) and torch.equal(other, out)
 
 
 @pytest.mark.parametrize("W", [4, 16])
