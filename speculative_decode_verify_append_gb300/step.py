@@ -155,14 +155,17 @@ class DeltaStep:
         self.out = torch.empty((num_slots, window, num_v_heads, 128), dtype=torch.bfloat16, device=dev)
         self.deltas = torch.empty((num_slots, window, num_v_heads, 128), device=dev)
         self.status = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.prompt_out = torch.empty((max_tokens, num_v_heads, 128), dtype=torch.bfloat16, device=dev)
+        self.prompt_out = torch.zeros((max_tokens, num_v_heads, 128), dtype=torch.bfloat16, device=dev)
         nbytes = prompt_delta_workspace_size(max_tokens, num_slots, num_k_heads, num_v_heads) if max_tokens else 0
         self.workspace = torch.empty(nbytes, dtype=torch.uint8, device=dev)
 
     def prompt(self, q, k, v, log_decay, beta, cu_tokens, slots, seq_lens=None, stream=None):
         """Packed prompts (q, k [T][Hk][128], v [T][Hv][128]); lanes with seq_lens 0
-        start from zeros.  Returns out [T][Hv][128], which the next prompt
-        writes again."""
+        start from zeros, the others, and without seq_lens all, go on from what
+        their slots hold: a slot that another request had is started with 0.
+        Returns out [T][Hv][128], which the next prompt writes again.  Rows of a
+        lane that is skipped (status says so) and rows outside the lanes are not
+        written: they hold zeros or an earlier call's."""
         out = self.prompt_out[:q.shape[0]]
         prompt_delta(self.state, q, k, v, log_decay, beta, cu_tokens, slots, self.scale, out, self.workspace, seq_lens,
                      self.qk_eps, self.status, stream)
