@@ -258,6 +258,8 @@ typedef enum {
  *   positions  : nullable int32 [num_lanes][n_new]: the position of every row,
  *                for a draft tree (L_b + a slot's depth).  NULL: L_b + i.  The
  *                row goes to cache slot L_b + i either way.
+ *   num_q_heads is a multiple of the cache's num_kv_heads (else
+ *   SDVA_ERR_INVALID).
  *   q_out      : bf16 [num_lanes][n_new][num_q_heads][128] (out)
  *   k_out      : nullable bf16 [num_lanes][n_new][num_kv_heads][128] (out): the
  *                turned keys.
