@@ -91,14 +91,19 @@ __device__ __forceinline__ void split_f16(float2 x, uint32_t& hi, uint32_t& lo) 
 
 __device__ __forceinline__ float2 f16x2_to_f32(uint32_t x) { return __half22float2(*reinterpret_cast<const __half2*>(&x)); }
 
-// x in two parts of 11 bits, off by 2^-22 |x| at most in all of fp32's range (of lo what is behind them does not count).
+// The upper 11 bits of x.
+__device__ __forceinline__ float upper_11(float x) { return __uint_as_float(__float_as_uint(x) & 0xFFFFE000u); }
+// x in two parts of 11 bits, off by 2^-22 |x| at most in all of fp32's range.
 __device__ __forceinline__ void split_tf32(float x, float& hi, float& lo) {
   hi = to_tf32(x);
+  lo = upper_11(x - hi);
+}
+// x rounded to 22 bits, and those in two parts.
+__device__ __forceinline__ float round_22(float x) { return __uint_as_float((__float_as_uint(x) + 2u) & ~3u); }
+__device__ __forceinline__ void split_22(float x, float& hi, float& lo) {
+  hi = upper_11(x);
   lo = x - hi;
 }
-// x rounded to 22 bits, of which a product in tf32 takes the upper 11, and the others.
-__device__ __forceinline__ float round_22(float x) { return __uint_as_float((__float_as_uint(x) + 2u) & ~3u); }
-__device__ __forceinline__ float below_tf32(float x) { return x - __uint_as_float(__float_as_uint(x) & 0xFFFFE000u); }
 
 __device__ __forceinline__ float max3(float x, float y, float z) {
   float r;

@@ -617,8 +617,9 @@ __global__ void __launch_bounds__(kWarps * 64, kWarps == 2 ? 3 : 1) state_kernel
     for (int i = 0, y = 0; i < 4; ++i)
 #pragma unroll
       for (int j = 0; j <= i; ++j, ++y) {
-        Th[y] = *reinterpret_cast<const float2*>(T + t_at(8 * i + g, 8 * j + 2 * c));  // whose low 13 bits do not count
-        Tl[y] = make_float2(below_tf32(Th[y].x), below_tf32(Th[y].y));
+        const float2 z = *reinterpret_cast<const float2*>(T + t_at(8 * i + g, 8 * j + 2 * c));
+        split_22(z.x, Th[y].x, Tl[y].x);
+        split_22(z.y, Th[y].y, Tl[y].y);
       }
     float u[4][4] = {};
 #pragma unroll

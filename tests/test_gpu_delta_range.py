@@ -257,3 +257,49 @@ def test_value_rows_of_different_sizes(power, what):
         sdva.verify_delta(state, *x, _i32([0]), SCALE, out, deltas)
         out, deltas, x = out[0], None if deltas is None else deltas[0], [y[0] for y in x]
     _check(before[0], out, deltas, None if what == "recorded" else state[0], *x)
+
+
+@pytest.mark.parametrize("power", [-100, 100])
+@pytest.mark.parametrize("what", ["prompt", "recorded", "committed"])
+def test_values_near_the_ends_of_fp32(power, what):
+    import speculative_decode_verify_append_gb300 as sdva
+    n = 40 if what == "prompt" else 12
+    x = _sized((n,) if what == "prompt" else (1, n))
+    x[2] *= 2.0 ** power
+    state = torch.randn((1, 2, D, D), generator=_gen(4), device="cuda") * 2.0 ** power
+    before, st = state.clone(), _status()
+    if what == "prompt":
+        out, deltas = torch.empty((n, 2, D), dtype=torch.bfloat16, device="cuda"), None
+        sdva.prompt_delta(state, *x, _i32([0, n]), _i32([0]), SCALE, out, _workspace(n, 1, 1, 2), status=st)
+    else:
+        out = torch.empty((1, n, 2, D), dtype=torch.bfloat16, device="cuda")
+        deltas = torch.empty((1, n, 2, D), device="cuda") if what == "recorded" else None
+        sdva.verify_delta(state, *x, _i32([0]), SCALE, out, deltas, status=st)
+        out, deltas, x = out[0], None if deltas is None else deltas[0], [y[0] for y in x]
+    assert int(st.item()) == 0
+    _check(before[0], out, deltas, None if what == "recorded" else state[0], *x)
+
+
+@pytest.mark.parametrize("what", ["prompt", "recorded", "committed"])
+def test_a_state_that_is_forgotten_and_one_that_is_replaced(what):
+    """Large states that a token forgets (a decay of 0), and small ones behind which all is larger."""
+    import speculative_decode_verify_append_gb300 as sdva
+    n = 40 if what == "prompt" else 12
+    x = _sized((2 * n,) if what == "prompt" else (2, n))
+    state = torch.randn((2, 2, D, D), generator=_gen(5), device="cuda")
+    state[0] *= 2.0 ** 90
+    state[1] *= 2.0 ** -90
+    x[2].view(2, n, 2, D)[0, :5] *= 2.0 ** 90
+    x[3].view(2, n, 2)[0, 5] = -INF
+    before, st = state.clone(), _status()
+    out = torch.empty(x[2].shape, dtype=torch.bfloat16, device="cuda")
+    if what == "prompt":
+        deltas = None
+        sdva.prompt_delta(state, *x, _i32([0, n, 2 * n]), _i32([0, 1]), SCALE, out, _workspace(2 * n, 2, 1, 2), status=st)
+        out, x = out.view(2, n, 2, D), [y.view(2, n, *y.shape[1:]) for y in x]
+    else:
+        deltas = torch.empty((2, n, 2, D), device="cuda") if what == "recorded" else None
+        sdva.verify_delta(state, *x, _i32([0, 1]), SCALE, out, deltas, status=st)
+    assert int(st.item()) == 0
+    for i in range(2):
+        _check(before[i], out[i], None if deltas is None else deltas[i], None if what == "recorded" else state[i], *(y[i] for y in x))
