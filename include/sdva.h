@@ -669,8 +669,9 @@ int token_logprobs(const void* logits, int logits_dtype, int64_t row_stride, int
  *   state, q, k, v, out and deltas are 16-byte aligned (else SDVA_ERR_INVALID).
  * Precondition: the values of a lane's rows and of the state that it starts
  * from are finite (log decays: or -inf), and they, the states and updates that
- * follow, their products and, with a qk_eps of 0, the squares of q and k stay in
- * fp32's range, 2^16 below its upper end (a row of zeros has no direction then).
+ * follow, their products and the squares of q and k stay in fp32's range, 2^16
+ * below its upper end; with a qk_eps of 0 the squares do not underflow either (a
+ * row of zeros has no direction then).
  * That a token's map expands (beta |kn|^2 above 2, log decays above 0) is allowed.
  * Other lanes' and other rows' values do not reach a lane.
  * Accuracy: states, updates and sums are fp32.  Products on the tensor cores

@@ -34,7 +34,7 @@
 // failed there, the calls below took 668, 445, 119 and 11.5 us.
 //
 // 16 / 32 heads: one prompt of 16,384 tokens 722 us, of which 104 are
-// chunk_kernel's (shared memory comes first: L1 was at 65% of its peak, DRAM at 17%)
+// chunk_kernel's (shared memory comes first: L1 is at 79% of its peak, DRAM at 16%)
 // and the rest 512 chunks at 1.21 us; eight of 2,048 486 us.  8 / 24 heads, eight
 // prompts of 1 to 2,011 tokens 126 us; 4 / 8 heads, 40 tokens 10.5.  A chunk is
 // 158 products of 16 x 8 x 16 (or 8, tf32) a warp, 8 cycles each, in some 2,300

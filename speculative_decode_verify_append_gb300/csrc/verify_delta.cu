@@ -30,10 +30,10 @@
 //
 // 64 lanes, 16 / 32 heads (134 MB of states), and what a copy's rate would take:
 // a plain step 43.6 us (40.4), 16 rows recorded 44.7 (26.4), committed 66.3
-// (44.0), the commit of up to 16 updates 52.3 (43.3).  8 lanes of 16 rows 7.3 us,
-// one lane's commit 3.5.  A window's CTA lives some 11,000 cycles (clock readings
-// in the kernel): the loads take 5,000, S k' and S q' 3,000 (T is there by then)
-// and the rest 3,000; with two on an SM, 128 KB are under way.
+// (44.0), the commit of up to 16 updates, 4.7 on average, 52.3 (41.1).  8 lanes of
+// 16 rows 7.3 us, one lane's commit 3.5.  A window's CTA lives some 10,500 cycles
+// (clock readings in the kernel): the loads take 5,400, S k' and S q' 2,900 (T is
+// there by then) and the rest 2,100; with two on an SM, 128 KB are under way.
 #include "delta_common.cuh"
 
 namespace sdva {
